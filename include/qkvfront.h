@@ -59,12 +59,14 @@ extern "C" {
 #define QKVF_ERR_SIZES 7         /* cos_sin_rows < 1, num_pages < 1, or too large */
 #define QKVF_ERR_VARIANT 8       /* an explicit variant that this shape cannot use */
 #define QKVF_ERR_ARG 9           /* any other bad argument */
+#define QKVF_ERR_LAYOUT 10       /* head counts, head_dim, rotary width, dtype or strides (rope*, prefix_attn) */
 
 /* ---- device status bits (qkv_front_status) ------------------------------- */
 #define QKVF_STATUS_BAD_SLOT 1u      /* a slot >= num_pages * 16: that token's insert skipped */
 #define QKVF_STATUS_BAD_POSITION 2u  /* a position outside [0, cos_sin_rows): its q/k heads and insert skipped */
 #define QKVF_STATUS_WAIT_TIMEOUT 4u  /* a bounded wait in the kernel gave up: outputs of that call are invalid */
-#define QKVF_STATUS_BAD_REQUEST 8u   /* attn2: a request with L < 8, L beyond its table, or a page outside the cache: its rows skipped */
+#define QKVF_STATUS_BAD_REQUEST 8u   /* attn2: a request with L < 8, L beyond its table, or a page outside the cache: its rows skipped;
+                                        prefix_attn: a length beyond its table or a page outside the cache: its rows skipped */
 
 /*
  * qkv_front: check the call, then launch the fused front.
@@ -354,6 +356,168 @@ int attn2_split_kv_noalloc(const uint16_t *qkv, const uint16_t *kv_cache, int64_
                            const int32_t *block_table, int max_blocks, const int32_t *context_lens,
                            int num_reqs, int N, int num_kv_heads, int window, float scale, float eps,
                            uint16_t *out, int splits, void *stream);
+
+/*
+ * The operators below serve any head layout around a paged cache
+ * [num_pages, num_kv_heads, 16, 2 head_dim] (K | V per slot, as the front's
+ * cache has at head_dim 64).  A [tokens, heads, head_dim] array is given by
+ * its pointer and its token and head strides in elements (the last dimension
+ * is contiguous), so the q, k and v columns of packed projection rows are
+ * passed as they lie; strides are 0..2^36, and an output's heads must not
+ * overlap one another.  A pointer is aligned to its elements; cos_sin and
+ * kv_cache to 16 bytes.  Rows that are 16-byte aligned throughout move in
+ * 16-byte accesses.  Every refusal has its reason in the *_unsupported
+ * function beside it.
+ */
+
+/* ---- element types, rotary layouts, rotary scalings ---------------------- */
+#define QKVF_DTYPE_BF16 0
+#define QKVF_DTYPE_FP16 1
+#define QKVF_DTYPE_FP32 2        /* rope only */
+
+#define QKVF_ROPE_INTERLEAVED 0  /* pair i: columns 2i, 2i + 1 */
+#define QKVF_ROPE_HALF 1         /* pair i: columns i, i + rot_dim / 2 */
+
+#define QKVF_ROPE_NONE 0         /* f_i = base^(-2i / rot_dim) */
+#define QKVF_ROPE_LINEAR 1       /* f_i / factor: every position compressed */
+#define QKVF_ROPE_BASE 2         /* base * factor^(rot_dim / (rot_dim - 2)): the slowest pair stretched by factor */
+#define QKVF_ROPE_RAMP 3         /* by parts: with n_i = original_len f_i / 2 pi turns over the original length and
+                                    g = clamp((n_i - slow) / (fast - slow), 0, 1): (1 - g) f_i / factor + g f_i */
+
+/*
+ * rope_table: the cos | sin rows of positions first .. first + rows - 1, as
+ * qkv_front, rope and rope_kv_append read them:
+ *   table[r][i] = magnitude cos(p f_i), table[r][rot_dim / 2 + i] = magnitude sin(p f_i), p = first + r,
+ * with the pairs' frequencies f_i scaled for long contexts as named above
+ * (factor >= 1; original_len, slow and fast are read by QKVF_ROPE_RAMP only).
+ * Angles are kept modulo one turn in 64-bit fixed point: their error is that
+ * of the 64-bit frequency, not of a 32-bit product, at any position.
+ *   table    [rows, rot_dim] fp32, device memory, 16-byte aligned
+ *   rows 0..2^32 (0: no launch), first 0..2^40, rot_dim even 2..512,
+ *   base in (1, 1e30], magnitude in (0, 1e6].
+ * Asynchronous on `stream`, PDL-launched; allocates nothing.
+ */
+int rope_table(float *table, int64_t first, int64_t rows, int rot_dim, double base, int scaling, double factor,
+               int64_t original_len, double slow, double fast, double magnitude, void *stream);
+
+const char *rope_table_unsupported(const float *table, int64_t first, int64_t rows, int rot_dim, double base,
+                                   int scaling, double factor, int64_t original_len, double slow, double fast,
+                                   double magnitude);
+
+/*
+ * rope: rotate the first rot_dim columns of every head by its token's
+ * position; the columns behind them are copied.
+ *   (a, b) -> (a c - b s, b c + a s), c | s = row positions[t] of cos_sin;
+ *   inverse = 1: s negated, the gradient of the rotation with respect to x.
+ *   x, out   [T, heads, head_dim] of dtype (bf16, fp16 or fp32), strided;
+ *            out may be x itself (same pointer and strides), otherwise it
+ *            must not overlap x.
+ *   positions [T] int64; a position outside [0, cos_sin_rows) leaves its
+ *            token's heads of out as they were and raises
+ *            QKVF_STATUS_BAD_POSITION.
+ *   cos_sin  [cos_sin_rows, rot_dim] fp32: cos in columns 0 .. rot_dim/2 - 1,
+ *            sin behind them.
+ *   T 0..2^24, heads 1..4096, head_dim 2..512, rot_dim even 2..head_dim.
+ * Products and sums in FP32, one rounding to dtype.  PDL-launched; allocates
+ * nothing.
+ */
+int rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, const int64_t *positions,
+         const float *cos_sin, int64_t cos_sin_rows, void *out, int64_t out_token_stride,
+         int64_t out_head_stride, int T, int heads, int head_dim, int rot_dim, int layout, int inverse,
+         int dtype, void *stream);
+
+const char *rope_unsupported(const void *x, int64_t x_token_stride, int64_t x_head_stride,
+                             const int64_t *positions, const float *cos_sin, int64_t cos_sin_rows, void *out,
+                             int64_t out_token_stride, int64_t out_head_stride, int T, int heads, int head_dim,
+                             int rot_dim, int layout, int inverse, int dtype);
+
+/*
+ * rope_kv_append: rotate q into q_out, rotate k and write it with v into each
+ * token's cache slot: the step between a projection and prefix_attn.
+ *   q, q_out [T, q_heads, head_dim], k, v [T, num_kv_heads, head_dim] of dtype
+ *            (bf16 or fp16), strided; q_out may be q itself, otherwise it must
+ *            not overlap q, k or v.  q_heads 0 (q and q_out NULL): append only.
+ *   positions, cos_sin as for rope; slots [T] int64 as for qkv_front: a
+ *            negative slot inserts nothing, a slot >= 16 num_pages is skipped
+ *            and raises QKVF_STATUS_BAD_SLOT; a bad position leaves the
+ *            token's q_out heads and slot as they were and raises
+ *            QKVF_STATUS_BAD_POSITION.  Tokens must name distinct slots.
+ *   kv_cache [num_pages, num_kv_heads, 16, 2 head_dim] of dtype; only the
+ *            named slots change.
+ *   T 0..2^24, head_dim a multiple of 8 up to 512, num_kv_heads 1..1024.
+ * PDL-launched; allocates nothing.
+ */
+int rope_kv_append(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+                   int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                   int64_t v_head_stride, const int64_t *positions, const int64_t *slots, const float *cos_sin,
+                   int64_t cos_sin_rows, void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                   void *kv_cache, int64_t num_pages, int T, int q_heads, int num_kv_heads, int head_dim,
+                   int rot_dim, int layout, int dtype, void *stream);
+
+const char *rope_kv_append_unsupported(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                       const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                                       const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                                       const int64_t *positions, const int64_t *slots, const float *cos_sin,
+                                       int64_t cos_sin_rows, void *q_out, int64_t q_out_token_stride,
+                                       int64_t q_out_head_stride, void *kv_cache, int64_t num_pages, int T,
+                                       int q_heads, int num_kv_heads, int head_dim, int rot_dim, int layout,
+                                       int dtype);
+
+/*
+ * prefix_attn: paged decode attention of num_reqs requests that share a
+ * prefix; the prefix's keys are read once for all of them.  Row (request r,
+ * its token i of q_len, q head h) attends to the prefix's prefix_len keys and
+ * to its request's own keys j <= L_r - q_len + i under one softmax:
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = ln sum_j exp(s_j),  s_j = scale q . k_j.
+ * A row that sees no key gives out = 0 and lse = -infinity.
+ *   q            [num_reqs q_len, q_heads, head_dim] of dtype (bf16 or fp16),
+ *                16-byte aligned, strides multiples of 8; head h reads KV head
+ *                h / (q_heads / num_kv_heads).
+ *   kv_cache     [num_pages, num_kv_heads, 16, 2 head_dim] of dtype.
+ *   prefix_pages [prefix_blocks] int32: prefix key j is slot j % 16 of page
+ *                prefix_pages[j / 16]; prefix_len one int32 on the device,
+ *                0 .. 16 prefix_blocks.  Both may be NULL when prefix_blocks is 0.
+ *   block_table  [num_reqs, max_blocks] int32: the same for each request's own
+ *                keys (NULL when max_blocks is 0); entries past a length are
+ *                not read.
+ *   context_lens [num_reqs] int32: L_r, the request's own keys, the step's
+ *                q_len tokens among them (0 .. 16 max_blocks; shorter than
+ *                q_len leaves the first rows with the prefix alone).  Negative:
+ *                a padding request, its rows of out and lse left as they were.
+ *   out          [num_reqs q_len, q_heads, head_dim] of dtype, contiguous;
+ *   lse          [num_reqs q_len, q_heads] fp32, or NULL.
+ *   workspace    device memory, 256-byte aligned, prefix_attn_workspace_bytes
+ *                bytes, overlapping no other argument, no initial contents
+ *                needed; one workspace serves one stream at a time.
+ * A request whose length is beyond its table, or whose table names a page
+ * outside the cache, is skipped (its rows left as they were) and raises
+ * QKVF_STATUS_BAD_REQUEST; a bad prefix does so for every request.  Cache
+ * slots past a length are never used, whatever they hold.
+ *   head_dim 64 or 128, q_heads 1..64 times num_kv_heads (1..64), q_len
+ *   1..1024, num_reqs 0..65535, num_reqs q_len q_heads <= 2^26.
+ * Scores, softmax statistics and sums in FP32; the weights exp(s - m) are
+ * rounded to dtype for the product with V.  The lengths stay on the device,
+ * so a captured call serves every step up to its tables' widths.
+ * PDL-launched; allocates nothing.
+ */
+int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *kv_cache,
+                int64_t num_pages, const int32_t *prefix_pages, int prefix_blocks, const int32_t *prefix_len,
+                const int32_t *block_table, int max_blocks, const int32_t *context_lens, int num_reqs, int q_len,
+                int q_heads, int num_kv_heads, int head_dim, float scale, int dtype, void *out, float *lse,
+                void *workspace, size_t workspace_bytes, void *stream);
+
+const char *prefix_attn_unsupported(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                    const void *kv_cache, int64_t num_pages, const int32_t *prefix_pages,
+                                    int prefix_blocks, const int32_t *prefix_len, const int32_t *block_table,
+                                    int max_blocks, const int32_t *context_lens, int num_reqs, int q_len,
+                                    int q_heads, int num_kv_heads, int head_dim, float scale, int dtype,
+                                    const void *out, const float *lse, const void *workspace,
+                                    size_t workspace_bytes);
+
+/* Workspace bytes prefix_attn needs on the current device (0 on bad input).
+ * A workspace for some prefix_blocks and max_blocks serves smaller ones too. */
+size_t prefix_attn_workspace_bytes(int num_reqs, int q_len, int q_heads, int num_kv_heads, int head_dim,
+                                   int prefix_blocks, int max_blocks);
 
 
 /* Static text of a QKVF_* return code. */

@@ -35,8 +35,10 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -1444,6 +1446,9 @@ int launch_front(const uint16_t *x, const uint16_t *W, const int64_t *positions,
 #include "qknorm_rope_kv_insert.cuh"
 #include "layer_front.cuh"
 #include "attn2.cuh"
+#include "rope.cuh"
+#include "rope_kv_append.cuh"
+#include "prefix_attn.cuh"
 
 using namespace qkvf;
 
@@ -1462,6 +1467,7 @@ const char *qkv_front_strerror(int code)
     case QKVF_ERR_SIZES: return "cos_sin_rows and num_pages must be >= 1";
     case QKVF_ERR_VARIANT: return "this variant cannot run this shape";
     case QKVF_ERR_ARG: return "bad argument (overlapping buffers or out-of-range setting)";
+    case QKVF_ERR_LAYOUT: return "head counts, head_dim, rotary width, dtype or strides this operator does not take";
     default: return "unknown qkv_front error";
     }
 }

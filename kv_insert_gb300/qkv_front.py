@@ -15,6 +15,7 @@ supports_call).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 import threading
@@ -29,6 +30,10 @@ Q_PER_KV = 8
 PAGE_SLOTS = 16
 SLOT_WIDTH = 128
 MAX_TOKENS = 16
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 
 CONSUMER_DEFAULT, CONSUMER_MMA_SYNC, CONSUMER_TCGEN05, CONSUMER_RESIDENT = 0, 1, 2, 3
 
@@ -115,6 +120,20 @@ def load() -> ctypes.CDLL:
         lib.attn2_split_kv_splits.restype = i32
         lib.attn2_split_kv_noalloc.argtypes = a2 + [i32, vp]
         lib.attn2_split_kv_noalloc.restype = i32
+        f64, size = ctypes.c_double, ctypes.c_size_t
+        table = [vp, i64, i64, i32, f64, i32, f64, i64, f64, f64, f64]
+        rope_args = [vp, i64, i64, vp, vp, i64, vp, i64, i64, i32, i32, i32, i32, i32, i32, i32]
+        append = [vp, i64, i64] * 3 + [vp, vp, vp, i64, vp, i64, i64, vp, i64] + [i32] * 7
+        prefix = ([vp, i64, i64, vp, i64, vp, i32, vp, vp, i32, vp] + [i32] * 5
+                  + [ctypes.c_float, i32, vp, vp, vp, size])
+        for name, args in (("rope_table", table), ("rope", rope_args), ("rope_kv_append", append),
+                           ("prefix_attn", prefix)):
+            getattr(lib, name).argtypes = args + [vp]
+            getattr(lib, name).restype = i32
+            getattr(lib, name + "_unsupported").argtypes = args
+            getattr(lib, name + "_unsupported").restype = ctypes.c_char_p
+        lib.prefix_attn_workspace_bytes.argtypes = [i32] * 7
+        lib.prefix_attn_workspace_bytes.restype = size
         lib.qkv_front_set_pdl.argtypes = [i32]
         lib.qkv_front_set_pdl.restype = i32
         _lib = lib
@@ -126,7 +145,7 @@ def header_functions() -> list[str]:
     text = open(HEADER).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(
-        r"\b((?:qkv_front|qknorm_rope_kv_insert|layer_front|attn2)\w*)\s*\(", text)))
+        r"\b((?:qkv_front|qknorm_rope_kv_insert|layer_front|attn2|rope|prefix_attn)\w*)\s*\(", text)))
 
 
 def strerror(code: int) -> str:
@@ -583,6 +602,280 @@ def attn2_split_kv(qkv, kv_cache, block_table, context_lens, workspace, out=None
     with torch.cuda.device(qkv.device):
         _check(load().attn2_split_kv(*args, int(splits), workspace.data_ptr(), workspace.numel(),
                                      _stream(stream)))
+    return out
+
+
+# ---- rotary positions, rotated cache append, shared-prefix attention --------
+
+class _OnDevice:
+    """`with` block that makes a device current only when it is not."""
+
+    def __init__(self, index: int):
+        self._guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _run(name: str, index: int, args: tuple, stream) -> None:
+    """Call the library's `name` on device `index`; a refusal carries its reason."""
+    lib = _lib or load()
+    with _OnDevice(index):
+        code = getattr(lib, name)(*args, _stream(stream))
+        if code != 0:
+            why = getattr(lib, name + "_unsupported")(*args)
+            raise QkvFrontError(code, why.decode() if why else strerror(code))
+
+
+def _why(name: str, index: int, args: tuple) -> str | None:
+    with _OnDevice(index):
+        r = getattr(load(), name + "_unsupported")(*args)
+    return None if r is None else r.decode()
+
+
+def _new(shape, dtype, device, stream):
+    """An output of a call on `stream` (None: the current stream): allocated
+    for that stream, so the allocator never hands it memory that another
+    stream's work still uses."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _heads(t, name: str, device, dtypes=None, shape=None):
+    """The (pointer, token stride, head stride) of a [tokens, heads, head_dim]
+    tensor with a contiguous last dimension."""
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]"
+                         + ("" if shape is None else f" {shape}") + f", not {tuple(t.shape)}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if max(t.shape) > 1 << 30:   # beyond the C ABI's int sizes
+        raise ValueError(f"{name} is too large: {tuple(t.shape)}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
+    ts, hs, es = t.stride()
+    if es != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), ts, hs
+
+
+def _index(t, name: str, dtype, shape, device):
+    if (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda
+            or t.device != device):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {shape} on {device}")
+    return t.data_ptr()
+
+
+def _table(cos_sin, head_dim: int, device):
+    if (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous()
+            or not cos_sin.is_cuda or cos_sin.device != device):
+        raise ValueError(f"cos_sin must be a contiguous fp32 CUDA tensor [rows, rot_dim] on {device}")
+    if cos_sin.shape[1] > head_dim:
+        raise ValueError(f"cos_sin rotates {cos_sin.shape[1]} columns of {head_dim}-wide heads")
+    return cos_sin.data_ptr(), cos_sin.shape[0]
+
+
+def _layout(layout: str) -> int:
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, not {layout!r}")
+    return ROPE_LAYOUTS[layout]
+
+
+def _cache(kv_cache, head_dim: int, dtype, device):
+    if (kv_cache.dtype != dtype or kv_cache.dim() != 4 or kv_cache.shape[2] != PAGE_SLOTS
+            or kv_cache.shape[3] != 2 * head_dim or not kv_cache.is_contiguous()
+            or not kv_cache.is_cuda or kv_cache.device != device):
+        raise ValueError(f"kv_cache must be a contiguous {dtype} CUDA tensor "
+                         f"[pages, num_kv_heads, {PAGE_SLOTS}, {2 * head_dim}] on {device}")
+    return kv_cache.data_ptr(), kv_cache.shape[0]
+
+
+def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: str = "none",
+               factor: float = 1.0, original_len: int = 0, slow: float = 1.0, fast: float = 32.0,
+               magnitude: float | None = None, first_position: int = 0, out=None, device=None,
+               stream=None):
+    """cos | sin rows of positions first_position .. first_position + rows - 1,
+    fp32 [rows, rot_dim], made on the device.  `scaling` stretches the
+    frequencies for contexts `factor` times longer: "linear" (every position
+    compressed), "base" (the base raised so that the slowest pair turns
+    `factor` times slower), "ramp" (pairs that turn more than `fast` times over
+    original_len positions kept, fewer than `slow` times compressed, a linear
+    ramp between).  magnitude multiplies cos and sin; by default 1, for "ramp"
+    0.1 ln(factor) + 1."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, not {scaling!r}")
+    if not 0 <= rows <= 1 << 32 or not 2 <= rot_dim <= 512:
+        raise ValueError("rows must be 0..2^32 and rot_dim 2..512")
+    if not 0 <= first_position <= 1 << 40 or not 0 <= original_len <= 1 << 40:
+        raise ValueError("first_position and original_len must be 0..2^40")
+    if out is None:
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        out = _new((rows, rot_dim), torch.float32, device, stream)
+    elif (not out.is_cuda or out.dtype != torch.float32 or tuple(out.shape) != (rows, rot_dim)
+          or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous fp32 CUDA tensor [{rows}, {rot_dim}]")
+    if magnitude is None:
+        magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "ramp" and factor > 0 else 1.0
+    _run("rope_table", out.device.index,
+         (out.data_ptr(), first_position, rows, rot_dim, base, ROPE_SCALINGS[scaling], factor,
+          original_len, slow, fast, magnitude), stream)
+    return out
+
+
+def _rope_args(x, positions, cos_sin, out, layout, inverse):
+    device = x.device
+    px, xt, xh = _heads(x, "x", device, DTYPES)
+    T, heads, dim = x.shape
+    po, ot, oh = _heads(out, "out", device, (x.dtype,), (T, heads, dim))
+    pt, rows = _table(cos_sin, dim, device)
+    return (px, xt, xh, _index(positions, "positions", torch.int64, (T,), device), pt, rows, po, ot,
+            oh, T, heads, dim, cos_sin.shape[1], _layout(layout), inverse, DTYPES[x.dtype])
+
+
+def rope_unsupported(x, positions, cos_sin, out, layout: str = "interleaved") -> str | None:
+    """Why rope (and rope_backward) would refuse this call, or None."""
+    try:
+        args = _rope_args(x, positions, cos_sin, out, layout, 0)
+    except ValueError as e:
+        return str(e)
+    return _why("rope", x.device.index, args)
+
+
+def _rope(x, positions, cos_sin, out, layout, inverse, stream):
+    if out is None:
+        out = _new(x.shape, x.dtype, x.device, stream)
+    _run("rope", x.device.index, _rope_args(x, positions, cos_sin, out, layout, inverse), stream)
+    return out
+
+
+def rope(x, positions, cos_sin, out=None, layout: str = "interleaved", stream=None):
+    """x [tokens, heads, head_dim] (bf16, fp16 or fp32; any strides, last
+    dimension contiguous) with the first cos_sin.shape[1] columns of every head
+    rotated by row positions[t] of cos_sin; the other columns are copied.
+    layout: pairs (2i, 2i + 1) "interleaved" or (i, i + rot_dim / 2) "half".
+    out=x rotates in place.  Returns out."""
+    return _rope(x, positions, cos_sin, out, layout, 0, stream)
+
+
+def rope_backward(grad_out, positions, cos_sin, out=None, layout: str = "interleaved", stream=None):
+    """The gradient of rope with respect to x: grad_out turned back by the same
+    angles.  out=grad_out writes it in place.  Returns out."""
+    return _rope(grad_out, positions, cos_sin, out, layout, 1, stream)
+
+
+def _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout):
+    device, dtypes = k.device, (torch.bfloat16, torch.float16)
+    pk, kt, kh = _heads(k, "k", device, dtypes)
+    T, nkv, dim = k.shape
+    pv, vt, vh = _heads(v, "v", device, (k.dtype,), (T, nkv, dim))
+    pc, pages = _cache(kv_cache, dim, k.dtype, device)
+    if kv_cache.shape[1] != nkv:
+        raise ValueError(f"{nkv} k heads for a cache of {kv_cache.shape[1]} KV heads")
+    pt, rows = _table(cos_sin, dim, device)
+    pq = po = None
+    q_heads = qt = qh = ot = oh = 0
+    if q is not None and q.shape[1] > 0:
+        q_heads = q.shape[1]
+        pq, qt, qh = _heads(q, "q", device, (k.dtype,), (T, q_heads, dim))
+        po, ot, oh = _heads(q_out, "q_out", device, (k.dtype,), (T, q_heads, dim))
+    return (pq, qt, qh, pk, kt, kh, pv, vt, vh,
+            _index(positions, "positions", torch.int64, (T,), device),
+            _index(slots, "slots", torch.int64, (T,), device), pt, rows, po, ot, oh, pc, pages, T,
+            q_heads, nkv, dim, cos_sin.shape[1], _layout(layout), DTYPES[k.dtype])
+
+
+def rope_kv_append_unsupported(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
+                               layout: str = "interleaved") -> str | None:
+    """Why rope_kv_append would refuse this call (into q_out), or None."""
+    try:
+        args = _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout)
+    except ValueError as e:
+        return str(e)
+    return _why("rope_kv_append", k.device.index, args)
+
+
+def rope_kv_append(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
+                   layout: str = "interleaved", stream=None):
+    """Rotate q [tokens, q_heads, head_dim] into q_out (q_out=q: in place; None:
+    a new tensor) and write the rotated k and v [tokens, num_kv_heads, head_dim]
+    into kv_cache [pages, num_kv_heads, 16, 2 head_dim] at each token's slot.
+    q=None appends only.  bf16 or fp16, any strides.  Returns q_out."""
+    if q is not None and q_out is None:
+        q_out = _new(q.shape, q.dtype, q.device, stream)
+    _run("rope_kv_append", k.device.index,
+         _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout), stream)
+    return q_out
+
+
+def prefix_attn_workspace_bytes(num_reqs: int, q_len: int, q_heads: int, num_kv_heads: int,
+                                head_dim: int, prefix_blocks: int, max_blocks: int) -> int:
+    """Workspace bytes of prefix_attn on the current device (0: bad sizes)."""
+    return int((_lib or load()).prefix_attn_workspace_bytes(num_reqs, q_len, q_heads, num_kv_heads,
+                                                            head_dim, prefix_blocks, max_blocks))
+
+
+def _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace, q_len,
+                 scale, out, lse):
+    device = q.device
+    pq, qt, qh = _heads(q, "q", device, (torch.bfloat16, torch.float16))
+    T, heads, dim = q.shape
+    if q_len < 1 or T % q_len:
+        raise ValueError(f"{T} q rows are not whole requests of {q_len} tokens")
+    R = T // q_len
+    pc, pages = _cache(kv_cache, dim, q.dtype, device)
+    pp = pl = None
+    nb = prefix_pages.shape[0] if prefix_pages is not None else 0
+    if nb:
+        pp = _index(prefix_pages, "prefix_pages", torch.int32, (nb,), device)
+        pl = _index(prefix_len, "prefix_len", torch.int32, (1,), device)
+    mb = block_table.shape[1] if block_table is not None else 0
+    pb = _index(block_table, "block_table", torch.int32, (R, mb), device) if mb else None
+    po = _index(out, "out", q.dtype, (T, heads, dim), device)
+    ps = None if lse is None else _index(lse, "lse", torch.float32, (T, heads), device)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be a contiguous uint8 CUDA tensor on q's device")
+    return (pq, qt, qh, pc, pages, pp, nb, pl, pb, mb,
+            _index(context_lens, "context_lens", torch.int32, (R,), device), R, q_len, heads,
+            kv_cache.shape[1], dim, dim ** -0.5 if scale is None else scale, DTYPES[q.dtype], po, ps,
+            workspace.data_ptr(), workspace.numel())
+
+
+def prefix_attn_unsupported(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace,
+                            out, q_len: int = 1, scale=None, lse=None) -> str | None:
+    """Why prefix_attn would refuse this call into `out`, or None."""
+    try:
+        args = _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace,
+                            q_len, scale, out, lse)
+    except ValueError as e:
+        return str(e)
+    return _why("prefix_attn", q.device.index, args)
+
+
+def prefix_attn(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace,
+                q_len: int = 1, scale=None, out=None, lse=None, stream=None):
+    """Paged decode attention of requests that share a prefix, read once for
+    all of them.  q [num_reqs q_len, q_heads, head_dim] (bf16 or fp16);
+    kv_cache [pages, num_kv_heads, 16, 2 head_dim]; prefix_pages int32 [blocks]
+    and prefix_len int32 [1] (both None: no prefix); block_table int32
+    [num_reqs, max_blocks] and context_lens int32 [num_reqs]: each request's
+    own keys, its q_len current tokens among them (a negative length: a padding
+    request, left alone); workspace: uint8, prefix_attn_workspace_bytes long.
+    scale: None for head_dim^-1/2.  lse: fp32 [num_reqs q_len, q_heads], filled
+    with the rows' ln sum exp when given.  Returns out."""
+    if out is None:
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _run("prefix_attn", q.device.index,
+         _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace, q_len,
+                      scale, out, lse), stream)
     return out
 
 
