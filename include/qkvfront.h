@@ -494,7 +494,7 @@ const char *rope_kv_append_unsupported(const void *q, int64_t q_token_stride, in
  * QKVF_STATUS_BAD_REQUEST; a bad prefix does so for every request.  Cache
  * slots past a length are never used, whatever they hold.
  *   head_dim 64 or 128, q_heads 1..64 times num_kv_heads (1..64), q_len
- *   1..1024, num_reqs 0..65535, num_reqs q_len q_heads <= 2^26.
+ *   1..1024, num_reqs 0..65535, num_reqs q_len q_heads <= 2^24.
  * Scores, softmax statistics and sums in FP32; the weights exp(s - m) are
  * rounded to dtype for the product with V.  The lengths stay on the device,
  * so a captured call serves every step up to its tables' widths.

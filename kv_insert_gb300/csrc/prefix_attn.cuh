@@ -10,102 +10,767 @@ namespace qkvf {
 
 constexpr int kPaMaxRequests = 65535;
 constexpr int kPaMaxQLen = 1024;
-constexpr int kPaMaxGroup = 64;   // q heads per KV head
+constexpr int kPaMaxGroup = 64;          // q heads per KV head
+constexpr int kPaTile = 128;             // query rows of one tcgen05.mma tile
+constexpr int kPaThreads = 384;          // 2 softmax groups of 4 warps, 2 producer warps, 2 MMA warps
+constexpr int kPaMaxSplits = 64;         // key splits of a tile, prefix and own keys each
+constexpr float kPaGrow = 8.f;           // a row's maximum may lag by 2^8 before O is rescaled
+
+// Shapes by head width: a block of keys is one ring stage (K and V, 32 KB)
+// and one S tile; each of the two rings holds `slots` of them.
+template <int D>
+struct PaShape {
+    static constexpr int keys = D == 64 ? 128 : 64;
+    static constexpr int pages = keys / kPageSlots;
+    static constexpr int slots = D == 64 ? 3 : 2;
+    static constexpr int nblk = 2 * D / 64;                    // 64-column blocks of a slot: K then V
+    static constexpr uint32_t page_bytes = kPageSlots * 4 * D; // one box
+    static constexpr uint32_t stage_bytes = pages * page_bytes;
+    static constexpr uint32_t q_bytes = kPaTile * 2 * D;
+    // tensor memory columns: S of both groups, O of both, P (packed pairs) of both
+    static constexpr uint32_t tS = 0, tO = 2 * keys, tP = tO + 2 * D, cols = 512;
+    static_assert(tP + keys <= cols && stage_bytes == 32768, "tensor memory and ring");
+};
+
+struct PaSmem {   // offsets from the 1024-byte aligned base
+    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, drain, slot_bad, tmem, flags, total;
+};
+
+template <int D>
+__host__ __device__ inline PaSmem pa_smem()
+{
+    using Sh = PaShape<D>;
+    PaSmem L;
+    uint32_t off = 0;
+    L.q = off;
+    off += 2 * Sh::q_bytes;
+    L.ring = off;
+    off += 2 * Sh::slots * Sh::stage_bytes;
+    L.full = off;
+    off += 2 * Sh::slots * 8;
+    L.empty = off;
+    off += 2 * Sh::slots * 8;
+    L.qready = off;
+    off += 16;
+    L.sfull = off;
+    off += 16;
+    L.sfree = off;
+    off += 16;
+    L.pready = off;
+    off += 16;
+    L.pvdone = off;
+    off += 16;
+    L.drain = off;
+    off += 16;
+    L.slot_bad = off;
+    off += 2 * Sh::slots * 4;
+    L.tmem = off;
+    off += 8;
+    L.flags = off;
+    off += 16;
+    L.total = off + 1024;
+    return L;
+}
 
 struct PrefixParams {
     const void *q;
-    const void *kv_cache;
     const int32_t *prefix_pages;
     const int32_t *prefix_len;
     const int32_t *block_table;
     const int32_t *context_lens;
     void *out;
     float *lse;
+    float *ws_o;      // partial O [split][row][D], prefix splits first
+    float2 *ws_ml;    // partial (maximum in log2 units, sum) [row][split]
     int64_t num_pages;
     int64_t q_ts, q_hs;
+    unsigned long long wait_limit_ns;
     int prefix_blocks, max_blocks;
-    int R, q_len, q_heads, nkv, dim;
-    float scale;
+    int R, q_len, q_heads, nkv, group;
+    int rows;         // R * q_len * q_heads
+    int tiles;        // 128-row tiles of a KV head's rows, for the prefix
+    int own_tiles;    // the same for one request's rows
+    int sp, ss;       // key splits of the prefix and of a request's own keys
+    int pair;         // prefix: both groups of a CTA on one key stream
+    float scale_log2;
 };
 
-constexpr int kPaWarps = 4;
+// One unit of work: a tile of query rows against a range of key blocks
+struct PaItem {
+    const int32_t *pages;
+    int g;           // KV head
+    int tok0;        // first token of the row set the tile is cut from
+    int row0, rows;  // the tile's first row in that set, and its rows (1..128)
+    int kb0, kb1;    // key blocks
+    int keys;        // keys that some row of the tile sees
+    int limit0;      // keys that token 0 of the row set sees; later tokens see `step` more each
+    int step;
+    int split;       // partial slot
+};
 
-// One warp per row: lane l scores key 32 c + l of chunk c, then every lane
-// accumulates dims l, l + 32, ... of the weighted V rows.
-template <class E, int D>
-__global__ void __launch_bounds__(32 * kPaWarps) prefix_attn_kernel(const PrefixParams p)
+__device__ __forceinline__ int pa_prefix_len(const PrefixParams &p)
 {
-    __shared__ float qs[kPaWarps][D];
-    if (threadIdx.x == 0) griddep_launch_dependents();
-    griddep_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kPaWarps + warp;
-    if (row >= (int64_t)p.R * p.q_len * p.q_heads) return;
-    const int t = (int)(row / p.q_heads), h = (int)(row % p.q_heads), r = t / p.q_len, i = t % p.q_len;
-    const int g = h / (p.q_heads / p.nkv);
-    const int L = p.context_lens[r], P = p.prefix_blocks > 0 ? *p.prefix_len : 0;
-    if (L < 0) return;   // a padding request
-    bool bad = L > p.max_blocks * kPageSlots || P < 0 || P > p.prefix_blocks * kPageSlots;
-    const int32_t *bt = p.block_table + (size_t)r * p.max_blocks;
-    if (!bad) {
-        for (int b = lane; b < (P + kPageSlots - 1) / kPageSlots; b += 32)
-            bad |= p.prefix_pages[b] < 0 || p.prefix_pages[b] >= p.num_pages;
-        for (int b = lane; b < (L + kPageSlots - 1) / kPageSlots; b += 32) bad |= bt[b] < 0 || bt[b] >= p.num_pages;
+    if (p.prefix_blocks == 0) return 0;
+    const int P = *p.prefix_len;
+    return P > p.prefix_blocks * kPageSlots ? -1 : P;
+}
+
+// Prefix item: tile `tile` of KV head g, split s
+template <int D>
+__device__ __forceinline__ PaItem pa_prefix_item(const PrefixParams &p, int P, int tile, int g, int s)
+{
+    constexpr int KB = PaShape<D>::keys;
+    const int nb = (P + KB - 1) / KB, all = p.R * p.q_len * p.group;
+    PaItem it;
+    it.pages = p.prefix_pages;
+    it.g = g;
+    it.tok0 = 0;
+    it.row0 = tile * kPaTile;
+    it.rows = min(kPaTile, all - it.row0);
+    it.kb0 = (int)((int64_t)s * nb / p.sp);
+    it.kb1 = (int)((int64_t)(s + 1) * nb / p.sp);
+    it.keys = P;
+    it.limit0 = P;
+    it.step = 0;
+    it.split = s;
+    return it;
+}
+
+// Keys that some row of a request's tile sees: its last token's
+__device__ __forceinline__ int pa_own_keys(const PrefixParams &p, int L, int tile)
+{
+    if (L > p.max_blocks * kPageSlots) return 0;
+    const int last = min(p.q_len - 1, (tile * kPaTile + kPaTile - 1) / p.group);
+    return max(0, L - p.q_len + last + 1);
+}
+
+template <int D>
+__device__ __forceinline__ PaItem pa_own_item(const PrefixParams &p, int r, int L, int tile, int g, int s)
+{
+    constexpr int KB = PaShape<D>::keys;
+    PaItem it;
+    it.keys = pa_own_keys(p, L, tile);
+    const int nb = (it.keys + KB - 1) / KB;
+    it.pages = p.block_table + (size_t)r * p.max_blocks;
+    it.g = g;
+    it.tok0 = r * p.q_len;
+    it.row0 = tile * kPaTile;
+    it.rows = min(kPaTile, p.q_len * p.group - it.row0);
+    it.kb0 = (int)((int64_t)s * nb / p.ss);
+    it.kb1 = (int)((int64_t)(s + 1) * nb / p.ss);
+    it.limit0 = L - p.q_len + 1;
+    it.step = 1;
+    it.split = p.sp + s;
+    return it;
+}
+
+// The CTA's work in order.  First the shared items (pair): both groups take
+// the same key blocks against the two tiles of a 256-row block.  Then each
+// group's own items, 2 gridDim.x workers in all: the prefix against the only
+// tile (not pair), and the requests' own keys.
+template <int D>
+struct PaWork {
+    const PrefixParams &p;
+    int P, w;
+    int idx, end, stride;
+    bool shared;
+    __device__ __forceinline__ PaWork(const PrefixParams &prm, int prefix, int group) : p(prm), P(prefix), w(group)
+    {
+        shared = p.pair != 0;
+        if (shared) {
+            idx = blockIdx.x;
+            stride = gridDim.x;
+            end = P > 0 ? (p.tiles + 1) / 2 * p.nkv * p.sp : 0;
+        }
+        if (!shared || idx >= end) second();
     }
-    if (__any_sync(0xffffffffu, bad)) {
-        if (lane == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
-        return;
+    __device__ __forceinline__ void second()
+    {
+        shared = false;
+        idx = 2 * blockIdx.x + w;
+        stride = 2 * gridDim.x;
+        end = P < 0 ? 0 : (p.pair ? 0 : p.nkv * p.sp) + p.R * p.nkv * p.own_tiles * p.ss;
     }
-    const uint16_t *q = static_cast<const uint16_t *>(p.q) + t * p.q_ts + h * p.q_hs;
-    for (int d = lane; d < D; d += 32) qs[warp][d] = E::get(q[d]) * p.scale;
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[D / 32];
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
-    for (int part = 0; part < 2; ++part) {
-        const int32_t *pages = part == 0 ? p.prefix_pages : bt;
-        const int keys = part == 0 ? P : max(0, L - p.q_len + i + 1);
-        for (int c = 0; c < keys; c += 32) {
-            const int j = c + lane;
-            const uint16_t *kv = static_cast<const uint16_t *>(p.kv_cache);
-            float s = -INFINITY;
-            if (j < keys) {
-                kv += (((int64_t)pages[j / kPageSlots] * p.nkv + g) * kPageSlots + j % kPageSlots) * (2 * D);
-                s = 0.f;
-                for (int d = 0; d < D; ++d) s = fmaf(qs[warp][d], E::get(kv[d]), s);
+    // The next item with key blocks; false at the end.  A shared item whose
+    // second tile does not exist has rows <= 0 for group 1.
+    __device__ __forceinline__ bool next(PaItem &it, bool &is_shared)
+    {
+        while (true) {
+            if (shared) {
+                const int i = idx;
+                idx += stride;
+                const int rb = (p.tiles + 1) / 2, tile = 2 * (i % rb) + w, gs = i / rb;
+                it = pa_prefix_item<D>(p, P, tile, gs % p.nkv, gs / p.nkv);
+                is_shared = true;
+                if (idx >= end) second();
+            } else {
+                if (idx >= end) return false;
+                int i = idx;
+                idx += stride;
+                const int single = p.pair ? 0 : p.nkv * p.sp;
+                if (i < single) {
+                    it = pa_prefix_item<D>(p, P, 0, i % p.nkv, i / p.nkv);
+                } else {
+                    i -= single;
+                    const int g = i % p.nkv, rr = i / p.nkv, r = rr % p.R, ts = rr / p.R;
+                    it = pa_own_item<D>(p, r, p.context_lens[r], ts % p.own_tiles, g, ts / p.own_tiles);
+                }
+                is_shared = false;
             }
-            float mx = s;
+            if (it.kb1 > it.kb0) return true;
+        }
+    }
+};
+
+// Ring position of step n: shared steps alternate between the two rings, a
+// group's own steps stay in its ring
+struct PaRings {
+    int cnt[2];
+    __device__ __forceinline__ int take(int ring) { return cnt[ring]++; }
+};
+
+// ---- tensor memory, 32 lanes x 32 columns per warp -------------------------
+
+#define PA_REGS8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define PA_IN8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+
+__device__ __forceinline__ void pa_tmem_ld32(uint32_t addr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : PA_REGS8(r, 0), PA_REGS8(r, 8), PA_REGS8(r, 16), PA_REGS8(r, 24)
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void pa_tmem_st32(uint32_t addr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        PA_IN8(r, 0), PA_IN8(r, 8), PA_IN8(r, 16), PA_IN8(r, 24)
+        : "memory");
+}
+
+__device__ __forceinline__ void pa_tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D += A B with A (the weights) in tensor memory
+__device__ __forceinline__ void pa_umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of a 128-byte-swizzled operand: `sbo` bytes between 8-row groups
+// (8-key groups of V), `lbo` bytes between 64-column blocks of V
+__device__ __forceinline__ uint64_t pa_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// kind::f16, FP32 accumulator, M = 128: bf16 or fp16 operands, B MN-major for V
+template <class E>
+__device__ __forceinline__ constexpr uint32_t pa_idesc(int n, bool b_mn)
+{
+    constexpr uint32_t fmt = E::is_bf16 ? 1u : 0u;
+    return 1u << 4 | fmt << 7 | fmt << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+           (uint32_t)(kPaTile >> 4) << 24;
+}
+
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+template <class E, int D>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
+{
+    using Sh = PaShape<D>;
+    constexpr int KB = Sh::keys, NS = Sh::slots;
+    extern __shared__ uint8_t pa_smem_dyn[];
+    uint8_t *smem = pa_smem_dyn + ((1024u - (smem_u32(pa_smem_dyn) & 1023u)) & 1023u);
+    const PaSmem LY = pa_smem<D>();
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + LY.flags);   // [0]: a wait gave up
+    volatile int *slot_bad = reinterpret_cast<volatile int *>(smem + LY.slot_bad);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * NS; ++i) {
+            mbar_init(sb + LY.full + 8 * i, 1);
+            mbar_init(sb + LY.empty + 8 * i, 2);   // both groups' (or one group's two) commits
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(sb + LY.qready + 8 * w, 128);
+            mbar_init(sb + LY.sfull + 8 * w, 1);
+            mbar_init(sb + LY.sfree + 8 * w, 4);
+            mbar_init(sb + LY.pready + 8 * w, 4);
+            mbar_init(sb + LY.pvdone + 8 * w, 1);
+            mbar_init(sb + LY.drain + 8 * w, 1);
+        }
+        flags[0] = 0;
+        fence_barrier_init();
+        griddep_launch_dependents();
+    }
+    if (warp == 0) a2_tmem_alloc<Sh::cols>(sb + LY.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + LY.tmem);
+    griddep_wait();   // every input comes from the kernels before this one
+    const int P = pa_prefix_len(p);
+    const auto wait = [&](uint32_t bar, int n) {   // until phase n of bar is complete
+        return mbar_try_wait(bar, (uint32_t)n & 1) || bounded_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns, true);
+    };
+
+    if (warp >= 8 && warp < 10) {
+        // ---- produce: ring w's blocks, one 128-byte-swizzled box per page ----
+        const int w = warp - 8;
+        if (lane == 0) tma_prefetch_map(&tmKV);
+        PaWork<D> work(p, P, w);
+        PaItem it;
+        bool shared, stop = false;
+        int step = 0, k = 0;   // shared steps; steps of this ring
+        unsigned bad_any = 0u;
+        while (!stop && work.next(it, shared)) {
+            const int pg0 = it.kb0 * Sh::pages;
+            const int pg1 = min(it.kb1 * Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots);
+            int next = pg0 + lane < pg1 ? it.pages[pg0 + lane] : 0;
+            for (int c = pg0; c < pg1 && !stop; c += 32) {
+                int page = next;
+                if (c + 32 + lane < pg1) next = it.pages[c + 32 + lane];
+                bool bad = false;
+                if (c + lane < pg1 && (page < 0 || page >= p.num_pages)) {   // flagged, page 0 in its place
+                    bad = true;
+                    page = 0;
+                }
+                const unsigned bads = __ballot_sync(0xffffffffu, bad);
+                bad_any |= bads;
+                for (int b0 = c; b0 < min(c + 32, pg1); b0 += Sh::pages) {
+                    if (shared && (step++ & 1) != w) continue;
+                    const int n = min(Sh::pages, pg1 - b0);
+                    const int slot = k % NS, use = k / NS, st = w * NS + slot;
+                    ++k;
+                    int ok = 1;
+                    if (lane == 0) {
+                        ok = use == 0 || wait(sb + LY.empty + 8 * st, use - 1);
+                        if (ok) {
+                            slot_bad[st] = (bads >> (b0 - c)) & ((1u << Sh::pages) - 1u);
+                            mbar_expect_tx(sb + LY.full + 8 * st, (uint32_t)n * Sh::page_bytes);
+                        }
+                    }
+                    if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                        --k;
+                        stop = true;
+                        break;
+                    }
+                    const int i = c + lane - b0;
+                    if (i >= 0 && i < n)
+                        asm volatile(
+                            "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%3, %3, %3, %3, %4}], [%2];" ::"r"(sb + LY.ring + st * Sh::stage_bytes + i * Sh::page_bytes),
+                            "l"(reinterpret_cast<uint64_t>(&tmKV)), "r"(sb + LY.full + 8 * st), "r"(0),
+                            "r"(page * p.nkv + it.g)
+                            : "memory");
+                }
+            }
+        }
+        if (lane == 0) {
+            if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
+            if (flags[0])   // our copies land before the CTA leaves
+                for (int j = max(0, k - NS); j < k; ++j)
+                    bounded_wait(sb + LY.full + 8 * (w * NS + j % NS), (uint32_t)((j / NS) & 1), flags, p.wait_limit_ns, false);
+        }
+        __syncwarp();
+    } else if (warp >= 10) {
+        // ---- multiply: one thread issues group w's S = Q K^T and O += P V ----
+        const int w = warp - 10;
+        if (lane == 0) {
+            PaWork<D> work(p, P, w);
+            PaItem it;
+            bool shared, ok = true;
+            int step = 0, k[2] = {0, 0};
+            int items = 0, blk = 0;   // items and blocks of this group so far
+            const uint32_t sq = sb + LY.q + w * Sh::q_bytes;
+            const uint32_t dS = tmem + Sh::tS + w * KB, dO = tmem + Sh::tO + w * D, dP = tmem + Sh::tP + w * (KB / 2);
+            while (ok && work.next(it, shared)) {
+                const int n = it.kb1 - it.kb0;
+                if (it.rows <= 0) {   // no second tile: hand the blocks back
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int ring = step++ & 1, kk = k[ring]++, st = ring * NS + kk % NS;
+                        ok = wait(sb + LY.full + 8 * st, kk / NS);
+                        if (ok) mbar_arrive(sb + LY.empty + 8 * st);
+                    }
+                    continue;
+                }
+                ok = wait(sb + LY.qready + 8 * w, items++);
+                int st_prev = 0, pages_prev = 0;
+                for (int j = 0; j <= n && ok; ++j) {
+                    int st = 0, pages = 0;
+                    if (j < n) {   // S of block j
+                        const int ring = shared ? (step++ & 1) : w, kk = k[ring]++;
+                        st = ring * NS + kk % NS;
+                        pages = min(Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots - (it.kb0 + j) * Sh::pages);
+                        ok = wait(sb + LY.full + 8 * st, kk / NS) &&
+                             (blk == 0 || wait(sb + LY.sfree + 8 * w, blk - 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t kst = sb + LY.ring + st * Sh::stage_bytes;
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.f : mn;
-            const float w = j < keys ? expf(s - base) : 0.f, al = expf(m - base);
-            float sum = w;
+                        for (int i = 0; i < D / 16; ++i)
+                            umma_bf16(dS, pa_desc(sq + (i / 4) * (kPaTile * 128) + (i % 4) * 32, 16, 1024),
+                                      pa_desc(kst + (i / 4) * 1024 + (i % 4) * 32, 16, Sh::nblk * 1024),
+                                      pa_idesc<E>(KB, false), i != 0);
+                        umma_commit(sb + LY.sfull + 8 * w);
+                        ++blk;
+                    }
+                    if (j > 0) {   // O += P V of block j - 1
+                        const int done = j < n ? blk - 2 : blk - 1;
+                        ok = wait(sb + LY.pready + 8 * w, done);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t vst = sb + LY.ring + st_prev * Sh::stage_bytes + (D / 64) * 1024;
+                        for (int i = 0; i < pages_prev; ++i)
+                            pa_umma_ts(dO, dP + 8 * i, pa_desc(vst + i * Sh::page_bytes, 1024, Sh::nblk * 1024),
+                                       pa_idesc<E>(D, true), j > 1 || i > 0);
+                        umma_commit(sb + LY.empty + 8 * st_prev);
+                        if (!shared) umma_commit(sb + LY.empty + 8 * st_prev);
+                        umma_commit(sb + LY.pvdone + 8 * w);
+                    }
+                    st_prev = st;
+                    pages_prev = pages;
+                }
+            }
+            // every MMA of this thread is done before tensor memory is freed
+            umma_commit(sb + LY.drain + 8 * w);
+            bounded_wait(sb + LY.drain + 8 * w, 0, flags, p.wait_limit_ns, false);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: thread = row of the group's tile ----------------------
+        const int w = warp >> 2, wq = warp & 3, row = threadIdx.x & 127;
+        const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+        const uint32_t aS = tmem + Sh::tS + w * KB + lane_base, aO = tmem + Sh::tO + w * D + lane_base,
+                       aP = tmem + Sh::tP + w * (KB / 2) + lane_base;
+        uint8_t *sq = smem + LY.q + w * Sh::q_bytes;
+        PaWork<D> work(p, P, w);
+        PaItem it;
+        bool shared, ok = true;
+        int step = 0, k[2] = {0, 0}, blk = 0;
+        const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
+        while (ok && work.next(it, shared)) {
+            const int n = it.kb1 - it.kb0;
+            if (it.rows <= 0) {
+                for (int j = 0; j < n; ++j) ++k[step++ & 1];
+                continue;
+            }
+            const bool active = 32 * wq < it.rows, valid = row < it.rows;
+            const int m = it.row0 + row, tok = m / p.group, head = it.g * p.group + m % p.group;
+            const int64_t grow = (int64_t)(it.tok0 + tok) * p.q_heads + head;   // output row
+            if (active) {   // the previous item's last S was observed: its Q is no longer read
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    static_cast<const uint16_t *>(p.q) + (it.tok0 + tok) * p.q_ts + head * p.q_hs);
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            l = l * al + sum;
-            m = mn;
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(sq + (c / 8) * (kPaTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            mbar_arrive(sb + LY.qready + 8 * w);
+            const int limit = it.limit0 + it.step * tok;   // keys this row sees
+            float mu = -INFINITY, l = 0.f;
+            int bad = 0;
+            for (int j = 0; j < n; ++j, ++blk) {
+                const int ring = shared ? (step++ & 1) : w, kk = k[ring]++, st = ring * NS + kk % NS;
+                const int key0 = (it.kb0 + j) * KB;
+                ok = wait(sb + LY.sfull + 8 * w, blk);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                bad |= slot_bad[st];
+                if (active) {
+                    uint32_t s[KB];
+                    tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) o[k] *= al;
-            for (int jj = 0; jj < 32 && c + jj < keys; ++jj) {
-                const float wj = __shfl_sync(0xffffffffu, w, jj);
-                const uint16_t *vj = reinterpret_cast<const uint16_t *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kv), jj));
+                    for (int c = 0; c < KB; c += 32) pa_tmem_ld32(aS + c, s + c);
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
+                    if (__any_sync(0xffffffffu, limit < key0 + KB)) {
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) o[k] = fmaf(wj, E::get(vj[D + 32 * k + lane]), o[k]);
+                        for (int c = 0; c < KB; ++c)
+                            if (key0 + c >= limit) s[c] = 0xff800000u;   // -inf, whatever the slot holds
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < KB; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    // a row's maximum follows only when it grew by more than 2^8: the
+                    // weights stay below 2^8 and O is seldom rescaled
+                    const bool grew = top > mu + kPaGrow || (mu == -INFINITY && top > mu);
+                    if (__any_sync(0xffffffffu, grew)) {
+                        const float al = grew ? a2_ex2(mu - top) : 1.f;
+                        if (grew) mu = top;
+                        l *= al;
+                        if (j > 0) {
+                            ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                pa_tmem_ld32(aO + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                pa_tmem_st32(aO + c, o);
+                            }
+                        }
+                    }
+                    const float base = mu == -INFINITY ? 0.f : mu;
+                    const uint64_t nb2 = f2_pack(-base, -base);
+                    uint64_t sum[4] = {0, 0, 0, 0};
+                    uint32_t pk[KB / 2];
+#pragma unroll
+                    for (int c = 0; c < KB; c += 2) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), cc, nb2), a, b);
+                        a = a2_ex2(a);
+                        b = a2_ex2(b);
+                        sum[(c >> 1) & 3] = f2_add(sum[(c >> 1) & 3], f2_pack(a, b));
+                        pk[c / 2] = E::pack(a, b);
+                    }
+                    float a, b;
+                    f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
+                    l += a + b;
+                    if (j > 0) {   // the weights of block j - 1 have been read
+                        ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int c = 0; c < KB / 2; c += 32) pa_tmem_st32(aP + c, pk + c);
+                    pa_tmem_st_wait();
+                    tc_fence_before();
+                } else {
+                    if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
+                    if (j > 0) {   // not two arrivals in one phase of pready
+                        ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
+                        if (!ok) break;
+                    }
+                }
+                // the V rows of the last page behind the keys: whatever they hold
+                // must not meet a zero weight
+                if (it.keys < key0 + KB && (it.keys & (kPageSlots - 1))) {
+                    ok = __all_sync(0xffffffffu, wait(sb + LY.full + 8 * st, kk / NS));
+                    if (!ok) break;
+                    const int pg = (it.keys - key0) / kPageSlots, s0 = it.keys & (kPageSlots - 1);
+                    for (int c = row; c < (kPageSlots - s0) * (D / 8); c += 128) {
+                        const int s = s0 + c / (D / 8), ch = c % (D / 8);
+                        *reinterpret_cast<uint4 *>(smem + LY.ring + st * Sh::stage_bytes + pg * Sh::page_bytes +
+                                                   (s >> 3) * (Sh::nblk * 1024) + (D / 64 + ch / 8) * 1024 +
+                                                   (s & 7) * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb + LY.pready + 8 * w);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
+            if (!ok) break;
+            if (active) {
+                tc_fence_after();
+                float *dst = p.ws_o + ((int64_t)it.split * p.rows + grow) * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    pa_tmem_ld32(aO + c, o);
+                    tmem_ld_wait();
+                    if (valid)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            __stcg(reinterpret_cast<uint4 *>(dst + c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                }
+                tc_fence_before();
+                // a sum below zero marks a partial over a page outside the cache
+                if (valid) __stcg(p.ws_ml + grow * (p.sp + p.ss) + it.split, make_float2(mu, bad ? -1.f : l));
             }
         }
     }
-    uint16_t *out = static_cast<uint16_t *>(p.out) + row * D;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) out[32 * k + lane] = E::put(l == 0.f ? 0.f : o[k] / l);
-    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) a2_tmem_dealloc<Sh::cols>(tmem);
 }
 
-size_t prefix_attn_workspace(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int prefix_blocks,
-                             int max_blocks)
+// Joins a row's partials in split order: D / 4 lanes per row.  Which splits
+// hold keys follows from the lengths, as in the kernel that wrote them.
+constexpr int kPaMergeThreads = 128;
+
+template <class E, int D>
+__global__ void __launch_bounds__(kPaMergeThreads) prefix_merge_kernel(const __grid_constant__ PrefixParams p)
 {
-    (void)num_reqs, (void)q_len, (void)q_heads, (void)nkv, (void)head_dim, (void)prefix_blocks, (void)max_blocks;
-    return 256;
+    constexpr int LPR = D / 4, KB = PaShape<D>::keys;
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();
+    const int64_t row = (int64_t)blockIdx.x * (kPaMergeThreads / LPR) + threadIdx.x / LPR;
+    const int d = threadIdx.x % LPR;
+    if (row >= p.rows) return;
+    const int t = (int)(row / p.q_heads), h = (int)(row % p.q_heads), r = t / p.q_len;
+    const int P = pa_prefix_len(p), L = p.context_lens[r];
+    if (L < 0 && P >= 0) return;   // a padding request
+    if (P < 0 || L > p.max_blocks * kPageSlots) {
+        if (d == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
+        return;
+    }
+    const int own = pa_own_keys(p, L, ((t - r * p.q_len) * p.group + h % p.group) / kPaTile);
+    const int nb[2] = {(P + KB - 1) / KB, (own + KB - 1) / KB}, n[2] = {p.sp, p.ss};
+    const float2 *ml = p.ws_ml + row * (p.sp + p.ss);
+    float M = -INFINITY;
+    bool bad = false;
+    for (int part = 0, s0 = 0; part < 2; s0 += n[part], ++part)
+        for (int s = 0; s < n[part]; ++s)
+            if ((int)((int64_t)s * nb[part] / n[part]) < (int)((int64_t)(s + 1) * nb[part] / n[part])) {
+                const float2 v = __ldcg(ml + s0 + s);
+                M = fmaxf(M, v.x);
+                bad |= v.y < 0.f;
+            }
+    if (bad) return;
+    const float base = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int part = 0, s0 = 0; part < 2; s0 += n[part], ++part)
+        for (int s = 0; s < n[part]; ++s)
+            if ((int)((int64_t)s * nb[part] / n[part]) < (int)((int64_t)(s + 1) * nb[part] / n[part])) {
+                const float2 v = __ldcg(ml + s0 + s);
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + ((int64_t)(s0 + s) * p.rows + row) * D) + d);
+                const float f = exp2f(v.x - base);
+                l = fmaf(v.y, f, l);
+                o.x = fmaf(x.x, f, o.x);
+                o.y = fmaf(x.y, f, o.y);
+                o.z = fmaf(x.z, f, o.z);
+                o.w = fmaf(x.w, f, o.w);
+            }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const uint2 y = l == 0.f ? make_uint2(0u, 0u) : make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * D + 4 * d) = y;
+    if (p.lse && d == 0) p.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+}
+
+// ---- host: splits, workspace, launch ---------------------------------------
+
+struct PaPlan {
+    int tiles, own_tiles, pair, sp, ss, sp_max, ss_max;
+};
+
+// The split (1..most) that ends soonest when `units` row tiles times the
+// splits run in waves of `workers`, each taking blocks / split steps and about
+// two steps of start and end.
+int pa_split(int64_t units, int64_t workers, int64_t blocks, int most)
+{
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s <= most; ++s) {
+        const double cost = (double)((units * s + workers - 1) / workers) * ((double)((blocks + s - 1) / s) + 2.0);
+        if (cost < least * 0.999) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+int pa_most(int64_t units, int64_t workers, int64_t blocks)
+{
+    int64_t most = (2 * workers + units - 1) / units;
+    if (most > blocks) most = blocks;
+    if (most > kPaMaxSplits) most = kPaMaxSplits;
+    return most < 1 ? 1 : (int)most;
+}
+
+PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int prefix_blocks, int max_blocks, int sms)
+{
+    const int keys = head_dim == 64 ? PaShape<64>::keys : PaShape<128>::keys, ppb = keys / kPageSlots;
+    const int group = q_heads / nkv;
+    PaPlan pl;
+    pl.tiles = (int)(((int64_t)num_reqs * q_len * group + kPaTile - 1) / kPaTile);
+    pl.own_tiles = (q_len * group + kPaTile - 1) / kPaTile;
+    pl.pair = pl.tiles > 1;
+    const int64_t nb = (prefix_blocks + ppb - 1) / ppb, no = (max_blocks + ppb - 1) / ppb;
+    const int64_t units = (int64_t)(pl.pair ? (pl.tiles + 1) / 2 : 1) * nkv, workers = pl.pair ? sms : 2 * sms;
+    pl.sp_max = pa_most(units, workers, nb);
+    pl.sp = pa_split(units, workers, nb, pl.sp_max);
+    const int64_t own = (int64_t)num_reqs * nkv * pl.own_tiles;
+    pl.ss_max = pa_most(own, 2 * sms, no);
+    pl.ss = pa_split(own, 2 * sms, no, pl.ss_max);
+    return pl;
+}
+
+// Partials: (sp_max + ss_max) x rows of O, maximum and sum, in FP32.  The
+// bounds grow with the tables' widths, so a workspace serves narrower ones.
+size_t prefix_attn_workspace(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int prefix_blocks,
+                             int max_blocks, int sms)
+{
+    const PaPlan pl = pa_plan(num_reqs, q_len, q_heads, nkv, head_dim, prefix_blocks, max_blocks, sms);
+    return (size_t)num_reqs * q_len * q_heads * (pl.sp_max + pl.ss_max) * (head_dim * 4 + 8) + 256;
+}
+
+template <class E, int D>
+bool prepare_prefix_kernel()
+{
+    return cudaFuncSetAttribute((const void *)prefix_attn_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)pa_smem<D>().total) == cudaSuccess;
+}
+
+bool prepare_prefix_kernels()
+{
+    return prepare_prefix_kernel<Bf16, 64>() && prepare_prefix_kernel<Bf16, 128>() &&
+           prepare_prefix_kernel<Fp16, 64>() && prepare_prefix_kernel<Fp16, 128>();
+}
+
+// The cache as dim 0 = 64 columns of a slot, dim 1 = slot % 8, dim 2 = the
+// slot's 64-column blocks (K, then V), dim 3 = slot / 8, dim 4 = (page, KV
+// head): a box is one page of one KV head, its 8-slot groups of every block 1
+// KB each and equally far apart from page to page.
+int encode_prefix_map(const void *kv_cache, int64_t num_pages, int nkv, int head_dim, bool bf16, CUtensorMap *m)
+{
+    const cuuint64_t slot = (cuuint64_t)head_dim * 4;   // bytes of a slot
+    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)head_dim / 32, 2, (cuuint64_t)num_pages * nkv};
+    const cuuint64_t strides[4] = {slot, 128, 8 * slot, kPageSlots * slot};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)head_dim / 32, 2, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, (void *)kv_cache,
+                    dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QKVF_OK
+               : QKVF_ERR_CUDA;
+}
+
+template <class E, int D>
+int launch_prefix(const CUtensorMap &map, const PrefixParams &prm, int sms, void *stream)
+{
+    const int64_t shared = prm.pair ? (int64_t)(prm.tiles + 1) / 2 * prm.nkv * prm.sp : 0;
+    const int64_t single = (prm.pair ? 0 : (int64_t)prm.nkv * prm.sp) + (int64_t)prm.R * prm.nkv * prm.own_tiles * prm.ss;
+    int64_t grid = (single + 1) / 2 > shared ? (single + 1) / 2 : shared;
+    if (grid > sms) grid = sms;
+    const int rc = launch_pdl(prefix_attn_kernel<E, D>, dim3((unsigned)grid), dim3(kPaThreads), (size_t)pa_smem<D>().total,
+                              stream, map, prm);
+    if (rc != QKVF_OK) return rc;
+    constexpr int rows = kPaMergeThreads / (D / 4);
+    return launch_pdl(prefix_merge_kernel<E, D>, dim3((unsigned)((prm.rows + rows - 1) / rows)), dim3(kPaMergeThreads), 0,
+                      stream, prm);
 }
 
 const char *check_prefix_shape(int num_reqs, int q_len, int q_heads, int num_kv_heads, int head_dim,
@@ -122,7 +787,7 @@ const char *check_prefix_shape(int num_reqs, int q_len, int q_heads, int num_kv_
     *code = QKVF_ERR_SIZES;
     if (prefix_blocks < 0 || prefix_blocks > (1 << 24) || max_blocks < 0 || max_blocks > (1 << 24))
         return "prefix_blocks and max_blocks must be 0..2^24";
-    if ((int64_t)num_reqs * q_len * q_heads > (int64_t(1) << 26)) return "num_reqs * q_len * q_heads must be <= 2^26";
+    if ((int64_t)num_reqs * q_len * q_heads > (int64_t(1) << 24)) return "num_reqs * q_len * q_heads must be <= 2^24";
     *code = QKVF_OK;
     return nullptr;
 }
@@ -157,16 +822,13 @@ const char *check_prefix_args(const void *q, int64_t q_ts, int64_t q_hs, const v
         !aligned(prefix_len, 4) || !aligned(lse, 4))
         return "the tables, lengths and lse must be 4-byte aligned";
     if (!aligned(workspace, 256)) return "the workspace must be 256-byte aligned";
-    *code = QKVF_ERR_SIZES;
-    const size_t need = prefix_attn_workspace(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks);
-    if (need == 0 || workspace_bytes < need) return "the workspace is too small";
     *code = QKVF_ERR_ARG;
     const size_t rows = (size_t)num_reqs * q_len * q_heads;
     const View vq = view_of(q, num_reqs * q_len, q_ts, q_heads, q_hs, head_dim, 2);
     const void *parts[] = {vq.ptr, kv_cache, context_lens, block_table, prefix_pages, prefix_len, out, lse, workspace};
     const size_t bytes[] = {vq.extent, (size_t)num_pages * num_kv_heads * kPageSlots * 2 * head_dim * 2,
                             (size_t)num_reqs * 4, (size_t)num_reqs * max_blocks * 4, (size_t)prefix_blocks * 4,
-                            prefix_blocks > 0 ? (size_t)4 : 0, rows * head_dim * 2, lse ? rows * 4 : 0, need};
+                            prefix_blocks > 0 ? (size_t)4 : 0, rows * head_dim * 2, lse ? rows * 4 : 0, workspace_bytes};
     for (int o = 6; o < 9; ++o)   // each output and the workspace against everything before it
         for (int i = 0; i < o; ++i)
             if (overlap(parts[i], bytes[i], parts[o], bytes[o])) return "out, lse or the workspace overlaps another argument";
@@ -184,7 +846,9 @@ size_t prefix_attn_workspace_bytes(int num_reqs, int q_len, int q_heads, int num
     int code;
     if (qkvf::check_prefix_shape(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks, &code))
         return 0;
-    return qkvf::prefix_attn_workspace(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks);
+    qkvf::DeviceState *d;
+    if (qkvf::probe_device(&d) != QKVF_OK) return 0;
+    return qkvf::prefix_attn_workspace(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks, d->sms);
 }
 
 const char *prefix_attn_unsupported(const void *q, int64_t q_token_stride, int64_t q_head_stride,
@@ -201,9 +865,14 @@ const char *prefix_attn_unsupported(const void *q, int64_t q_token_stride, int64
                                               num_reqs, q_len, q_heads, num_kv_heads, head_dim, scale, dtype, out,
                                               lse, workspace, workspace_bytes, &code);
     if (why) return why;
+    if (num_reqs == 0) return nullptr;
     qkvf::DeviceState *d;
     const int rc = qkvf::probe_device(&d);
-    return rc == QKVF_OK ? nullptr : qkv_front_strerror(rc);
+    if (rc != QKVF_OK) return qkv_front_strerror(rc);
+    return workspace_bytes < qkvf::prefix_attn_workspace(num_reqs, q_len, q_heads, num_kv_heads, head_dim,
+                                                         prefix_blocks, max_blocks, d->sms)
+               ? "the workspace is too small"
+               : nullptr;
 }
 
 int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *kv_cache,
@@ -219,11 +888,18 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
         return code;
     if (num_reqs == 0) return QKVF_OK;
     qkvf::DeviceState *d;
-    const int rc = qkvf::probe_device(&d);
+    int rc = qkvf::probe_device(&d);
     if (rc != QKVF_OK) return rc;
+    if (workspace_bytes < qkvf::prefix_attn_workspace(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks,
+                                                      max_blocks, d->sms))
+        return QKVF_ERR_SIZES;
+    const bool bf16 = dtype == QKVF_DTYPE_BF16;
+    CUtensorMap map;
+    rc = qkvf::encode_prefix_map(kv_cache, num_pages, num_kv_heads, head_dim, bf16, &map);
+    if (rc != QKVF_OK) return rc;
+    const qkvf::PaPlan pl = qkvf::pa_plan(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks, d->sms);
     qkvf::PrefixParams prm = {};
     prm.q = q;
-    prm.kv_cache = kv_cache;
     prm.prefix_pages = prefix_pages;
     prm.prefix_len = prefix_len;
     prm.block_table = block_table;
@@ -233,20 +909,28 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     prm.num_pages = num_pages;
     prm.q_ts = q_token_stride;
     prm.q_hs = q_head_stride;
+    prm.wait_limit_ns = qkvf::g_wait_limit_ns;
     prm.prefix_blocks = prefix_blocks;
     prm.max_blocks = max_blocks;
     prm.R = num_reqs;
     prm.q_len = q_len;
     prm.q_heads = q_heads;
     prm.nkv = num_kv_heads;
-    prm.dim = head_dim;
-    prm.scale = scale;
-    const int64_t rows = (int64_t)num_reqs * q_len * q_heads;
-    auto kernel = dtype == QKVF_DTYPE_BF16
-                      ? (head_dim == 64 ? qkvf::prefix_attn_kernel<qkvf::Bf16, 64> : qkvf::prefix_attn_kernel<qkvf::Bf16, 128>)
-                      : (head_dim == 64 ? qkvf::prefix_attn_kernel<qkvf::Fp16, 64> : qkvf::prefix_attn_kernel<qkvf::Fp16, 128>);
-    return qkvf::launch_pdl(kernel, dim3((unsigned)((rows + qkvf::kPaWarps - 1) / qkvf::kPaWarps)),
-                            dim3(32 * qkvf::kPaWarps), 0, stream, prm);
+    prm.group = q_heads / num_kv_heads;
+    prm.rows = num_reqs * q_len * q_heads;
+    prm.tiles = pl.tiles;
+    prm.own_tiles = pl.own_tiles;
+    prm.sp = pl.sp;
+    prm.ss = pl.ss;
+    prm.pair = pl.pair;
+    prm.scale_log2 = scale * 1.4426950408889634f;
+    prm.ws_o = static_cast<float *>(workspace);
+    prm.ws_ml = reinterpret_cast<float2 *>(prm.ws_o + (size_t)prm.rows * (pl.sp + pl.ss) * head_dim);
+    if (bf16)
+        return head_dim == 64 ? qkvf::launch_prefix<qkvf::Bf16, 64>(map, prm, d->sms, stream)
+                              : qkvf::launch_prefix<qkvf::Bf16, 128>(map, prm, d->sms, stream);
+    return head_dim == 64 ? qkvf::launch_prefix<qkvf::Fp16, 64>(map, prm, d->sms, stream)
+                          : qkvf::launch_prefix<qkvf::Fp16, 128>(map, prm, d->sms, stream);
 }
 
 }  // extern "C"

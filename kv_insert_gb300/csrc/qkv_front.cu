@@ -1168,6 +1168,7 @@ constexpr bool kDefaultTC = false;     // consumer: tcgen05 (true) or mma.sync
 
 bool prepare_epi_kernel();
 bool prepare_attn2_kernel();
+bool prepare_prefix_kernels();
 
 int probe_device(DeviceState **out)
 {
@@ -1210,7 +1211,7 @@ int probe_device(DeviceState **out)
             if (cudaFuncSetAttribute(res[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)res_smem_bytes(i ? 16 : 8)) != cudaSuccess)
                 return QKVF_ERR_CUDA;
-        if (!prepare_epi_kernel() || !prepare_attn2_kernel()) return QKVF_ERR_CUDA;
+        if (!prepare_epi_kernel() || !prepare_attn2_kernel() || !prepare_prefix_kernels()) return QKVF_ERR_CUDA;
         d.prepared = true;
     }
     *out = &d;

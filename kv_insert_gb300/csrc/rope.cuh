@@ -22,11 +22,23 @@ struct Bf16 {
     using store = uint16_t;
     static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
     static __device__ __forceinline__ uint16_t put(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+    static constexpr bool is_bf16 = true;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
 };
 struct Fp16 {
     using store = uint16_t;
     static __device__ __forceinline__ float get(uint16_t v) { return __half2float(__ushort_as_half(v)); }
     static __device__ __forceinline__ uint16_t put(float v) { return __half_as_ushort(__float2half_rn(v)); }
+    static constexpr bool is_bf16 = false;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
 };
 struct Fp32 {
     using store = float;
