@@ -115,20 +115,21 @@ __device__ __forceinline__ int pa_prefix_len(const PrefixParams &p)
     return P > p.prefix_blocks * kPageSlots ? -1 : P;
 }
 
-// Prefix item: tile `tile` of KV head g, split s
+// Prefix item: tile `tile` of KV head g, split s.  The key blocks are dealt
+// evenly to min(splits, blocks) splits, the others are empty.
 template <int D>
 __device__ __forceinline__ PaItem pa_prefix_item(const PrefixParams &p, int P, int tile, int g, int s)
 {
     constexpr int KB = PaShape<D>::keys;
-    const int nb = (P + KB - 1) / KB, all = p.R * p.q_len * p.group;
+    const int nb = (P + KB - 1) / KB, all = p.R * p.q_len * p.group, n = min(p.sp, nb);
     PaItem it;
     it.pages = p.prefix_pages;
     it.g = g;
     it.tok0 = 0;
     it.row0 = tile * kPaTile;
     it.rows = min(kPaTile, all - it.row0);
-    it.kb0 = (int)((int64_t)s * nb / p.sp);
-    it.kb1 = (int)((int64_t)(s + 1) * nb / p.sp);
+    it.kb0 = s < n ? (int)((int64_t)s * nb / n) : 0;
+    it.kb1 = s < n ? (int)((int64_t)(s + 1) * nb / n) : 0;
     it.keys = P;
     it.limit0 = P;
     it.step = 0;
@@ -150,14 +151,14 @@ __device__ __forceinline__ PaItem pa_own_item(const PrefixParams &p, int r, int 
     constexpr int KB = PaShape<D>::keys;
     PaItem it;
     it.keys = pa_own_keys(p, L, tile);
-    const int nb = (it.keys + KB - 1) / KB;
+    const int nb = (it.keys + KB - 1) / KB, n = min(p.ss, nb);
     it.pages = p.block_table + (size_t)r * p.max_blocks;
     it.g = g;
     it.tok0 = r * p.q_len;
     it.row0 = tile * kPaTile;
     it.rows = min(kPaTile, p.q_len * p.group - it.row0);
-    it.kb0 = (int)((int64_t)s * nb / p.ss);
-    it.kb1 = (int)((int64_t)(s + 1) * nb / p.ss);
+    it.kb0 = s < n ? (int)((int64_t)s * nb / n) : 0;
+    it.kb1 = s < n ? (int)((int64_t)(s + 1) * nb / n) : 0;
     it.limit0 = L - p.q_len + 1;
     it.step = 1;
     it.split = p.sp + s;
@@ -222,11 +223,20 @@ struct PaWork {
     }
 };
 
-// Ring position of step n: shared steps alternate between the two rings, a
-// group's own steps stay in its ring
-struct PaRings {
-    int cnt[2];
-    __device__ __forceinline__ int take(int ring) { return cnt[ring]++; }
+// Ring position of a step: shared steps alternate between the two rings, a
+// group's own steps stay in its ring w
+template <int NS>
+struct PaRing {
+    int w, shared_steps = 0, own_steps = 0;
+    int st, use;   // stage and how often it was used before
+    __device__ __forceinline__ explicit PaRing(int group) : w(group) {}
+    __device__ __forceinline__ void take(bool shared)
+    {
+        const int ring = shared ? shared_steps & 1 : w;
+        const int k = shared ? shared_steps++ >> 1 : ((shared_steps + 1 - w) >> 1) + own_steps++;
+        st = ring * NS + k % NS;
+        use = k / NS;
+    }
 };
 
 // ---- tensor memory, 32 lanes x 32 columns per warp -------------------------
@@ -250,6 +260,40 @@ __device__ __forceinline__ void pa_tmem_st32(uint32_t addr, const uint32_t *r)
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
         PA_IN8(r, 0), PA_IN8(r, 8), PA_IN8(r, 16), PA_IN8(r, 24)
         : "memory");
+}
+
+__device__ __forceinline__ void pa_tmem_st16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        PA_IN8(r, 0), PA_IN8(r, 8)
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void pa_tmem_st(uint32_t addr, const uint32_t *r)
+{
+    static_assert(N == 16 || N == 32, "columns per store");
+    if constexpr (N == 32)
+        pa_tmem_st32(addr, r);
+    else
+        pa_tmem_st16(addr, r);
+}
+
+// N scores of this thread's row; near an edge those from `limit` on become
+// -infinity, whatever their slots hold
+template <int N>
+__device__ __forceinline__ void pa_load_scores(uint32_t addr, uint32_t *s, bool edge, int limit)
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 32) pa_tmem_ld32(addr + c, s + c);
+    tmem_ld_wait();
+    if (edge) {
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+            if (c >= limit) s[c] = 0xff800000u;
+    }
 }
 
 __device__ __forceinline__ void pa_tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -340,7 +384,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         PaWork<D> work(p, P, w);
         PaItem it;
         bool shared, stop = false;
-        int step = 0, k = 0;   // shared steps; steps of this ring
+        PaRing<NS> ring(w);
+        int mine = 0;   // steps loaded into this ring
         unsigned bad_any = 0u;
         while (!stop && work.next(it, shared)) {
             const int pg0 = it.kb0 * Sh::pages;
@@ -357,23 +402,23 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 const unsigned bads = __ballot_sync(0xffffffffu, bad);
                 bad_any |= bads;
                 for (int b0 = c; b0 < min(c + 32, pg1); b0 += Sh::pages) {
-                    if (shared && (step++ & 1) != w) continue;
+                    ring.take(shared);
+                    const int st = ring.st;
+                    if (st / NS != w) continue;   // the other producer's
                     const int n = min(Sh::pages, pg1 - b0);
-                    const int slot = k % NS, use = k / NS, st = w * NS + slot;
-                    ++k;
                     int ok = 1;
                     if (lane == 0) {
-                        ok = use == 0 || wait(sb + LY.empty + 8 * st, use - 1);
+                        ok = ring.use == 0 || wait(sb + LY.empty + 8 * st, ring.use - 1);
                         if (ok) {
                             slot_bad[st] = (bads >> (b0 - c)) & ((1u << Sh::pages) - 1u);
                             mbar_expect_tx(sb + LY.full + 8 * st, (uint32_t)n * Sh::page_bytes);
                         }
                     }
                     if (!__shfl_sync(0xffffffffu, ok, 0)) {
-                        --k;
                         stop = true;
                         break;
                     }
+                    ++mine;
                     const int i = c + lane - b0;
                     if (i >= 0 && i < n)
                         asm volatile(
@@ -388,7 +433,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (lane == 0) {
             if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
             if (flags[0])   // our copies land before the CTA leaves
-                for (int j = max(0, k - NS); j < k; ++j)
+                for (int j = max(0, mine - NS); j < mine; ++j)
                     bounded_wait(sb + LY.full + 8 * (w * NS + j % NS), (uint32_t)((j / NS) & 1), flags, p.wait_limit_ns, false);
         }
         __syncwarp();
@@ -399,7 +444,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             PaWork<D> work(p, P, w);
             PaItem it;
             bool shared, ok = true;
-            int step = 0, k[2] = {0, 0};
+            PaRing<NS> ring(w);
             int items = 0, blk = 0;   // items and blocks of this group so far
             const uint32_t sq = sb + LY.q + w * Sh::q_bytes;
             const uint32_t dS = tmem + Sh::tS + w * KB, dO = tmem + Sh::tO + w * D, dP = tmem + Sh::tP + w * (KB / 2);
@@ -407,9 +452,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 const int n = it.kb1 - it.kb0;
                 if (it.rows <= 0) {   // no second tile: hand the blocks back
                     for (int j = 0; j < n && ok; ++j) {
-                        const int ring = step++ & 1, kk = k[ring]++, st = ring * NS + kk % NS;
-                        ok = wait(sb + LY.full + 8 * st, kk / NS);
-                        if (ok) mbar_arrive(sb + LY.empty + 8 * st);
+                        ring.take(true);
+                        ok = wait(sb + LY.full + 8 * ring.st, ring.use);
+                        if (ok) mbar_arrive(sb + LY.empty + 8 * ring.st);
                     }
                     continue;
                 }
@@ -418,10 +463,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 for (int j = 0; j <= n && ok; ++j) {
                     int st = 0, pages = 0;
                     if (j < n) {   // S of block j
-                        const int ring = shared ? (step++ & 1) : w, kk = k[ring]++;
-                        st = ring * NS + kk % NS;
+                        ring.take(shared);
+                        st = ring.st;
                         pages = min(Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots - (it.kb0 + j) * Sh::pages);
-                        ok = wait(sb + LY.full + 8 * st, kk / NS) &&
+                        ok = wait(sb + LY.full + 8 * st, ring.use) &&
                              (blk == 0 || wait(sb + LY.sfree + 8 * w, blk - 1));
                         if (!ok) break;
                         tc_fence_after();
@@ -466,12 +511,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         PaWork<D> work(p, P, w);
         PaItem it;
         bool shared, ok = true;
-        int step = 0, k[2] = {0, 0}, blk = 0;
+        PaRing<NS> ring(w);
+        int blk = 0;
         const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
         while (ok && work.next(it, shared)) {
             const int n = it.kb1 - it.kb0;
             if (it.rows <= 0) {
-                for (int j = 0; j < n; ++j) ++k[step++ & 1];
+                for (int j = 0; j < n; ++j) ring.take(true);
                 continue;
             }
             const bool active = 32 * wq < it.rows, valid = row < it.rows;
@@ -492,29 +538,26 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             float mu = -INFINITY, l = 0.f;
             int bad = 0;
             for (int j = 0; j < n; ++j, ++blk) {
-                const int ring = shared ? (step++ & 1) : w, kk = k[ring]++, st = ring * NS + kk % NS;
+                ring.take(shared);
+                const int st = ring.st;
                 const int key0 = (it.kb0 + j) * KB;
                 ok = wait(sb + LY.sfull + 8 * w, blk);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 bad |= slot_bad[st];
                 if (active) {
-                    uint32_t s[KB];
                     tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < KB; c += 32) pa_tmem_ld32(aS + c, s + c);
-                    tmem_ld_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
-                    if (__any_sync(0xffffffffu, limit < key0 + KB)) {
-#pragma unroll
-                        for (int c = 0; c < KB; ++c)
-                            if (key0 + c >= limit) s[c] = 0xff800000u;   // -inf, whatever the slot holds
-                    }
+                    // first pass: the row's maximum.  The second half of S is read
+                    // again for the weights rather than held (168 registers)
+                    const bool edge = __any_sync(0xffffffffu, limit < key0 + KB);
+                    uint32_t s[KB / 2];
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < KB; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                    for (int half = 1; half >= 0; --half) {
+                        pa_load_scores<KB / 2>(aS + half * (KB / 2), s, edge, limit - key0 - half * (KB / 2));
+#pragma unroll
+                        for (int c = 0; c < KB / 2; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                    }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
                     // a row's maximum follows only when it grew by more than 2^8: the
                     // weights stay below 2^8 and O is seldom rescaled
@@ -541,26 +584,34 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     const float base = mu == -INFINITY ? 0.f : mu;
                     const uint64_t nb2 = f2_pack(-base, -base);
                     uint64_t sum[4] = {0, 0, 0, 0};
-                    uint32_t pk[KB / 2];
-#pragma unroll
-                    for (int c = 0; c < KB; c += 2) {
-                        float a, b;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), cc, nb2), a, b);
-                        a = a2_ex2(a);
-                        b = a2_ex2(b);
-                        sum[(c >> 1) & 3] = f2_add(sum[(c >> 1) & 3], f2_pack(a, b));
-                        pk[c / 2] = E::pack(a, b);
-                    }
-                    float a, b;
-                    f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
-                    l += a + b;
                     if (j > 0) {   // the weights of block j - 1 have been read
                         ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
                         if (!ok) break;
                         tc_fence_after();
                     }
 #pragma unroll
-                    for (int c = 0; c < KB / 2; c += 32) pa_tmem_st32(aP + c, pk + c);
+                    for (int half = 0; half < 2; ++half) {
+                        if (half) {
+                            pa_load_scores<KB / 2>(aS + KB / 2, s, edge, limit - key0 - KB / 2);
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
+                        }
+                        uint32_t pk[KB / 4];
+#pragma unroll
+                        for (int c = 0; c < KB / 2; c += 2) {
+                            float a, b;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), cc, nb2), a, b);
+                            a = a2_ex2(a);
+                            b = a2_ex2(b);
+                            sum[(c >> 1) & 3] = f2_add(sum[(c >> 1) & 3], f2_pack(a, b));
+                            pk[c / 2] = E::pack(a, b);
+                        }
+                        pa_tmem_st<KB / 4>(aP + half * (KB / 4), pk);
+                    }
+                    float a, b;
+                    f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
+                    l += a + b;
                     pa_tmem_st_wait();
                     tc_fence_before();
                 } else {
@@ -573,7 +624,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 // the V rows of the last page behind the keys: whatever they hold
                 // must not meet a zero weight
                 if (it.keys < key0 + KB && (it.keys & (kPageSlots - 1))) {
-                    ok = __all_sync(0xffffffffu, wait(sb + LY.full + 8 * st, kk / NS));
+                    ok = __all_sync(0xffffffffu, wait(sb + LY.full + 8 * st, ring.use));
                     if (!ok) break;
                     const int pg = (it.keys - key0) / kPageSlots, s0 = it.keys & (kPageSlots - 1);
                     for (int c = row; c < (kPageSlots - s0) * (D / 8); c += 128) {
@@ -615,58 +666,91 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (warp == 0) a2_tmem_dealloc<Sh::cols>(tmem);
 }
 
-// Joins a row's partials in split order: D / 4 lanes per row.  Which splits
-// hold keys follows from the lengths, as in the kernel that wrote them.
-constexpr int kPaMergeThreads = 128;
+// Joins a row's partials, one warp per row: lane l holds the maximum and sum
+// of partials l, l + 32, ...; their weights go to shared memory, and O is
+// summed with 8 partials' loads in flight (D / 4 lanes a partial, so at
+// D = 64 each half warp takes every other one).  The order is fixed by the
+// split counts: the same bits every time.
+constexpr int kPaMergeWarps = 4;
 
 template <class E, int D>
-__global__ void __launch_bounds__(kPaMergeThreads) prefix_merge_kernel(const __grid_constant__ PrefixParams p)
+__global__ void __launch_bounds__(32 * kPaMergeWarps) prefix_merge_kernel(const __grid_constant__ PrefixParams p)
 {
-    constexpr int LPR = D / 4, KB = PaShape<D>::keys;
+    constexpr int LPR = D / 4, PAR = 32 / LPR, KB = PaShape<D>::keys;
+    __shared__ float weight[kPaMergeWarps][2 * kPaMaxSplits];
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
-    const int64_t row = (int64_t)blockIdx.x * (kPaMergeThreads / LPR) + threadIdx.x / LPR;
-    const int d = threadIdx.x % LPR;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x * kPaMergeWarps + warp;
     if (row >= p.rows) return;
-    const int t = (int)(row / p.q_heads), h = (int)(row % p.q_heads), r = t / p.q_len;
+    const int t = row / p.q_heads, h = row - t * p.q_heads, r = t / p.q_len;
     const int P = pa_prefix_len(p), L = p.context_lens[r];
+    const float2 *ml = p.ws_ml + (int64_t)row * (p.sp + p.ss);
     if (L < 0 && P >= 0) return;   // a padding request
     if (P < 0 || L > p.max_blocks * kPageSlots) {
-        if (d == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
+        if (lane == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
         return;
     }
     const int own = pa_own_keys(p, L, ((t - r * p.q_len) * p.group + h % p.group) / kPaTile);
-    const int nb[2] = {(P + KB - 1) / KB, (own + KB - 1) / KB}, n[2] = {p.sp, p.ss};
-    const float2 *ml = p.ws_ml + row * (p.sp + p.ss);
+    // partials 0 .. np - 1 over the prefix, np .. n - 1 (slots sp ..) over its own keys
+    const int np = min(p.sp, (P + KB - 1) / KB), n = np + min(p.ss, (own + KB - 1) / KB), skip = p.sp - np;
+    float2 v[2 * kPaMaxSplits / 32];
     float M = -INFINITY;
     bool bad = false;
-    for (int part = 0, s0 = 0; part < 2; s0 += n[part], ++part)
-        for (int s = 0; s < n[part]; ++s)
-            if ((int)((int64_t)s * nb[part] / n[part]) < (int)((int64_t)(s + 1) * nb[part] / n[part])) {
-                const float2 v = __ldcg(ml + s0 + s);
-                M = fmaxf(M, v.x);
-                bad |= v.y < 0.f;
-            }
-    if (bad) return;
+#pragma unroll
+    for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i) {
+        const int s = lane + 32 * i;
+        v[i] = s < n ? __ldcg(ml + s + (s < np ? 0 : skip)) : make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, v[i].x);
+        bad |= v[i].y < 0.f;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (__any_sync(0xffffffffu, bad)) return;   // a page outside the cache
     const float base = M == -INFINITY ? 0.f : M;
     float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i) {
+        const float f = exp2f(v[i].x - base);
+        weight[warp][lane + 32 * i] = f;
+        l = fmaf(v[i].y, f, l);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    __syncwarp();
+    const int d = lane % LPR;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int part = 0, s0 = 0; part < 2; s0 += n[part], ++part)
-        for (int s = 0; s < n[part]; ++s)
-            if ((int)((int64_t)s * nb[part] / n[part]) < (int)((int64_t)(s + 1) * nb[part] / n[part])) {
-                const float2 v = __ldcg(ml + s0 + s);
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + ((int64_t)(s0 + s) * p.rows + row) * D) + d);
-                const float f = exp2f(v.x - base);
-                l = fmaf(v.y, f, l);
-                o.x = fmaf(x.x, f, o.x);
-                o.y = fmaf(x.y, f, o.y);
-                o.z = fmaf(x.z, f, o.z);
-                o.w = fmaf(x.w, f, o.w);
+    const float4 *src = reinterpret_cast<const float4 *>(p.ws_o + (int64_t)row * D) + d;
+    const int64_t step = (int64_t)p.rows * (D / 4);
+    for (int s0 = lane / LPR; s0 < n; s0 += 8 * PAR) {
+        float4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int s = s0 + i * PAR;
+            if (s < n) x[i] = __ldcg(src + (s + (s < np ? 0 : skip)) * step);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int s = s0 + i * PAR;
+            if (s < n) {
+                const float f = weight[warp][s];
+                o.x = fmaf(x[i].x, f, o.x);
+                o.y = fmaf(x[i].y, f, o.y);
+                o.z = fmaf(x[i].z, f, o.z);
+                o.w = fmaf(x[i].w, f, o.w);
             }
+        }
+    }
+    if constexpr (PAR == 2) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const uint2 y = l == 0.f ? make_uint2(0u, 0u) : make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * D + 4 * d) = y;
-    if (p.lse && d == 0) p.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+    if (lane < LPR) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + (int64_t)row * D + 4 * d) = y;
+    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
 }
 
 // ---- host: splits, workspace, launch ---------------------------------------
@@ -768,9 +852,8 @@ int launch_prefix(const CUtensorMap &map, const PrefixParams &prm, int sms, void
     const int rc = launch_pdl(prefix_attn_kernel<E, D>, dim3((unsigned)grid), dim3(kPaThreads), (size_t)pa_smem<D>().total,
                               stream, map, prm);
     if (rc != QKVF_OK) return rc;
-    constexpr int rows = kPaMergeThreads / (D / 4);
-    return launch_pdl(prefix_merge_kernel<E, D>, dim3((unsigned)((prm.rows + rows - 1) / rows)), dim3(kPaMergeThreads), 0,
-                      stream, prm);
+    return launch_pdl(prefix_merge_kernel<E, D>, dim3((unsigned)((prm.rows + kPaMergeWarps - 1) / kPaMergeWarps)),
+                      dim3(32 * kPaMergeWarps), 0, stream, prm);
 }
 
 const char *check_prefix_shape(int num_reqs, int q_len, int q_heads, int num_kv_heads, int head_dim,
