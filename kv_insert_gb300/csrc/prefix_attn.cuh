@@ -27,9 +27,10 @@ struct PaShape {
     static constexpr uint32_t page_bytes = kPageSlots * 4 * D; // one box
     static constexpr uint32_t stage_bytes = pages * page_bytes;
     static constexpr uint32_t q_bytes = kPaTile * 2 * D;
-    // tensor memory columns: S of both groups, O of both, P (packed pairs) of both
-    static constexpr uint32_t tS = 0, tO = 2 * keys, tP = tO + 2 * D, cols = 512;
-    static_assert(tP + keys <= cols && stage_bytes == 32768, "tensor memory and ring");
+    // tensor memory columns: three units of keys / 2 columns a group for S and
+    // the weights, then both groups' O
+    static constexpr uint32_t tSP = 0, tO = 3 * keys, cols = 512;
+    static_assert(tO + 2 * D <= cols && stage_bytes == 32768, "tensor memory and ring");
 };
 
 struct PaSmem {   // offsets from the 1024-byte aligned base
@@ -88,10 +89,11 @@ struct PrefixParams {
     int prefix_blocks, max_blocks;
     int R, q_len, q_heads, nkv, group;
     int rows;         // R * q_len * q_heads
-    int tiles;        // 128-row tiles of a KV head's rows, for the prefix
-    int own_tiles;    // the same for one request's rows
+    int tiles;        // 128-row tiles of a KV head's rows (the tile kernel)
+    int pair;         // both groups of a CTA on one key stream
+    int small;        // the prefix's rows fit the rows kernel
+    int own_rows, own_tiles;   // rows of one tile of a request's rows, tiles of a request
     int sp, ss;       // key splits of the prefix and of a request's own keys
-    int pair;         // prefix: both groups of a CTA on one key stream
     float scale_log2;
 };
 
@@ -100,7 +102,7 @@ struct PaItem {
     const int32_t *pages;
     int g;           // KV head
     int tok0;        // first token of the row set the tile is cut from
-    int row0, rows;  // the tile's first row in that set, and its rows (1..128)
+    int row0, rows;  // the tile's first row in that set, and its rows
     int kb0, kb1;    // key blocks
     int keys;        // keys that some row of the tile sees
     int limit0;      // keys that token 0 of the row set sees; later tokens see `step` more each
@@ -115,25 +117,30 @@ __device__ __forceinline__ int pa_prefix_len(const PrefixParams &p)
     return P > p.prefix_blocks * kPageSlots ? -1 : P;
 }
 
-// Prefix item: tile `tile` of KV head g, split s.  The key blocks are dealt
-// evenly to min(splits, blocks) splits, the others are empty.
-template <int D>
-__device__ __forceinline__ PaItem pa_prefix_item(const PrefixParams &p, int P, int tile, int g, int s)
+// The nb key blocks of a row set dealt evenly to min(splits, nb) splits; the
+// splits behind those are empty
+__device__ __forceinline__ void pa_deal(PaItem &it, int nb, int splits, int s)
 {
-    constexpr int KB = PaShape<D>::keys;
-    const int nb = (P + KB - 1) / KB, all = p.R * p.q_len * p.group, n = min(p.sp, nb);
+    const int n = min(splits, nb);
+    it.kb0 = s < n ? (int)((int64_t)s * nb / n) : 0;
+    it.kb1 = s < n ? (int)((int64_t)(s + 1) * nb / n) : 0;
+}
+
+// The prefix: tile `tile` (of `tile_rows` rows) of KV head g, split s, blocks of KB keys
+template <int KB>
+__device__ __forceinline__ PaItem pa_prefix_item(const PrefixParams &p, int P, int tile_rows, int tile, int g, int s)
+{
     PaItem it;
     it.pages = p.prefix_pages;
     it.g = g;
     it.tok0 = 0;
-    it.row0 = tile * kPaTile;
-    it.rows = min(kPaTile, all - it.row0);
-    it.kb0 = s < n ? (int)((int64_t)s * nb / n) : 0;
-    it.kb1 = s < n ? (int)((int64_t)(s + 1) * nb / n) : 0;
+    it.row0 = tile * tile_rows;
+    it.rows = min(tile_rows, p.R * p.q_len * p.group - it.row0);
     it.keys = P;
     it.limit0 = P;
     it.step = 0;
     it.split = s;
+    pa_deal(it, (P + KB - 1) / KB, p.sp, s);
     return it;
 }
 
@@ -141,99 +148,49 @@ __device__ __forceinline__ PaItem pa_prefix_item(const PrefixParams &p, int P, i
 __device__ __forceinline__ int pa_own_keys(const PrefixParams &p, int L, int tile)
 {
     if (L > p.max_blocks * kPageSlots) return 0;
-    const int last = min(p.q_len - 1, (tile * kPaTile + kPaTile - 1) / p.group);
+    const int last = min(p.q_len - 1, (tile * p.own_rows + p.own_rows - 1) / p.group);
     return max(0, L - p.q_len + last + 1);
 }
 
-template <int D>
-__device__ __forceinline__ PaItem pa_own_item(const PrefixParams &p, int r, int L, int tile, int g, int s)
-{
-    constexpr int KB = PaShape<D>::keys;
-    PaItem it;
-    it.keys = pa_own_keys(p, L, tile);
-    const int nb = (it.keys + KB - 1) / KB, n = min(p.ss, nb);
-    it.pages = p.block_table + (size_t)r * p.max_blocks;
-    it.g = g;
-    it.tok0 = r * p.q_len;
-    it.row0 = tile * kPaTile;
-    it.rows = min(kPaTile, p.q_len * p.group - it.row0);
-    it.kb0 = s < n ? (int)((int64_t)s * nb / n) : 0;
-    it.kb1 = s < n ? (int)((int64_t)(s + 1) * nb / n) : 0;
-    it.limit0 = L - p.q_len + 1;
-    it.step = 1;
-    it.split = p.sp + s;
-    return it;
-}
-
-// The CTA's work in order.  First the shared items (pair): both groups take
-// the same key blocks against the two tiles of a 256-row block.  Then each
-// group's own items, 2 gridDim.x workers in all: the prefix against the only
-// tile (not pair), and the requests' own keys.
+// The tile kernel's work in order: prefix items only.  pair: a CTA's two
+// groups take the same key blocks against the two tiles of a 256-row block (a
+// second tile that does not exist has rows <= 0); otherwise the only tile's
+// splits go to 2 gridDim.x groups.
 template <int D>
 struct PaWork {
     const PrefixParams &p;
-    int P, w;
-    int idx, end, stride;
-    bool shared;
+    int P, w, idx, end, stride;
     __device__ __forceinline__ PaWork(const PrefixParams &prm, int prefix, int group) : p(prm), P(prefix), w(group)
     {
-        shared = p.pair != 0;
-        if (shared) {
-            idx = blockIdx.x;
-            stride = gridDim.x;
-            end = P > 0 ? (p.tiles + 1) / 2 * p.nkv * p.sp : 0;
-        }
-        if (!shared || idx >= end) second();
+        idx = p.pair ? blockIdx.x : 2 * blockIdx.x + w;
+        stride = p.pair ? gridDim.x : 2 * gridDim.x;
+        end = P > 0 ? (p.pair ? (p.tiles + 1) / 2 : 1) * p.nkv * p.sp : 0;
     }
-    __device__ __forceinline__ void second()
+    __device__ __forceinline__ bool next(PaItem &it)   // the next item with key blocks
     {
-        shared = false;
-        idx = 2 * blockIdx.x + w;
-        stride = 2 * gridDim.x;
-        end = P < 0 ? 0 : (p.pair ? 0 : p.nkv * p.sp) + p.R * p.nkv * p.own_tiles * p.ss;
-    }
-    // The next item with key blocks; false at the end.  A shared item whose
-    // second tile does not exist has rows <= 0 for group 1.
-    __device__ __forceinline__ bool next(PaItem &it, bool &is_shared)
-    {
-        while (true) {
-            if (shared) {
-                const int i = idx;
+        for (; idx < end; idx += stride) {
+            const int rb = p.pair ? (p.tiles + 1) / 2 : 1, tile = p.pair ? 2 * (idx % rb) + w : 0, gs = idx / rb;
+            it = pa_prefix_item<PaShape<D>::keys>(p, P, kPaTile, tile, gs % p.nkv, gs / p.nkv);
+            if (it.kb1 > it.kb0) {
                 idx += stride;
-                const int rb = (p.tiles + 1) / 2, tile = 2 * (i % rb) + w, gs = i / rb;
-                it = pa_prefix_item<D>(p, P, tile, gs % p.nkv, gs / p.nkv);
-                is_shared = true;
-                if (idx >= end) second();
-            } else {
-                if (idx >= end) return false;
-                int i = idx;
-                idx += stride;
-                const int single = p.pair ? 0 : p.nkv * p.sp;
-                if (i < single) {
-                    it = pa_prefix_item<D>(p, P, 0, i % p.nkv, i / p.nkv);
-                } else {
-                    i -= single;
-                    const int g = i % p.nkv, rr = i / p.nkv, r = rr % p.R, ts = rr / p.R;
-                    it = pa_own_item<D>(p, r, p.context_lens[r], ts % p.own_tiles, g, ts / p.own_tiles);
-                }
-                is_shared = false;
+                return true;
             }
-            if (it.kb1 > it.kb0) return true;
         }
+        return false;
     }
 };
 
-// Ring position of a step: shared steps alternate between the two rings, a
-// group's own steps stay in its ring w
+// Ring position of a group's step n: with pair the steps alternate between
+// the two rings, otherwise they stay in ring w
 template <int NS>
 struct PaRing {
-    int w, shared_steps = 0, own_steps = 0;
+    int w, pair, n = 0;
     int st, use;   // stage and how often it was used before
-    __device__ __forceinline__ explicit PaRing(int group) : w(group) {}
-    __device__ __forceinline__ void take(bool shared)
+    __device__ __forceinline__ PaRing(int group, int both) : w(group), pair(both) {}
+    __device__ __forceinline__ void take()
     {
-        const int ring = shared ? shared_steps & 1 : w;
-        const int k = shared ? shared_steps++ >> 1 : ((shared_steps + 1 - w) >> 1) + own_steps++;
+        const int ring = pair ? n & 1 : w, k = pair ? n >> 1 : n;
+        ++n;
         st = ring * NS + k % NS;
         use = k / NS;
     }
@@ -319,6 +276,15 @@ __device__ __forceinline__ uint64_t pa_desc(uint32_t saddr, uint32_t lbo, uint32
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+__device__ __forceinline__ void pa_load_page(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c4)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(c4)
+        : "memory");
+}
+
 // kind::f16, FP32 accumulator, M = 128: bf16 or fp16 operands, B MN-major for V
 template <class E>
 __device__ __forceinline__ constexpr uint32_t pa_idesc(int n, bool b_mn)
@@ -337,10 +303,10 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
 
 template <class E, int D>
 __global__ void __launch_bounds__(kPaThreads, 1)
-    prefix_attn_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
+    prefix_tile_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
 {
     using Sh = PaShape<D>;
-    constexpr int KB = Sh::keys, NS = Sh::slots;
+    constexpr int KB = Sh::keys, NS = Sh::slots, U = KB / 2;
     extern __shared__ uint8_t pa_smem_dyn[];
     uint8_t *smem = pa_smem_dyn + ((1024u - (smem_u32(pa_smem_dyn) & 1023u)) & 1023u);
     const PaSmem LY = pa_smem<D>();
@@ -352,7 +318,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * NS; ++i) {
             mbar_init(sb + LY.full + 8 * i, 1);
-            mbar_init(sb + LY.empty + 8 * i, 2);   // both groups' (or one group's two) commits
+            mbar_init(sb + LY.empty + 8 * i, p.pair ? 2 : 1);   // the groups that read the stage
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(sb + LY.qready + 8 * w, 128);
@@ -364,7 +330,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         flags[0] = 0;
         fence_barrier_init();
-        griddep_launch_dependents();
     }
     if (warp == 0) a2_tmem_alloc<Sh::cols>(sb + LY.tmem);
     tc_fence_before();
@@ -372,6 +337,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + LY.tmem);
     griddep_wait();   // every input comes from the kernels before this one
+    // released only now: the rows kernel behind this one reads the same inputs
+    // without a wait of its own
+    if (threadIdx.x == 0) griddep_launch_dependents();
     const int P = pa_prefix_len(p);
     const auto wait = [&](uint32_t bar, int n) {   // until phase n of bar is complete
         return mbar_try_wait(bar, (uint32_t)n & 1) || bounded_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns, true);
@@ -383,11 +351,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (lane == 0) tma_prefetch_map(&tmKV);
         PaWork<D> work(p, P, w);
         PaItem it;
-        bool shared, stop = false;
-        PaRing<NS> ring(w);
+        bool stop = false;
+        PaRing<NS> ring(w, p.pair);
         int mine = 0;   // steps loaded into this ring
         unsigned bad_any = 0u;
-        while (!stop && work.next(it, shared)) {
+        while (!stop && work.next(it)) {
             const int pg0 = it.kb0 * Sh::pages;
             const int pg1 = min(it.kb1 * Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots);
             int next = pg0 + lane < pg1 ? it.pages[pg0 + lane] : 0;
@@ -402,7 +370,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 const unsigned bads = __ballot_sync(0xffffffffu, bad);
                 bad_any |= bads;
                 for (int b0 = c; b0 < min(c + 32, pg1); b0 += Sh::pages) {
-                    ring.take(shared);
+                    ring.take();
                     const int st = ring.st;
                     if (st / NS != w) continue;   // the other producer's
                     const int n = min(Sh::pages, pg1 - b0);
@@ -421,12 +389,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     ++mine;
                     const int i = c + lane - b0;
                     if (i >= 0 && i < n)
-                        asm volatile(
-                            "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                            " [%0], [%1, {%3, %3, %3, %3, %4}], [%2];" ::"r"(sb + LY.ring + st * Sh::stage_bytes + i * Sh::page_bytes),
-                            "l"(reinterpret_cast<uint64_t>(&tmKV)), "r"(sb + LY.full + 8 * st), "r"(0),
-                            "r"(page * p.nkv + it.g)
-                            : "memory");
+                        pa_load_page(sb + LY.ring + st * Sh::stage_bytes + i * Sh::page_bytes, &tmKV,
+                                     sb + LY.full + 8 * st, page * p.nkv + it.g);
                 }
             }
         }
@@ -443,16 +407,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (lane == 0) {
             PaWork<D> work(p, P, w);
             PaItem it;
-            bool shared, ok = true;
-            PaRing<NS> ring(w);
+            bool ok = true;
+            PaRing<NS> ring(w, p.pair);
             int items = 0, blk = 0;   // items and blocks of this group so far
             const uint32_t sq = sb + LY.q + w * Sh::q_bytes;
-            const uint32_t dS = tmem + Sh::tS + w * KB, dO = tmem + Sh::tO + w * D, dP = tmem + Sh::tP + w * (KB / 2);
-            while (ok && work.next(it, shared)) {
+            const uint32_t dSP = tmem + Sh::tSP + w * 3 * U, dO = tmem + Sh::tO + w * D;
+            while (ok && work.next(it)) {
                 const int n = it.kb1 - it.kb0;
                 if (it.rows <= 0) {   // no second tile: hand the blocks back
                     for (int j = 0; j < n && ok; ++j) {
-                        ring.take(true);
+                        ring.take();
                         ok = wait(sb + LY.full + 8 * ring.st, ring.use);
                         if (ok) mbar_arrive(sb + LY.empty + 8 * ring.st);
                     }
@@ -463,34 +427,35 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 for (int j = 0; j <= n && ok; ++j) {
                     int st = 0, pages = 0;
                     if (j < n) {   // S of block j
-                        ring.take(shared);
+                        ring.take();
                         st = ring.st;
                         pages = min(Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots - (it.kb0 + j) * Sh::pages);
-                        ok = wait(sb + LY.full + 8 * st, ring.use) &&
-                             (blk == 0 || wait(sb + LY.sfree + 8 * w, blk - 1));
+                        // S of the block before has been read, and the weights of
+                        // the one before that, whose columns this S takes
+                        ok = wait(sb + LY.full + 8 * st, ring.use) && (blk < 1 || wait(sb + LY.sfree + 8 * w, blk - 1)) &&
+                             (blk < 2 || wait(sb + LY.pvdone + 8 * w, blk - 2));
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t kst = sb + LY.ring + st * Sh::stage_bytes;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
-                            umma_bf16(dS, pa_desc(sq + (i / 4) * (kPaTile * 128) + (i % 4) * 32, 16, 1024),
+                            umma_bf16(dSP + (blk & 1) * U, pa_desc(sq + (i / 4) * (kPaTile * 128) + (i % 4) * 32, 16, 1024),
                                       pa_desc(kst + (i / 4) * 1024 + (i % 4) * 32, 16, Sh::nblk * 1024),
                                       pa_idesc<E>(KB, false), i != 0);
                         umma_commit(sb + LY.sfull + 8 * w);
                         ++blk;
                     }
                     if (j > 0) {   // O += P V of block j - 1
-                        const int done = j < n ? blk - 2 : blk - 1;
-                        ok = wait(sb + LY.pready + 8 * w, done);
+                        const int b = j < n ? blk - 2 : blk - 1;
+                        ok = wait(sb + LY.pready + 8 * w, b);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t vst = sb + LY.ring + st_prev * Sh::stage_bytes + (D / 64) * 1024;
                         for (int i = 0; i < pages_prev; ++i)
-                            pa_umma_ts(dO, dP + 8 * i, pa_desc(vst + i * Sh::page_bytes, 1024, Sh::nblk * 1024),
+                            pa_umma_ts(dO, dSP + (b & 1) * 2 * U + 8 * i, pa_desc(vst + i * Sh::page_bytes, 1024, Sh::nblk * 1024),
                                        pa_idesc<E>(D, true), j > 1 || i > 0);
-                        umma_commit(sb + LY.empty + 8 * st_prev);
-                        if (!shared) umma_commit(sb + LY.empty + 8 * st_prev);
                         umma_commit(sb + LY.pvdone + 8 * w);
+                        umma_commit(sb + LY.empty + 8 * st_prev);
                     }
                     st_prev = st;
                     pages_prev = pages;
@@ -505,19 +470,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         // ---- softmax: thread = row of the group's tile ----------------------
         const int w = warp >> 2, wq = warp & 3, row = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-        const uint32_t aS = tmem + Sh::tS + w * KB + lane_base, aO = tmem + Sh::tO + w * D + lane_base,
-                       aP = tmem + Sh::tP + w * (KB / 2) + lane_base;
+        const uint32_t aSP = tmem + Sh::tSP + w * 3 * U + lane_base, aO = tmem + Sh::tO + w * D + lane_base;
         uint8_t *sq = smem + LY.q + w * Sh::q_bytes;
         PaWork<D> work(p, P, w);
         PaItem it;
-        bool shared, ok = true;
-        PaRing<NS> ring(w);
+        bool ok = true;
+        PaRing<NS> ring(w, p.pair);
         int blk = 0;
         const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
-        while (ok && work.next(it, shared)) {
+        while (ok && work.next(it)) {
             const int n = it.kb1 - it.kb0;
             if (it.rows <= 0) {
-                for (int j = 0; j < n; ++j) ring.take(true);
+                ring.n += n;
                 continue;
             }
             const bool active = 32 * wq < it.rows, valid = row < it.rows;
@@ -526,19 +490,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             if (active) {   // the previous item's last S was observed: its Q is no longer read
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     static_cast<const uint16_t *>(p.q) + (it.tok0 + tok) * p.q_ts + head * p.q_hs);
+                uint4 v[D / 8];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(sq + (c / 8) * (kPaTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
-                }
+                for (int c = 0; c < D / 8; ++c) v[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint4 *>(sq + (c / 8) * (kPaTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             mbar_arrive(sb + LY.qready + 8 * w);
-            const int limit = it.limit0 + it.step * tok;   // keys this row sees
             float mu = -INFINITY, l = 0.f;
             int bad = 0;
             for (int j = 0; j < n; ++j, ++blk) {
-                ring.take(shared);
+                ring.take();
                 const int st = ring.st;
                 const int key0 = (it.kb0 + j) * KB;
                 ok = wait(sb + LY.sfull + 8 * w, blk);
@@ -547,18 +511,27 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 bad |= slot_bad[st];
                 if (active) {
                     tc_fence_after();
-                    // first pass: the row's maximum.  The second half of S is read
-                    // again for the weights rather than held (168 registers)
-                    const bool edge = __any_sync(0xffffffffu, limit < key0 + KB);
-                    uint32_t s[KB / 2];
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    // S of even blocks lies in units 0 and 1 of the group's three
+                    // (KB / 2 columns each), of odd ones in 1 and 2; the weights
+                    // take the outer unit once its scores are in registers: the
+                    // next S needs the middle unit and the one at the other end.
+                    // First pass: the row's maximum; the middle unit's scores
+                    // are read again rather than held.
+                    const int outer = blk & 1;   // which half of the keys lies in the outer unit
+                    const bool edge = it.keys < key0 + KB;
+                    uint32_t s[U];
+                    float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int half = 1; half >= 0; --half) {
-                        pa_load_scores<KB / 2>(aS + half * (KB / 2), s, edge, limit - key0 - half * (KB / 2));
+                    for (int pass = 0; pass < 2; ++pass) {
+                        const int half = pass ? outer : outer ^ 1;
+                        pa_load_scores<U>(aSP + (pass ? 2 * outer : 1) * U, s, edge, it.keys - key0 - half * U);
 #pragma unroll
-                        for (int c = 0; c < KB / 2; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                        for (int c = 0; c < U; c += 4) {
+                            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+                            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
+                        }
                     }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    const float top = fmaxf(mx[0], mx[1]) * p.scale_log2;
                     // a row's maximum follows only when it grew by more than 2^8: the
                     // weights stay below 2^8 and O is seldom rescaled
                     const bool grew = top > mu + kPaGrow || (mu == -INFINITY && top > mu);
@@ -584,22 +557,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     const float base = mu == -INFINITY ? 0.f : mu;
                     const uint64_t nb2 = f2_pack(-base, -base);
                     uint64_t sum[4] = {0, 0, 0, 0};
-                    if (j > 0) {   // the weights of block j - 1 have been read
-                        ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (half) {
-                            pa_load_scores<KB / 2>(aS + KB / 2, s, edge, limit - key0 - KB / 2);
+                    for (int pass = 0; pass < 2; ++pass) {
+                        const int half = pass ? outer ^ 1 : outer;
+                        if (pass) {
+                            pa_load_scores<U>(aSP + U, s, edge, it.keys - key0 - half * U);
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
                         }
-                        uint32_t pk[KB / 4];
+                        uint32_t pk[U / 2];
 #pragma unroll
-                        for (int c = 0; c < KB / 2; c += 2) {
+                        for (int c = 0; c < U; c += 2) {
                             float a, b;
                             f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), cc, nb2), a, b);
                             a = a2_ex2(a);
@@ -607,19 +576,15 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                             sum[(c >> 1) & 3] = f2_add(sum[(c >> 1) & 3], f2_pack(a, b));
                             pk[c / 2] = E::pack(a, b);
                         }
-                        pa_tmem_st<KB / 4>(aP + half * (KB / 4), pk);
+                        pa_tmem_st<U / 2>(aSP + 2 * outer * U + half * (U / 2), pk);
                     }
                     float a, b;
                     f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
                     l += a + b;
                     pa_tmem_st_wait();
                     tc_fence_before();
-                } else {
-                    if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
-                    if (j > 0) {   // not two arrivals in one phase of pready
-                        ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
-                        if (!ok) break;
-                    }
+                } else if (lane == 0) {
+                    mbar_arrive(sb + LY.sfree + 8 * w);
                 }
                 // the V rows of the last page behind the keys: whatever they hold
                 // must not meet a zero weight
@@ -635,7 +600,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                __syncwarp();
+                // no second arrival before the phase of the block before is complete
+                if (blk > 0) ok = __all_sync(0xffffffffu, wait(sb + LY.pready + 8 * w, blk - 1));
+                if (!ok) break;
                 if (lane == 0) mbar_arrive(sb + LY.pready + 8 * w);
             }
             if (!ok) break;
@@ -666,6 +633,357 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (warp == 0) a2_tmem_dealloc<Sh::cols>(tmem);
 }
 
+// ---- few rows: mma.sync over small CTAs ------------------------------------
+//
+// A tile of 16 or 64 rows against a range of its own key blocks: four warps
+// and a producer per CTA, several CTAs per SM, so that many short key lists
+// are in flight at once.  16 rows: warp w takes page w of each 64-key stage
+// and the four partials are joined in shared memory; 64 rows: warp w takes
+// rows 16 w .. against every page.
+
+constexpr int kPrThreads = 160;
+constexpr int kPrKeys = 64, kPrPages = kPrKeys / kPageSlots;
+
+template <int D>
+struct PrShape {
+    static constexpr int slots = D == 64 ? 3 : 2;
+    static constexpr int nblk = 2 * D / 64;
+    static constexpr uint32_t page_bytes = kPageSlots * 4 * D;
+    static constexpr uint32_t stage_bytes = kPrPages * page_bytes;
+    static constexpr uint32_t ring_bytes = slots * stage_bytes;
+    static constexpr uint32_t smem = ring_bytes + slots * 20 + 16 + 1024;
+    static constexpr int ostride = D + 4;   // floats per row of a warp's partial, over the ring
+    static_assert(4 * 16 * (ostride + 2) * 4 <= ring_bytes, "the warps' partials fit the ring");
+};
+
+template <int D, int RT>
+constexpr int pr_ctas_per_sm()
+{
+    return RT == 16 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
+}
+
+template <class E>
+__device__ __forceinline__ void pr_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (E::is_bf16)
+        mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <class E, int D, int RT>
+__global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, RT>())
+    prefix_rows_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
+{
+    using Sh = PrShape<D>;
+    constexpr int NS = Sh::slots, NP = RT == 16 ? 1 : kPrPages;
+    extern __shared__ uint8_t pr_smem_dyn[];
+    uint8_t *smem = pr_smem_dyn + ((1024u - (smem_u32(pr_smem_dyn) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem), full0 = sb + Sh::ring_bytes, empty0 = full0 + 8 * NS;
+    volatile int *slot_bad = reinterpret_cast<volatile int *>(smem + Sh::ring_bytes + 16 * NS);
+    volatile int *flags = slot_bad + NS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 4);
+        }
+        flags[0] = 0;
+        fence_barrier_init();
+        griddep_launch_dependents();
+    }
+    __syncthreads();
+    // Behind the tile kernel every input is already written (that kernel has
+    // waited for it before this one could start), and only the grid as a whole
+    // must not end before it: the last CTA waits, at its end.
+    const bool behind = !p.small && p.prefix_blocks > 0;
+    if (!behind) griddep_wait();
+    const auto wait = [&](uint32_t bar, int n) {
+        return mbar_try_wait(bar, (uint32_t)n & 1) || bounded_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns, true);
+    };
+
+    // ---- the item: the prefix (few rows in all), then the requests' own keys
+    int idx = blockIdx.x;
+    const int np = p.small && p.prefix_blocks > 0 ? p.nkv * p.sp : 0;
+    const bool own = idx >= np;
+    idx -= own ? np : 0;
+    const int g = idx % p.nkv, rest = idx / p.nkv;
+    const int r = own ? rest % p.R : 0, ts = own ? rest / p.R : 0;
+    const int tile = own ? ts % p.own_tiles : 0, split = own ? ts / p.own_tiles : rest;
+    const int32_t *pages = own ? p.block_table + (size_t)r * p.max_blocks : p.prefix_pages;
+    // the first split starts at page 0: its entries need not wait for a length
+    int first_entry = 0;
+    if (warp == 4 && split == 0 && lane < (own ? p.max_blocks : p.prefix_blocks)) first_entry = pages[lane];
+    const int P = pa_prefix_len(p), L = own ? p.context_lens[r] : 0;
+    PaItem it;
+    if (own) {
+        it.keys = P < 0 ? 0 : pa_own_keys(p, L, tile);
+        it.tok0 = r * p.q_len;
+        it.row0 = tile * RT;
+        it.rows = min(RT, p.q_len * p.group - it.row0);
+        it.limit0 = L - p.q_len + 1;
+        it.step = 1;
+        it.split = p.sp + split;
+        pa_deal(it, (it.keys + kPrKeys - 1) / kPrKeys, p.ss, split);
+    } else {
+        it = pa_prefix_item<kPrKeys>(p, max(P, 0), RT, 0, g, split);
+    }
+    const int n = it.kb1 - it.kb0;   // stages
+    if (n <= 0) {
+        if (behind && blockIdx.x == gridDim.x - 1) griddep_wait();
+        return;
+    }
+    const int pg0 = it.kb0 * kPrPages;
+    const int pg1 = min(it.kb1 * kPrPages, (it.keys + kPageSlots - 1) / kPageSlots);
+
+    const int gq = lane >> 2, t = lane & 3;
+    float o[D / 8][4], m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
+    int bad = 0;
+    bool ok = true;
+    const int row_a = (RT == 64 ? 16 * warp : 0) + gq, row_b = row_a + 8;
+    if (warp == 4) {
+        // ---- produce ---------------------------------------------------------
+        const uint64_t policy = policy_evict_first();   // these keys are read once
+        unsigned bad_any = 0u;
+        bool stop = false;
+        int j = 0;
+        int next = pg0 + lane < pg1 ? (split == 0 ? first_entry : pages[pg0 + lane]) : 0;
+        for (int c = pg0; c < pg1 && !stop; c += 32) {
+            int page = next;
+            if (c + 32 + lane < pg1) next = pages[c + 32 + lane];
+            bool wrong = false;
+            if (c + lane < pg1 && (page < 0 || page >= p.num_pages)) {   // flagged, page 0 in its place
+                wrong = true;
+                page = 0;
+            }
+            const unsigned bads = __ballot_sync(0xffffffffu, wrong);
+            bad_any |= bads;
+            for (int b0 = c; b0 < min(c + 32, pg1); b0 += kPrPages, ++j) {
+                const int st = j % NS, use = j / NS, np_ = min(kPrPages, pg1 - b0);
+                int okl = 1;
+                if (lane == 0) {
+                    okl = use == 0 || wait(empty0 + 8 * st, use - 1);
+                    if (okl) {
+                        slot_bad[st] = (bads >> (b0 - c)) & 15u;
+                        mbar_expect_tx(full0 + 8 * st, (uint32_t)np_ * Sh::page_bytes);
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, okl, 0)) {
+                    stop = true;
+                    break;
+                }
+                const int i = c + lane - b0;
+                if (i >= 0 && i < np_)
+                    tma_load_page(sb + st * Sh::stage_bytes + i * Sh::page_bytes, &tmKV, full0 + 8 * st, page * p.nkv + g, policy);
+            }
+        }
+        if (lane == 0) {
+            if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
+            if (flags[0])
+                for (int k = max(0, j - NS); k < j; ++k)
+                    bounded_wait(full0 + 8 * (k % NS), (uint32_t)((k / NS) & 1), flags, p.wait_limit_ns, false);
+        }
+        __syncwarp();
+    } else {
+        // ---- compute: rows gq and gq + 8 of the warp's 16, mma.sync layout ----
+        const int ma = it.row0 + row_a, mb = it.row0 + row_b, ta = ma / p.group, tb = mb / p.group;
+        const bool va = row_a < it.rows, vb = row_b < it.rows;
+        uint32_t qa[D / 16][4];
+        {
+            const uint16_t *qp = static_cast<const uint16_t *>(p.q);
+            const uint16_t *pa = qp + (it.tok0 + ta) * p.q_ts + (g * p.group + ma - ta * p.group) * p.q_hs + 2 * t;
+            const uint16_t *pb = qp + (it.tok0 + tb) * p.q_ts + (g * p.group + mb - tb * p.group) * p.q_hs + 2 * t;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                qa[k][0] = va ? *reinterpret_cast<const uint32_t *>(pa + 16 * k) : 0u;
+                qa[k][1] = vb ? *reinterpret_cast<const uint32_t *>(pb + 16 * k) : 0u;
+                qa[k][2] = va ? *reinterpret_cast<const uint32_t *>(pa + 16 * k + 8) : 0u;
+                qa[k][3] = vb ? *reinterpret_cast<const uint32_t *>(pb + 16 * k + 8) : 0u;
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+        const int lim_a = it.limit0 + it.step * ta, lim_b = it.limit0 + it.step * tb;
+        const bool rows_here = RT == 16 || 16 * warp < it.rows;
+        for (int j = 0; j < n; ++j) {
+            const int st = j % NS;
+            ok = __all_sync(0xffffffffu, wait(full0 + 8 * st, j / NS));
+            if (!ok) break;
+            bad |= slot_bad[st];
+            const int left = pg1 - pg0 - j * kPrPages;   // pages from this stage on
+            const int b_lo = RT == 16 ? warp : 0;         // the warp's pages of the stage: b_lo ..
+            if (rows_here && b_lo < left) {
+                const uint32_t base = sb + st * Sh::stage_bytes + b_lo * Sh::page_bytes;
+                const int key0 = (it.kb0 + j) * kPrKeys + b_lo * kPageSlots;
+                float sc[2 * NP][4];
+#pragma unroll
+                for (int b = 0; b < NP; ++b) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[2 * b + h][e] = 0.f;
+                    if (b < left)
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const int ch = 2 * k + ((lane >> 3) & 1);   // 8-dim chunk; key lane % 8 (+ 8 for lanes 16 ..)
+                            uint32_t b0, b1, b2, b3;
+                            ldsm_x4(base + b * Sh::page_bytes + (lane >> 4) * (Sh::nblk * 1024) + (ch >> 3) * 1024 +
+                                        (lane & 7) * 128 + (((ch & 7) ^ (lane & 7)) << 4),
+                                    b0, b1, b2, b3);
+                            pr_mma<E>(sc[2 * b], qa[k], b0, b1);
+                            pr_mma<E>(sc[2 * b + 1], qa[k], b2, b3);
+                        }
+                }
+                if (__any_sync(0xffffffffu, min(lim_a, lim_b) < key0 + NP * kPageSlots))
+#pragma unroll
+                    for (int b = 0; b < 2 * NP; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + 8 * b + 2 * t + (e & 1) >= (e >= 2 ? lim_b : lim_a)) sc[b][e] = -INFINITY;
+                float mx_a = -INFINITY, mx_b = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 2 * NP; ++b) {
+                    mx_a = fmaxf(fmaxf(mx_a, sc[b][0]), sc[b][1]);
+                    mx_b = fmaxf(fmaxf(mx_b, sc[b][2]), sc[b][3]);
+                }
+#pragma unroll
+                for (int off = 1; off <= 2; off <<= 1) {
+                    mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
+                    mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
+                }
+                const float mn_a = fmaxf(m_a, mx_a * p.scale_log2), mn_b = fmaxf(m_b, mx_b * p.scale_log2);
+                const float base_a = mn_a == -INFINITY ? 0.f : mn_a, base_b = mn_b == -INFINITY ? 0.f : mn_b;
+                if (__any_sync(0xffffffffu, mn_a != m_a || mn_b != m_b)) {
+                    const float al_a = a2_ex2(m_a - base_a), al_b = a2_ex2(m_b - base_b);
+                    l_a *= al_a;
+                    l_b *= al_b;
+#pragma unroll
+                    for (int d = 0; d < D / 8; ++d) {
+                        o[d][0] *= al_a;
+                        o[d][1] *= al_a;
+                        o[d][2] *= al_b;
+                        o[d][3] *= al_b;
+                    }
+                    m_a = mn_a;
+                    m_b = mn_b;
+                }
+#pragma unroll
+                for (int b = 0; b < 2 * NP; ++b) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[b][e] = a2_ex2(fmaf(sc[b][e], p.scale_log2, e >= 2 ? -base_b : -base_a));
+                    l_a += sc[b][0] + sc[b][1];
+                    l_b += sc[b][2] + sc[b][3];
+                }
+#pragma unroll
+                for (int b = 0; b < NP; ++b)
+                    if (b < left) {
+                        const uint32_t pf[4] = {E::pack(sc[2 * b][0], sc[2 * b][1]), E::pack(sc[2 * b][2], sc[2 * b][3]),
+                                                E::pack(sc[2 * b + 1][0], sc[2 * b + 1][1]), E::pack(sc[2 * b + 1][2], sc[2 * b + 1][3])};
+                        // V rows behind the keys, whatever they hold, must not
+                        // meet a zero weight: b0 / b2 hold keys 2t, 2t + 1 of
+                        // the page, b1 / b3 keys 8 + 2t, 9 + 2t
+                        const int in = it.keys - (key0 + b * kPageSlots);
+                        uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
+                        if (in < kPageSlots) {
+                            m0 = (2 * t < in ? 0xffffu : 0u) | (2 * t + 1 < in ? 0xffff0000u : 0u);
+                            m1 = (2 * t + 8 < in ? 0xffffu : 0u) | (2 * t + 9 < in ? 0xffff0000u : 0u);
+                        }
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const int ch = 2 * k + (lane >> 4);   // key lane % 8 (+ 8 for lanes 8 .. 15, 24 ..)
+                            uint32_t b0, b1, b2, b3;
+                            ldsm_x4_trans(base + b * Sh::page_bytes + ((lane >> 3) & 1) * (Sh::nblk * 1024) +
+                                              (D / 64 + (ch >> 3)) * 1024 + (lane & 7) * 128 + (((ch & 7) ^ (lane & 7)) << 4),
+                                          b0, b1, b2, b3);
+                            pr_mma<E>(o[2 * k], pf, b0 & m0, b1 & m1);
+                            pr_mma<E>(o[2 * k + 1], pf, b2 & m0, b3 & m1);
+                        }
+                    }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * st);
+        }
+#pragma unroll
+        for (int off = 1; off <= 2; off <<= 1) {
+            l_a += __shfl_xor_sync(0xffffffffu, l_a, off);
+            l_b += __shfl_xor_sync(0xffffffffu, l_b, off);
+        }
+    }
+    const int64_t head0 = (int64_t)it.tok0 * p.q_heads + (int64_t)g * p.group;
+    const auto out_row = [&](int row) {   // output row of row `row` of the tile
+        const int m = it.row0 + row, tok = m / p.group;
+        return head0 + (int64_t)tok * p.q_heads + (m - tok * p.group);
+    };
+    float *ws = p.ws_o + (int64_t)it.split * p.rows * D;
+    const int splits = p.sp + p.ss;
+    if constexpr (RT == 64) {
+        if (warp < 4 && ok) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int row = half ? row_b : row_a;
+                if (row < it.rows) {
+                    const int64_t gr = out_row(row);
+#pragma unroll
+                    for (int d = 0; d < D / 8; ++d)
+                        __stcg(reinterpret_cast<float2 *>(ws + gr * D + 8 * d + 2 * t), make_float2(o[d][2 * half], o[d][2 * half + 1]));
+                    if (t == 0) __stcg(p.ws_ml + gr * splits + it.split, make_float2(half ? m_b : m_a, bad ? -1.f : (half ? l_b : l_a)));
+                }
+            }
+        }
+    } else {
+        // join the four warps' partials over the drained ring, in warp order
+        __syncthreads();
+        float *part = reinterpret_cast<float *>(smem), *ml = part + 4 * 16 * Sh::ostride;
+        if (warp < 4) {
+            float *mine = part + warp * 16 * Sh::ostride;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+                *reinterpret_cast<float2 *>(mine + gq * Sh::ostride + 8 * d + 2 * t) = make_float2(o[d][0], o[d][1]);
+                *reinterpret_cast<float2 *>(mine + (gq + 8) * Sh::ostride + 8 * d + 2 * t) = make_float2(o[d][2], o[d][3]);
+            }
+            if (t == 0) {
+                *reinterpret_cast<float2 *>(ml + 2 * (16 * warp + gq)) = make_float2(m_a, l_a);
+                *reinterpret_cast<float2 *>(ml + 2 * (16 * warp + gq + 8)) = make_float2(m_b, l_b);
+            }
+        }
+        __syncthreads();
+        const int row = threadIdx.x >> 3, c = threadIdx.x & 7;   // 8 threads a row
+        if (row < it.rows && row < 16 && !flags[0]) {
+            float f[4], M = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[2 * (16 * w + row)]);
+            const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                f[w] = a2_ex2(ml[2 * (16 * w + row)] - base);
+                l = fmaf(ml[2 * (16 * w + row) + 1], f[w], l);
+            }
+            const int64_t gr = out_row(row);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float4 v = *reinterpret_cast<const float4 *>(part + (16 * w + row) * Sh::ostride + 32 * k + 4 * c);
+                    x.x = fmaf(v.x, f[w], x.x);
+                    x.y = fmaf(v.y, f[w], x.y);
+                    x.z = fmaf(v.z, f[w], x.z);
+                    x.w = fmaf(v.w, f[w], x.w);
+                }
+                __stcg(reinterpret_cast<float4 *>(ws + gr * D + 32 * k + 4 * c), x);
+            }
+            if (c == 0) __stcg(p.ws_ml + gr * splits + it.split, make_float2(M, bad ? -1.f : l));
+        }
+    }
+    if (behind && blockIdx.x == gridDim.x - 1) griddep_wait();
+}
+
 // Joins a row's partials, one warp per row: lane l holds the maximum and sum
 // of partials l, l + 32, ...; their weights go to shared memory, and O is
 // summed with 8 partials' loads in flight (D / 4 lanes a partial, so at
@@ -676,7 +994,7 @@ constexpr int kPaMergeWarps = 4;
 template <class E, int D>
 __global__ void __launch_bounds__(32 * kPaMergeWarps) prefix_merge_kernel(const __grid_constant__ PrefixParams p)
 {
-    constexpr int LPR = D / 4, PAR = 32 / LPR, KB = PaShape<D>::keys;
+    constexpr int LPR = D / 4, PAR = 32 / LPR;
     __shared__ float weight[kPaMergeWarps][2 * kPaMaxSplits];
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
@@ -691,9 +1009,10 @@ __global__ void __launch_bounds__(32 * kPaMergeWarps) prefix_merge_kernel(const 
         if (lane == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
         return;
     }
-    const int own = pa_own_keys(p, L, ((t - r * p.q_len) * p.group + h % p.group) / kPaTile);
+    const int own = pa_own_keys(p, L, ((t - r * p.q_len) * p.group + h % p.group) / p.own_rows);
+    const int pkeys = p.small ? kPrKeys : PaShape<D>::keys;
     // partials 0 .. np - 1 over the prefix, np .. n - 1 (slots sp ..) over its own keys
-    const int np = min(p.sp, (P + KB - 1) / KB), n = np + min(p.ss, (own + KB - 1) / KB), skip = p.sp - np;
+    const int np = min(p.sp, (P + pkeys - 1) / pkeys), n = np + min(p.ss, (own + kPrKeys - 1) / kPrKeys), skip = p.sp - np;
     float2 v[2 * kPaMaxSplits / 32];
     float M = -INFINITY;
     bool bad = false;
@@ -756,18 +1075,18 @@ __global__ void __launch_bounds__(32 * kPaMergeWarps) prefix_merge_kernel(const 
 // ---- host: splits, workspace, launch ---------------------------------------
 
 struct PaPlan {
-    int tiles, own_tiles, pair, sp, ss, sp_max, ss_max;
+    int small, tiles, pair, own_rows, own_tiles, sp, ss, sp_max, ss_max;
 };
 
 // The split (1..most) that ends soonest when `units` row tiles times the
 // splits run in waves of `workers`, each taking blocks / split steps and about
-// two steps of start and end.
-int pa_split(int64_t units, int64_t workers, int64_t blocks, int most)
+// `over` steps of start and end.
+int pa_split(int64_t units, int64_t workers, int64_t blocks, int most, double over)
 {
     int best = 1;
     double least = 1e300;
     for (int s = 1; s <= most; ++s) {
-        const double cost = (double)((units * s + workers - 1) / workers) * ((double)((blocks + s - 1) / s) + 2.0);
+        const double cost = (double)((units * s + workers - 1) / workers) * ((double)((blocks + s - 1) / s) + over);
         if (cost < least * 0.999) {
             least = cost;
             best = s;
@@ -786,19 +1105,24 @@ int pa_most(int64_t units, int64_t workers, int64_t blocks)
 
 PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int prefix_blocks, int max_blocks, int sms)
 {
-    const int keys = head_dim == 64 ? PaShape<64>::keys : PaShape<128>::keys, ppb = keys / kPageSlots;
     const int group = q_heads / nkv;
+    const int64_t all = (int64_t)num_reqs * q_len * group;   // rows of a KV head
     PaPlan pl;
-    pl.tiles = (int)(((int64_t)num_reqs * q_len * group + kPaTile - 1) / kPaTile);
-    pl.own_tiles = (q_len * group + kPaTile - 1) / kPaTile;
-    pl.pair = pl.tiles > 1;
-    const int64_t nb = (prefix_blocks + ppb - 1) / ppb, no = (max_blocks + ppb - 1) / ppb;
-    const int64_t units = (int64_t)(pl.pair ? (pl.tiles + 1) / 2 : 1) * nkv, workers = pl.pair ? sms : 2 * sms;
+    pl.small = all <= 16;
+    pl.tiles = (int)((all + kPaTile - 1) / kPaTile);
+    pl.pair = !pl.small && pl.tiles > 1;
+    pl.own_rows = q_len * group <= 16 ? 16 : 64;
+    pl.own_tiles = (q_len * group + pl.own_rows - 1) / pl.own_rows;
+    const int ctas = pl.own_rows == 16 ? (head_dim == 64 ? 4 : 3) : (head_dim == 64 ? 3 : 2);   // rows kernel, per SM
+    const int keys = pl.small ? kPrKeys : head_dim == 64 ? PaShape<64>::keys : PaShape<128>::keys, ppb = keys / kPageSlots;
+    const int64_t nb = (prefix_blocks + ppb - 1) / ppb, no = (max_blocks + kPrPages - 1) / kPrPages;
+    const int64_t units = (int64_t)(pl.pair ? (pl.tiles + 1) / 2 : 1) * nkv;
+    const int64_t workers = pl.small ? ctas * sms : pl.pair ? sms : 2 * sms;
     pl.sp_max = pa_most(units, workers, nb);
-    pl.sp = pa_split(units, workers, nb, pl.sp_max);
+    pl.sp = pa_split(units, workers, nb, pl.sp_max, pl.small ? 6.0 : 3.0);
     const int64_t own = (int64_t)num_reqs * nkv * pl.own_tiles;
-    pl.ss_max = pa_most(own, 2 * sms, no);
-    pl.ss = pa_split(own, 2 * sms, no, pl.ss_max);
+    pl.ss_max = pa_most(own, ctas * sms, no);
+    pl.ss = pa_split(own, ctas * sms, no, pl.ss_max, 6.0);
     return pl;
 }
 
@@ -814,8 +1138,10 @@ size_t prefix_attn_workspace(int num_reqs, int q_len, int q_heads, int nkv, int 
 template <class E, int D>
 bool prepare_prefix_kernel()
 {
-    return cudaFuncSetAttribute((const void *)prefix_attn_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)pa_smem<D>().total) == cudaSuccess;
+    constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    return cudaFuncSetAttribute((const void *)prefix_tile_kernel<E, D>, attr, (int)pa_smem<D>().total) == cudaSuccess &&
+           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
+           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 64>, attr, (int)PrShape<D>::smem) == cudaSuccess;
 }
 
 bool prepare_prefix_kernels()
@@ -845,13 +1171,22 @@ int encode_prefix_map(const void *kv_cache, int64_t num_pages, int nkv, int head
 template <class E, int D>
 int launch_prefix(const CUtensorMap &map, const PrefixParams &prm, int sms, void *stream)
 {
-    const int64_t shared = prm.pair ? (int64_t)(prm.tiles + 1) / 2 * prm.nkv * prm.sp : 0;
-    const int64_t single = (prm.pair ? 0 : (int64_t)prm.nkv * prm.sp) + (int64_t)prm.R * prm.nkv * prm.own_tiles * prm.ss;
-    int64_t grid = (single + 1) / 2 > shared ? (single + 1) / 2 : shared;
-    if (grid > sms) grid = sms;
-    const int rc = launch_pdl(prefix_attn_kernel<E, D>, dim3((unsigned)grid), dim3(kPaThreads), (size_t)pa_smem<D>().total,
-                              stream, map, prm);
-    if (rc != QKVF_OK) return rc;
+    int rc = QKVF_OK;
+    if (!prm.small && prm.prefix_blocks > 0) {
+        int64_t grid = (int64_t)prm.nkv * prm.sp;
+        grid = prm.pair ? grid * ((prm.tiles + 1) / 2) : (grid + 1) / 2;
+        if (grid > sms) grid = sms;
+        rc = launch_pdl(prefix_tile_kernel<E, D>, dim3((unsigned)grid), dim3(kPaThreads), (size_t)pa_smem<D>().total,
+                        stream, map, prm);
+        if (rc != QKVF_OK) return rc;
+    }
+    const int64_t items = (prm.small && prm.prefix_blocks > 0 ? (int64_t)prm.nkv * prm.sp : 0) +
+                          (prm.max_blocks > 0 ? (int64_t)prm.R * prm.nkv * prm.own_tiles * prm.ss : 0);
+    if (items > 0) {
+        rc = launch_pdl(prm.own_rows == 16 ? prefix_rows_kernel<E, D, 16> : prefix_rows_kernel<E, D, 64>,
+                        dim3((unsigned)items), dim3(kPrThreads), (size_t)PrShape<D>::smem, stream, map, prm);
+        if (rc != QKVF_OK) return rc;
+    }
     return launch_pdl(prefix_merge_kernel<E, D>, dim3((unsigned)((prm.rows + kPaMergeWarps - 1) / kPaMergeWarps)),
                       dim3(32 * kPaMergeWarps), 0, stream, prm);
 }
@@ -1002,6 +1337,8 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     prm.group = q_heads / num_kv_heads;
     prm.rows = num_reqs * q_len * q_heads;
     prm.tiles = pl.tiles;
+    prm.small = pl.small;
+    prm.own_rows = pl.own_rows;
     prm.own_tiles = pl.own_tiles;
     prm.sp = pl.sp;
     prm.ss = pl.ss;
