@@ -34,7 +34,7 @@ struct PaShape {
 };
 
 struct PaSmem {   // offsets from the 1024-byte aligned base
-    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, drain, slot_bad, tmem, flags, total;
+    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, odone, drain, slot_bad, tmem, flags, total;
 };
 
 template <int D>
@@ -60,6 +60,8 @@ __host__ __device__ inline PaSmem pa_smem()
     L.pready = off;
     off += 16;
     L.pvdone = off;
+    off += 16;
+    L.odone = off;
     off += 16;
     L.drain = off;
     off += 16;
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             mbar_init(sb + LY.sfree + 8 * w, 4);
             mbar_init(sb + LY.pready + 8 * w, 4);
             mbar_init(sb + LY.pvdone + 8 * w, 1);
+            mbar_init(sb + LY.odone + 8 * w, 1);
             mbar_init(sb + LY.drain + 8 * w, 1);
         }
         flags[0] = 0;
@@ -410,7 +413,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             bool ok = true;
             PaRing<NS> ring(w, p.pair);
             int items = 0, blk = 0;   // items and blocks of this group so far
-            const uint32_t sq = sb + LY.q + w * Sh::q_bytes;
+            const uint64_t qd = pa_desc(sb + LY.q + w * Sh::q_bytes, 16, 1024);
+            const uint64_t kd0 = pa_desc(sb + LY.ring, 16, Sh::nblk * 1024);
+            const uint64_t vd0 = pa_desc(sb + LY.ring + (D / 64) * 1024, 1024, Sh::nblk * 1024);
             const uint32_t dSP = tmem + Sh::tSP + w * 3 * U, dO = tmem + Sh::tO + w * D;
             while (ok && work.next(it)) {
                 const int n = it.kb1 - it.kb0;
@@ -436,11 +441,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                              (blk < 2 || wait(sb + LY.pvdone + 8 * w, blk - 2));
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t kst = sb + LY.ring + st * Sh::stage_bytes;
+                        // descriptors: constant steps (16 bytes each) from the tile's first
+                        const uint64_t kd = kd0 + (uint32_t)st * (Sh::stage_bytes / 16);
+                        const uint32_t dS = dSP + (blk & 1) * U;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
-                            umma_bf16(dSP + (blk & 1) * U, pa_desc(sq + (i / 4) * (kPaTile * 128) + (i % 4) * 32, 16, 1024),
-                                      pa_desc(kst + (i / 4) * 1024 + (i % 4) * 32, 16, Sh::nblk * 1024),
+                            umma_bf16(dS, qd + (i / 4) * (kPaTile * 8) + (i % 4) * 2, kd + (i / 4) * 64 + (i % 4) * 2,
                                       pa_idesc<E>(KB, false), i != 0);
                         umma_commit(sb + LY.sfull + 8 * w);
                         ++blk;
@@ -450,16 +456,20 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                         ok = wait(sb + LY.pready + 8 * w, b);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t vst = sb + LY.ring + st_prev * Sh::stage_bytes + (D / 64) * 1024;
-                        for (int i = 0; i < pages_prev; ++i)
-                            pa_umma_ts(dO, dSP + (b & 1) * 2 * U + 8 * i, pa_desc(vst + i * Sh::page_bytes, 1024, Sh::nblk * 1024),
-                                       pa_idesc<E>(D, true), j > 1 || i > 0);
+                        const uint64_t vd = vd0 + (uint32_t)st_prev * (Sh::stage_bytes / 16);
+                        const uint32_t dP = dSP + (b & 1) * 2 * U;
+                        const uint32_t acc = j > 1;
+#pragma unroll
+                        for (int i = 0; i < Sh::pages; ++i)
+                            if (i < pages_prev)
+                                pa_umma_ts(dO, dP + 8 * i, vd + i * (Sh::page_bytes / 16), pa_idesc<E>(D, true), i > 0 ? 1u : acc);
                         umma_commit(sb + LY.pvdone + 8 * w);
                         umma_commit(sb + LY.empty + 8 * st_prev);
                     }
                     st_prev = st;
                     pages_prev = pages;
                 }
+                if (ok) umma_commit(sb + LY.odone + 8 * w);
             }
             // every MMA of this thread is done before tensor memory is freed
             umma_commit(sb + LY.drain + 8 * w);
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         PaItem it;
         bool ok = true;
         PaRing<NS> ring(w, p.pair);
-        int blk = 0;
+        int blk = 0, items = 0;
         const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
         while (ok && work.next(it)) {
             const int n = it.kb1 - it.kb0;
@@ -606,7 +616,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 if (lane == 0) mbar_arrive(sb + LY.pready + 8 * w);
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
+            // (not on pvdone, whose last two phases may both be open: a parity
+            // tells a phase only from its neighbours)
+            ok = __all_sync(0xffffffffu, wait(sb + LY.odone + 8 * w, items++));
             if (!ok) break;
             if (active) {
                 tc_fence_after();
