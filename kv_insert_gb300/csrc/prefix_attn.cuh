@@ -13,8 +13,8 @@ constexpr int kPaMaxQLen = 1024;
 constexpr int kPaMaxGroup = 64;          // q heads per KV head
 constexpr int kPaTile = 128;             // query rows of one tcgen05.mma tile
 constexpr int kPaThreads = 384;          // 2 softmax groups of 4 warps, 2 producer warps, 2 MMA warps
+constexpr float kPaMost = 16384.f;       // a row's weights of a block may add up to this before its maximum follows
 constexpr int kPaMaxSplits = 64;         // key splits of a tile, prefix and own keys each
-constexpr float kPaGrow = 8.f;           // a row's maximum may lag by 2^8 before O is rescaled
 
 // Shapes by head width: a block of keys is one ring stage (K and V, 32 KB)
 // and one S tile; each of the two rings holds `slots` of them.
@@ -34,14 +34,14 @@ struct PaShape {
 };
 
 struct PaSmem {   // offsets from the 1024-byte aligned base
-    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, odone, drain, slot_bad, tmem, flags, total;
+    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, odone, drain, stagger, slot_bad, tmem, flags, total;
 };
 
 template <int D>
-__host__ __device__ inline PaSmem pa_smem()
+__host__ __device__ constexpr PaSmem pa_smem()
 {
     using Sh = PaShape<D>;
-    PaSmem L;
+    PaSmem L = {};
     uint32_t off = 0;
     L.q = off;
     off += 2 * Sh::q_bytes;
@@ -65,6 +65,8 @@ __host__ __device__ inline PaSmem pa_smem()
     off += 16;
     L.drain = off;
     off += 16;
+    L.stagger = off;
+    off += 8;
     L.slot_bad = off;
     off += 2 * Sh::slots * 4;
     L.tmem = off;
@@ -198,6 +200,17 @@ struct PaRing {
     }
 };
 
+// The bounded wait, polled for some microseconds before it first reads the
+// timer: a reading costs more than a step's usual wait (16 x 128 rows over
+// 32K keys, whole call: XX -> YY us)
+__device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity, volatile int *flags, unsigned long long limit_ns)
+{
+#pragma unroll 1
+    for (int i = 0; i < 512; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return bounded_wait(bar, parity, flags, limit_ns, true);
+}
+
 // ---- tensor memory, 32 lanes x 32 columns per warp -------------------------
 
 #define PA_REGS8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
@@ -212,15 +225,6 @@ __device__ __forceinline__ void pa_tmem_ld32(uint32_t addr, uint32_t *r)
         : "r"(addr));
 }
 
-__device__ __forceinline__ void pa_tmem_st32(uint32_t addr, const uint32_t *r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-        PA_IN8(r, 0), PA_IN8(r, 8), PA_IN8(r, 16), PA_IN8(r, 24)
-        : "memory");
-}
-
 __device__ __forceinline__ void pa_tmem_st16(uint32_t addr, const uint32_t *r)
 {
     asm volatile(
@@ -233,11 +237,8 @@ __device__ __forceinline__ void pa_tmem_st16(uint32_t addr, const uint32_t *r)
 template <int N>
 __device__ __forceinline__ void pa_tmem_st(uint32_t addr, const uint32_t *r)
 {
-    static_assert(N == 16 || N == 32, "columns per store");
-    if constexpr (N == 32)
-        pa_tmem_st32(addr, r);
-    else
-        pa_tmem_st16(addr, r);
+#pragma unroll
+    for (int c = 0; c < N; c += 16) pa_tmem_st16(addr + c, r + c);
 }
 
 // N scores of this thread's row; near an edge those from `limit` on become
@@ -303,6 +304,39 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
+template <int N>
+__device__ __forceinline__ float pa_max(const uint32_t (&s)[N], float m)
+{
+    float a = m, b = m;
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+        a = fmaxf(fmaxf(a, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+        b = fmaxf(fmaxf(b, __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
+    }
+    return fmaxf(a, b);
+}
+
+// The weights 2^(scale s - mu) of N scores, rounded and packed in pairs; returns their sum
+template <class E, int N>
+__device__ __forceinline__ float pa_weights(const uint32_t (&s)[N], uint32_t (&pk)[N / 2], uint64_t scale2, float mu)
+{
+    const float base = mu == -INFINITY ? 0.f : -mu;
+    const uint64_t nb2 = f2_pack(base, base);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        float a, b;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, nb2), a, b);
+        a = a2_ex2(a);
+        b = a2_ex2(b);
+        sum[(c >> 1) & 1] = f2_add(sum[(c >> 1) & 1], f2_pack(a, b));
+        pk[c / 2] = E::pack(a, b);
+    }
+    float a, b;
+    f2_unpack(f2_add(sum[0], sum[1]), a, b);
+    return a + b;
+}
+
 template <class E, int D>
 __global__ void __launch_bounds__(kPaThreads, 1)
     prefix_tile_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
@@ -331,6 +365,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             mbar_init(sb + LY.odone + 8 * w, 1);
             mbar_init(sb + LY.drain + 8 * w, 1);
         }
+        mbar_init(sb + LY.stagger, 1);
         flags[0] = 0;
         fence_barrier_init();
     }
@@ -345,7 +380,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (threadIdx.x == 0) griddep_launch_dependents();
     const int P = pa_prefix_len(p);
     const auto wait = [&](uint32_t bar, int n) {   // until phase n of bar is complete
-        return mbar_try_wait(bar, (uint32_t)n & 1) || bounded_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns, true);
+        return pa_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns);
     };
 
     if (warp >= 8 && warp < 10) {
@@ -427,7 +462,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     }
                     continue;
                 }
-                ok = wait(sb + LY.qready + 8 * w, items++);
+                // group 1 starts half a step behind group 0, so that one's exponentials
+                // run while the other waits for its products
+                ok = wait(sb + LY.qready + 8 * w, items) && (w == 0 || items > 0 || wait(sb + LY.stagger, 0));
+                ++items;
                 int st_prev = 0, pages_prev = 0;
                 for (int j = 0; j <= n && ok; ++j) {
                     int st = 0, pages = 0;
@@ -436,9 +474,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                         st = ring.st;
                         pages = min(Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots - (it.kb0 + j) * Sh::pages);
                         // S of the block before has been read, and the weights of
-                        // the one before that, whose columns this S takes
+                        // the one before that, whose columns this S takes (an
+                        // item's end has waited for all of its products)
                         ok = wait(sb + LY.full + 8 * st, ring.use) && (blk < 1 || wait(sb + LY.sfree + 8 * w, blk - 1)) &&
-                             (blk < 2 || wait(sb + LY.pvdone + 8 * w, blk - 2));
+                             (j < 2 || wait(sb + LY.pvdone + 8 * w, blk - 2));
                         if (!ok) break;
                         tc_fence_after();
                         // descriptors: constant steps (16 bytes each) from the tile's first
@@ -458,7 +497,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                         tc_fence_after();
                         const uint64_t vd = vd0 + (uint32_t)st_prev * (Sh::stage_bytes / 16);
                         const uint32_t dP = dSP + (b & 1) * 2 * U;
-                        const uint32_t acc = j > 1;
+                        const uint32_t acc = j > 1;   // the item's first product overwrites O
 #pragma unroll
                         for (int i = 0; i < Sh::pages; ++i)
                             if (i < pages_prev)
@@ -477,7 +516,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- softmax: thread = row of the group's tile ----------------------
+// ---- softmax: thread = row of the group's tile ----------------------
+        // S of even blocks lies in units 0 and 1 of the group's three (KB / 2
+        // columns each), of odd ones in 1 and 2.  The weights take the outer
+        // unit's columns; the middle one and the unit at the other end are free
+        // for the next S while this block's weights are still being made.
         const int w = warp >> 2, wq = warp & 3, row = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
         const uint32_t aSP = tmem + Sh::tSP + w * 3 * U + lane_base, aO = tmem + Sh::tO + w * D + lane_base;
@@ -495,9 +538,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 continue;
             }
             const bool active = 32 * wq < it.rows, valid = row < it.rows;
-            const int m = it.row0 + row, tok = m / p.group, head = it.g * p.group + m % p.group;
+            const int m = it.row0 + row, tok = m / p.group, head = it.g * p.group + m - tok * p.group;
             const int64_t grow = (int64_t)(it.tok0 + tok) * p.q_heads + head;   // output row
-            if (active) {   // the previous item's last S was observed: its Q is no longer read
+            if (active) {   // the previous item is done: its Q is no longer read
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     static_cast<const uint16_t *>(p.q) + (it.tok0 + tok) * p.q_ts + head * p.q_hs);
                 uint4 v[D / 8];
@@ -515,90 +558,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 ring.take();
                 const int st = ring.st;
                 const int key0 = (it.kb0 + j) * KB;
-                ok = wait(sb + LY.sfull + 8 * w, blk);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, wait(sb + LY.sfull + 8 * w, blk));
                 if (!ok) break;
                 bad |= slot_bad[st];
-                if (active) {
-                    tc_fence_after();
-                    // S of even blocks lies in units 0 and 1 of the group's three
-                    // (KB / 2 columns each), of odd ones in 1 and 2; the weights
-                    // take the outer unit once its scores are in registers: the
-                    // next S needs the middle unit and the one at the other end.
-                    // First pass: the row's maximum; the middle unit's scores
-                    // are read again rather than held.
-                    const int outer = blk & 1;   // which half of the keys lies in the outer unit
-                    const bool edge = it.keys < key0 + KB;
-                    uint32_t s[U];
-                    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int pass = 0; pass < 2; ++pass) {
-                        const int half = pass ? outer : outer ^ 1;
-                        pa_load_scores<U>(aSP + (pass ? 2 * outer : 1) * U, s, edge, it.keys - key0 - half * U);
-#pragma unroll
-                        for (int c = 0; c < U; c += 4) {
-                            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
-                            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
-                        }
-                    }
-                    const float top = fmaxf(mx[0], mx[1]) * p.scale_log2;
-                    // a row's maximum follows only when it grew by more than 2^8: the
-                    // weights stay below 2^8 and O is seldom rescaled
-                    const bool grew = top > mu + kPaGrow || (mu == -INFINITY && top > mu);
-                    if (__any_sync(0xffffffffu, grew)) {
-                        const float al = grew ? a2_ex2(mu - top) : 1.f;
-                        if (grew) mu = top;
-                        l *= al;
-                        if (j > 0) {
-                            ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                pa_tmem_ld32(aO + c, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                pa_tmem_st32(aO + c, o);
-                            }
-                        }
-                    }
-                    const float base = mu == -INFINITY ? 0.f : mu;
-                    const uint64_t nb2 = f2_pack(-base, -base);
-                    uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int pass = 0; pass < 2; ++pass) {
-                        const int half = pass ? outer ^ 1 : outer;
-                        if (pass) {
-                            pa_load_scores<U>(aSP + U, s, edge, it.keys - key0 - half * U);
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
-                        }
-                        uint32_t pk[U / 2];
-#pragma unroll
-                        for (int c = 0; c < U; c += 2) {
-                            float a, b;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), cc, nb2), a, b);
-                            a = a2_ex2(a);
-                            b = a2_ex2(b);
-                            sum[(c >> 1) & 3] = f2_add(sum[(c >> 1) & 3], f2_pack(a, b));
-                            pk[c / 2] = E::pack(a, b);
-                        }
-                        pa_tmem_st<U / 2>(aSP + 2 * outer * U + half * (U / 2), pk);
-                    }
-                    float a, b;
-                    f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
-                    l += a + b;
-                    pa_tmem_st_wait();
-                    tc_fence_before();
-                } else if (lane == 0) {
-                    mbar_arrive(sb + LY.sfree + 8 * w);
-                }
                 // the V rows of the last page behind the keys: whatever they hold
                 // must not meet a zero weight
-                if (it.keys < key0 + KB && (it.keys & (kPageSlots - 1))) {
+                const bool edge = it.keys < key0 + KB;
+                if (edge && (it.keys & (kPageSlots - 1))) {
                     ok = __all_sync(0xffffffffu, wait(sb + LY.full + 8 * st, ring.use));
                     if (!ok) break;
                     const int pg = (it.keys - key0) / kPageSlots, s0 = it.keys & (kPageSlots - 1);
@@ -610,14 +576,73 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                // no second arrival before the phase of the block before is complete
-                if (blk > 0) ok = __all_sync(0xffffffffu, wait(sb + LY.pready + 8 * w, blk - 1));
+                const int outer = blk & 1;   // the half of the keys in the outer unit
+                const uint32_t aOut = aSP + 2 * outer * U, aMid = aSP + U;
+                const int left_out = it.keys - key0 - outer * U, left_mid = it.keys - key0 - (outer ^ 1) * U;
+                tc_fence_after();
+                if (active) {
+                    uint32_t s[U], pa[U / 2], pb[U / 2];
+                    if (j == 0) {   // the row's first maximum
+                        pa_load_scores<U>(aMid, s, edge, left_mid);
+                        mu = pa_max(s, -INFINITY);
+                        pa_load_scores<U>(aOut, s, edge, left_out);
+                        mu = pa_max(s, mu) * p.scale_log2;
+                    } else {
+                        pa_load_scores<U>(aOut, s, edge, left_out);
+                    }
+                    // The weights against the maximum so far.  Later scores may exceed
+                    // it as long as a block's weights stay below 2^14 in sum (so no
+                    // maximum is taken per block); otherwise it follows and O is rescaled.
+                    float sum = pa_weights<E>(s, pa, cc, mu);
+                    pa_load_scores<U>(aMid, s, edge, left_mid);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(sb + LY.sfree + 8 * w);
+                        if (blk == 0 && w == 0 && wq == 0) mbar_arrive(sb + LY.stagger);
+                    }
+                    sum += pa_weights<E>(s, pb, cc, mu);
+                    if (__any_sync(0xffffffffu, !(sum < kPaMost))) {
+                        uint32_t so[U];
+                        pa_load_scores<U>(aOut, so, edge, left_out);
+                        const float top = pa_max(so, pa_max(s, -INFINITY)) * p.scale_log2;
+                        const float al = top > mu ? a2_ex2(mu - top) : 1.f;
+                        mu = fmaxf(mu, top);
+                        l *= al;
+                        if (j > 0) {
+                            ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld_x16(aO + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                pa_tmem_st16(aO + c, o);
+                            }
+                        }
+                        sum = pa_weights<E>(s, pb, cc, mu);
+                        sum += pa_weights<E>(so, pa, cc, mu);
+                    }
+                    l += sum;
+                    pa_tmem_st<U / 2>(aOut + outer * (U / 2), pa);
+                    pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pb);
+                    pa_tmem_st_wait();
+                    tc_fence_before();
+                } else if (lane == 0) {
+                    mbar_arrive(sb + LY.sfree + 8 * w);
+                }
+                // not before the product of the block before: its phase of pready is
+                // then complete and has been seen (a parity tells neighbours only)
+                if (blk > 0) ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
                 if (!ok) break;
+                __syncwarp();
                 if (lane == 0) mbar_arrive(sb + LY.pready + 8 * w);
             }
             if (!ok) break;
-            // (not on pvdone, whose last two phases may both be open: a parity
-            // tells a phase only from its neighbours)
+            // (not on pvdone, whose last two phases may both be open)
             ok = __all_sync(0xffffffffu, wait(sb + LY.odone + 8 * w, items++));
             if (!ok) break;
             if (active) {
@@ -715,7 +740,7 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, RT>())
     const bool behind = !p.small && p.prefix_blocks > 0;
     if (!behind) griddep_wait();
     const auto wait = [&](uint32_t bar, int n) {
-        return mbar_try_wait(bar, (uint32_t)n & 1) || bounded_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns, true);
+        return pa_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns);
     };
 
     // ---- the item: the prefix (few rows in all), then the requests' own keys
@@ -1150,6 +1175,7 @@ size_t prefix_attn_workspace(int num_reqs, int q_len, int q_heads, int nkv, int 
 template <class E, int D>
 bool prepare_prefix_kernel()
 {
+    static_assert(pa_smem<D>().total <= (uint32_t)kMaxSmemPerCta, "shared memory");
     constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     return cudaFuncSetAttribute((const void *)prefix_tile_kernel<E, D>, attr, (int)pa_smem<D>().total) == cudaSuccess &&
            cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&

@@ -165,6 +165,7 @@ CASES = [  # R, q_len, nkv, G, D, prefix, own lengths
     (70, 2, 1, 5, 128, 4099, [2 + k % 3 for k in range(70)]), (1, 1, 1, 2, 64, 20011, [9000]),
     (2, 1, 64, 1, 64, 33, [2, 3]), (1, 7, 3, 33, 64, 640, [7]), (300, 1, 1, 1, 64, 31, [k % 50 for k in range(300)]),
     (9, 1, 1, 8, 64, 128, [-1, 5, -3, 0, 128, 384, -1, 16, 1]), (3, 1, 1, 4, 64, 0, [-1, 0, 700]),
+    (75, 1, 50, 4, 64, 3000, [k % 9 for k in range(75)]), (700, 1, 8, 8, 128, 600, [k % 3 for k in range(700)]),
     (1, 1, 2, 8, 128, 70000, [1]), (6, 1, 8, 8, 128, 3000, [100, 2000, 1, 0, 513, 1024]),
 ]
 
