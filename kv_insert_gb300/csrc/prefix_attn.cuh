@@ -34,7 +34,7 @@ struct PaShape {
 };
 
 struct PaSmem {   // offsets from the 1024-byte aligned base
-    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, odone, drain, stagger, slot_bad, tmem, flags, total;
+    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, odone, drain, slot_bad, tmem, flags, total;
 };
 
 template <int D>
@@ -57,16 +57,14 @@ __host__ __device__ constexpr PaSmem pa_smem()
     off += 16;
     L.sfree = off;
     off += 16;
-    L.pready = off;
-    off += 16;
+    L.pready = off;   // [block % 2][group]
+    off += 32;
     L.pvdone = off;
     off += 16;
     L.odone = off;
     off += 16;
     L.drain = off;
     off += 16;
-    L.stagger = off;
-    off += 8;
     L.slot_bad = off;
     off += 2 * Sh::slots * 4;
     L.tmem = off;
@@ -200,15 +198,29 @@ struct PaRing {
     }
 };
 
-// The bounded wait, polled for some microseconds before it first reads the
-// timer: a reading costs more than a step's usual wait (16 x 128 rows over
-// 32K keys, whole call: XX -> YY us)
-__device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity, volatile int *flags, unsigned long long limit_ns)
+// Until the phase of this parity completes, at most limit_ns: then flags[0] is
+// set, later waits return at once, and every role leaves at its next block.
+__device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile int *flags, unsigned long long limit_ns)
 {
 #pragma unroll 1
-    for (int i = 0; i < 512; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return bounded_wait(bar, parity, flags, limit_ns, true);
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return;
+    bounded_wait(bar, parity, flags, limit_ns, true);
+}
+
+// One lane of a converged warp, known to the compiler as one (its operands of
+// tcgen05 instructions then stay in uniform registers)
+__device__ __forceinline__ bool pa_elect()
+{
+    uint32_t mine;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(mine));
+    return mine != 0;
 }
 
 // ---- tensor memory, 32 lanes x 32 columns per warp -------------------------
@@ -337,56 +349,34 @@ __device__ __forceinline__ float pa_weights(const uint32_t (&s)[N], uint32_t (&p
     return a + b;
 }
 
+// The roles of the tile kernel's warps.  Every loop over items and blocks is
+// the same in each of them.
 template <class E, int D>
-__global__ void __launch_bounds__(kPaThreads, 1)
-    prefix_tile_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
-{
+struct PaTile {
     using Sh = PaShape<D>;
-    constexpr int KB = Sh::keys, NS = Sh::slots, U = KB / 2;
-    extern __shared__ uint8_t pa_smem_dyn[];
-    uint8_t *smem = pa_smem_dyn + ((1024u - (smem_u32(pa_smem_dyn) & 1023u)) & 1023u);
-    const PaSmem LY = pa_smem<D>();
-    const uint32_t sb = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int *flags = reinterpret_cast<volatile int *>(smem + LY.flags);   // [0]: a wait gave up
-    volatile int *slot_bad = reinterpret_cast<volatile int *>(smem + LY.slot_bad);
+    static constexpr int KB = Sh::keys, NS = Sh::slots, U = KB / 2;
+    static constexpr PaSmem LY = pa_smem<D>();
+    const CUtensorMap *map;
+    const PrefixParams &p;
+    uint8_t *smem;
+    uint32_t sb;
+    int P, lane;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2 * NS; ++i) {
-            mbar_init(sb + LY.full + 8 * i, 1);
-            mbar_init(sb + LY.empty + 8 * i, p.pair ? 2 : 1);   // the groups that read the stage
-        }
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(sb + LY.qready + 8 * w, 128);
-            mbar_init(sb + LY.sfull + 8 * w, 1);
-            mbar_init(sb + LY.sfree + 8 * w, 4);
-            mbar_init(sb + LY.pready + 8 * w, 4);
-            mbar_init(sb + LY.pvdone + 8 * w, 1);
-            mbar_init(sb + LY.odone + 8 * w, 1);
-            mbar_init(sb + LY.drain + 8 * w, 1);
-        }
-        mbar_init(sb + LY.stagger, 1);
-        flags[0] = 0;
-        fence_barrier_init();
+    __device__ __forceinline__ volatile int *flags() const { return reinterpret_cast<volatile int *>(smem + LY.flags); }
+    __device__ __forceinline__ volatile int *slot_bad() const { return reinterpret_cast<volatile int *>(smem + LY.slot_bad); }
+    __device__ __forceinline__ void wait(uint32_t bar, int n) const   // until phase n of bar is complete
+    {
+        pa_wait(sb + bar, (uint32_t)n & 1, flags(), p.wait_limit_ns);
     }
-    if (warp == 0) a2_tmem_alloc<Sh::cols>(sb + LY.tmem);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + LY.tmem);
-    griddep_wait();   // every input comes from the kernels before this one
-    // released only now: the rows kernel behind this one reads the same inputs
-    // without a wait of its own
-    if (threadIdx.x == 0) griddep_launch_dependents();
-    const int P = pa_prefix_len(p);
-    const auto wait = [&](uint32_t bar, int n) {   // until phase n of bar is complete
-        return pa_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns);
-    };
+    __device__ __forceinline__ int pages_from(const PaItem &it, int block) const   // of a block, with keys
+    {
+        return min(Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots - block * Sh::pages);
+    }
 
-    if (warp >= 8 && warp < 10) {
-        // ---- produce: ring w's blocks, one 128-byte-swizzled box per page ----
-        const int w = warp - 8;
-        if (lane == 0) tma_prefetch_map(&tmKV);
+    // ---- produce: ring w's blocks, one 128-byte-swizzled box per page ----
+    __device__ __forceinline__ void produce(int w) const
+    {
+        if (lane == 0) tma_prefetch_map(map);
         PaWork<D> work(p, P, w);
         PaItem it;
         bool stop = false;
@@ -412,126 +402,146 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     const int st = ring.st;
                     if (st / NS != w) continue;   // the other producer's
                     const int n = min(Sh::pages, pg1 - b0);
-                    int ok = 1;
-                    if (lane == 0) {
-                        ok = ring.use == 0 || wait(sb + LY.empty + 8 * st, ring.use - 1);
-                        if (ok) {
-                            slot_bad[st] = (bads >> (b0 - c)) & ((1u << Sh::pages) - 1u);
-                            mbar_expect_tx(sb + LY.full + 8 * st, (uint32_t)n * Sh::page_bytes);
-                        }
-                    }
-                    if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                    if (ring.use > 0) wait(LY.empty + 8 * st, ring.use - 1);
+                    __syncwarp();
+                    if (__any_sync(0xffffffffu, flags()[0])) {
                         stop = true;
                         break;
                     }
+                    if (lane == 0) {
+                        slot_bad()[st] = (bads >> (b0 - c)) & ((1u << Sh::pages) - 1u);
+                        mbar_expect_tx(sb + LY.full + 8 * st, (uint32_t)n * Sh::page_bytes);
+                    }
+                    __syncwarp();
                     ++mine;
                     const int i = c + lane - b0;
                     if (i >= 0 && i < n)
-                        pa_load_page(sb + LY.ring + st * Sh::stage_bytes + i * Sh::page_bytes, &tmKV,
+                        pa_load_page(sb + LY.ring + st * Sh::stage_bytes + i * Sh::page_bytes, map,
                                      sb + LY.full + 8 * st, page * p.nkv + it.g);
                 }
             }
         }
         if (lane == 0) {
             if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
-            if (flags[0])   // our copies land before the CTA leaves
+            if (flags()[0])   // our copies land before the CTA leaves
                 for (int j = max(0, mine - NS); j < mine; ++j)
-                    bounded_wait(sb + LY.full + 8 * (w * NS + j % NS), (uint32_t)((j / NS) & 1), flags, p.wait_limit_ns, false);
+                    bounded_wait(sb + LY.full + 8 * (w * NS + j % NS), (uint32_t)((j / NS) & 1), flags(), p.wait_limit_ns, false);
         }
         __syncwarp();
-    } else if (warp >= 10) {
-        // ---- multiply: one thread issues group w's S = Q K^T and O += P V ----
-        const int w = warp - 10;
-        if (lane == 0) {
-            PaWork<D> work(p, P, w);
-            PaItem it;
-            bool ok = true;
-            PaRing<NS> ring(w, p.pair);
-            int items = 0, blk = 0;   // items and blocks of this group so far
-            const uint64_t qd = pa_desc(sb + LY.q + w * Sh::q_bytes, 16, 1024);
-            const uint64_t kd0 = pa_desc(sb + LY.ring, 16, Sh::nblk * 1024);
-            const uint64_t vd0 = pa_desc(sb + LY.ring + (D / 64) * 1024, 1024, Sh::nblk * 1024);
-            const uint32_t dSP = tmem + Sh::tSP + w * 3 * U, dO = tmem + Sh::tO + w * D;
-            while (ok && work.next(it)) {
-                const int n = it.kb1 - it.kb0;
-                if (it.rows <= 0) {   // no second tile: hand the blocks back
-                    for (int j = 0; j < n && ok; ++j) {
-                        ring.take();
-                        ok = wait(sb + LY.full + 8 * ring.st, ring.use);
-                        if (ok) mbar_arrive(sb + LY.empty + 8 * ring.st);
-                    }
-                    continue;
+    }
+
+    // ---- multiply: group W's S = Q K^T and O += P V ----------------------
+    template <int W>
+    __device__ __forceinline__ void multiply() const
+    {
+        PaWork<D> work(p, P, W);
+        PaItem it;
+        PaRing<NS> ring(W, p.pair);
+        int items = 0, blk = 0;   // items and blocks of this group so far
+        const uint64_t qd = pa_desc(sb + LY.q + W * Sh::q_bytes, 16, 1024);
+        const uint64_t kd0 = pa_desc(sb + LY.ring, 16, Sh::nblk * 1024);
+        const uint64_t vd0 = pa_desc(sb + LY.ring + (D / 64) * 1024, 1024, Sh::nblk * 1024);
+        constexpr uint32_t dSP = Sh::tSP + W * 3 * U, dO = Sh::tO + W * D;
+        bool stop = false;
+        while (!stop && work.next(it)) {
+            const int n = it.kb1 - it.kb0;
+            if (it.rows <= 0) {   // no second tile: hand the blocks back
+                for (int j = 0; j < n && !stop; ++j) {
+                    ring.take();
+                    wait(LY.full + 8 * ring.st, ring.use);
+                    __syncwarp();
+                    stop = __any_sync(0xffffffffu, flags()[0]);
+                    if (lane == 0) mbar_arrive(sb + LY.empty + 8 * ring.st);
                 }
-                // group 1 starts half a step behind group 0, so that one's exponentials
-                // run while the other waits for its products
-                ok = wait(sb + LY.qready + 8 * w, items) && (w == 0 || items > 0 || wait(sb + LY.stagger, 0));
-                ++items;
-                int st_prev = 0, pages_prev = 0;
-                for (int j = 0; j <= n && ok; ++j) {
-                    int st = 0, pages = 0;
-                    if (j < n) {   // S of block j
-                        ring.take();
-                        st = ring.st;
-                        pages = min(Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots - (it.kb0 + j) * Sh::pages);
-                        // S of the block before has been read, and the weights of
-                        // the one before that, whose columns this S takes (an
-                        // item's end has waited for all of its products)
-                        ok = wait(sb + LY.full + 8 * st, ring.use) && (blk < 1 || wait(sb + LY.sfree + 8 * w, blk - 1)) &&
-                             (j < 2 || wait(sb + LY.pvdone + 8 * w, blk - 2));
-                        if (!ok) break;
-                        tc_fence_after();
-                        // descriptors: constant steps (16 bytes each) from the tile's first
-                        const uint64_t kd = kd0 + (uint32_t)st * (Sh::stage_bytes / 16);
-                        const uint32_t dS = dSP + (blk & 1) * U;
+                continue;
+            }
+            wait(LY.qready + 8 * W, items);
+            ++items;
+            int st_prev = 0, pages_prev = 0;
+            for (int j = 0; j <= n && !stop; ++j) {
+                int st = 0, pages = 0;
+                if (j < n) {   // S of block j
+                    ring.take();
+                    st = ring.st;
+                    pages = pages_from(it, it.kb0 + j);
+                    wait(LY.full + 8 * st, ring.use);
+                    // S of the block before has been read, and the weights of the
+                    // one before that, whose columns this S takes (an item's end
+                    // has waited for all of its products)
+                    if (blk > 0) wait(LY.sfree + 8 * W, blk - 1);
+                    if (j > 1) wait(LY.pvdone + 8 * W, blk - 2);
+                    __syncwarp();
+                    tc_fence_after();
+                    // descriptors: constant steps (16 bytes each) from the tile's first
+                    const uint64_t kd = kd0 + (uint32_t)st * (Sh::stage_bytes / 16);
+                    const uint32_t dS = dSP + (blk & 1) * U;
+                    if (pa_elect()) {
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
                             umma_bf16(dS, qd + (i / 4) * (kPaTile * 8) + (i % 4) * 2, kd + (i / 4) * 64 + (i % 4) * 2,
                                       pa_idesc<E>(KB, false), i != 0);
-                        umma_commit(sb + LY.sfull + 8 * w);
-                        ++blk;
+                        umma_commit(sb + LY.sfull + 8 * W);
                     }
-                    if (j > 0) {   // O += P V of block j - 1
-                        const int b = j < n ? blk - 2 : blk - 1;
-                        ok = wait(sb + LY.pready + 8 * w, b);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = vd0 + (uint32_t)st_prev * (Sh::stage_bytes / 16);
-                        const uint32_t dP = dSP + (b & 1) * 2 * U;
-                        const uint32_t acc = j > 1;   // the item's first product overwrites O
+                    __syncwarp();
+                    ++blk;
+                }
+                if (j > 0) {   // O += P V of block j - 1
+                    const int b = j < n ? blk - 2 : blk - 1;
+                    wait(LY.pready + 16 * (b & 1) + 8 * W, b >> 1);
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint64_t vd = vd0 + (uint32_t)st_prev * (Sh::stage_bytes / 16);
+                    const uint32_t dP = dSP + (b & 1) * 2 * U;
+                    const uint32_t acc = j > 1;   // the item's first product overwrites O
+                    if (pages_prev == Sh::pages) {
+                        if (pa_elect()) {
 #pragma unroll
-                        for (int i = 0; i < Sh::pages; ++i)
-                            if (i < pages_prev)
+                            for (int i = 0; i < Sh::pages; ++i)
                                 pa_umma_ts(dO, dP + 8 * i, vd + i * (Sh::page_bytes / 16), pa_idesc<E>(D, true), i > 0 ? 1u : acc);
-                        umma_commit(sb + LY.pvdone + 8 * w);
+                            umma_commit(sb + LY.pvdone + 8 * W);
+                            umma_commit(sb + LY.empty + 8 * st_prev);
+                        }
+                    } else if (pa_elect()) {
+                        for (int i = 0; i < pages_prev; ++i)
+                            pa_umma_ts(dO, dP + 8 * i, vd + i * (Sh::page_bytes / 16), pa_idesc<E>(D, true), i > 0 ? 1u : acc);
+                        umma_commit(sb + LY.pvdone + 8 * W);
                         umma_commit(sb + LY.empty + 8 * st_prev);
                     }
-                    st_prev = st;
-                    pages_prev = pages;
+                    __syncwarp();
                 }
-                if (ok) umma_commit(sb + LY.odone + 8 * w);
+                st_prev = st;
+                pages_prev = pages;
+                stop = __any_sync(0xffffffffu, flags()[0]);
             }
-            // every MMA of this thread is done before tensor memory is freed
-            umma_commit(sb + LY.drain + 8 * w);
-            bounded_wait(sb + LY.drain + 8 * w, 0, flags, p.wait_limit_ns, false);
+            if (pa_elect()) umma_commit(sb + LY.odone + 8 * W);
+            __syncwarp();
         }
+        // every MMA of this warp is done before tensor memory is freed (the same
+        // lane is elected each time: commits cover the MMAs of one thread)
+        if (pa_elect()) umma_commit(sb + LY.drain + 8 * W);
         __syncwarp();
-    } else {
-// ---- softmax: thread = row of the group's tile ----------------------
-        // S of even blocks lies in units 0 and 1 of the group's three (KB / 2
-        // columns each), of odd ones in 1 and 2.  The weights take the outer
-        // unit's columns; the middle one and the unit at the other end are free
-        // for the next S while this block's weights are still being made.
-        const int w = warp >> 2, wq = warp & 3, row = threadIdx.x & 127;
+        if (lane == 0) bounded_wait(sb + LY.drain + 8 * W, 0, flags(), p.wait_limit_ns, false);
+        __syncwarp();
+    }
+
+    // ---- softmax: thread = row of group w's tile -------------------------
+    // S of even blocks lies in units 0 and 1 of the group's three (KB / 2
+    // columns each), of odd ones in 1 and 2.  The weights take the outer unit's
+    // columns; the middle one and the unit at the other end are free for the
+    // next S while this block's weights are still being made.
+    __device__ __forceinline__ void softmax(int w, int wq) const
+    {
+        const int row = 32 * wq + lane;
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-        const uint32_t aSP = tmem + Sh::tSP + w * 3 * U + lane_base, aO = tmem + Sh::tO + w * D + lane_base;
+        const uint32_t aSP = Sh::tSP + w * 3 * U + lane_base, aO = Sh::tO + w * D + lane_base;
         uint8_t *sq = smem + LY.q + w * Sh::q_bytes;
         PaWork<D> work(p, P, w);
         PaItem it;
-        bool ok = true;
         PaRing<NS> ring(w, p.pair);
         int blk = 0, items = 0;
         const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
-        while (ok && work.next(it)) {
+        bool stop = false;
+        while (!stop && work.next(it)) {
             const int n = it.kb1 - it.kb0;
             if (it.rows <= 0) {
                 ring.n += n;
@@ -558,28 +568,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 ring.take();
                 const int st = ring.st;
                 const int key0 = (it.kb0 + j) * KB;
-                ok = __all_sync(0xffffffffu, wait(sb + LY.sfull + 8 * w, blk));
-                if (!ok) break;
-                bad |= slot_bad[st];
-                // the V rows of the last page behind the keys: whatever they hold
-                // must not meet a zero weight
+                wait(LY.sfull + 8 * w, blk);
+                __syncwarp();
+                tc_fence_after();
+                const int dead = flags()[0];   // read here, looked at when it has come
+                bad |= slot_bad()[st];
                 const bool edge = it.keys < key0 + KB;
-                if (edge && (it.keys & (kPageSlots - 1))) {
-                    ok = __all_sync(0xffffffffu, wait(sb + LY.full + 8 * st, ring.use));
-                    if (!ok) break;
-                    const int pg = (it.keys - key0) / kPageSlots, s0 = it.keys & (kPageSlots - 1);
-                    for (int c = row; c < (kPageSlots - s0) * (D / 8); c += 128) {
-                        const int s = s0 + c / (D / 8), ch = c % (D / 8);
-                        *reinterpret_cast<uint4 *>(smem + LY.ring + st * Sh::stage_bytes + pg * Sh::page_bytes +
-                                                   (s >> 3) * (Sh::nblk * 1024) + (D / 64 + ch / 8) * 1024 +
-                                                   (s & 7) * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
+                if (edge) zero_tail(it, st, ring.use, key0, row);
                 const int outer = blk & 1;   // the half of the keys in the outer unit
                 const uint32_t aOut = aSP + 2 * outer * U, aMid = aSP + U;
                 const int left_out = it.keys - key0 - outer * U, left_mid = it.keys - key0 - (outer ^ 1) * U;
-                tc_fence_after();
                 if (active) {
                     uint32_t s[U], pa[U / 2], pb[U / 2];
                     if (j == 0) {   // the row's first maximum
@@ -597,10 +595,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     pa_load_scores<U>(aMid, s, edge, left_mid);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(sb + LY.sfree + 8 * w);
-                        if (blk == 0 && w == 0 && wq == 0) mbar_arrive(sb + LY.stagger);
-                    }
+                    if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
                     sum += pa_weights<E>(s, pb, cc, mu);
                     if (__any_sync(0xffffffffu, !(sum < kPaMost))) {
                         uint32_t so[U];
@@ -610,8 +605,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                         mu = fmaxf(mu, top);
                         l *= al;
                         if (j > 0) {
-                            ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
-                            if (!ok) break;
+                            wait(LY.pvdone + 8 * w, blk - 1);
+                            __syncwarp();
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
@@ -629,23 +624,22 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                     l += sum;
                     pa_tmem_st<U / 2>(aOut + outer * (U / 2), pa);
                     pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pb);
-                    pa_tmem_st_wait();
-                    tc_fence_before();
                 } else if (lane == 0) {
                     mbar_arrive(sb + LY.sfree + 8 * w);
                 }
-                // not before the product of the block before: its phase of pready is
-                // then complete and has been seen (a parity tells neighbours only)
-                if (blk > 0) ok = __all_sync(0xffffffffu, wait(sb + LY.pvdone + 8 * w, blk - 1));
-                if (!ok) break;
+                if (active) pa_tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sb + LY.pready + 8 * w);
+                // (two barriers in turn: this S says that the weights of the block
+                // two back have been multiplied, so that phase has been seen)
+                if (lane == 0) mbar_arrive(sb + LY.pready + 16 * outer + 8 * w);
+                if (dead) break;
             }
-            if (!ok) break;
             // (not on pvdone, whose last two phases may both be open)
-            ok = __all_sync(0xffffffffu, wait(sb + LY.odone + 8 * w, items++));
-            if (!ok) break;
-            if (active) {
+            wait(LY.odone + 8 * w, items++);
+            __syncwarp();
+            stop = __any_sync(0xffffffffu, flags()[0]);
+            if (active && !stop) {
                 tc_fence_after();
                 float *dst = p.ws_o + ((int64_t)it.split * p.rows + grow) * D;
 #pragma unroll
@@ -664,10 +658,77 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             }
         }
     }
+
+    // The V rows of the last page behind the keys: whatever they hold must not
+    // meet a zero weight
+    __device__ __forceinline__ void zero_tail(const PaItem &it, int st, int use, int key0, int row) const
+    {
+        const int s0 = it.keys & (kPageSlots - 1);
+        if (s0 == 0) return;
+        wait(LY.full + 8 * st, use);
+        const int pg = (it.keys - key0) / kPageSlots;
+        for (int c = row; c < (kPageSlots - s0) * (D / 8); c += 128) {
+            const int s = s0 + c / (D / 8), ch = c % (D / 8);
+            *reinterpret_cast<uint4 *>(smem + LY.ring + st * Sh::stage_bytes + pg * Sh::page_bytes +
+                                       (s >> 3) * (Sh::nblk * 1024) + (D / 64 + ch / 8) * 1024 +
+                                       (s & 7) * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+    }
+};
+
+template <class E, int D>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    prefix_tile_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
+{
+    using Sh = PaShape<D>;
+    constexpr PaSmem LY = pa_smem<D>();
+    extern __shared__ uint8_t pa_smem_dyn[];
+    uint8_t *smem = pa_smem_dyn + ((1024u - (smem_u32(pa_smem_dyn) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * Sh::slots; ++i) {
+            mbar_init(sb + LY.full + 8 * i, 1);
+            mbar_init(sb + LY.empty + 8 * i, p.pair ? 2 : 1);   // the groups that read the stage
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(sb + LY.qready + 8 * w, 128);
+            mbar_init(sb + LY.sfull + 8 * w, 1);
+            mbar_init(sb + LY.sfree + 8 * w, 4);
+            mbar_init(sb + LY.pready + 8 * w, 4);
+            mbar_init(sb + LY.pready + 16 + 8 * w, 4);
+            mbar_init(sb + LY.pvdone + 8 * w, 1);
+            mbar_init(sb + LY.odone + 8 * w, 1);
+            mbar_init(sb + LY.drain + 8 * w, 1);
+        }
+        *reinterpret_cast<volatile int *>(smem + LY.flags) = 0;
+        fence_barrier_init();
+    }
+    // all of tensor memory (one CTA per SM): it starts at column 0
+    if (warp == 0) a2_tmem_alloc<Sh::cols>(sb + LY.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) a2_tmem_dealloc<Sh::cols>(tmem);
+    griddep_wait();   // every input comes from the kernels before this one
+    // released only now: the rows kernel behind this one reads the same inputs
+    // without a wait of its own
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    const PaTile<E, D> tile{&tmKV, p, smem, sb, __reduce_max_sync(0xffffffffu, pa_prefix_len(p)), lane};
+    if (warp < 8)
+        tile.softmax(warp >> 2, warp & 3);
+    else if (warp < 10)
+        tile.produce(warp - 8);
+    else if (warp == 10)
+        tile.template multiply<0>();
+    else
+        tile.template multiply<1>();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) a2_tmem_dealloc<Sh::cols>(0u);
 }
 
 // ---- few rows: mma.sync over small CTAs ------------------------------------
@@ -740,7 +801,7 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, RT>())
     const bool behind = !p.small && p.prefix_blocks > 0;
     if (!behind) griddep_wait();
     const auto wait = [&](uint32_t bar, int n) {
-        return pa_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns);
+        return mbar_try_wait(bar, (uint32_t)n & 1) || bounded_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns, true);
     };
 
     // ---- the item: the prefix (few rows in all), then the requests' own keys
