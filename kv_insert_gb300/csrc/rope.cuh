@@ -159,55 +159,211 @@ const char *check_rope_table_args(const float *table, int64_t first, int64_t row
 
 // ---- the rotation ----------------------------------------------------------
 
+// One call of rope (nkv = 0) or of rope_kv_append: the heads of a token in the
+// order q, k, v.  q is rotated into out, k into the K half of the token's
+// cache slot, v copied into the V half.
 struct RopeParams {
-    const void *x;
+    const void *q, *k, *v;
     void *out;
+    void *kv_cache;
     const int64_t *positions;
+    const int64_t *slots;
     const float *cos_sin;
     int64_t cos_rows;
-    int64_t x_ts, x_hs, o_ts, o_hs;   // strides in elements
-    int T, heads, dim, rot;
-    int half_layout;
+    int64_t slot_end;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;   // strides in elements
+    int T, q_heads, nkv, dim, rot;
+    int in_place;    // out is q: the columns behind rot are where they belong
     float sign;      // -1: the gradient
-    int in_place;    // the columns behind rot are already where they belong
+    // the vector kernel's threads: unit u of a head group of a token
+    int units, groups, tokens;   // units of a head, head groups of a token, tokens of a grid row
+    uint32_t unit_m, unit_s, group_m, group_s;
 };
 
-// (a, b) turned: each result is two FP32 products and a sum, rounded once more
-// to the output's type
+// n / d for n < 2^31 by a product and a shift
+void fast_div(uint32_t d, uint32_t *m, uint32_t *s)
+{
+    uint32_t l = 0;
+    while ((uint64_t(1) << l) < d) ++l;
+    *s = l;
+    *m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1);
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, uint32_t m, uint32_t s) { return (__umulhi(n, m) + n) >> s; }
+
+// (a, b) turned: a product and a fused sum in FP32, rounded once more to the
+// output's type
 __device__ __forceinline__ void rope_pair(float a, float b, float c, float s, float &ya, float &yb)
 {
     ya = fmaf(a, c, -(b * s));
     yb = fmaf(b, c, a * s);
 }
 
-// One CTA per token (round robin), one pair or one copied column per thread.
+// A token's indices: whether its heads are rotated and its slot written, with
+// the status bits of those that are not.  `first`: the thread that reports.
+struct RopeToken {
+    const float *row;   // its cos | sin row, null: leave the token alone
+    int64_t slot;       // the element offset of its slot for KV head 0, or -1
+};
+
+__device__ __forceinline__ RopeToken rope_token(const RopeParams &p, int64_t t, bool first)
+{
+    RopeToken k;
+    const int64_t pos = p.positions[t], slot = p.nkv ? p.slots[t] : -1;
+    const bool pos_ok = pos >= 0 && pos < p.cos_rows;
+    k.row = pos_ok ? p.cos_sin + pos * p.rot : nullptr;
+    k.slot = pos_ok && slot >= 0 && slot < p.slot_end
+                 ? ((slot / kPageSlots) * p.nkv * kPageSlots + slot % kPageSlots) * (2 * (int64_t)p.dim)
+                 : -1;
+    if (first && (!pos_ok || slot >= p.slot_end))
+        atomicOr(&g_status, (pos_ok ? 0u : QKVF_STATUS_BAD_POSITION) | (slot >= p.slot_end ? QKVF_STATUS_BAD_SLOT : 0u));
+    return k;
+}
+
+// Head h of token t: where it is read and written; dst null: not at all
+template <class S>
+__device__ __forceinline__ void rope_head(const RopeParams &p, int64_t t, int h, const RopeToken &k, const S *&src, S *&dst)
+{
+    if (h < p.q_heads) {
+        src = static_cast<const S *>(p.q) + t * p.q_ts + h * p.q_hs;
+        dst = static_cast<S *>(p.out) + t * p.o_ts + h * p.o_hs;
+    } else {
+        const bool is_v = h >= p.q_heads + p.nkv;
+        const int g = h - p.q_heads - (is_v ? p.nkv : 0);
+        src = is_v ? static_cast<const S *>(p.v) + t * p.v_ts + g * p.v_hs : static_cast<const S *>(p.k) + t * p.k_ts + g * p.k_hs;
+        dst = k.slot < 0 ? nullptr
+                         : static_cast<S *>(p.kv_cache) + k.slot + (int64_t)g * kPageSlots * 2 * p.dim + (is_v ? p.dim : 0);
+    }
+}
+
+// 16-byte kernel: every row starts on 16 bytes.  A unit is one 16-byte chunk
+// of a head (interleaved pairs) or chunk u of the first half of its rotated
+// columns with its partner in the second (half pairs; the chunks behind the
+// rotated columns are units of their own).  A thread takes unit u of kHeads
+// neighbouring heads of a token, so that the token's cos | sin values are read
+// once for all of them and kHeads (2 kHeads) loads are in flight.
+template <class E, bool kHalf>
+struct RopeVec {
+    using S = typename E::store;
+    static constexpr int vec = 16 / sizeof(S);
+    static constexpr int heads = kHalf ? 4 : 8;
+    static constexpr int pairs = kHalf ? vec : vec / 2;   // rotation pairs of a unit
+    union Chunk {
+        uint4 v;
+        S e[vec];
+    };
+};
+
+template <class E, bool kHalf>
+__global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ RopeParams p)
+{
+    using V = RopeVec<E, kHalf>;
+    using S = typename V::S;
+    using Chunk = typename V::Chunk;
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t lin = blockIdx.x * 256 + threadIdx.x;
+    const uint32_t rest = div_by(lin, p.unit_m, p.unit_s), u = lin - rest * p.units;
+    const uint32_t tl = div_by(rest, p.group_m, p.group_s), grp = rest - tl * p.groups;
+    const int64_t t = (int64_t)blockIdx.y * p.tokens + tl;
+    if ((int)tl >= p.tokens || t >= p.T) return;
+    const RopeToken tok = rope_token(p, t, u == 0 && grp == 0);
+    const int heads = p.q_heads + 2 * p.nkv, h0 = grp * V::heads, half = p.rot >> 1;
+    const bool rotated = kHalf ? (int)u < half / V::vec : (int)u * V::pairs < half;
+    // first chunk of the unit, and its partner's distance (half pairs)
+    const int c0 = kHalf && !rotated ? half / V::vec + u : u;
+    Chunk x[V::heads], y[kHalf ? V::heads : 1];
+#pragma unroll
+    for (int i = 0; i < V::heads; ++i) {
+        const S *src;
+        S *dst;
+        if (h0 + i >= heads) break;
+        rope_head<S>(p, t, h0 + i, tok, src, dst);
+        x[i].v = *reinterpret_cast<const uint4 *>(src + c0 * V::vec);
+        if (kHalf && rotated) y[kHalf ? i : 0].v = *reinterpret_cast<const uint4 *>(src + half + c0 * V::vec);
+    }
+    if (!tok.row) return;
+    float c[V::pairs], s[V::pairs];
+    if (rotated) {
+        const int i0 = u * V::pairs;
+        if (p.rot % 8 == 0 && (kHalf || V::pairs % 4 == 0)) {   // both halves of the row on 16 bytes
+#pragma unroll
+            for (int i = 0; i < V::pairs; i += 4) {
+                if (V::pairs % 4 == 0) {
+                    *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(tok.row + i0 + i);
+                    *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(tok.row + half + i0 + i);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V::pairs; ++i) {
+                const bool in = i0 + i < half;
+                c[i] = in ? tok.row[i0 + i] : 1.f;
+                s[i] = in ? tok.row[half + i0 + i] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V::pairs; ++i) s[i] *= p.sign;
+    }
+#pragma unroll
+    for (int i = 0; i < V::heads; ++i) {
+        const int h = h0 + i;
+        if (h >= heads) break;
+        const S *src;
+        S *dst;
+        rope_head<S>(p, t, h, tok, src, dst);
+        if (!dst) continue;
+        const bool turn = rotated && h < p.q_heads + p.nkv;
+        if (turn) {
+            Chunk &a = x[i], &b = kHalf ? y[kHalf ? i : 0] : x[i];
+#pragma unroll
+            for (int k = 0; k < V::pairs; ++k) {
+                const int ia = kHalf ? k : 2 * k, ib = kHalf ? k : 2 * k + 1;
+                if (!kHalf && (int)u * V::pairs + k >= half) break;   // a chunk the rotated columns end in
+                float ya, yb;
+                rope_pair(E::get(a.e[ia]), E::get(b.e[ib]), c[k], s[k], ya, yb);
+                a.e[ia] = E::put(ya);
+                b.e[ib] = E::put(yb);
+            }
+        } else if (h < p.q_heads && p.in_place) {
+            continue;
+        }
+        *reinterpret_cast<uint4 *>(dst + c0 * V::vec) = x[i].v;
+        if (kHalf && rotated) *reinterpret_cast<uint4 *>(dst + half + c0 * V::vec) = y[kHalf ? i : 0].v;
+    }
+}
+
+// Element kernel, for rows off the 16-byte grid and half pairs whose distance
+// is not whole chunks: lanes over a head's pairs and copied columns, warps over
+// the token's heads.
 template <class E>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p)
+__global__ void __launch_bounds__(256) rope_element_kernel(const __grid_constant__ RopeParams p, int half_layout)
 {
     using S = typename E::store;
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
-    const int half = p.rot >> 1, units = half + (p.in_place ? 0 : p.dim - p.rot);
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const int64_t pos = p.positions[t];
-        if (pos < 0 || pos >= p.cos_rows) {
-            if (threadIdx.x == 0) atomicOr(&g_status, QKVF_STATUS_BAD_POSITION);
-            continue;
-        }
-        const float *row = p.cos_sin + pos * p.rot;
-        for (int u = threadIdx.x; u < units * p.heads; u += blockDim.x) {
-            const int h = u / units, i = u % units;
-            const S *src = static_cast<const S *>(p.x) + t * p.x_ts + h * p.x_hs;
-            S *dst = static_cast<S *>(p.out) + t * p.o_ts + h * p.o_hs;
-            if (i < half) {
-                const int ca = p.half_layout ? i : 2 * i, cb = p.half_layout ? i + half : 2 * i + 1;
-                float ya, yb;
-                rope_pair(E::get(src[ca]), E::get(src[cb]), row[i], p.sign * row[half + i], ya, yb);
-                dst[ca] = E::put(ya);
-                dst[cb] = E::put(yb);
-            } else {
-                dst[p.rot + i - half] = src[p.rot + i - half];
-            }
+    const int half = p.rot >> 1, tail = p.dim - p.rot, heads = p.q_heads + 2 * p.nkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const RopeToken tok = rope_token(p, t, threadIdx.x == 0);
+        if (!tok.row) continue;
+        for (int h = warp; h < heads; h += 8) {
+            const S *src;
+            S *dst;
+            rope_head<S>(p, t, h, tok, src, dst);
+            if (!dst) continue;
+            const bool copy_all = h >= p.q_heads + p.nkv;
+            if (!copy_all)
+                for (int i = lane; i < half; i += 32) {
+                    const int ca = half_layout ? i : 2 * i, cb = half_layout ? i + half : 2 * i + 1;
+                    float ya, yb;
+                    rope_pair(E::get(src[ca]), E::get(src[cb]), tok.row[i], p.sign * tok.row[half + i], ya, yb);
+                    dst[ca] = E::put(ya);
+                    dst[cb] = E::put(yb);
+                }
+            if (copy_all)
+                for (int i = lane; i < p.dim; i += 32) dst[i] = src[i];
+            else if (tail && !(h < p.q_heads && p.in_place))
+                for (int i = lane; i < tail; i += 32) dst[p.rot + i] = src[p.rot + i];
         }
     }
 }
@@ -273,6 +429,40 @@ int launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, void
         return QKVF_ERR_CUDA;
     }
     return QKVF_OK;
+}
+
+template <class E, bool kHalf>
+int launch_rope_vec(RopeParams &prm, void *stream)
+{
+    using V = RopeVec<E, kHalf>;
+    prm.units = kHalf ? (prm.dim - prm.rot / 2) / V::vec : prm.dim / V::vec;
+    prm.groups = (prm.q_heads + 2 * prm.nkv + V::heads - 1) / V::heads;
+    fast_div(prm.units, &prm.unit_m, &prm.unit_s);
+    fast_div(prm.groups, &prm.group_m, &prm.group_s);
+    const int64_t per = (int64_t)prm.units * prm.groups, most = (int64_t(1) << 30) / per;   // a grid row's tokens
+    prm.tokens = (int)(prm.T < most ? prm.T : most);
+    return launch_pdl(rope_vec_kernel<E, kHalf>,
+                      dim3((unsigned)((prm.tokens * per + 255) / 256), (unsigned)((prm.T + prm.tokens - 1) / prm.tokens)),
+                      dim3(256), 0, stream, prm);
+}
+
+// The 16-byte kernel where every row it touches starts on 16 bytes and the
+// partner of a half-layout chunk is a chunk; the element kernel elsewhere
+// (16384 x 32 x 128 bf16, half layout: XX us and YY us).
+template <class E>
+int launch_rope(RopeParams &prm, bool half_layout, int sms, void *stream)
+{
+    constexpr int vec = 16 / (int)sizeof(typename E::store);
+    const auto whole = [&](const void *ptr, int64_t ts, int64_t hs, int heads) {
+        return heads == 0 || (aligned(ptr, 16) && (prm.T == 1 || ts % vec == 0) && (heads == 1 || hs % vec == 0));
+    };
+    if (prm.dim % vec == 0 && (!half_layout || prm.rot / 2 % vec == 0) && whole(prm.q, prm.q_ts, prm.q_hs, prm.q_heads) &&
+        whole(prm.out, prm.o_ts, prm.o_hs, prm.q_heads) && whole(prm.k, prm.k_ts, prm.k_hs, prm.nkv) &&
+        whole(prm.v, prm.v_ts, prm.v_hs, prm.nkv))
+        return half_layout ? launch_rope_vec<E, true>(prm, stream) : launch_rope_vec<E, false>(prm, stream);
+    const int64_t most = (int64_t)sms * 8;
+    return launch_pdl(rope_element_kernel<E>, dim3((unsigned)(prm.T < most ? prm.T : most)), dim3(256), 0, stream, prm,
+                      (int)half_layout);
 }
 
 }  // namespace qkvf
@@ -356,28 +546,25 @@ int rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, const int
     const int rc = qkvf::probe_device(&d);
     if (rc != QKVF_OK) return rc;
     qkvf::RopeParams prm = {};
-    prm.x = x;
+    prm.q = x;
     prm.out = out;
     prm.positions = positions;
     prm.cos_sin = cos_sin;
     prm.cos_rows = cos_sin_rows;
-    prm.x_ts = x_token_stride;
-    prm.x_hs = x_head_stride;
+    prm.q_ts = x_token_stride;
+    prm.q_hs = x_head_stride;
     prm.o_ts = out_token_stride;
     prm.o_hs = out_head_stride;
     prm.T = T;
-    prm.heads = heads;
+    prm.q_heads = heads;
     prm.dim = head_dim;
     prm.rot = rot_dim;
-    prm.half_layout = layout == QKVF_ROPE_HALF;
-    prm.sign = inverse ? -1.f : 1.f;
     prm.in_place = x == out;
-    const int64_t most = (int64_t)d->sms * 8;
-    const dim3 grid((unsigned)(T < most ? T : most));
-    auto kernel = dtype == QKVF_DTYPE_BF16   ? qkvf::rope_kernel<qkvf::Bf16>
-                  : dtype == QKVF_DTYPE_FP16 ? qkvf::rope_kernel<qkvf::Fp16>
-                                             : qkvf::rope_kernel<qkvf::Fp32>;
-    return qkvf::launch_pdl(kernel, grid, dim3(256), 0, stream, prm);
+    prm.sign = inverse ? -1.f : 1.f;
+    const bool half = layout == QKVF_ROPE_HALF;
+    return dtype == QKVF_DTYPE_BF16   ? qkvf::launch_rope<qkvf::Bf16>(prm, half, d->sms, stream)
+           : dtype == QKVF_DTYPE_FP16 ? qkvf::launch_rope<qkvf::Fp16>(prm, half, d->sms, stream)
+                                      : qkvf::launch_rope<qkvf::Fp32>(prm, half, d->sms, stream);
 }
 
 }  // extern "C"

@@ -2,73 +2,11 @@
 // into the paged cache, for any head width, rotary layout and strides
 // (included by qkv_front.cu after rope.cuh: one translation unit).
 //
-// The rotation is rope.cuh's; token t's k head g goes to the K half and its v
-// head g to the V half of slot slots[t] of KV head g, as in
-// qknorm_rope_kv_insert (which also norms, for one fixed layout).
+// The kernels are rope.cuh's, over the heads q, k and v of a token: k head g
+// goes to the K half and v head g to the V half of slot slots[t] of KV head g,
+// as in qknorm_rope_kv_insert (which also norms, for one fixed layout).
 
 namespace qkvf {
-
-struct AppendParams {
-    const void *q, *k, *v;
-    void *q_out;
-    void *kv_cache;
-    const int64_t *positions;
-    const int64_t *slots;
-    const float *cos_sin;
-    int64_t cos_rows;
-    int64_t slot_end;
-    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;   // strides in elements
-    int T, q_heads, nkv, dim, rot;
-    int half_layout;
-    int q_in_place;
-};
-
-// One CTA per token (round robin), one pair or one copied column per thread.
-template <class E>
-__global__ void __launch_bounds__(256) rope_kv_append_kernel(const AppendParams p)
-{
-    using S = typename E::store;
-    if (threadIdx.x == 0) griddep_launch_dependents();
-    griddep_wait();
-    const int half = p.rot >> 1, units = half + p.dim - p.rot;
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const int64_t pos = p.positions[t], slot = p.slots[t];
-        const bool pos_ok = pos >= 0 && pos < p.cos_rows;
-        const bool ins = pos_ok && slot >= 0 && slot < p.slot_end;
-        if (threadIdx.x == 0 && (!pos_ok || slot >= p.slot_end))
-            atomicOr(&g_status, (pos_ok ? 0u : QKVF_STATUS_BAD_POSITION) |
-                                    (slot >= p.slot_end ? QKVF_STATUS_BAD_SLOT : 0u));
-        if (!pos_ok) continue;
-        const float *row = p.cos_sin + pos * p.rot;
-        S *crow = static_cast<S *>(p.kv_cache);
-        if (ins)
-            crow += ((slot / kPageSlots) * p.nkv * kPageSlots + slot % kPageSlots) * (2 * (int64_t)p.dim);
-        const int64_t head_step = (int64_t)kPageSlots * 2 * p.dim;   // one KV head of a page
-        const int rotated = p.q_heads + p.nkv;
-        for (int u = threadIdx.x; u < units * rotated; u += blockDim.x) {
-            const int h = u / units, i = u % units;
-            const bool is_q = h < p.q_heads;
-            if (!is_q && !ins) continue;
-            const S *src = is_q ? static_cast<const S *>(p.q) + t * p.q_ts + h * p.q_hs
-                                : static_cast<const S *>(p.k) + t * p.k_ts + (h - p.q_heads) * p.k_hs;
-            S *dst = is_q ? static_cast<S *>(p.q_out) + t * p.o_ts + h * p.o_hs : crow + (h - p.q_heads) * head_step;
-            if (i < half) {
-                const int ca = p.half_layout ? i : 2 * i, cb = p.half_layout ? i + half : 2 * i + 1;
-                float ya, yb;
-                rope_pair(E::get(src[ca]), E::get(src[cb]), row[i], row[half + i], ya, yb);
-                dst[ca] = E::put(ya);
-                dst[cb] = E::put(yb);
-            } else if (!is_q || !p.q_in_place) {
-                dst[p.rot + i - half] = src[p.rot + i - half];
-            }
-        }
-        if (ins)
-            for (int u = threadIdx.x; u < p.dim * p.nkv; u += blockDim.x) {
-                const int g = u / p.dim, i = u % p.dim;
-                crow[g * head_step + p.dim + i] = (static_cast<const S *>(p.v) + t * p.v_ts + g * p.v_hs)[i];
-            }
-    }
-}
 
 const char *check_append_args(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts,
                               int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs,
@@ -168,11 +106,11 @@ int rope_kv_append(const void *q, int64_t q_token_stride, int64_t q_head_stride,
     qkvf::DeviceState *d;
     const int rc = qkvf::probe_device(&d);
     if (rc != QKVF_OK) return rc;
-    qkvf::AppendParams prm = {};
+    qkvf::RopeParams prm = {};
     prm.q = q;
     prm.k = k;
     prm.v = v;
-    prm.q_out = q_out;
+    prm.out = q_out;
     prm.kv_cache = kv_cache;
     prm.positions = positions;
     prm.slots = slots;
@@ -192,13 +130,11 @@ int rope_kv_append(const void *q, int64_t q_token_stride, int64_t q_head_stride,
     prm.nkv = num_kv_heads;
     prm.dim = head_dim;
     prm.rot = rot_dim;
-    prm.half_layout = layout == QKVF_ROPE_HALF;
-    prm.q_in_place = q == q_out;
-    const int64_t most = (int64_t)d->sms * 8;
-    const dim3 grid((unsigned)(T < most ? T : most));
-    auto kernel = dtype == QKVF_DTYPE_BF16 ? qkvf::rope_kv_append_kernel<qkvf::Bf16>
-                                           : qkvf::rope_kv_append_kernel<qkvf::Fp16>;
-    return qkvf::launch_pdl(kernel, grid, dim3(256), 0, stream, prm);
+    prm.in_place = q == q_out;
+    prm.sign = 1.f;
+    const bool half = layout == QKVF_ROPE_HALF;
+    return dtype == QKVF_DTYPE_BF16 ? qkvf::launch_rope<qkvf::Bf16>(prm, half, d->sms, stream)
+                                    : qkvf::launch_rope<qkvf::Fp16>(prm, half, d->sms, stream);
 }
 
 }  // extern "C"
