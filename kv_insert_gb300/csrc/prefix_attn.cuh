@@ -1226,11 +1226,9 @@ PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int 
 
 // Partials: (sp_max + ss_max) x rows of O, maximum and sum, in FP32.  The
 // bounds grow with the tables' widths, so a workspace serves narrower ones.
-size_t prefix_attn_workspace(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int prefix_blocks,
-                             int max_blocks, int sms)
+size_t pa_workspace(const PaPlan &pl, int64_t rows, int head_dim)
 {
-    const PaPlan pl = pa_plan(num_reqs, q_len, q_heads, nkv, head_dim, prefix_blocks, max_blocks, sms);
-    return (size_t)num_reqs * q_len * q_heads * (pl.sp_max + pl.ss_max) * (head_dim * 4 + 8) + 256;
+    return (size_t)rows * (pl.sp_max + pl.ss_max) * (head_dim * 4 + 8) + 256;
 }
 
 template <class E, int D>
@@ -1365,7 +1363,8 @@ size_t prefix_attn_workspace_bytes(int num_reqs, int q_len, int q_heads, int num
         return 0;
     qkvf::DeviceState *d;
     if (qkvf::probe_device(&d) != QKVF_OK) return 0;
-    return qkvf::prefix_attn_workspace(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks, d->sms);
+    return qkvf::pa_workspace(qkvf::pa_plan(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks, d->sms),
+                              (int64_t)num_reqs * q_len * q_heads, head_dim);
 }
 
 const char *prefix_attn_unsupported(const void *q, int64_t q_token_stride, int64_t q_head_stride,
@@ -1386,8 +1385,8 @@ const char *prefix_attn_unsupported(const void *q, int64_t q_token_stride, int64
     qkvf::DeviceState *d;
     const int rc = qkvf::probe_device(&d);
     if (rc != QKVF_OK) return qkv_front_strerror(rc);
-    return workspace_bytes < qkvf::prefix_attn_workspace(num_reqs, q_len, q_heads, num_kv_heads, head_dim,
-                                                         prefix_blocks, max_blocks, d->sms)
+    return workspace_bytes < prefix_attn_workspace_bytes(num_reqs, q_len, q_heads, num_kv_heads, head_dim,
+                                                         prefix_blocks, max_blocks)
                ? "the workspace is too small"
                : nullptr;
 }
@@ -1407,14 +1406,12 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     qkvf::DeviceState *d;
     int rc = qkvf::probe_device(&d);
     if (rc != QKVF_OK) return rc;
-    if (workspace_bytes < qkvf::prefix_attn_workspace(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks,
-                                                      max_blocks, d->sms))
-        return QKVF_ERR_SIZES;
+    const qkvf::PaPlan pl = qkvf::pa_plan(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks, d->sms);
+    if (workspace_bytes < qkvf::pa_workspace(pl, (int64_t)num_reqs * q_len * q_heads, head_dim)) return QKVF_ERR_SIZES;
     const bool bf16 = dtype == QKVF_DTYPE_BF16;
     CUtensorMap map;
     rc = qkvf::encode_prefix_map(kv_cache, num_pages, num_kv_heads, head_dim, bf16, &map);
     if (rc != QKVF_OK) return rc;
-    const qkvf::PaPlan pl = qkvf::pa_plan(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks, d->sms);
     qkvf::PrefixParams prm = {};
     prm.q = q;
     prm.prefix_pages = prefix_pages;

@@ -113,21 +113,26 @@ struct RopeTableParams {
     uint64_t rate[kRtMaxPairs];
 };
 
+// A thread keeps one pair and walks the rows: the next row's phase is a 64-bit
+// sum.  The phase's top 32 bits, signed, are its angle in 2^-31 half turns.
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ RopeTableParams p)
 {
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x)
-        for (int i = threadIdx.x; i < p.half; i += blockDim.x) {
-            const uint64_t phase = (uint64_t)(p.first + row) * p.rate[i];
-            // twice the signed fraction of a turn: [-1, 1) half turns
-            const float h = __ll2float_rn((long long)phase) * 0x1p-63f;
-            float sn, cs;
-            sincospif(h, &sn, &cs);
-            float *dst = p.table + row * (2 * p.half);
-            dst[i] = cs * p.magnitude;
-            dst[p.half + i] = sn * p.magnitude;
-        }
+    const int per = 256 / p.half;   // rows of a CTA at a time
+    const int r = threadIdx.x / p.half, i = threadIdx.x - r * p.half;
+    if (r >= per) return;
+    const int64_t row0 = (int64_t)blockIdx.x * per + r, step = (int64_t)gridDim.x * per;
+    const uint64_t rate = p.rate[i];
+    uint64_t phase = (uint64_t)(p.first + row0) * rate;
+    const uint64_t turn = (uint64_t)step * rate;
+    float *dst = p.table + row0 * (2 * p.half) + i;
+    for (int64_t row = row0; row < p.rows; row += step, phase += turn, dst += step * (2 * p.half)) {
+        float sn, cs;
+        sincospif((float)(int)(uint32_t)(phase >> 32) * 0x1p-31f, &sn, &cs);
+        dst[0] = cs * p.magnitude;
+        dst[p.half] = sn * p.magnitude;
+    }
 }
 
 const char *check_rope_table_args(const float *table, int64_t first, int64_t rows, int rot_dim, double base,
@@ -176,7 +181,7 @@ struct RopeParams {
     int in_place;    // out is q: the columns behind rot are where they belong
     float sign;      // -1: the gradient
     // the vector kernel's threads: unit u of a head group of a token
-    int units, groups, tokens;   // units of a head, head groups of a token, tokens of a grid row
+    int units, q_groups, groups, tokens;   // units of a head, head groups of q and of all, tokens of a grid row
     uint32_t unit_m, unit_s, group_m, group_s;
 };
 
@@ -205,10 +210,9 @@ struct RopeToken {
     int64_t slot;       // the element offset of its slot for KV head 0, or -1
 };
 
-__device__ __forceinline__ RopeToken rope_token(const RopeParams &p, int64_t t, bool first)
+__device__ __forceinline__ RopeToken rope_token(const RopeParams &p, int64_t pos, int64_t slot, bool first)
 {
     RopeToken k;
-    const int64_t pos = p.positions[t], slot = p.nkv ? p.slots[t] : -1;
     const bool pos_ok = pos >= 0 && pos < p.cos_rows;
     k.row = pos_ok ? p.cos_sin + pos * p.rot : nullptr;
     k.slot = pos_ok && slot >= 0 && slot < p.slot_end
@@ -235,30 +239,68 @@ __device__ __forceinline__ void rope_head(const RopeParams &p, int64_t t, int h,
     }
 }
 
-// 16-byte kernel: every row starts on 16 bytes.  A unit is one 16-byte chunk
-// of a head (interleaved pairs) or chunk u of the first half of its rotated
-// columns with its partner in the second (half pairs; the chunks behind the
-// rotated columns are units of their own).  A thread takes unit u of kHeads
-// neighbouring heads of a token, so that the token's cos | sin values are read
-// once for all of them and kHeads (2 kHeads) loads are in flight.
-template <class E, bool kHalf>
-struct RopeVec {
-    using S = typename E::store;
-    static constexpr int vec = 16 / sizeof(S);
-    static constexpr int heads = kHalf ? 4 : 8;
-    static constexpr int pairs = kHalf ? vec : vec / 2;   // rotation pairs of a unit
-    union Chunk {
-        uint4 v;
-        S e[vec];
-    };
+// The 16-byte kernels' threads: every row starts on 16 bytes, a thread takes
+// the same columns of kHeads neighbouring heads of a token (all q, all k or
+// all v), so that the token's cos | sin values are read once for them and that
+// many loads are in flight.
+template <class S>
+struct RopeHeads {
+    const S *src;
+    S *dst;
+    int64_t src_step, dst_step;
+    int h0, n;
+    bool is_q, is_v;
+    __device__ __forceinline__ RopeHeads(const RopeParams &p, int64_t t, int grp, int kHeads)
+    {
+        int count = p.q_heads;
+        is_q = grp < p.q_groups;
+        is_v = false;
+        h0 = grp * kHeads;
+        src = static_cast<const S *>(p.q) + t * p.q_ts;
+        dst = static_cast<S *>(p.out) + t * p.o_ts;
+        src_step = p.q_hs;
+        dst_step = p.o_hs;
+        if (!is_q) {
+            const int kg = (p.nkv + kHeads - 1) / kHeads;
+            is_v = grp >= p.q_groups + kg;
+            h0 = (grp - p.q_groups - (is_v ? kg : 0)) * kHeads;
+            count = p.nkv;
+            src = is_v ? static_cast<const S *>(p.v) + t * p.v_ts : static_cast<const S *>(p.k) + t * p.k_ts;
+            src_step = is_v ? p.v_hs : p.k_hs;
+            dst_step = (int64_t)kPageSlots * 2 * p.dim;
+        }
+        src += h0 * src_step;
+        n = min(kHeads, count - h0);
+    }
+    // Where the heads are written, once the token's indices are known; false: nowhere
+    __device__ __forceinline__ bool place(const RopeParams &p, const RopeToken &tok)
+    {
+        if (!tok.row) return false;
+        if (!is_q) {
+            if (tok.slot < 0) return false;
+            dst = static_cast<S *>(p.kv_cache) + tok.slot + (is_v ? p.dim : 0);
+        }
+        dst += h0 * dst_step;
+        return true;
+    }
 };
 
-template <class E, bool kHalf>
+template <class E>
+union RopeChunk {
+    static constexpr int vec = 16 / sizeof(typename E::store);
+    uint4 v;
+    typename E::store e[vec];
+};
+
+// A unit is one 16-byte chunk of a head (interleaved pairs), or chunk u of the
+// first half of its rotated columns with its partner in the second (half
+// pairs; the chunks behind the rotated columns are units of their own).
+template <class E, bool kHalf, int kHeads>
 __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ RopeParams p)
 {
-    using V = RopeVec<E, kHalf>;
-    using S = typename V::S;
-    using Chunk = typename V::Chunk;
+    using S = typename E::store;
+    using Chunk = RopeChunk<E>;
+    constexpr int vec = Chunk::vec, pairs = kHalf ? vec : vec / 2;   // rotation pairs of a unit
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
     const uint32_t lin = blockIdx.x * 256 + threadIdx.x;
@@ -266,75 +308,136 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ R
     const uint32_t tl = div_by(rest, p.group_m, p.group_s), grp = rest - tl * p.groups;
     const int64_t t = (int64_t)blockIdx.y * p.tokens + tl;
     if ((int)tl >= p.tokens || t >= p.T) return;
-    const RopeToken tok = rope_token(p, t, u == 0 && grp == 0);
-    const int heads = p.q_heads + 2 * p.nkv, h0 = grp * V::heads, half = p.rot >> 1;
-    const bool rotated = kHalf ? (int)u < half / V::vec : (int)u * V::pairs < half;
-    // first chunk of the unit, and its partner's distance (half pairs)
-    const int c0 = kHalf && !rotated ? half / V::vec + u : u;
-    Chunk x[V::heads], y[kHalf ? V::heads : 1];
+    const int64_t pos = p.positions[t], slot = p.nkv ? p.slots[t] : -1;
+    const int half = p.rot >> 1;
+    const bool rotated = kHalf ? (int)u < half / vec : (int)u * pairs < half;
+    const int c0 = kHalf && !rotated ? half / vec + u : u;   // the unit's first chunk
+    RopeHeads<S> hd(p, t, grp, kHeads);
+    const S *src = hd.src + c0 * vec;
+    Chunk x[kHeads], y[kHalf ? kHeads : 1];
 #pragma unroll
-    for (int i = 0; i < V::heads; ++i) {
-        const S *src;
-        S *dst;
-        if (h0 + i >= heads) break;
-        rope_head<S>(p, t, h0 + i, tok, src, dst);
-        x[i].v = *reinterpret_cast<const uint4 *>(src + c0 * V::vec);
-        if (kHalf && rotated) y[kHalf ? i : 0].v = *reinterpret_cast<const uint4 *>(src + half + c0 * V::vec);
-    }
-    if (!tok.row) return;
-    float c[V::pairs], s[V::pairs];
-    if (rotated) {
-        const int i0 = u * V::pairs;
-        if (p.rot % 8 == 0 && (kHalf || V::pairs % 4 == 0)) {   // both halves of the row on 16 bytes
-#pragma unroll
-            for (int i = 0; i < V::pairs; i += 4) {
-                if (V::pairs % 4 == 0) {
-                    *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(tok.row + i0 + i);
-                    *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(tok.row + half + i0 + i);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V::pairs; ++i) {
-                const bool in = i0 + i < half;
-                c[i] = in ? tok.row[i0 + i] : 1.f;
-                s[i] = in ? tok.row[half + i0 + i] : 0.f;
-            }
+    for (int i = 0; i < kHeads; ++i)
+        if (i < hd.n) {
+            x[i].v = *reinterpret_cast<const uint4 *>(src + i * hd.src_step);
+            if (kHalf && rotated) y[kHalf ? i : 0].v = *reinterpret_cast<const uint4 *>(src + i * hd.src_step + half);
         }
+    const RopeToken tok = rope_token(p, pos, slot, u == 0 && grp == 0);
+    if (!hd.place(p, tok)) return;
+    S *dst = hd.dst + c0 * vec;
+    if (!rotated || hd.is_v) {
+        if (hd.is_q && p.in_place) return;
 #pragma unroll
-        for (int i = 0; i < V::pairs; ++i) s[i] *= p.sign;
+        for (int i = 0; i < kHeads; ++i)
+            if (i < hd.n) {
+                *reinterpret_cast<uint4 *>(dst + i * hd.dst_step) = x[i].v;
+                if (kHalf && rotated) *reinterpret_cast<uint4 *>(dst + i * hd.dst_step + half) = y[kHalf ? i : 0].v;
+            }
+        return;
+    }
+    float c[pairs], s[pairs];
+    const int i0 = u * pairs;
+    if (pairs % 4 == 0 && p.rot % 8 == 0) {   // both halves of the row on 16 bytes
+#pragma unroll
+        for (int i = 0; i + 4 <= pairs; i += 4) {
+            *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(tok.row + i0 + i);
+            *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(tok.row + half + i0 + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < pairs; ++i) {
+            const bool in = i0 + i < half;
+            c[i] = in ? tok.row[i0 + i] : 1.f;
+            s[i] = in ? tok.row[half + i0 + i] : 0.f;
+        }
     }
 #pragma unroll
-    for (int i = 0; i < V::heads; ++i) {
-        const int h = h0 + i;
-        if (h >= heads) break;
-        const S *src;
-        S *dst;
-        rope_head<S>(p, t, h, tok, src, dst);
-        if (!dst) continue;
-        const bool turn = rotated && h < p.q_heads + p.nkv;
-        if (turn) {
+    for (int i = 0; i < pairs; ++i) s[i] *= p.sign;
+    const int whole = kHalf ? pairs : min(pairs, half - i0);   // the rotated columns may end in a chunk
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        if (i < hd.n) {
             Chunk &a = x[i], &b = kHalf ? y[kHalf ? i : 0] : x[i];
 #pragma unroll
-            for (int k = 0; k < V::pairs; ++k) {
-                const int ia = kHalf ? k : 2 * k, ib = kHalf ? k : 2 * k + 1;
-                if (!kHalf && (int)u * V::pairs + k >= half) break;   // a chunk the rotated columns end in
-                float ya, yb;
-                rope_pair(E::get(a.e[ia]), E::get(b.e[ib]), c[k], s[k], ya, yb);
-                a.e[ia] = E::put(ya);
-                b.e[ib] = E::put(yb);
-            }
-        } else if (h < p.q_heads && p.in_place) {
-            continue;
+            for (int k = 0; k < pairs; ++k)
+                if (kHalf || k < whole) {
+                    const int ia = kHalf ? k : 2 * k, ib = kHalf ? k : 2 * k + 1;
+                    float ya, yb;
+                    rope_pair(E::get(a.e[ia]), E::get(b.e[ib]), c[k], s[k], ya, yb);
+                    a.e[ia] = E::put(ya);
+                    b.e[ib] = E::put(yb);
+                }
+            *reinterpret_cast<uint4 *>(dst + i * hd.dst_step) = x[i].v;
+            if (kHalf) *reinterpret_cast<uint4 *>(dst + i * hd.dst_step + half) = y[kHalf ? i : 0].v;
         }
-        *reinterpret_cast<uint4 *>(dst + c0 * V::vec) = x[i].v;
-        if (kHalf && rotated) *reinterpret_cast<uint4 *>(dst + half + c0 * V::vec) = y[kHalf ? i : 0].v;
-    }
 }
 
-// Element kernel, for rows off the 16-byte grid and half pairs whose distance
-// is not whole chunks: lanes over a head's pairs and copied columns, warps over
-// the token's heads.
+// Half pairs whose distance is not whole chunks: the CTA's heads (256 / units
+// whole groups of 8) go through shared memory.  Global memory moves in 16-byte
+// chunks; in between, a warp takes 32 neighbouring pairs of a group's heads, so
+// that cos, sin and both columns are neighbouring words for its lanes.
+constexpr int kRopeStagedHeads = 8;
+
+template <class E>
+__global__ void __launch_bounds__(256) rope_staged_kernel(const __grid_constant__ RopeParams p)
+{
+    using S = typename E::store;
+    constexpr int vec = RopeChunk<E>::vec, kHeads = kRopeStagedHeads;
+    __shared__ uint4 stage[256 * kHeads];
+    __shared__ const float *table[256];   // a group's cos | sin row (null: nothing to turn)
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();
+    const int per = 256 / p.units;
+    const int r = div_by(threadIdx.x, p.unit_m, p.unit_s), u = threadIdx.x - r * p.units;
+    const uint32_t rest = blockIdx.x * per + r;
+    const uint32_t tl = div_by(rest, p.group_m, p.group_s), grp = rest - tl * p.groups;
+    const int64_t t = (int64_t)blockIdx.y * p.tokens + tl;
+    const bool mine = r < per && (int)tl < p.tokens && t < p.T;
+    const int64_t pos = mine ? p.positions[t] : -1, slot = mine && p.nkv ? p.slots[t] : -1;
+    RopeHeads<S> hd(p, mine ? t : 0, mine ? grp : 0, kHeads);
+    uint4 *rows = stage + r * kHeads * p.units + u;   // the group's heads, p.units chunks each
+    if (mine) {
+        uint4 x[kHeads];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+            if (i < hd.n) x[i] = *reinterpret_cast<const uint4 *>(hd.src + i * hd.src_step + u * vec);
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+            if (i < hd.n) rows[i * p.units] = x[i];
+    }
+    bool put = false;
+    if (mine) {
+        const RopeToken tok = rope_token(p, pos, slot, u == 0 && grp == 0);
+        put = hd.place(p, tok);
+        if (u == 0) table[r] = put && !hd.is_v ? tok.row : nullptr;
+    } else if (r < per && u == 0) {
+        table[r] = nullptr;
+    }
+    __syncthreads();
+    const int half = p.rot >> 1, blocks = (half + 31) / 32;
+    for (int w = threadIdx.x >> 5; w < per * blocks; w += 8) {
+        const int g = w / blocks, i = (w - g * blocks) * 32 + (threadIdx.x & 31);
+        const float *row = table[g];
+        if (!row || i >= half) continue;
+        const float c = row[i], s = p.sign * row[half + i];
+        S *e = reinterpret_cast<S *>(stage + g * kHeads * p.units) + i;   // heads past the group's last: unread
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) {
+            S *a = e + k * p.dim;
+            float ya, yb;
+            rope_pair(E::get(a[0]), E::get(a[half]), c, s, ya, yb);
+            a[0] = E::put(ya);
+            a[half] = E::put(yb);
+        }
+    }
+    __syncthreads();
+    if (!put || (hd.is_q && p.in_place && u * vec >= p.rot)) return;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        if (i < hd.n) *reinterpret_cast<uint4 *>(hd.dst + i * hd.dst_step + u * vec) = rows[i * p.units];
+}
+
+// Element kernel, for rows off the 16-byte grid: lanes over a head's pairs and
+// copied columns, warps over the token's heads.
 template <class E>
 __global__ void __launch_bounds__(256) rope_element_kernel(const __grid_constant__ RopeParams p, int half_layout)
 {
@@ -344,7 +447,7 @@ __global__ void __launch_bounds__(256) rope_element_kernel(const __grid_constant
     const int half = p.rot >> 1, tail = p.dim - p.rot, heads = p.q_heads + 2 * p.nkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const RopeToken tok = rope_token(p, t, threadIdx.x == 0);
+        const RopeToken tok = rope_token(p, p.positions[t], p.nkv ? p.slots[t] : -1, threadIdx.x == 0);
         if (!tok.row) continue;
         for (int h = warp; h < heads; h += 8) {
             const S *src;
@@ -431,35 +534,56 @@ int launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, void
     return QKVF_OK;
 }
 
-template <class E, bool kHalf>
-int launch_rope_vec(RopeParams &prm, void *stream)
+// The grid of a 16-byte kernel: `units` columns' threads a head group, groups
+// of `heads` heads, `whole` head groups a CTA (0: threads dealt without gaps)
+dim3 rope_grid(RopeParams &prm, int units, int heads, int whole)
 {
-    using V = RopeVec<E, kHalf>;
-    prm.units = kHalf ? (prm.dim - prm.rot / 2) / V::vec : prm.dim / V::vec;
-    prm.groups = (prm.q_heads + 2 * prm.nkv + V::heads - 1) / V::heads;
+    prm.units = units;
+    prm.q_groups = (prm.q_heads + heads - 1) / heads;
+    prm.groups = prm.q_groups + 2 * ((prm.nkv + heads - 1) / heads);
     fast_div(prm.units, &prm.unit_m, &prm.unit_s);
     fast_div(prm.groups, &prm.group_m, &prm.group_s);
-    const int64_t per = (int64_t)prm.units * prm.groups, most = (int64_t(1) << 30) / per;   // a grid row's tokens
+    const int64_t most = (int64_t(1) << 30) / ((int64_t)units * prm.groups);   // a grid row's tokens
     prm.tokens = (int)(prm.T < most ? prm.T : most);
-    return launch_pdl(rope_vec_kernel<E, kHalf>,
-                      dim3((unsigned)((prm.tokens * per + 255) / 256), (unsigned)((prm.T + prm.tokens - 1) / prm.tokens)),
-                      dim3(256), 0, stream, prm);
+    const int64_t work = (int64_t)prm.tokens * prm.groups;
+    const int64_t ctas = whole ? (work + whole - 1) / whole : (work * units + 255) / 256;
+    return dim3((unsigned)ctas, (unsigned)((prm.T + prm.tokens - 1) / prm.tokens));
 }
 
-// The 16-byte kernel where every row it touches starts on 16 bytes and the
-// partner of a half-layout chunk is a chunk; the element kernel elsewhere
-// (16384 x 32 x 128 bf16, half layout: XX us and YY us).
+template <class E, bool kHalf, int kHeads>
+int launch_rope_vec(RopeParams &prm, void *stream)
+{
+    const int units = (kHalf ? prm.dim - prm.rot / 2 : prm.dim) / RopeChunk<E>::vec;
+    const dim3 grid = rope_grid(prm, units, kHeads, 0);
+    return launch_pdl(rope_vec_kernel<E, kHalf, kHeads>, grid, dim3(256), 0, stream, prm);
+}
+
+// Rows that all start on 16 bytes take a 16-byte kernel: whole chunks where
+// the half layout's partner of a chunk is a chunk (16384 x 32 x 128 bf16:
+// 41.4 us, the copy peak), otherwise through shared memory (11704 x 43 x 128,
+// 82 of them rotated: 62.2 us, and 106.8 us in the element kernel).  Several
+// heads a thread where there are several (with one head of 256 a token and
+// 100000 tokens 60.5 us, against 30.9 with one or two).  Rows off the 16-byte
+// grid go element by element.
 template <class E>
 int launch_rope(RopeParams &prm, bool half_layout, int sms, void *stream)
 {
-    constexpr int vec = 16 / (int)sizeof(typename E::store);
+    constexpr int vec = RopeChunk<E>::vec;
     const auto whole = [&](const void *ptr, int64_t ts, int64_t hs, int heads) {
         return heads == 0 || (aligned(ptr, 16) && (prm.T == 1 || ts % vec == 0) && (heads == 1 || hs % vec == 0));
     };
-    if (prm.dim % vec == 0 && (!half_layout || prm.rot / 2 % vec == 0) && whole(prm.q, prm.q_ts, prm.q_hs, prm.q_heads) &&
+    if (prm.dim % vec == 0 && whole(prm.q, prm.q_ts, prm.q_hs, prm.q_heads) &&
         whole(prm.out, prm.o_ts, prm.o_hs, prm.q_heads) && whole(prm.k, prm.k_ts, prm.k_hs, prm.nkv) &&
-        whole(prm.v, prm.v_ts, prm.v_hs, prm.nkv))
-        return half_layout ? launch_rope_vec<E, true>(prm, stream) : launch_rope_vec<E, false>(prm, stream);
+        whole(prm.v, prm.v_ts, prm.v_hs, prm.nkv)) {
+        if (half_layout && prm.rot / 2 % vec) {
+            const int units = prm.dim / vec, per = 256 / units;
+            const dim3 grid = rope_grid(prm, units, kRopeStagedHeads, per);
+            return launch_pdl(rope_staged_kernel<E>, grid, dim3(256), 0, stream, prm);
+        }
+        const bool few = (prm.q_heads > prm.nkv ? prm.q_heads : prm.nkv) <= 2;
+        if (half_layout) return few ? launch_rope_vec<E, true, 1>(prm, stream) : launch_rope_vec<E, true, 4>(prm, stream);
+        return few ? launch_rope_vec<E, false, 2>(prm, stream) : launch_rope_vec<E, false, 8>(prm, stream);
+    }
     const int64_t most = (int64_t)sms * 8;
     return launch_pdl(rope_element_kernel<E>, dim3((unsigned)(prm.T < most ? prm.T : most)), dim3(256), 0, stream, prm,
                       (int)half_layout);
@@ -511,8 +635,9 @@ int rope_table(float *table, int64_t first, int64_t rows, int rot_dim, double ba
         }
         prm.rate[i] = (uint64_t)ldexp(f / kTurn, 64);   // f <= 1: below 2^62
     }
-    const int64_t most = (int64_t)d->sms * 8;
-    return qkvf::launch_pdl(qkvf::rope_table_kernel, dim3((unsigned)(rows < most ? rows : most)), dim3(256), 0,
+    const int per = 256 / prm.half;
+    const int64_t want = (rows + per - 1) / per, most = (int64_t)d->sms * 8;
+    return qkvf::launch_pdl(qkvf::rope_table_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256), 0,
                             stream, prm);
 }
 

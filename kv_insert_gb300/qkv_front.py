@@ -607,33 +607,27 @@ def attn2_split_kv(qkv, kv_cache, block_table, context_lens, workspace, out=None
 
 # ---- rotary positions, rotated cache append, shared-prefix attention --------
 
-class _OnDevice:
-    """`with` block that makes a device current only when it is not."""
-
-    def __init__(self, index: int):
-        self._guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _raw_stream(stream, index: int) -> int:
+    """The cudaStream_t of a call on device `index` (None: its current stream)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _run(name: str, index: int, args: tuple, stream) -> None:
     """Call the library's `name` on device `index`; a refusal carries its reason."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _run(name, index, args, stream)
     lib = _lib or load()
-    with _OnDevice(index):
-        code = getattr(lib, name)(*args, _stream(stream))
-        if code != 0:
-            why = getattr(lib, name + "_unsupported")(*args)
-            raise QkvFrontError(code, why.decode() if why else strerror(code))
+    code = getattr(lib, name)(*args, _raw_stream(stream, index))
+    if code != 0:
+        why = getattr(lib, name + "_unsupported")(*args)
+        raise QkvFrontError(code, why.decode() if why else strerror(code))
 
 
 def _why(name: str, index: int, args: tuple) -> str | None:
-    with _OnDevice(index):
+    with torch.cuda.device(index):
         r = getattr(load(), name + "_unsupported")(*args)
     return None if r is None else r.decode()
 
@@ -650,38 +644,43 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _heads(t, name: str, device, dtypes=None, shape=None):
-    """The (pointer, token stride, head stride) of a [tokens, heads, head_dim]
-    tensor with a contiguous last dimension."""
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]"
-                         + ("" if shape is None else f" {shape}") + f", not {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if max(t.shape) > 1 << 30:   # beyond the C ABI's int sizes
-        raise ValueError(f"{name} is too large: {tuple(t.shape)}")
-    if dtypes is not None and t.dtype not in dtypes:
+_MOST = 1 << 30   # the C ABI's sizes are ints
+
+
+def _heads(t, name: str, index: int, dtypes, shape=None):
+    """(pointer, token stride, head stride) of a [tokens, heads, head_dim] CUDA
+    tensor on device `index` with a contiguous last dimension."""
+    if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, on the other tensors' device")
+    dims = t.shape
+    if len(dims) != 3 or (shape is not None and dims != shape):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]"
+                         + ("" if shape is None else f" = {tuple(shape)}") + f", not {tuple(dims)}")
+    if dims[0] > _MOST or dims[1] > _MOST or dims[2] > _MOST:
+        raise ValueError(f"{name} is too large: {tuple(dims)}")
     ts, hs, es = t.stride()
-    if es != 1 and t.shape[2] > 1:
+    if es != 1 and dims[2] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     return t.data_ptr(), ts, hs
 
 
-def _index(t, name: str, dtype, shape, device):
-    if (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda
-            or t.device != device):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {shape} on {device}")
+def _index(t, name: str, dtype, shape, index: int):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {shape}, on the other tensors' device")
     return t.data_ptr()
 
 
-def _table(cos_sin, head_dim: int, device):
-    if (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous()
-            or not cos_sin.is_cuda or cos_sin.device != device):
-        raise ValueError(f"cos_sin must be a contiguous fp32 CUDA tensor [rows, rot_dim] on {device}")
-    if cos_sin.shape[1] > head_dim:
-        raise ValueError(f"cos_sin rotates {cos_sin.shape[1]} columns of {head_dim}-wide heads")
-    return cos_sin.data_ptr(), cos_sin.shape[0]
+def _table(cos_sin, head_dim: int, index: int):
+    dims = cos_sin.shape
+    if (cos_sin.dtype is not torch.float32 or cos_sin.get_device() != index or len(dims) != 2
+            or not cos_sin.is_contiguous()):
+        raise ValueError("cos_sin must be a contiguous fp32 CUDA tensor [rows, rot_dim], on the other "
+                         "tensors' device")
+    if dims[1] > head_dim:
+        raise ValueError(f"cos_sin rotates {dims[1]} columns of {head_dim}-wide heads")
+    return cos_sin.data_ptr(), dims[0], dims[1]
 
 
 def _layout(layout: str) -> int:
@@ -690,13 +689,13 @@ def _layout(layout: str) -> int:
     return ROPE_LAYOUTS[layout]
 
 
-def _cache(kv_cache, head_dim: int, dtype, device):
-    if (kv_cache.dtype != dtype or kv_cache.dim() != 4 or kv_cache.shape[2] != PAGE_SLOTS
-            or kv_cache.shape[3] != 2 * head_dim or not kv_cache.is_contiguous()
-            or not kv_cache.is_cuda or kv_cache.device != device):
-        raise ValueError(f"kv_cache must be a contiguous {dtype} CUDA tensor "
-                         f"[pages, num_kv_heads, {PAGE_SLOTS}, {2 * head_dim}] on {device}")
-    return kv_cache.data_ptr(), kv_cache.shape[0]
+def _cache(kv_cache, head_dim: int, dtype, index: int):
+    dims = kv_cache.shape
+    if (kv_cache.dtype is not dtype or kv_cache.get_device() != index or len(dims) != 4
+            or dims[2] != PAGE_SLOTS or dims[3] != 2 * head_dim or not kv_cache.is_contiguous()):
+        raise ValueError(f"kv_cache must be a contiguous {dtype} CUDA tensor [pages, num_kv_heads, "
+                         f"{PAGE_SLOTS}, {2 * head_dim}], on the other tensors' device")
+    return kv_cache.data_ptr(), dims[0], dims[1]
 
 
 def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -732,13 +731,13 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: str = "n
 
 
 def _rope_args(x, positions, cos_sin, out, layout, inverse):
-    device = x.device
-    px, xt, xh = _heads(x, "x", device, DTYPES)
-    T, heads, dim = x.shape
-    po, ot, oh = _heads(out, "out", device, (x.dtype,), (T, heads, dim))
-    pt, rows = _table(cos_sin, dim, device)
-    return (px, xt, xh, _index(positions, "positions", torch.int64, (T,), device), pt, rows, po, ot,
-            oh, T, heads, dim, cos_sin.shape[1], _layout(layout), inverse, DTYPES[x.dtype])
+    index, shape = x.get_device(), x.shape
+    px, xt, xh = _heads(x, "x", index, DTYPES)
+    T, heads, dim = shape
+    po, ot, oh = _heads(out, "out", index, (x.dtype,), shape)
+    pt, rows, rot = _table(cos_sin, dim, index)
+    return (px, xt, xh, _index(positions, "positions", torch.int64, (T,), index), pt, rows, po, ot, oh, T,
+            heads, dim, rot, _layout(layout), inverse, DTYPES[x.dtype])
 
 
 def rope_unsupported(x, positions, cos_sin, out, layout: str = "interleaved") -> str | None:
@@ -747,13 +746,14 @@ def rope_unsupported(x, positions, cos_sin, out, layout: str = "interleaved") ->
         args = _rope_args(x, positions, cos_sin, out, layout, 0)
     except ValueError as e:
         return str(e)
-    return _why("rope", x.device.index, args)
+    return _why("rope", x.get_device(), args)
 
 
 def _rope(x, positions, cos_sin, out, layout, inverse, stream):
     if out is None:
         out = _new(x.shape, x.dtype, x.device, stream)
-    _run("rope", x.device.index, _rope_args(x, positions, cos_sin, out, layout, inverse), stream)
+    args = _rope_args(x, positions, cos_sin, out, layout, inverse)
+    _run("rope", x.get_device(), args, stream)
     return out
 
 
@@ -772,25 +772,29 @@ def rope_backward(grad_out, positions, cos_sin, out=None, layout: str = "interle
     return _rope(grad_out, positions, cos_sin, out, layout, 1, stream)
 
 
+_HALF_TYPES = (torch.bfloat16, torch.float16)
+
+
 def _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout):
-    device, dtypes = k.device, (torch.bfloat16, torch.float16)
-    pk, kt, kh = _heads(k, "k", device, dtypes)
-    T, nkv, dim = k.shape
-    pv, vt, vh = _heads(v, "v", device, (k.dtype,), (T, nkv, dim))
-    pc, pages = _cache(kv_cache, dim, k.dtype, device)
-    if kv_cache.shape[1] != nkv:
-        raise ValueError(f"{nkv} k heads for a cache of {kv_cache.shape[1]} KV heads")
-    pt, rows = _table(cos_sin, dim, device)
+    index, dtype, shape = k.get_device(), k.dtype, k.shape
+    pk, kt, kh = _heads(k, "k", index, _HALF_TYPES)
+    T, nkv, dim = shape
+    pv, vt, vh = _heads(v, "v", index, (dtype,), shape)
+    pc, pages, cache_heads = _cache(kv_cache, dim, dtype, index)
+    if cache_heads != nkv:
+        raise ValueError(f"{nkv} k heads for a cache of {cache_heads} KV heads")
+    pt, rows, rot = _table(cos_sin, dim, index)
     pq = po = None
     q_heads = qt = qh = ot = oh = 0
-    if q is not None and q.shape[1] > 0:
-        q_heads = q.shape[1]
-        pq, qt, qh = _heads(q, "q", device, (k.dtype,), (T, q_heads, dim))
-        po, ot, oh = _heads(q_out, "q_out", device, (k.dtype,), (T, q_heads, dim))
-    return (pq, qt, qh, pk, kt, kh, pv, vt, vh,
-            _index(positions, "positions", torch.int64, (T,), device),
-            _index(slots, "slots", torch.int64, (T,), device), pt, rows, po, ot, oh, pc, pages, T,
-            q_heads, nkv, dim, cos_sin.shape[1], _layout(layout), DTYPES[k.dtype])
+    if q is not None and q.dim() == 3 and q.shape[1] == 0:
+        q = None
+    if q is not None:
+        q_heads = q.shape[1] if q.dim() == 3 else 0
+        pq, qt, qh = _heads(q, "q", index, (dtype,), (T, q_heads, dim))
+        po, ot, oh = _heads(q_out, "q_out", index, (dtype,), (T, q_heads, dim))
+    return (pq, qt, qh, pk, kt, kh, pv, vt, vh, _index(positions, "positions", torch.int64, (T,), index),
+            _index(slots, "slots", torch.int64, (T,), index), pt, rows, po, ot, oh, pc, pages, T, q_heads,
+            nkv, dim, rot, _layout(layout), DTYPES[dtype])
 
 
 def rope_kv_append_unsupported(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
@@ -800,7 +804,7 @@ def rope_kv_append_unsupported(q, k, v, positions, slots, cos_sin, kv_cache, q_o
         args = _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout)
     except ValueError as e:
         return str(e)
-    return _why("rope_kv_append", k.device.index, args)
+    return _why("rope_kv_append", k.get_device(), args)
 
 
 def rope_kv_append(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
@@ -811,8 +815,8 @@ def rope_kv_append(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
     q=None appends only.  bf16 or fp16, any strides.  Returns q_out."""
     if q is not None and q_out is None:
         q_out = _new(q.shape, q.dtype, q.device, stream)
-    _run("rope_kv_append", k.device.index,
-         _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout), stream)
+    args = _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout)
+    _run("rope_kv_append", k.get_device(), args, stream)
     return q_out
 
 
@@ -825,28 +829,31 @@ def prefix_attn_workspace_bytes(num_reqs: int, q_len: int, q_heads: int, num_kv_
 
 def _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace, q_len,
                  scale, out, lse):
-    device = q.device
-    pq, qt, qh = _heads(q, "q", device, (torch.bfloat16, torch.float16))
-    T, heads, dim = q.shape
+    index, dtype, shape = q.get_device(), q.dtype, q.shape
+    pq, qt, qh = _heads(q, "q", index, _HALF_TYPES)
+    T, heads, dim = shape
     if q_len < 1 or T % q_len:
         raise ValueError(f"{T} q rows are not whole requests of {q_len} tokens")
     R = T // q_len
-    pc, pages = _cache(kv_cache, dim, q.dtype, device)
-    pp = pl = None
-    nb = prefix_pages.shape[0] if prefix_pages is not None else 0
-    if nb:
-        pp = _index(prefix_pages, "prefix_pages", torch.int32, (nb,), device)
-        pl = _index(prefix_len, "prefix_len", torch.int32, (1,), device)
-    mb = block_table.shape[1] if block_table is not None else 0
-    pb = _index(block_table, "block_table", torch.int32, (R, mb), device) if mb else None
-    po = _index(out, "out", q.dtype, (T, heads, dim), device)
-    ps = None if lse is None else _index(lse, "lse", torch.float32, (T, heads), device)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+    pc, pages, nkv = _cache(kv_cache, dim, dtype, index)
+    pp = pl = pb = ps = None
+    nb = mb = 0
+    if prefix_pages is not None and prefix_pages.numel():
+        nb = prefix_pages.shape[0]
+        pp = _index(prefix_pages, "prefix_pages", torch.int32, (nb,), index)
+        pl = _index(prefix_len, "prefix_len", torch.int32, (1,), index)
+    if block_table is not None and block_table.numel():
+        mb = block_table.shape[1] if block_table.dim() == 2 else 0
+        pb = _index(block_table, "block_table", torch.int32, (R, mb), index)
+    po = _index(out, "out", dtype, shape, index)
+    if lse is not None:
+        ps = _index(lse, "lse", torch.float32, (T, heads), index)
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError("workspace must be a contiguous uint8 CUDA tensor on q's device")
     return (pq, qt, qh, pc, pages, pp, nb, pl, pb, mb,
-            _index(context_lens, "context_lens", torch.int32, (R,), device), R, q_len, heads,
-            kv_cache.shape[1], dim, dim ** -0.5 if scale is None else scale, DTYPES[q.dtype], po, ps,
-            workspace.data_ptr(), workspace.numel())
+            _index(context_lens, "context_lens", torch.int32, (R,), index), R, q_len, heads, nkv, dim,
+            dim ** -0.5 if scale is None else scale, DTYPES[dtype], po, ps, workspace.data_ptr(),
+            workspace.numel())
 
 
 def prefix_attn_unsupported(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace,
@@ -857,7 +864,7 @@ def prefix_attn_unsupported(q, kv_cache, prefix_pages, prefix_len, block_table, 
                             q_len, scale, out, lse)
     except ValueError as e:
         return str(e)
-    return _why("prefix_attn", q.device.index, args)
+    return _why("prefix_attn", q.get_device(), args)
 
 
 def prefix_attn(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace,
@@ -873,9 +880,9 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens
     with the rows' ln sum exp when given.  Returns out."""
     if out is None:
         out = _new(q.shape, q.dtype, q.device, stream)
-    _run("prefix_attn", q.device.index,
-         _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace, q_len,
-                      scale, out, lse), stream)
+    args = _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace, q_len,
+                        scale, out, lse)
+    _run("prefix_attn", q.get_device(), args, stream)
     return out
 
 
