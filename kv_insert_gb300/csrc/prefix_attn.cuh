@@ -34,7 +34,7 @@ struct PaShape {
 };
 
 struct PaSmem {   // offsets from the 1024-byte aligned base
-    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, odone, drain, slot_bad, tmem, flags, total;
+    uint32_t q, ring, full, empty, qready, sfull, sfree, pready, pvdone, odone, drain, tmem, flags, total;
 };
 
 template <int D>
@@ -65,8 +65,6 @@ __host__ __device__ constexpr PaSmem pa_smem()
     off += 16;
     L.drain = off;
     off += 16;
-    L.slot_bad = off;
-    off += 2 * Sh::slots * 4;
     L.tmem = off;
     off += 8;
     L.flags = off;
@@ -199,7 +197,7 @@ struct PaRing {
 };
 
 // Until the phase of this parity completes, at most limit_ns: then flags[0] is
-// set, later waits return at once, and every role leaves at its next block.
+// set, every later wait of the CTA is short, and its results are void.
 __device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile int *flags, unsigned long long limit_ns)
 {
 #pragma unroll 1
@@ -328,11 +326,10 @@ __device__ __forceinline__ float pa_max(const uint32_t (&s)[N], float m)
     return fmaxf(a, b);
 }
 
-// The weights 2^(scale s - mu) of N scores, rounded and packed in pairs; returns their sum
+// The weights 2^(scale s + base) of N scores, rounded and packed in pairs; returns their sum
 template <class E, int N>
-__device__ __forceinline__ float pa_weights(const uint32_t (&s)[N], uint32_t (&pk)[N / 2], uint64_t scale2, float mu)
+__device__ __forceinline__ float pa_weights(const uint32_t (&s)[N], uint32_t (&pk)[N / 2], uint64_t scale2, float base)
 {
-    const float base = mu == -INFINITY ? 0.f : -mu;
     const uint64_t nb2 = f2_pack(base, base);
     uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -363,11 +360,11 @@ struct PaTile {
     int P, lane;
 
     __device__ __forceinline__ volatile int *flags() const { return reinterpret_cast<volatile int *>(smem + LY.flags); }
-    __device__ __forceinline__ volatile int *slot_bad() const { return reinterpret_cast<volatile int *>(smem + LY.slot_bad); }
     __device__ __forceinline__ void wait(uint32_t bar, int n) const   // until phase n of bar is complete
     {
         pa_wait(sb + bar, (uint32_t)n & 1, flags(), p.wait_limit_ns);
     }
+    __device__ __forceinline__ bool dead() const { return flags()[0] != 0; }
     __device__ __forceinline__ int pages_from(const PaItem &it, int block) const   // of a block, with keys
     {
         return min(Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots - block * Sh::pages);
@@ -379,15 +376,15 @@ struct PaTile {
         if (lane == 0) tma_prefetch_map(map);
         PaWork<D> work(p, P, w);
         PaItem it;
-        bool stop = false;
+        bool ok = true;
         PaRing<NS> ring(w, p.pair);
         int mine = 0;   // steps loaded into this ring
         unsigned bad_any = 0u;
-        while (!stop && work.next(it)) {
+        while (ok && work.next(it)) {
             const int pg0 = it.kb0 * Sh::pages;
             const int pg1 = min(it.kb1 * Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots);
             int next = pg0 + lane < pg1 ? it.pages[pg0 + lane] : 0;
-            for (int c = pg0; c < pg1 && !stop; c += 32) {
+            for (int c = pg0; c < pg1 && ok; c += 32) {
                 int page = next;
                 if (c + 32 + lane < pg1) next = it.pages[c + 32 + lane];
                 bool bad = false;
@@ -395,8 +392,11 @@ struct PaTile {
                     bad = true;
                     page = 0;
                 }
-                const unsigned bads = __ballot_sync(0xffffffffu, bad);
-                bad_any |= bads;
+                if (__any_sync(0xffffffffu, bad)) {   // seen by the softmax before these keys' products are
+                    bad_any = 1u;
+                    flags()[1] = 1;
+                    __syncwarp();
+                }
                 for (int b0 = c; b0 < min(c + 32, pg1); b0 += Sh::pages) {
                     ring.take();
                     const int st = ring.st;
@@ -404,14 +404,9 @@ struct PaTile {
                     const int n = min(Sh::pages, pg1 - b0);
                     if (ring.use > 0) wait(LY.empty + 8 * st, ring.use - 1);
                     __syncwarp();
-                    if (__any_sync(0xffffffffu, flags()[0])) {
-                        stop = true;
-                        break;
-                    }
-                    if (lane == 0) {
-                        slot_bad()[st] = (bads >> (b0 - c)) & ((1u << Sh::pages) - 1u);
-                        mbar_expect_tx(sb + LY.full + 8 * st, (uint32_t)n * Sh::page_bytes);
-                    }
+                    ok = !__any_sync(0xffffffffu, dead());
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(sb + LY.full + 8 * st, (uint32_t)n * Sh::page_bytes);
                     __syncwarp();
                     ++mine;
                     const int i = c + lane - b0;
@@ -423,7 +418,7 @@ struct PaTile {
         }
         if (lane == 0) {
             if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
-            if (flags()[0])   // our copies land before the CTA leaves
+            if (dead())   // our copies land before the CTA leaves
                 for (int j = max(0, mine - NS); j < mine; ++j)
                     bounded_wait(sb + LY.full + 8 * (w * NS + j % NS), (uint32_t)((j / NS) & 1), flags(), p.wait_limit_ns, false);
         }
@@ -442,34 +437,31 @@ struct PaTile {
         const uint64_t kd0 = pa_desc(sb + LY.ring, 16, Sh::nblk * 1024);
         const uint64_t vd0 = pa_desc(sb + LY.ring + (D / 64) * 1024, 1024, Sh::nblk * 1024);
         constexpr uint32_t dSP = Sh::tSP + W * 3 * U, dO = Sh::tO + W * D;
-        bool stop = false;
-        while (!stop && work.next(it)) {
+        while (work.next(it)) {
             const int n = it.kb1 - it.kb0;
             if (it.rows <= 0) {   // no second tile: hand the blocks back
-                for (int j = 0; j < n && !stop; ++j) {
+                for (int j = 0; j < n; ++j) {
                     ring.take();
                     wait(LY.full + 8 * ring.st, ring.use);
                     __syncwarp();
-                    stop = __any_sync(0xffffffffu, flags()[0]);
                     if (lane == 0) mbar_arrive(sb + LY.empty + 8 * ring.st);
                 }
                 continue;
             }
-            wait(LY.qready + 8 * W, items);
-            ++items;
+            wait(LY.qready + 8 * W, items++);
             int st_prev = 0, pages_prev = 0;
-            for (int j = 0; j <= n && !stop; ++j) {
+            for (int j = 0; j <= n; ++j) {
                 int st = 0, pages = 0;
                 if (j < n) {   // S of block j
                     ring.take();
                     st = ring.st;
                     pages = pages_from(it, it.kb0 + j);
-                    wait(LY.full + 8 * st, ring.use);
                     // S of the block before has been read, and the weights of the
                     // one before that, whose columns this S takes (an item's end
                     // has waited for all of its products)
-                    if (blk > 0) wait(LY.sfree + 8 * W, blk - 1);
+                    wait(LY.full + 8 * st, ring.use);
                     if (j > 1) wait(LY.pvdone + 8 * W, blk - 2);
+                    if (blk > 0) wait(LY.sfree + 8 * W, blk - 1);
                     __syncwarp();
                     tc_fence_after();
                     // descriptors: constant steps (16 bytes each) from the tile's first
@@ -511,7 +503,6 @@ struct PaTile {
                 }
                 st_prev = st;
                 pages_prev = pages;
-                stop = __any_sync(0xffffffffu, flags()[0]);
             }
             if (pa_elect()) umma_commit(sb + LY.odone + 8 * W);
             __syncwarp();
@@ -540,8 +531,7 @@ struct PaTile {
         PaRing<NS> ring(w, p.pair);
         int blk = 0, items = 0;
         const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
-        bool stop = false;
-        while (!stop && work.next(it)) {
+        while (work.next(it)) {
             const int n = it.kb1 - it.kb0;
             if (it.rows <= 0) {
                 ring.n += n;
@@ -563,46 +553,43 @@ struct PaTile {
             }
             mbar_arrive(sb + LY.qready + 8 * w);
             float mu = -INFINITY, l = 0.f;
-            int bad = 0;
             for (int j = 0; j < n; ++j, ++blk) {
-                ring.take();
-                const int st = ring.st;
-                const int key0 = (it.kb0 + j) * KB;
                 wait(LY.sfull + 8 * w, blk);
                 __syncwarp();
                 tc_fence_after();
-                const int dead = flags()[0];   // read here, looked at when it has come
-                bad |= slot_bad()[st];
-                const bool edge = it.keys < key0 + KB;
-                if (edge) zero_tail(it, st, ring.use, key0, row);
+                int keys = KB;   // of the block
+                if (j == n - 1 && it.keys < it.kb1 * KB) {
+                    keys = it.keys - (it.kb1 - 1) * KB;
+                    zero_tail(ring, keys, row);
+                }
+                ++ring.n;
                 const int outer = blk & 1;   // the half of the keys in the outer unit
-                const uint32_t aOut = aSP + 2 * outer * U, aMid = aSP + U;
-                const int left_out = it.keys - key0 - outer * U, left_mid = it.keys - key0 - (outer ^ 1) * U;
-                if (active) {
-                    uint32_t s[U], pa[U / 2], pb[U / 2];
-                    if (j == 0) {   // the row's first maximum
-                        pa_load_scores<U>(aMid, s, edge, left_mid);
-                        mu = pa_max(s, -INFINITY);
-                        pa_load_scores<U>(aOut, s, edge, left_out);
-                        mu = pa_max(s, mu) * p.scale_log2;
-                    } else {
-                        pa_load_scores<U>(aOut, s, edge, left_out);
+#pragma unroll
+                for (int unit = 0; unit < 2; ++unit) {
+                    const int half = outer ^ unit;
+                    uint32_t s[U], pk[U / 2];
+                    if (active) pa_load_scores<U>(aSP + (unit ? 1 : 2 * outer) * U, s, keys < KB, keys - half * U);
+                    if (unit) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
                     }
+                    if (!active) continue;
                     // The weights against the maximum so far.  Later scores may exceed
-                    // it as long as a block's weights stay below 2^14 in sum (so no
-                    // maximum is taken per block); otherwise it follows and O is rescaled.
-                    float sum = pa_weights<E>(s, pa, cc, mu);
-                    pa_load_scores<U>(aMid, s, edge, left_mid);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
-                    sum += pa_weights<E>(s, pb, cc, mu);
-                    if (__any_sync(0xffffffffu, !(sum < kPaMost))) {
-                        uint32_t so[U];
-                        pa_load_scores<U>(aOut, so, edge, left_out);
-                        const float top = pa_max(so, pa_max(s, -INFINITY)) * p.scale_log2;
-                        const float al = top > mu ? a2_ex2(mu - top) : 1.f;
-                        mu = fmaxf(mu, top);
+                    // it as long as a half's weights stay below 2^14 in sum (so no
+                    // maximum is taken per block); otherwise it follows, to a power of
+                    // two, and what was made against the old one is rescaled.  (No
+                    // maximum yet: the sum is not finite.)
+                    float base = -mu, sum;
+                    for (bool again = false;; again = true) {
+                        sum = pa_weights<E>(s, pk, cc, base);
+                        if (again || !__any_sync(0xffffffffu, !(sum < kPaMost))) break;
+                        // (only this row's own scores move it, not a neighbour's)
+                        const float top = ceilf(pa_max(s, -INFINITY) * p.scale_log2);
+                        const bool grew = top > mu && !(sum < kPaMost);
+                        const float al = grew ? a2_ex2(mu - top) : 1.f;
+                        if (grew) mu = top;
+                        base = mu == -INFINITY ? 0.f : -mu;
                         l *= al;
                         if (j > 0) {
                             wait(LY.pvdone + 8 * w, blk - 1);
@@ -618,14 +605,21 @@ struct PaTile {
                                 pa_tmem_st16(aO + c, o);
                             }
                         }
-                        sum = pa_weights<E>(s, pb, cc, mu);
-                        sum += pa_weights<E>(so, pa, cc, mu);
+                        if (unit) {   // the outer half's weights, not multiplied yet
+                            pa_tmem_st_wait();
+#pragma unroll 1
+                            for (int c = 0; c < U / 2; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld_x16(aSP + 2 * outer * U + outer * (U / 2) + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = E::pack(E::lo(o[e]) * al, E::hi(o[e]) * al);
+                                pa_tmem_st16(aSP + 2 * outer * U + outer * (U / 2) + c, o);
+                            }
+                        }
                     }
                     l += sum;
-                    pa_tmem_st<U / 2>(aOut + outer * (U / 2), pa);
-                    pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pb);
-                } else if (lane == 0) {
-                    mbar_arrive(sb + LY.sfree + 8 * w);
+                    pa_tmem_st<U / 2>(aSP + 2 * outer * U + half * (U / 2), pk);
                 }
                 if (active) pa_tmem_st_wait();
                 tc_fence_before();
@@ -633,13 +627,11 @@ struct PaTile {
                 // (two barriers in turn: this S says that the weights of the block
                 // two back have been multiplied, so that phase has been seen)
                 if (lane == 0) mbar_arrive(sb + LY.pready + 16 * outer + 8 * w);
-                if (dead) break;
             }
             // (not on pvdone, whose last two phases may both be open)
             wait(LY.odone + 8 * w, items++);
             __syncwarp();
-            stop = __any_sync(0xffffffffu, flags()[0]);
-            if (active && !stop) {
+            if (active && !__any_sync(0xffffffffu, dead())) {
                 tc_fence_after();
                 float *dst = p.ws_o + ((int64_t)it.split * p.rows + grow) * D;
 #pragma unroll
@@ -653,25 +645,25 @@ struct PaTile {
                             __stcg(reinterpret_cast<uint4 *>(dst + c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                 }
                 tc_fence_before();
-                // a sum below zero marks a partial over a page outside the cache
-                if (valid) __stcg(p.ws_ml + grow * (p.sp + p.ss) + it.split, make_float2(mu, bad ? -1.f : l));
+                // a sum below zero: a page outside the cache, which voids every row
+                if (valid) __stcg(p.ws_ml + grow * (p.sp + p.ss) + it.split, make_float2(mu, flags()[1] ? -1.f : l));
             }
         }
     }
 
-    // The V rows of the last page behind the keys: whatever they hold must not
-    // meet a zero weight
-    __device__ __forceinline__ void zero_tail(const PaItem &it, int st, int use, int key0, int row) const
+    // The V rows of an item's last page behind its keys (of `keys` in the
+    // block): whatever they hold must not meet a zero weight
+    __device__ __forceinline__ void zero_tail(PaRing<NS> ring, int keys, int row) const
     {
-        const int s0 = it.keys & (kPageSlots - 1);
+        const int s0 = keys & (kPageSlots - 1), pg = keys / kPageSlots;
         if (s0 == 0) return;
-        wait(LY.full + 8 * st, use);
-        const int pg = (it.keys - key0) / kPageSlots;
+        ring.take();
+        wait(LY.full + 8 * ring.st, ring.use);
+        uint8_t *page = smem + LY.ring + ring.st * Sh::stage_bytes + pg * Sh::page_bytes;
         for (int c = row; c < (kPageSlots - s0) * (D / 8); c += 128) {
             const int s = s0 + c / (D / 8), ch = c % (D / 8);
-            *reinterpret_cast<uint4 *>(smem + LY.ring + st * Sh::stage_bytes + pg * Sh::page_bytes +
-                                       (s >> 3) * (Sh::nblk * 1024) + (D / 64 + ch / 8) * 1024 +
-                                       (s & 7) * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(page + (s >> 3) * (Sh::nblk * 1024) + (D / 64 + ch / 8) * 1024 + (s & 7) * 128 +
+                                       (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -704,7 +696,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             mbar_init(sb + LY.odone + 8 * w, 1);
             mbar_init(sb + LY.drain + 8 * w, 1);
         }
-        *reinterpret_cast<volatile int *>(smem + LY.flags) = 0;
+        reinterpret_cast<volatile int *>(smem + LY.flags)[0] = 0;   // a wait gave up
+        reinterpret_cast<volatile int *>(smem + LY.flags)[1] = 0;   // a page outside the cache
         fence_barrier_init();
     }
     // all of tensor memory (one CTA per SM): it starts at column 0

@@ -28,6 +28,8 @@ struct Bf16 {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);
     }
+    static __device__ __forceinline__ float lo(uint32_t v) { return get((uint16_t)v); }
+    static __device__ __forceinline__ float hi(uint32_t v) { return get((uint16_t)(v >> 16)); }
 };
 struct Fp16 {
     using store = uint16_t;
@@ -39,6 +41,8 @@ struct Fp16 {
         const __half2 v = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);
     }
+    static __device__ __forceinline__ float lo(uint32_t v) { return get((uint16_t)v); }
+    static __device__ __forceinline__ float hi(uint32_t v) { return get((uint16_t)(v >> 16)); }
 };
 struct Fp32 {
     using store = float;
