@@ -91,7 +91,7 @@ struct PrefixParams {
     int rows;         // R * q_len * q_heads
     int tiles;        // 128-row tiles of a KV head's rows (the tile kernel)
     int pair;         // both groups of a CTA on one key stream
-    int small;        // the prefix's rows fit the rows kernel
+    int small, pre_rows;       // the prefix's rows are few: the rows kernel's, in a tile of pre_rows
     int own_rows, own_tiles;   // rows of one tile of a request's rows, tiles of a request
     int sp, ss;       // key splits of the prefix and of a request's own keys
     float scale_log2;
@@ -371,9 +371,10 @@ struct PaTile {
     }
 
     // ---- produce: ring w's blocks, one 128-byte-swizzled box per page ----
-    __device__ __forceinline__ void produce(int w) const
+    // (entry: this lane's table entry from page guess on, loaded before the
+    // prefix's length had come)
+    __device__ __forceinline__ void produce(int w, int guess, int entry) const
     {
-        if (lane == 0) tma_prefetch_map(map);
         PaWork<D> work(p, P, w);
         PaItem it;
         bool ok = true;
@@ -383,7 +384,7 @@ struct PaTile {
         while (ok && work.next(it)) {
             const int pg0 = it.kb0 * Sh::pages;
             const int pg1 = min(it.kb1 * Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots);
-            int next = pg0 + lane < pg1 ? it.pages[pg0 + lane] : 0;
+            int next = pg0 + lane < pg1 ? (pg0 == guess ? entry : it.pages[pg0 + lane]) : 0;
             for (int c = pg0; c < pg1 && ok; c += 32) {
                 int page = next;
                 if (c + 32 + lane < pg1) next = it.pages[c + 32 + lane];
@@ -709,11 +710,30 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // released only now: the rows kernel behind this one reads the same inputs
     // without a wait of its own
     if (threadIdx.x == 0) griddep_launch_dependents();
+    // What the first item needs besides the length is fetched beside it: its
+    // table entries as of a full table, its rows of q into L2.
+    int guess = -1, entry = 0;
+    if (warp < 8) {
+        const int idx = p.pair ? blockIdx.x : 2 * blockIdx.x + (warp >> 2), rb = p.pair ? (p.tiles + 1) / 2 : 1;
+        const int m = (p.pair ? 2 * (idx % rb) + (warp >> 2) : 0) * kPaTile + (threadIdx.x & 127), tok = m / p.group;
+        const char *row = reinterpret_cast<const char *>(static_cast<const uint16_t *>(p.q) + tok * p.q_ts +
+                                                         (idx / rb % p.nkv * p.group + m - tok * p.group) * p.q_hs);
+        if (tok < p.R * p.q_len)
+            for (int c = 0; c < 2 * D; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+    } else if (warp < 10) {
+        if (lane == 0) tma_prefetch_map(&tmKV);
+        PaWork<D> work(p, p.prefix_blocks * kPageSlots, warp - 8);
+        PaItem it;
+        if (work.next(it)) {
+            guess = it.kb0 * Sh::pages;
+            if (guess + lane < p.prefix_blocks) entry = it.pages[guess + lane];
+        }
+    }
     const PaTile<E, D> tile{&tmKV, p, smem, sb, __reduce_max_sync(0xffffffffu, pa_prefix_len(p)), lane};
     if (warp < 8)
         tile.softmax(warp >> 2, warp & 3);
     else if (warp < 10)
-        tile.produce(warp - 8);
+        tile.produce(warp - 8, guess, entry);
     else if (warp == 10)
         tile.template multiply<0>();
     else
@@ -766,68 +786,23 @@ __device__ __forceinline__ void pr_mma(float (&d)[4], const uint32_t (&a)[4], ui
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// One item against its key blocks: RT = 16 or 64 rows
 template <class E, int D, int RT>
-__global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, RT>())
-    prefix_rows_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
+__device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixParams &p, const PaItem &it, int first_entry,
+                                        uint8_t *smem)
 {
     using Sh = PrShape<D>;
     constexpr int NS = Sh::slots, NP = RT == 16 ? 1 : kPrPages;
-    extern __shared__ uint8_t pr_smem_dyn[];
-    uint8_t *smem = pr_smem_dyn + ((1024u - (smem_u32(pr_smem_dyn) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem), full0 = sb + Sh::ring_bytes, empty0 = full0 + 8 * NS;
     volatile int *slot_bad = reinterpret_cast<volatile int *>(smem + Sh::ring_bytes + 16 * NS);
     volatile int *flags = slot_bad + NS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, 4);
-        }
-        flags[0] = 0;
-        fence_barrier_init();
-        griddep_launch_dependents();
-    }
-    __syncthreads();
-    // Behind the tile kernel every input is already written (that kernel has
-    // waited for it before this one could start), and only the grid as a whole
-    // must not end before it: the last CTA waits, at its end.
-    const bool behind = !p.small && p.prefix_blocks > 0;
-    if (!behind) griddep_wait();
     const auto wait = [&](uint32_t bar, int n) {
         return mbar_try_wait(bar, (uint32_t)n & 1) || bounded_wait(bar, (uint32_t)n & 1, flags, p.wait_limit_ns, true);
     };
-
-    // ---- the item: the prefix (few rows in all), then the requests' own keys
-    int idx = blockIdx.x;
-    const int np = p.small && p.prefix_blocks > 0 ? p.nkv * p.sp : 0;
-    const bool own = idx >= np;
-    idx -= own ? np : 0;
-    const int g = idx % p.nkv, rest = idx / p.nkv;
-    const int r = own ? rest % p.R : 0, ts = own ? rest / p.R : 0;
-    const int tile = own ? ts % p.own_tiles : 0, split = own ? ts / p.own_tiles : rest;
-    const int32_t *pages = own ? p.block_table + (size_t)r * p.max_blocks : p.prefix_pages;
-    // the first split starts at page 0: its entries need not wait for a length
-    int first_entry = 0;
-    if (warp == 4 && split == 0 && lane < (own ? p.max_blocks : p.prefix_blocks)) first_entry = pages[lane];
-    const int P = pa_prefix_len(p), L = own ? p.context_lens[r] : 0;
-    PaItem it;
-    if (own) {
-        it.keys = P < 0 ? 0 : pa_own_keys(p, L, tile);
-        it.tok0 = r * p.q_len;
-        it.row0 = tile * RT;
-        it.rows = min(RT, p.q_len * p.group - it.row0);
-        it.limit0 = L - p.q_len + 1;
-        it.step = 1;
-        it.split = p.sp + split;
-        pa_deal(it, (it.keys + kPrKeys - 1) / kPrKeys, p.ss, split);
-    } else {
-        it = pa_prefix_item<kPrKeys>(p, max(P, 0), RT, 0, g, split);
-    }
+    const int g = it.g;
+    const int32_t *pages = it.pages;
     const int n = it.kb1 - it.kb0;   // stages
-    if (n <= 0) {
-        if (behind && blockIdx.x == gridDim.x - 1) griddep_wait();
-        return;
-    }
     const int pg0 = it.kb0 * kPrPages;
     const int pg1 = min(it.kb1 * kPrPages, (it.keys + kPageSlots - 1) / kPageSlots);
 
@@ -842,7 +817,7 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, RT>())
         unsigned bad_any = 0u;
         bool stop = false;
         int j = 0;
-        int next = pg0 + lane < pg1 ? (split == 0 ? first_entry : pages[pg0 + lane]) : 0;
+        int next = pg0 + lane < pg1 ? (pg0 == 0 ? first_entry : pages[pg0 + lane]) : 0;
         for (int c = pg0; c < pg1 && !stop; c += 32) {
             int page = next;
             if (c + 32 + lane < pg1) next = pages[c + 32 + lane];
@@ -1072,45 +1047,125 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, RT>())
             if (c == 0) __stcg(p.ws_ml + gr * splits + it.split, make_float2(M, bad ? -1.f : l));
         }
     }
+}
+
+// Prefix items (where the prefix's rows are few: p.small) in tiles of RTP
+// rows, then the requests' own keys in tiles of RTO.
+template <class E, int D, int RTP, int RTO>
+__global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP : RTO)>())
+    prefix_rows_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
+{
+    using Sh = PrShape<D>;
+    constexpr int NS = Sh::slots;
+    extern __shared__ uint8_t pr_smem_dyn[];
+    uint8_t *smem = pr_smem_dyn + ((1024u - (smem_u32(pr_smem_dyn) & 1023u)) & 1023u);
+    const uint32_t full0 = smem_u32(smem) + Sh::ring_bytes, empty0 = full0 + 8 * NS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 4);
+        }
+        reinterpret_cast<volatile int *>(smem + Sh::ring_bytes + 16 * NS)[NS] = 0;
+        fence_barrier_init();
+        griddep_launch_dependents();
+    }
+    __syncthreads();
+    // Behind the tile kernel every input is already written (that kernel has
+    // waited for it before this one could start), and only the grid as a whole
+    // must not end before it: the last CTA waits, at its end.
+    const bool behind = !p.small && p.prefix_blocks > 0;
+    if (!behind) griddep_wait();
+
+    int idx = blockIdx.x;
+    const int np = p.small && p.prefix_blocks > 0 ? p.nkv * p.sp : 0;
+    const bool own = idx >= np;
+    idx -= own ? np : 0;
+    const int g = idx % p.nkv, rest = idx / p.nkv;
+    const int r = own ? rest % p.R : 0, ts = own ? rest / p.R : 0;
+    const int tile = own ? ts % p.own_tiles : 0, split = own ? ts / p.own_tiles : rest;
+    const int32_t *pages = own ? p.block_table + (size_t)r * p.max_blocks : p.prefix_pages;
+    // the first split starts at page 0: its entries need not wait for a length
+    int first_entry = 0;
+    if (warp == 4 && split == 0 && lane < (own ? p.max_blocks : p.prefix_blocks)) first_entry = pages[lane];
+    const int P = pa_prefix_len(p), L = own ? p.context_lens[r] : 0;
+    PaItem it;
+    if (own) {
+        it.pages = pages;
+        it.g = g;
+        it.keys = P < 0 ? 0 : pa_own_keys(p, L, tile);
+        it.tok0 = r * p.q_len;
+        it.row0 = tile * RTO;
+        it.rows = min(RTO, p.q_len * p.group - it.row0);
+        it.limit0 = L - p.q_len + 1;
+        it.step = 1;
+        it.split = p.sp + split;
+        pa_deal(it, (it.keys + kPrKeys - 1) / kPrKeys, p.ss, split);
+    } else {
+        it = pa_prefix_item<kPrKeys>(p, max(P, 0), RTP, 0, g, split);
+    }
+    if (it.kb1 > it.kb0) {
+        if constexpr (RTP == RTO) {
+            pr_item<E, D, RTO>(tmKV, p, it, first_entry, smem);
+        } else {
+            if (own)
+                pr_item<E, D, RTO>(tmKV, p, it, first_entry, smem);
+            else
+                pr_item<E, D, RTP>(tmKV, p, it, first_entry, smem);
+        }
+    }
     if (behind && blockIdx.x == gridDim.x - 1) griddep_wait();
 }
 
-// Joins a row's partials, one warp per row: lane l holds the maximum and sum
-// of partials l, l + 32, ...; their weights go to shared memory, and O is
-// summed with 8 partials' loads in flight (D / 4 lanes a partial, so at
-// D = 64 each half warp takes every other one).  The order is fixed by the
-// split counts: the same bits every time.
-constexpr int kPaMergeWarps = 4;
+// Joins a row's partials: kWarps warps a row, D / 4 lanes a partial, the
+// partials dealt round robin.  The lengths, the maxima and sums and the first
+// partials' O are loaded side by side, before it is known which of the slots
+// hold keys (the others' contents are not used).  Sums in a fixed order: the
+// same bits every time.
+constexpr int kPaMergeThreads = 128;
+constexpr int kPaMergeAhead = 6;   // partials in flight per lane
 
-template <class E, int D>
-__global__ void __launch_bounds__(32 * kPaMergeWarps) prefix_merge_kernel(const __grid_constant__ PrefixParams p)
+template <class E, int D, int kWarps>
+__global__ void __launch_bounds__(kPaMergeThreads) prefix_merge_kernel(const __grid_constant__ PrefixParams p)
 {
-    constexpr int LPR = D / 4, PAR = 32 / LPR;
-    __shared__ float weight[kPaMergeWarps][2 * kPaMaxSplits];
+    constexpr int LPR = D / 4, PAR = kWarps * 32 / LPR, kRows = kPaMergeThreads / (32 * kWarps);
+    __shared__ float weight[kRows][2 * kPaMaxSplits];
+    __shared__ float4 part[kRows][kWarps][32];
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kPaMergeWarps + warp;
-    if (row >= p.rows) return;
+    const int rl = warp / kWarps, wr = warp % kWarps;   // the row of the CTA, the warp of the row
+    const int row = blockIdx.x * kRows + rl;
+    if (kWarps == 1 && row >= p.rows) return;   // (with 4 warps the CTA is one row)
     const int t = row / p.q_heads, h = row - t * p.q_heads, r = t / p.q_len;
+    const int slots = p.sp + p.ss;
+    const float2 *ml = p.ws_ml + (int64_t)row * slots;
+    const int first = wr * (32 / LPR) + lane / LPR, d = lane % LPR;   // this lane's first slot, its 4 columns
+    const float4 *src = reinterpret_cast<const float4 *>(p.ws_o + (int64_t)row * D) + d;
+    const int64_t step = (int64_t)p.rows * (D / 4);
     const int P = pa_prefix_len(p), L = p.context_lens[r];
-    const float2 *ml = p.ws_ml + (int64_t)row * (p.sp + p.ss);
+    float2 v[2 * kPaMaxSplits / 32];
+#pragma unroll
+    for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i)
+        if (lane + 32 * i < slots) v[i] = __ldcg(ml + lane + 32 * i);
+    float4 x[kPaMergeAhead];
+#pragma unroll
+    for (int i = 0; i < kPaMergeAhead; ++i)
+        if (first + i * PAR < slots) x[i] = __ldcg(src + (first + i * PAR) * step);
     if (L < 0 && P >= 0) return;   // a padding request
     if (P < 0 || L > p.max_blocks * kPageSlots) {
-        if (lane == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
+        if (lane == 0 && wr == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
         return;
     }
     const int own = pa_own_keys(p, L, ((t - r * p.q_len) * p.group + h % p.group) / p.own_rows);
     const int pkeys = p.small ? kPrKeys : PaShape<D>::keys;
-    // partials 0 .. np - 1 over the prefix, np .. n - 1 (slots sp ..) over its own keys
-    const int np = min(p.sp, (P + pkeys - 1) / pkeys), n = np + min(p.ss, (own + kPrKeys - 1) / kPrKeys), skip = p.sp - np;
-    float2 v[2 * kPaMaxSplits / 32];
+    const int np = min(p.sp, (P + pkeys - 1) / pkeys), no = p.sp + min(p.ss, (own + kPrKeys - 1) / kPrKeys);
+    const auto holds = [&](int s) { return s < np || (s >= p.sp && s < no); };
     float M = -INFINITY;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i) {
-        const int s = lane + 32 * i;
-        v[i] = s < n ? __ldcg(ml + s + (s < np ? 0 : skip)) : make_float2(-INFINITY, 0.f);
+        if (!holds(lane + 32 * i)) v[i] = make_float2(-INFINITY, 0.f);
         M = fmaxf(M, v[i].x);
         bad |= v[i].y < 0.f;
     }
@@ -1122,40 +1177,49 @@ __global__ void __launch_bounds__(32 * kPaMergeWarps) prefix_merge_kernel(const 
 #pragma unroll
     for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i) {
         const float f = exp2f(v[i].x - base);
-        weight[warp][lane + 32 * i] = f;
+        if (wr == 0) weight[rl][lane + 32 * i] = f;
         l = fmaf(v[i].y, f, l);
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    __syncwarp();
-    const int d = lane % LPR;
+    if (kWarps == 1)
+        __syncwarp();
+    else
+        __syncthreads();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 *src = reinterpret_cast<const float4 *>(p.ws_o + (int64_t)row * D) + d;
-    const int64_t step = (int64_t)p.rows * (D / 4);
-    for (int s0 = lane / LPR; s0 < n; s0 += 8 * PAR) {
-        float4 x[8];
+    for (int s0 = first; s0 < slots; s0 += kPaMergeAhead * PAR) {
+        if (s0 != first)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int s = s0 + i * PAR;
-            if (s < n) x[i] = __ldcg(src + (s + (s < np ? 0 : skip)) * step);
-        }
+            for (int i = 0; i < kPaMergeAhead; ++i)
+                if (holds(s0 + i * PAR)) x[i] = __ldcg(src + (s0 + i * PAR) * step);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int s = s0 + i * PAR;
-            if (s < n) {
-                const float f = weight[warp][s];
+        for (int i = 0; i < kPaMergeAhead; ++i)
+            if (holds(s0 + i * PAR)) {
+                const float f = weight[rl][s0 + i * PAR];
                 o.x = fmaf(x[i].x, f, o.x);
                 o.y = fmaf(x[i].y, f, o.y);
                 o.z = fmaf(x[i].z, f, o.z);
                 o.w = fmaf(x[i].w, f, o.w);
             }
-        }
     }
-    if constexpr (PAR == 2) {
+    if constexpr (LPR == 16) {
         o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
         o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
         o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
         o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+    }
+    if constexpr (kWarps > 1) {
+        part[rl][wr][lane] = o;
+        __syncthreads();
+        if (wr > 0) return;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 y = part[rl][w][lane];
+            o.x += y.x;
+            o.y += y.y;
+            o.z += y.z;
+            o.w += y.w;
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const uint2 y = l == 0.f ? make_uint2(0u, 0u) : make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
@@ -1166,7 +1230,7 @@ __global__ void __launch_bounds__(32 * kPaMergeWarps) prefix_merge_kernel(const 
 // ---- host: splits, workspace, launch ---------------------------------------
 
 struct PaPlan {
-    int small, tiles, pair, own_rows, own_tiles, sp, ss, sp_max, ss_max;
+    int small, pre_rows, tiles, pair, own_rows, own_tiles, sp, ss, sp_max, ss_max;
 };
 
 // The split (1..most) that ends soonest when `units` row tiles times the
@@ -1199,18 +1263,24 @@ PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int 
     const int group = q_heads / nkv;
     const int64_t all = (int64_t)num_reqs * q_len * group;   // rows of a KV head
     PaPlan pl;
-    pl.small = all <= 16;
+    // The rows kernel takes the prefix too while its tensor work hides behind
+    // the loads: 32 rows against 8 x 32K keys of 64 23.5 us, 24.8 in the tile
+    // kernel; 64 rows 11.9 against 14.2 over 4K keys, but 28.6 against 26.0 over 32K.
+    pl.small = all <= 32 || (all <= 64 && prefix_blocks <= 1024);
+    pl.pre_rows = all <= 16 ? 16 : 64;
     pl.tiles = (int)((all + kPaTile - 1) / kPaTile);
     pl.pair = !pl.small && pl.tiles > 1;
     pl.own_rows = q_len * group <= 16 ? 16 : 64;
     pl.own_tiles = (q_len * group + pl.own_rows - 1) / pl.own_rows;
-    const int ctas = pl.own_rows == 16 ? (head_dim == 64 ? 4 : 3) : (head_dim == 64 ? 3 : 2);   // rows kernel, per SM
+    const bool wide = pl.own_rows == 64 || (pl.small && pl.pre_rows == 64);
+    const int ctas = wide ? (head_dim == 64 ? 3 : 2) : (head_dim == 64 ? 4 : 3);   // of the rows kernel, per SM
     const int keys = pl.small ? kPrKeys : head_dim == 64 ? PaShape<64>::keys : PaShape<128>::keys, ppb = keys / kPageSlots;
     const int64_t nb = (prefix_blocks + ppb - 1) / ppb, no = (max_blocks + kPrPages - 1) / kPrPages;
     const int64_t units = (int64_t)(pl.pair ? (pl.tiles + 1) / 2 : 1) * nkv;
     const int64_t workers = pl.small ? ctas * sms : pl.pair ? sms : 2 * sms;
-    pl.sp_max = pa_most(units, workers, nb);
-    pl.sp = pa_split(units, workers, nb, pl.sp_max, pl.small ? 6.0 : 3.0);
+    pl.sp = pa_split(units, workers, nb, pa_most(units, workers, nb), pl.small ? 6.0 : 3.0);
+    // (up to 64 rows a narrower prefix may go to the other kernel: one bound for both)
+    pl.sp_max = all <= 64 ? pa_most(nkv, 4 * (int64_t)sms, (prefix_blocks + kPrPages - 1) / kPrPages) : pa_most(units, workers, nb);
     const int64_t own = (int64_t)num_reqs * nkv * pl.own_tiles;
     pl.ss_max = pa_most(own, ctas * sms, no);
     pl.ss = pa_split(own, ctas * sms, no, pl.ss_max, 6.0);
@@ -1230,8 +1300,9 @@ bool prepare_prefix_kernel()
     static_assert(pa_smem<D>().total <= (uint32_t)kMaxSmemPerCta, "shared memory");
     constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     return cudaFuncSetAttribute((const void *)prefix_tile_kernel<E, D>, attr, (int)pa_smem<D>().total) == cudaSuccess &&
-           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
-           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 64>, attr, (int)PrShape<D>::smem) == cudaSuccess;
+           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 16, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
+           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 64, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
+           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 64, 64>, attr, (int)PrShape<D>::smem) == cudaSuccess;
 }
 
 bool prepare_prefix_kernels()
@@ -1273,12 +1344,16 @@ int launch_prefix(const CUtensorMap &map, const PrefixParams &prm, int sms, void
     const int64_t items = (prm.small && prm.prefix_blocks > 0 ? (int64_t)prm.nkv * prm.sp : 0) +
                           (prm.max_blocks > 0 ? (int64_t)prm.R * prm.nkv * prm.own_tiles * prm.ss : 0);
     if (items > 0) {
-        rc = launch_pdl(prm.own_rows == 16 ? prefix_rows_kernel<E, D, 16> : prefix_rows_kernel<E, D, 64>,
+        rc = launch_pdl(prm.own_rows == 64                       ? prefix_rows_kernel<E, D, 64, 64>
+                        : prm.small && prm.pre_rows == 64 ? prefix_rows_kernel<E, D, 64, 16>
+                                                          : prefix_rows_kernel<E, D, 16, 16>,
                         dim3((unsigned)items), dim3(kPrThreads), (size_t)PrShape<D>::smem, stream, map, prm);
         if (rc != QKVF_OK) return rc;
     }
-    return launch_pdl(prefix_merge_kernel<E, D>, dim3((unsigned)((prm.rows + kPaMergeWarps - 1) / kPaMergeWarps)),
-                      dim3(32 * kPaMergeWarps), 0, stream, prm);
+    // four warps a row where there are more partials than one warp has in flight
+    if (prm.sp + prm.ss > kPaMergeAhead * 32 / (D / 4))
+        return launch_pdl(prefix_merge_kernel<E, D, 4>, dim3((unsigned)prm.rows), dim3(kPaMergeThreads), 0, stream, prm);
+    return launch_pdl(prefix_merge_kernel<E, D, 1>, dim3((unsigned)((prm.rows + 3) / 4)), dim3(kPaMergeThreads), 0, stream, prm);
 }
 
 const char *check_prefix_shape(int num_reqs, int q_len, int q_heads, int num_kv_heads, int head_dim,
@@ -1427,6 +1502,7 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     prm.rows = num_reqs * q_len * q_heads;
     prm.tiles = pl.tiles;
     prm.small = pl.small;
+    prm.pre_rows = pl.pre_rows;
     prm.own_rows = pl.own_rows;
     prm.own_tiles = pl.own_tiles;
     prm.sp = pl.sp;
