@@ -357,8 +357,11 @@ struct PaTile {
     const PrefixParams &p;
     uint8_t *smem;
     uint32_t sb;
-    int P, lane;
+    int lane;
 
+    // The prefix's length, the same register for the whole warp.  What a role's
+    // first item needs besides is fetched beside it.
+    __device__ __forceinline__ int length() const { return __reduce_max_sync(0xffffffffu, pa_prefix_len(p)); }
     __device__ __forceinline__ volatile int *flags() const { return reinterpret_cast<volatile int *>(smem + LY.flags); }
     __device__ __forceinline__ void wait(uint32_t bar, int n) const   // until phase n of bar is complete
     {
@@ -371,12 +374,16 @@ struct PaTile {
     }
 
     // ---- produce: ring w's blocks, one 128-byte-swizzled box per page ----
-    // (entry: this lane's table entry from page guess on, loaded before the
-    // prefix's length had come)
-    __device__ __forceinline__ void produce(int w, int guess, int entry) const
+    __device__ __forceinline__ void produce(int w) const
     {
-        PaWork<D> work(p, P, w);
+        if (lane == 0) tma_prefetch_map(map);
         PaItem it;
+        int guess = -1, entry = 0;   // the first entries as of a full table
+        if (PaWork<D>(p, p.prefix_blocks * kPageSlots, w).next(it)) {
+            guess = it.kb0 * Sh::pages;
+            if (guess + lane < p.prefix_blocks) entry = it.pages[guess + lane];
+        }
+        PaWork<D> work(p, length(), w);
         bool ok = true;
         PaRing<NS> ring(w, p.pair);
         int mine = 0;   // steps loaded into this ring
@@ -430,7 +437,7 @@ struct PaTile {
     template <int W>
     __device__ __forceinline__ void multiply() const
     {
-        PaWork<D> work(p, P, W);
+        PaWork<D> work(p, length(), W);
         PaItem it;
         PaRing<NS> ring(W, p.pair);
         int items = 0, blk = 0;   // items and blocks of this group so far
@@ -527,7 +534,15 @@ struct PaTile {
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
         const uint32_t aSP = Sh::tSP + w * 3 * U + lane_base, aO = Sh::tO + w * D + lane_base;
         uint8_t *sq = smem + LY.q + w * Sh::q_bytes;
-        PaWork<D> work(p, P, w);
+        {   // the first item's rows of q into L2
+            const int idx = p.pair ? blockIdx.x : 2 * blockIdx.x + w, rb = p.pair ? (p.tiles + 1) / 2 : 1;
+            const int m = (p.pair ? 2 * (idx % rb) + w : 0) * kPaTile + row, tok = m / p.group;
+            const char *q = reinterpret_cast<const char *>(static_cast<const uint16_t *>(p.q) + tok * p.q_ts +
+                                                           (idx / rb % p.nkv * p.group + m - tok * p.group) * p.q_hs);
+            if (tok < p.R * p.q_len)
+                for (int c = 0; c < 2 * D; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c));
+        }
+        PaWork<D> work(p, length(), w);
         PaItem it;
         PaRing<NS> ring(w, p.pair);
         int blk = 0, items = 0;
@@ -710,30 +725,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // released only now: the rows kernel behind this one reads the same inputs
     // without a wait of its own
     if (threadIdx.x == 0) griddep_launch_dependents();
-    // What the first item needs besides the length is fetched beside it: its
-    // table entries as of a full table, its rows of q into L2.
-    int guess = -1, entry = 0;
-    if (warp < 8) {
-        const int idx = p.pair ? blockIdx.x : 2 * blockIdx.x + (warp >> 2), rb = p.pair ? (p.tiles + 1) / 2 : 1;
-        const int m = (p.pair ? 2 * (idx % rb) + (warp >> 2) : 0) * kPaTile + (threadIdx.x & 127), tok = m / p.group;
-        const char *row = reinterpret_cast<const char *>(static_cast<const uint16_t *>(p.q) + tok * p.q_ts +
-                                                         (idx / rb % p.nkv * p.group + m - tok * p.group) * p.q_hs);
-        if (tok < p.R * p.q_len)
-            for (int c = 0; c < 2 * D; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
-    } else if (warp < 10) {
-        if (lane == 0) tma_prefetch_map(&tmKV);
-        PaWork<D> work(p, p.prefix_blocks * kPageSlots, warp - 8);
-        PaItem it;
-        if (work.next(it)) {
-            guess = it.kb0 * Sh::pages;
-            if (guess + lane < p.prefix_blocks) entry = it.pages[guess + lane];
-        }
-    }
-    const PaTile<E, D> tile{&tmKV, p, smem, sb, __reduce_max_sync(0xffffffffu, pa_prefix_len(p)), lane};
+    const PaTile<E, D> tile{&tmKV, p, smem, sb, lane};
     if (warp < 8)
         tile.softmax(warp >> 2, warp & 3);
     else if (warp < 10)
-        tile.produce(warp - 8, guess, entry);
+        tile.produce(warp - 8);
     else if (warp == 10)
         tile.template multiply<0>();
     else
@@ -1351,7 +1347,8 @@ int launch_prefix(const CUtensorMap &map, const PrefixParams &prm, int sms, void
         if (rc != QKVF_OK) return rc;
     }
     // four warps a row where there are more partials than one warp has in flight
-    if (prm.sp + prm.ss > kPaMergeAhead * 32 / (D / 4))
+    // and few rows (with 4096 rows of 128 and 10 partials one warp is faster)
+    if (prm.sp + prm.ss > kPaMergeAhead * 32 / (D / 4) && prm.rows <= 16 * sms)
         return launch_pdl(prefix_merge_kernel<E, D, 4>, dim3((unsigned)prm.rows), dim3(kPaMergeThreads), 0, stream, prm);
     return launch_pdl(prefix_merge_kernel<E, D, 1>, dim3((unsigned)((prm.rows + 3) / 4)), dim3(kPaMergeThreads), 0, stream, prm);
 }
