@@ -197,13 +197,25 @@ struct PaRing {
 };
 
 // Until the phase of this parity completes, at most limit_ns: then flags[0] is
-// set, every later wait of the CTA is short, and its results are void.
-__device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile int *flags, unsigned long long limit_ns)
+// set, every later wait of the CTA that honours it is short, and its results
+// are void.  (In line: a function call does not go with setmaxnreg.)
+__device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile int *flags, unsigned long long limit_ns,
+                                        bool honour = true)
 {
+    unsigned long long start = 0;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return;
-    bounded_wait(bar, parity, flags, limit_ns, true);
+    for (int i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if (i & 63) continue;
+        if (honour && flags[0]) return;
+        const unsigned long long now = global_ns();
+        if (start == 0) {
+            start = now;
+        } else if (now - start > limit_ns) {
+            flags[0] = 1;
+            atomicOr(&g_status, QKVF_STATUS_WAIT_TIMEOUT);
+            return;
+        }
+    }
 }
 
 // One lane of a converged warp, known to the compiler as one (its operands of
@@ -251,19 +263,32 @@ __device__ __forceinline__ void pa_tmem_st(uint32_t addr, const uint32_t *r)
     for (int c = 0; c < N; c += 16) pa_tmem_st16(addr + c, r + c);
 }
 
-// N scores of this thread's row; near an edge those from `limit` on become
-// -infinity, whatever their slots hold
+// N scores of this thread's row (and N more)
 template <int N>
-__device__ __forceinline__ void pa_load_scores(uint32_t addr, uint32_t *s, bool edge, int limit)
+__device__ __forceinline__ void pa_load_scores(uint32_t addr, uint32_t *s)
 {
 #pragma unroll
     for (int c = 0; c < N; c += 32) pa_tmem_ld32(addr + c, s + c);
     tmem_ld_wait();
-    if (edge) {
+}
+template <int N>
+__device__ __forceinline__ void pa_load_scores(uint32_t addr, uint32_t *s, uint32_t addr2, uint32_t *s2)
+{
 #pragma unroll
-        for (int c = 0; c < N; ++c)
-            if (c >= limit) s[c] = 0xff800000u;
+    for (int c = 0; c < N; c += 32) {
+        pa_tmem_ld32(addr + c, s + c);
+        pa_tmem_ld32(addr2 + c, s2 + c);
     }
+    tmem_ld_wait();
+}
+
+// The scores from `limit` on become -infinity, whatever their slots hold
+template <int N>
+__device__ __forceinline__ void pa_hide(uint32_t (&s)[N], int limit)
+{
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+        if (c >= limit) s[c] = 0xff800000u;
 }
 
 __device__ __forceinline__ void pa_tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -428,7 +453,7 @@ struct PaTile {
             if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
             if (dead())   // our copies land before the CTA leaves
                 for (int j = max(0, mine - NS); j < mine; ++j)
-                    bounded_wait(sb + LY.full + 8 * (w * NS + j % NS), (uint32_t)((j / NS) & 1), flags(), p.wait_limit_ns, false);
+                    pa_wait(sb + LY.full + 8 * (w * NS + j % NS), (uint32_t)((j / NS) & 1), flags(), p.wait_limit_ns, false);
         }
         __syncwarp();
     }
@@ -519,7 +544,7 @@ struct PaTile {
         // lane is elected each time: commits cover the MMAs of one thread)
         if (pa_elect()) umma_commit(sb + LY.drain + 8 * W);
         __syncwarp();
-        if (lane == 0) bounded_wait(sb + LY.drain + 8 * W, 0, flags(), p.wait_limit_ns, false);
+        if (lane == 0) pa_wait(sb + LY.drain + 8 * W, 0, flags(), p.wait_limit_ns, false);
         __syncwarp();
     }
 
@@ -580,28 +605,31 @@ struct PaTile {
                 }
                 ++ring.n;
                 const int outer = blk & 1;   // the half of the keys in the outer unit
-#pragma unroll
-                for (int unit = 0; unit < 2; ++unit) {
-                    const int half = outer ^ unit;
-                    uint32_t s[U], pk[U / 2];
-                    if (active) pa_load_scores<U>(aSP + (unit ? 1 : 2 * outer) * U, s, keys < KB, keys - half * U);
-                    if (unit) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
+                const uint32_t aOut = aSP + 2 * outer * U, aMid = aSP + U;
+                const int left_out = keys - outer * U, left_mid = keys - (outer ^ 1) * U;
+                if (active) {
+                    uint32_t so[U], sm[U], po[U / 2], pm[U / 2];
+                    pa_load_scores<U>(aOut, so, aMid, sm);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
+                    if (keys < KB) {
+                        pa_hide(so, left_out);
+                        pa_hide(sm, left_mid);
                     }
-                    if (!active) continue;
                     // The weights against the maximum so far.  Later scores may exceed
-                    // it as long as a half's weights stay below 2^14 in sum (so no
-                    // maximum is taken per block); otherwise it follows, to a power of
-                    // two, and what was made against the old one is rescaled.  (No
-                    // maximum yet: the sum is not finite.)
+                    // it as long as a block's weights stay below 2^14 in sum (so no
+                    // maximum is taken per block); otherwise it follows and O is
+                    // rescaled.  (No maximum yet: the sum is not finite.)
                     float base = -mu, sum;
                     for (bool again = false;; again = true) {
-                        sum = pa_weights<E>(s, pk, cc, base);
+                        sum = pa_weights<E>(so, po, cc, base);
+                        sum += pa_weights<E>(sm, pm, cc, base);
                         if (again || !__any_sync(0xffffffffu, !(sum < kPaMost))) break;
+                        pa_load_scores<U>(aOut, so);   // not overwritten yet
+                        if (keys < KB) pa_hide(so, left_out);
                         // (only this row's own scores move it, not a neighbour's)
-                        const float top = ceilf(pa_max(s, -INFINITY) * p.scale_log2);
+                        const float top = pa_max(so, pa_max(sm, -INFINITY)) * p.scale_log2;
                         const bool grew = top > mu && !(sum < kPaMost);
                         const float al = grew ? a2_ex2(mu - top) : 1.f;
                         if (grew) mu = top;
@@ -621,21 +649,12 @@ struct PaTile {
                                 pa_tmem_st16(aO + c, o);
                             }
                         }
-                        if (unit) {   // the outer half's weights, not multiplied yet
-                            pa_tmem_st_wait();
-#pragma unroll 1
-                            for (int c = 0; c < U / 2; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld_x16(aSP + 2 * outer * U + outer * (U / 2) + c, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = E::pack(E::lo(o[e]) * al, E::hi(o[e]) * al);
-                                pa_tmem_st16(aSP + 2 * outer * U + outer * (U / 2) + c, o);
-                            }
-                        }
                     }
                     l += sum;
-                    pa_tmem_st<U / 2>(aSP + 2 * outer * U + half * (U / 2), pk);
+                    pa_tmem_st<U / 2>(aOut + outer * (U / 2), po);
+                    pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pm);
+                } else if (lane == 0) {
+                    mbar_arrive(sb + LY.sfree + 8 * w);
                 }
                 if (active) pa_tmem_st_wait();
                 tc_fence_before();
@@ -726,14 +745,20 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // without a wait of its own
     if (threadIdx.x == 0) griddep_launch_dependents();
     const PaTile<E, D> tile{&tmKV, p, smem, sb, lane};
-    if (warp < 8)
+    // a softmax thread holds a row's whole S: its groups take registers from the
+    // other warpgroup (256 x 208 + 128 x 88 = 384 x 168, what the launch has)
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         tile.softmax(warp >> 2, warp & 3);
-    else if (warp < 10)
-        tile.produce(warp - 8);
-    else if (warp == 10)
-        tile.template multiply<0>();
-    else
-        tile.template multiply<1>();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp < 10)
+            tile.produce(warp - 8);
+        else if (warp == 10)
+            tile.template multiply<0>();
+        else
+            tile.template multiply<1>();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
