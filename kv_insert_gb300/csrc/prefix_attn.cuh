@@ -1279,6 +1279,29 @@ int pa_most(int64_t units, int64_t workers, int64_t blocks)
     return most < 1 ? 1 : (int)most;
 }
 
+// The tile kernel's split: its steps of `step` us each, the own keys' work
+// (`rest`, SM microseconds) on the SMs it leaves free meanwhile and behind it,
+// and `merge` us a split to join.  With 64 rows x 8 KV heads over 32K and up to
+// 1K own keys each, 9 splits (144 CTAs) take 60.8 us and 7 (112) 59.7 to 61.4; with 33
+// rows x 4 KV heads of 128 over 16K, 38 splits 30.5 and 18 26.1.
+int pa_tile_split(int64_t units, int64_t blocks, int most, int sms, bool pair, double step, double rest, double merge)
+{
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s <= most; ++s) {
+        const int64_t ctas = pair ? units * s : (units * s + 1) / 2, waves = (ctas + sms - 1) / sms;
+        const double tile = (double)waves * ((double)((blocks + s - 1) / s) * step + 5.0);
+        double left = rest - (ctas < sms ? (double)(sms - ctas) * tile : 0.0);
+        if (left < 0.0) left = 0.0;
+        const double cost = tile + left / sms + (rest > 0.0 ? 5.0 * left / rest : 0.0) + merge * s;
+        if (cost < least * 0.999) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int prefix_blocks, int max_blocks, int sms)
 {
     const int group = q_heads / nkv;
@@ -1299,12 +1322,19 @@ PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int 
     const int64_t nb = (prefix_blocks + ppb - 1) / ppb, no = (max_blocks + kPrPages - 1) / kPrPages;
     const int64_t units = (int64_t)(pl.pair ? (pl.tiles + 1) / 2 : 1) * nkv;
     const int64_t workers = pl.small ? ctas * sms : pl.pair ? sms : 2 * sms;
-    pl.sp = pa_split(units, workers, nb, pa_most(units, workers, nb), pl.small ? 6.0 : 3.0);
-    // (up to 64 rows a narrower prefix may go to the other kernel: one bound for both)
-    pl.sp_max = all <= 64 ? pa_most(nkv, 4 * (int64_t)sms, (prefix_blocks + kPrPages - 1) / kPrPages) : pa_most(units, workers, nb);
     const int64_t own = (int64_t)num_reqs * nkv * pl.own_tiles;
     pl.ss_max = pa_most(own, ctas * sms, no);
     pl.ss = pa_split(own, ctas * sms, no, pl.ss_max, 6.0);
+    if (pl.small) {
+        pl.sp = pa_split(units, workers, nb, pa_most(units, workers, nb), 6.0);
+    } else {
+        const double stage = (pl.own_rows == 64 ? 2.5 : 1.0) * (head_dim == 64 ? 0.2 : 0.4);
+        pl.sp = pa_tile_split(units, nb, pa_most(units, workers, nb), sms, pl.pair, head_dim == 64 ? 1.05 : 0.84,
+                              max_blocks > 0 ? (double)own * pl.ss * 0.6 + (double)own * no * stage : 0.0,
+                              (double)all * nkv * head_dim * 4 / 3e6);
+    }
+    // (up to 64 rows a narrower prefix may go to the other kernel: one bound for both)
+    pl.sp_max = all <= 64 ? pa_most(nkv, 4 * (int64_t)sms, (prefix_blocks + kPrPages - 1) / kPrPages) : pa_most(units, workers, nb);
     return pl;
 }
 
