@@ -479,7 +479,7 @@ const char *rope_kv_append_unsupported(const void *q, int64_t q_token_stride, in
  *                0 .. 16 prefix_blocks.  Both may be NULL when prefix_blocks is 0.
  *   block_table  [num_reqs, max_blocks] int32: the same for each request's own
  *                keys (NULL when max_blocks is 0); entries past a length are
- *                not read.
+ *                not used, whatever they hold.
  *   context_lens [num_reqs] int32: L_r, the request's own keys, the step's
  *                q_len tokens among them (0 .. 16 max_blocks; shorter than
  *                q_len leaves the first rows with the prefix alone).  Negative:

@@ -144,10 +144,11 @@ __device__ __forceinline__ PaItem pa_prefix_item(const PrefixParams &p, int P, i
     return it;
 }
 
-// Keys that some row of a request's tile sees: its last token's
+// Keys that some row of a request's tile sees: its last token's (none of a
+// padding request's: its length, any negative number, enters no sum)
 __device__ __forceinline__ int pa_own_keys(const PrefixParams &p, int L, int tile)
 {
-    if (L > p.max_blocks * kPageSlots) return 0;
+    if (L < 0 || L > p.max_blocks * kPageSlots) return 0;
     const int last = min(p.q_len - 1, (tile * p.own_rows + p.own_rows - 1) / p.group);
     return max(0, L - p.q_len + last + 1);
 }
@@ -1118,7 +1119,7 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
         it.tok0 = r * p.q_len;
         it.row0 = tile * RTO;
         it.rows = min(RTO, p.q_len * p.group - it.row0);
-        it.limit0 = L - p.q_len + 1;
+        it.limit0 = max(L, 0) - p.q_len + 1;
         it.step = 1;
         it.split = p.sp + split;
         pa_deal(it, (it.keys + kPrKeys - 1) / kPrKeys, p.ss, split);
@@ -1442,7 +1443,7 @@ const char *check_prefix_args(const void *q, int64_t q_ts, int64_t q_hs, const v
     if (!stride_ok(q_ts) || !stride_ok(q_hs) || q_ts % 8 || q_hs % 8)
         return "q's strides must be multiples of 8 elements, 0..2^36";
     *code = QKVF_ERR_SIZES;
-    if (num_pages < 1 || num_pages * num_kv_heads > (int64_t(1) << 31)) return "num_pages * num_kv_heads must be 1..2^31";
+    if (num_pages < 1 || num_pages > (int64_t(1) << 31) / num_kv_heads) return "num_pages * num_kv_heads must be 1..2^31";
     *code = QKVF_ERR_ARG;
     if (!(scale > 0.f) || !(scale <= 1e6f)) return "scale must be in (0, 1e6]";
     *code = QKVF_OK;

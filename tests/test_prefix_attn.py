@@ -60,6 +60,11 @@ def test_refusals(lib):
         assert call(lib, nb=0, pp=0, pl=0) in (5, 6) and call(lib, mb=0, bt=0) in (5, 6)
 
 
+def test_page_counts_past_64_bits(lib):
+    """num_pages * num_kv_heads is bounded without forming a product that wraps."""
+    assert call(lib, pages=1 << 62, nkv=4) == 7 and call(lib, pages=(1 << 63) - 1, nkv=8) == 7
+
+
 def test_binding_refusals():
     q = torch.zeros(4, 8, 64, dtype=BF)
     with pytest.raises(ValueError, match="CUDA"):
@@ -274,6 +279,18 @@ def test_bad_requests_are_skipped(dev):
         out, lse2 = attend(e, 2)
         assert qf.status() == qf.STATUS_BAD_REQUEST
         assert torch.all(out == 3.0) and torch.all(lse2 == 5.0), change
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L", [-1, -9, -(2 ** 31) + 3, -(2 ** 31)])
+def test_any_negative_length_is_padding(dev, L):
+    """Also where a request's rows are two tiles, whose first ends before the
+    request's last token: no sum with such a length may wrap."""
+    d = make(3, 10, 2, 8, 64, 100, [40, -1, 7], BF)
+    d["context_lens"][1] = L
+    out, lse = attend(d, 10)
+    check(d, 10, out, lse)
+    assert qf.status() == 0
 
 
 @pytest.mark.gpu
