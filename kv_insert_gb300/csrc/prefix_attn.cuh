@@ -14,7 +14,7 @@ constexpr int kPaMaxGroup = 64;          // q heads per KV head
 constexpr int kPaTile = 128;             // query rows of one tcgen05.mma tile
 constexpr int kPaThreads = 384;          // 2 softmax groups of 4 warps, 2 producer warps, 2 MMA warps
 constexpr float kPaMost = 16384.f;       // a row's weights of a block may add up to this before its maximum follows
-constexpr int kPaMaxSplits = 64;         // key splits of a tile, prefix and own keys each
+constexpr int kPaMaxSplits = 128;        // key splits of a tile, prefix and own keys each
 
 // Shapes by head width: a block of keys is one ring stage (K and V, 32 KB)
 // and one S tile; each of the two rings holds `slots` of them.
@@ -1144,13 +1144,14 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
 // partials' O are loaded side by side, before it is known which of the slots
 // hold keys (the others' contents are not used).  Sums in a fixed order: the
 // same bits every time.
-constexpr int kPaMergeThreads = 128;
 constexpr int kPaMergeAhead = 6;   // partials in flight per lane
 
+__host__ __device__ constexpr int pa_merge_threads(int warps) { return warps > 4 ? 32 * warps : 128; }
+
 template <class E, int D, int kWarps>
-__global__ void __launch_bounds__(kPaMergeThreads) prefix_merge_kernel(const __grid_constant__ PrefixParams p)
+__global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(const __grid_constant__ PrefixParams p)
 {
-    constexpr int LPR = D / 4, PAR = kWarps * 32 / LPR, kRows = kPaMergeThreads / (32 * kWarps);
+    constexpr int LPR = D / 4, PAR = kWarps * 32 / LPR, kRows = pa_merge_threads(kWarps) / (32 * kWarps);
     __shared__ float weight[kRows][2 * kPaMaxSplits];
     __shared__ float4 part[kRows][kWarps][32];
     if (threadIdx.x == 0) griddep_launch_dependents();
@@ -1158,7 +1159,7 @@ __global__ void __launch_bounds__(kPaMergeThreads) prefix_merge_kernel(const __g
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rl = warp / kWarps, wr = warp % kWarps;   // the row of the CTA, the warp of the row
     const int row = blockIdx.x * kRows + rl;
-    if (kWarps == 1 && row >= p.rows) return;   // (with 4 warps the CTA is one row)
+    if (kWarps == 1 && row >= p.rows) return;   // (with more warps the CTA is one row)
     const int t = row / p.q_heads, h = row - t * p.q_heads, r = t / p.q_len;
     const int slots = p.sp + p.ss;
     const float2 *ml = p.ws_ml + (int64_t)row * slots;
@@ -1186,22 +1187,24 @@ __global__ void __launch_bounds__(kPaMergeThreads) prefix_merge_kernel(const __g
     float M = -INFINITY;
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i) {
-        if (!holds(lane + 32 * i)) v[i] = make_float2(-INFINITY, 0.f);
-        M = fmaxf(M, v[i].x);
-        bad |= v[i].y < 0.f;
-    }
+    for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i)
+        if (32 * i < slots) {
+            if (!holds(lane + 32 * i)) v[i] = make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, v[i].x);
+            bad |= v[i].y < 0.f;
+        }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     if (__any_sync(0xffffffffu, bad)) return;   // a page outside the cache
     const float base = M == -INFINITY ? 0.f : M;
     float l = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i) {
-        const float f = exp2f(v[i].x - base);
-        if (wr == 0) weight[rl][lane + 32 * i] = f;
-        l = fmaf(v[i].y, f, l);
-    }
+    for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i)
+        if (32 * i < slots) {
+            const float f = exp2f(v[i].x - base);
+            if (wr == 0) weight[rl][lane + 32 * i] = f;
+            l = fmaf(v[i].y, f, l);
+        }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
     if (kWarps == 1)
@@ -1272,6 +1275,28 @@ int pa_split(int64_t units, int64_t workers, int64_t blocks, int most, double ov
     return best;
 }
 
+// The same where `others` CTAs of other_blocks steps follow in the grid: they
+// run on the workers that the prefix's last wave leaves, and behind it.  (8
+// rows against 8 heads of 64 and 128K keys: 45.5 us; 54.5 with the prefix alone
+// dealt to all workers and the own keys' 8 CTAs in a wave of their own.)
+int pa_rows_split(int64_t units, int64_t workers, int64_t blocks, int most, int64_t others, int64_t other_blocks)
+{
+    int best = 1;
+    double least = 1e300;
+    const double over = 6.0, other = (double)other_blocks + over;
+    for (int s = 1; s <= most; ++s) {
+        const int64_t n = units * s, waves = (n + workers - 1) / workers;
+        const double each = (double)((blocks + s - 1) / s) + over;
+        const int64_t left = others - (int64_t)((double)(waves * workers - n) * (each < other ? 1.0 : each / other));
+        const double cost = (double)waves * each + (left > 0 ? (double)((left + workers - 1) / workers) * other : 0.0);
+        if (cost < least * 0.999) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 int pa_most(int64_t units, int64_t workers, int64_t blocks)
 {
     int64_t most = (2 * workers + units - 1) / units;
@@ -1282,9 +1307,9 @@ int pa_most(int64_t units, int64_t workers, int64_t blocks)
 
 // The tile kernel's split: its steps of `step` us each, the own keys' work
 // (`rest`, SM microseconds) on the SMs it leaves free meanwhile and behind it,
-// and `merge` us a split to join.  With 64 rows x 8 KV heads over 32K and up to
-// 1K own keys each, 9 splits (144 CTAs) take 60.8 us and 7 (112) 59.7 to 61.4; with 33
-// rows x 4 KV heads of 128 over 16K, 38 splits 30.5 and 18 26.1.
+// and `merge` us a split to write and join.  With 64 rows x 8 KV heads over 32K
+// and up to 1K own keys each, 9 splits (144 CTAs) take 60.8 us and 7 (112) 59.7
+// to 61.4; with 33 rows x 4 KV heads of 128 over 16K, 38 splits 30.5 and 18 26.1.
 int pa_tile_split(int64_t units, int64_t blocks, int most, int sms, bool pair, double step, double rest, double merge)
 {
     int best = 1;
@@ -1309,9 +1334,13 @@ PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int 
     const int64_t all = (int64_t)num_reqs * q_len * group;   // rows of a KV head
     PaPlan pl;
     // The rows kernel takes the prefix too while its tensor work hides behind
-    // the loads: 32 rows against 8 x 32K keys of 64 23.5 us, 24.8 in the tile
-    // kernel; 64 rows 11.9 against 14.2 over 4K keys, but 28.6 against 26.0 over 32K.
-    pl.small = all <= 32 || (all <= 64 && prefix_blocks <= 1024);
+    // the tile kernel's start: up to 4 MB of it a KV head and 32 MB in all, or
+    // with one fragment of 16 rows at any length (there 14 us over 128K keys of
+    // one head, and 18 in the tile kernel).  32 rows against 8 heads of 64: 6.3
+    // us over 2K keys and 15.9 over 16K (tile kernel 9.3 and 17.6), but 26.3
+    // over 32K and 44 over 64K (22 and 32).
+    const int64_t wide_blocks = (int64_t)prefix_blocks * (head_dim / 64);
+    pl.small = all <= 16 || (all <= 64 && wide_blocks <= 1024 && nkv * wide_blocks <= 8192);
     pl.pre_rows = all <= 16 ? 16 : 64;
     pl.tiles = (int)((all + kPaTile - 1) / kPaTile);
     pl.pair = !pl.small && pl.tiles > 1;
@@ -1327,12 +1356,13 @@ PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int 
     pl.ss_max = pa_most(own, ctas * sms, no);
     pl.ss = pa_split(own, ctas * sms, no, pl.ss_max, 6.0);
     if (pl.small) {
-        pl.sp = pa_split(units, workers, nb, pa_most(units, workers, nb), 6.0);
+        pl.sp = pa_rows_split(units, workers, nb, pa_most(units, workers, nb), max_blocks > 0 ? own * pl.ss : 0,
+                              (no + pl.ss - 1) / pl.ss);
     } else {
         const double stage = (pl.own_rows == 64 ? 2.5 : 1.0) * (head_dim == 64 ? 0.2 : 0.4);
         pl.sp = pa_tile_split(units, nb, pa_most(units, workers, nb), sms, pl.pair, head_dim == 64 ? 1.05 : 0.84,
                               max_blocks > 0 ? (double)own * pl.ss * 0.6 + (double)own * no * stage : 0.0,
-                              (double)all * nkv * head_dim * 4 / 3e6);
+                              (double)all * nkv * head_dim * 4 / 2e6);
     }
     // (up to 64 rows a narrower prefix may go to the other kernel: one bound for both)
     pl.sp_max = all <= 64 ? pa_most(nkv, 4 * (int64_t)sms, (prefix_blocks + kPrPages - 1) / kPrPages) : pa_most(units, workers, nb);
@@ -1402,11 +1432,22 @@ int launch_prefix(const CUtensorMap &map, const PrefixParams &prm, int sms, void
                         dim3((unsigned)items), dim3(kPrThreads), (size_t)PrShape<D>::smem, stream, map, prm);
         if (rc != QKVF_OK) return rc;
     }
-    // four warps a row where there are more partials than one warp has in flight
-    // and few rows (with 4096 rows of 128 and 10 partials one warp is faster)
-    if (prm.sp + prm.ss > kPaMergeAhead * 32 / (D / 4) && prm.rows <= 16 * sms)
-        return launch_pdl(prefix_merge_kernel<E, D, 4>, dim3((unsigned)prm.rows), dim3(kPaMergeThreads), 0, stream, prm);
-    return launch_pdl(prefix_merge_kernel<E, D, 1>, dim3((unsigned)((prm.rows + 3) / 4)), dim3(kPaMergeThreads), 0, stream, prm);
+    // Several warps a row where there are more partials than one warp has in
+    // flight and few rows: with 4096 rows of 128 and 10 partials one is faster;
+    // 8 rows of 64 with 128 partials of a 128K prefix take 14.3 us in all with
+    // sixteen, 17.5 with eight; 256 rows with 65 partials 16.8 and 14.8.
+    constexpr int ahead = kPaMergeAhead * 32 / (D / 4);   // a warp's
+    const int splits = prm.sp + prm.ss;
+    const int64_t rows = prm.rows;
+    const int warps = splits <= ahead || rows > 16 * sms          ? 1
+                      : splits <= 4 * ahead || rows > 4 * sms ? 4
+                      : rows > sms                            ? 8
+                                                              : 16;
+    return launch_pdl(warps == 1   ? prefix_merge_kernel<E, D, 1>
+                      : warps == 4 ? prefix_merge_kernel<E, D, 4>
+                      : warps == 8 ? prefix_merge_kernel<E, D, 8>
+                                   : prefix_merge_kernel<E, D, 16>,
+                      dim3((unsigned)(warps == 1 ? (rows + 3) / 4 : rows)), dim3(pa_merge_threads(warps)), 0, stream, prm);
 }
 
 const char *check_prefix_shape(int num_reqs, int q_len, int q_heads, int num_kv_heads, int head_dim,

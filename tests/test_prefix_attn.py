@@ -189,6 +189,20 @@ def test_values(dev, case, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    (1, 1, 1, 8, 64, 20000, [9]), (5, 1, 1, 8, 128, 20001, [17, 0, 3, -1, 40]), (21, 1, 1, 8, 64, 30007, [5] * 21),
+    (70, 1, 1, 8, 128, 20000, [1, 20] * 35), (1, 1, 1, 1, 64, 0, [9003]), (2, 3, 2, 1, 128, 33, [9000, 2]),
+], ids=lambda c: "-".join(map(str, c[:6])))
+def test_many_partials(dev, case):
+    """Long keys of few heads: up to 128 splits of either kind, joined by
+    several warps a row."""
+    d = make(*case, BF)
+    out, lse = attend(d, case[1])
+    check(d, case[1], out, lse)
+    assert qf.status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale,size", [(0.5, 1.0), (1e-3, 1.0), (0.125, 12.0), (4.0, 3.0)])
 def test_scales_and_large_scores(dev, scale, size):
     """Nearly uniform weights, and scores whose maximum grows key after key."""
