@@ -273,14 +273,29 @@ __device__ __forceinline__ void pa_load_scores(uint32_t addr, uint32_t *s)
     tmem_ld_wait();
 }
 template <int N>
-__device__ __forceinline__ void pa_load_scores(uint32_t addr, uint32_t *s, uint32_t addr2, uint32_t *s2)
+__device__ __forceinline__ void pa_issue_scores(uint32_t addr, uint32_t *s, uint32_t addr2, uint32_t *s2)
 {
 #pragma unroll
     for (int c = 0; c < N; c += 32) {
         pa_tmem_ld32(addr + c, s + c);
         pa_tmem_ld32(addr2 + c, s2 + c);
     }
+}
+template <int N>
+__device__ __forceinline__ void pa_load_scores(uint32_t addr, uint32_t *s, uint32_t addr2, uint32_t *s2)
+{
+    pa_issue_scores<N>(addr, s, addr2, s2);
     tmem_ld_wait();
+}
+
+// Behind the wait for a load: no use of its registers moves ahead of here
+template <int N>
+__device__ __forceinline__ void pa_loaded(uint32_t (&s)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 8)
+        asm volatile("" : "+r"(s[c]), "+r"(s[c + 1]), "+r"(s[c + 2]), "+r"(s[c + 3]), "+r"(s[c + 4]), "+r"(s[c + 5]),
+                     "+r"(s[c + 6]), "+r"(s[c + 7]));
 }
 
 // The scores from `limit` on become -infinity, whatever their slots hold
@@ -378,6 +393,10 @@ template <class E, int D>
 struct PaTile {
     using Sh = PaShape<D>;
     static constexpr int KB = Sh::keys, NS = Sh::slots, U = KB / 2;
+    // Each S is loaded before the weights ahead of it are handed over: 64 rows
+    // x 8 KV heads of 8 over 128K keys 129.6 us, and 135.4 without.  With blocks of
+    // 64 keys S would not be there yet: 8 heads of 128 over 32K 70.5 us, 62.5 without.
+    static constexpr bool kAhead = D == 64;
     static constexpr PaSmem LY = pa_smem<D>();
     const CUtensorMap *map;
     const PrefixParams &p;
@@ -594,75 +613,118 @@ struct PaTile {
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             mbar_arrive(sb + LY.qready + 8 * w);
-            float mu = -INFINITY, l = 0.f;
-            for (int j = 0; j < n; ++j, ++blk) {
+            // S of block j: the item's keys in it
+            const auto scores = [&](int j) {
                 wait(LY.sfull + 8 * w, blk);
                 __syncwarp();
                 tc_fence_after();
-                int keys = KB;   // of the block
+                int keys = KB;
                 if (j == n - 1 && it.keys < it.kb1 * KB) {
                     keys = it.keys - (it.kb1 - 1) * KB;
                     zero_tail(ring, keys, row);
                 }
                 ++ring.n;
-                const int outer = blk & 1;   // the half of the keys in the outer unit
-                const uint32_t aOut = aSP + 2 * outer * U, aMid = aSP + U;
-                const int left_out = keys - outer * U, left_mid = keys - (outer ^ 1) * U;
-                if (active) {
-                    uint32_t so[U], sm[U], po[U / 2], pm[U / 2];
-                    pa_load_scores<U>(aOut, so, aMid, sm);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sb + LY.sfree + 8 * w);
-                    if (keys < KB) {
-                        pa_hide(so, left_out);
-                        pa_hide(sm, left_mid);
-                    }
-                    // The weights against the maximum so far.  Later scores may exceed
-                    // it as long as a block's weights stay below 2^14 in sum (so no
-                    // maximum is taken per block); otherwise it follows and O is
-                    // rescaled.  (No maximum yet: the sum is not finite.)
-                    float base = -mu, sum;
-                    for (bool again = false;; again = true) {
-                        sum = pa_weights<E>(so, po, cc, base);
-                        sum += pa_weights<E>(sm, pm, cc, base);
-                        if (again || !__any_sync(0xffffffffu, !(sum < kPaMost))) break;
-                        pa_load_scores<U>(aOut, so);   // not overwritten yet
-                        if (keys < KB) pa_hide(so, left_out);
-                        // (only this row's own scores move it, not a neighbour's)
-                        const float top = pa_max(so, pa_max(sm, -INFINITY)) * p.scale_log2;
-                        const bool grew = top > mu && !(sum < kPaMost);
-                        const float al = grew ? a2_ex2(mu - top) : 1.f;
-                        if (grew) mu = top;
-                        base = mu == -INFINITY ? 0.f : -mu;
-                        l *= al;
-                        if (j > 0) {
-                            wait(LY.pvdone + 8 * w, blk - 1);
-                            __syncwarp();
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld_x16(aO + c, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                pa_tmem_st16(aO + c, o);
-                            }
-                        }
-                    }
-                    l += sum;
-                    pa_tmem_st<U / 2>(aOut + outer * (U / 2), po);
-                    pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pm);
-                } else if (lane == 0) {
-                    mbar_arrive(sb + LY.sfree + 8 * w);
-                }
-                if (active) pa_tmem_st_wait();
+                return keys;
+            };
+            const auto arrive = [&](uint32_t bar) {   // for this warp, which has left tensor memory
                 tc_fence_before();
                 __syncwarp();
-                // (two barriers in turn: this S says that the weights of the block
-                // two back have been multiplied, so that phase has been seen)
-                if (lane == 0) mbar_arrive(sb + LY.pready + 16 * outer + 8 * w);
+                if (lane == 0) mbar_arrive(sb + bar);
+            };
+            // (two barriers in turn: S of block b says that the weights of block
+            // b - 2 have been multiplied, so that phase has been seen)
+            const auto pready = [&](int b) { return LY.pready + 16 * (b & 1) + 8 * w; };
+            float mu = -INFINITY, l = 0.f;
+            uint32_t so[U], sm[U];
+            int keys = KB, outer = 0;   // of the block; the half of the keys in the outer unit
+            // The weights of block j, against the maximum so far.  Later scores
+            // may exceed it as long as a block's weights stay below 2^14 in sum
+            // (so no maximum is taken per block); otherwise it follows and O is
+            // rescaled.  (No maximum yet: the sum is not finite.)
+            const auto weigh = [&](int j) {
+                const uint32_t aOut = aSP + 2 * outer * U;
+                uint32_t po[U / 2], pm[U / 2];
+                if (keys < KB) {
+                    pa_hide(so, keys - outer * U);
+                    pa_hide(sm, keys - (outer ^ 1) * U);
+                }
+                float base = -mu, sum;
+                for (bool again = false;; again = true) {
+                    sum = pa_weights<E>(so, po, cc, base);
+                    sum += pa_weights<E>(sm, pm, cc, base);
+                    if (again || !__any_sync(0xffffffffu, !(sum < kPaMost))) break;
+                    pa_load_scores<U>(aOut, so);   // not overwritten yet
+                    pa_loaded(so);
+                    if (keys < KB) pa_hide(so, keys - outer * U);
+                    // (only this row's own scores move it, not a neighbour's)
+                    const float top = pa_max(so, pa_max(sm, -INFINITY)) * p.scale_log2;
+                    const bool grew = top > mu && !(sum < kPaMost);
+                    const float al = grew ? a2_ex2(mu - top) : 1.f;
+                    if (grew) mu = top;
+                    base = mu == -INFINITY ? 0.f : -mu;
+                    l *= al;
+                    if (j > 0) {
+                        wait(LY.pvdone + 8 * w, blk - 1);
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld_x16(aO + c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                            pa_tmem_st16(aO + c, o);
+                        }
+                    }
+                }
+                l += sum;
+                pa_tmem_st<U / 2>(aOut + outer * (U / 2), po);
+                pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pm);
+            };
+            const auto load = [&]() {
+                pa_issue_scores<U>(aSP + 2 * outer * U, so, aSP + U, sm);
+            };
+            const auto loaded = [&]() {
+                tmem_ld_wait();
+                pa_loaded(so);
+                pa_loaded(sm);
+                arrive(LY.sfree + 8 * w);
+            };
+            if (kAhead && active) {
+                keys = scores(0);
+                outer = blk & 1;
+                load();
+                loaded();
+                for (int j = 0;; ++j) {
+                    weigh(j);
+                    const uint32_t ready = pready(blk++);
+                    if (j == n - 1) {
+                        pa_tmem_st_wait();
+                        arrive(ready);
+                        break;
+                    }
+                    keys = scores(j + 1);
+                    outer ^= 1;
+                    load();   // on its way to registers while the weights land
+                    pa_tmem_st_wait();
+                    arrive(ready);
+                    loaded();
+                }
+            } else {
+                for (int j = 0; j < n; ++j, ++blk) {
+                    keys = scores(j);
+                    outer = blk & 1;
+                    if (active) {
+                        load();
+                        loaded();
+                        weigh(j);
+                        pa_tmem_st_wait();
+                    } else {
+                        arrive(LY.sfree + 8 * w);
+                    }
+                    arrive(pready(blk));
+                }
             }
             // (not on pvdone, whose last two phases may both be open)
             wait(LY.odone + 8 * w, items++);
