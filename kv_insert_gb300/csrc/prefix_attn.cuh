@@ -640,7 +640,7 @@ struct PaTile {
             // The weights of block j, against the maximum so far.  Later scores
             // may exceed it as long as a block's weights stay below 2^14 in sum
             // (so no maximum is taken per block); otherwise it follows and O is
-            // rescaled.  (No maximum yet: the sum is not finite.)
+            // rescaled.  An item's first block starts there.
             const auto weigh = [&](int j) {
                 const uint32_t aOut = aSP + 2 * outer * U;
                 uint32_t po[U / 2], pm[U / 2];
@@ -648,14 +648,16 @@ struct PaTile {
                     pa_hide(so, keys - outer * U);
                     pa_hide(sm, keys - (outer ^ 1) * U);
                 }
-                float base = -mu, sum;
+                float base = -mu, sum = INFINITY;
                 for (bool again = false;; again = true) {
-                    sum = pa_weights<E>(so, po, cc, base);
-                    sum += pa_weights<E>(sm, pm, cc, base);
-                    if (again || !__any_sync(0xffffffffu, !(sum < kPaMost))) break;
-                    pa_load_scores<U>(aOut, so);   // not overwritten yet
-                    pa_loaded(so);
-                    if (keys < KB) pa_hide(so, keys - outer * U);
+                    if (again || j > 0) {
+                        sum = pa_weights<E>(so, po, cc, base);
+                        sum += pa_weights<E>(sm, pm, cc, base);
+                        if (again || !__any_sync(0xffffffffu, !(sum < kPaMost))) break;
+                        pa_load_scores<U>(aOut, so);   // not overwritten yet
+                        pa_loaded(so);
+                        if (keys < KB) pa_hide(so, keys - outer * U);
+                    }
                     // (only this row's own scores move it, not a neighbour's)
                     const float top = pa_max(so, pa_max(sm, -INFINITY)) * p.scale_log2;
                     const bool grew = top > mu && !(sum < kPaMost);
