@@ -5,6 +5,36 @@
 // prefix's keys 0 .. P - 1 and to its request's own keys j <= L_r - q_len + i,
 // under one softmax:
 //   s = scale q . k;  out = sum exp(s - m) v / sum exp(s - m);  lse = ln sum exp(s).
+// Both key ranges are split; every split leaves a partial (m, sum exp(s - m),
+// sum exp(s - m) v) per row in the workspace, in FP32, and a merge joins them:
+//   out = sum_k e^(m_k - M) o_k / sum_k e^(m_k - M) l_k,  M = max_k m_k.
+//
+// Three kernels, the second and third PDL-launched behind the first:
+//  * prefix_tile_kernel: all requests' rows against the prefix in tiles of 128
+//    rows on tcgen05, one CTA per SM.  Two groups of four softmax warps (a
+//    thread per row), each group on its own tile, both on the same key blocks
+//    (one tile: on two halves of the keys); two producer warps (TMA, a
+//    swizzled box per page) and an MMA warp per group.  S = Q K^T goes to
+//    tensor memory, the weights back into S's columns as the A operand of
+//    O += P V, so neither passes through shared memory.
+//  * prefix_rows_kernel: each request's own keys, and a prefix that few rows
+//    share, in tiles of 16 or 64 rows with mma.sync, two to four CTAs per SM.
+//    Many short key lists want many small CTAs in flight; it starts beside the
+//    tile kernel on the SMs that one leaves (its split is chosen with that work
+//    in mind) and follows on all of them.
+//  * prefix_merge_kernel: a row's partials, 1 to 16 warps a row.
+//
+// What bounds it.  A prefix of many rows is a dense product: 512 rows x 8 KV
+// heads of 64 over 32K keys are 34 GFLOP, 17.8 us at the 1930 TFLOP/s measured
+// for bf16, with 10 us of bytes.  A step of the tile kernel (two tiles against
+// 128 keys) takes ~1830 clocks: 1024 of them are the least that its 32768
+// exponentials need (8 a clock and scheduler), 1050 the tensor pipe's work
+// beside them, and the rest the hand-overs between softmax and MMA warps
+// (160 - 275 clocks each), which the two groups' warps on a scheduler spend
+// at the same time.  64 x 64 heads of 64 over 128K keys run in 125.5 us (1100
+// TFLOP/s); the 32K call with up to 1K own keys per request in 58 us.  With few
+// rows the keys' bytes bound it: 8 rows x 8 KV heads of 128 over 128K keys take
+// 82.6 us, 80.3 at the copy rate.  Short calls are two launches: 5.8 us.
 
 namespace qkvf {
 

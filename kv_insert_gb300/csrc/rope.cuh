@@ -6,6 +6,13 @@
 // pairs being columns (2i, 2i + 1) (interleaved) or (i, i + rot / 2) (half) of
 // the head's first rot columns; the columns behind them are copied.  The
 // gradient of a rotation is the turn by -p f_i: the same kernel with s negated.
+//
+// Bound by bytes: 16384 tokens x 32 heads of 128 (bf16) take 41.4 us, the
+// copy rate; 4096 tokens of 8 KV heads of 64 into the cache 16.2 us (12.7 at
+// the copy rate); a table of 131072 x 128 13.2 us (10.0; its sines and cosines
+// are the rest); 4099 x 25 heads of 80 (fp16, 32 columns rotated) 8.3 us, of
+// which 5.0 are bytes and ~2.4 the launch's start and first loads, as in every
+// call of a few tokens.
 
 namespace qkvf {
 
@@ -186,6 +193,7 @@ struct RopeParams {
     float sign;      // -1: the gradient
     // the vector kernel's threads: unit u of a head group of a token
     int units, q_groups, groups, tokens;   // units of a head, head groups of q and of all, tokens of a grid row
+    int q_per, kv_per;                     // heads of a group
     uint32_t unit_m, unit_s, group_m, group_s;
 };
 
@@ -254,27 +262,28 @@ struct RopeHeads {
     int64_t src_step, dst_step;
     int h0, n;
     bool is_q, is_v;
-    __device__ __forceinline__ RopeHeads(const RopeParams &p, int64_t t, int grp, int kHeads)
+    __device__ __forceinline__ RopeHeads(const RopeParams &p, int64_t t, int grp, int q_per, int kv_per)
     {
-        int count = p.q_heads;
+        int count = p.q_heads, per = q_per;
         is_q = grp < p.q_groups;
         is_v = false;
-        h0 = grp * kHeads;
+        h0 = grp * per;
         src = static_cast<const S *>(p.q) + t * p.q_ts;
         dst = static_cast<S *>(p.out) + t * p.o_ts;
         src_step = p.q_hs;
         dst_step = p.o_hs;
         if (!is_q) {
-            const int kg = (p.nkv + kHeads - 1) / kHeads;
+            const int kg = (p.groups - p.q_groups) >> 1;
             is_v = grp >= p.q_groups + kg;
-            h0 = (grp - p.q_groups - (is_v ? kg : 0)) * kHeads;
+            per = kv_per;
+            h0 = (grp - p.q_groups - (is_v ? kg : 0)) * per;
             count = p.nkv;
             src = is_v ? static_cast<const S *>(p.v) + t * p.v_ts : static_cast<const S *>(p.k) + t * p.k_ts;
             src_step = is_v ? p.v_hs : p.k_hs;
             dst_step = (int64_t)kPageSlots * 2 * p.dim;
         }
         src += h0 * src_step;
-        n = min(kHeads, count - h0);
+        n = min(per, count - h0);
     }
     // Where the heads are written, once the token's indices are known; false: nowhere
     __device__ __forceinline__ bool place(const RopeParams &p, const RopeToken &tok)
@@ -300,7 +309,7 @@ union RopeChunk {
 // first half of its rotated columns with its partner in the second (half
 // pairs; the chunks behind the rotated columns are units of their own).
 template <class E, bool kHalf, int kHeads>
-__global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(256, 4) rope_vec_kernel(const __grid_constant__ RopeParams p)
 {
     using S = typename E::store;
     using Chunk = RopeChunk<E>;
@@ -316,7 +325,7 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ R
     const int half = p.rot >> 1;
     const bool rotated = kHalf ? (int)u < half / vec : (int)u * pairs < half;
     const int c0 = kHalf && !rotated ? half / vec + u : u;   // the unit's first chunk
-    RopeHeads<S> hd(p, t, grp, kHeads);
+    RopeHeads<S> hd(p, t, grp, p.q_per, p.kv_per);
     const S *src = hd.src + c0 * vec;
     Chunk x[kHeads], y[kHalf ? kHeads : 1];
 #pragma unroll
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(256) rope_staged_kernel(const __grid_constant_
     const int64_t t = (int64_t)blockIdx.y * p.tokens + tl;
     const bool mine = r < per && (int)tl < p.tokens && t < p.T;
     const int64_t pos = mine ? p.positions[t] : -1, slot = mine && p.nkv ? p.slots[t] : -1;
-    RopeHeads<S> hd(p, mine ? t : 0, mine ? grp : 0, kHeads);
+    RopeHeads<S> hd(p, mine ? t : 0, mine ? grp : 0, kHeads, kHeads);
     uint4 *rows = stage + r * kHeads * p.units + u;   // the group's heads, p.units chunks each
     if (mine) {
         uint4 x[kHeads];
@@ -544,7 +553,12 @@ dim3 rope_grid(RopeParams &prm, int units, int heads, int whole)
 {
     prm.units = units;
     prm.q_groups = (prm.q_heads + heads - 1) / heads;
-    prm.groups = prm.q_groups + 2 * ((prm.nkv + heads - 1) / heads);
+    const int kv_groups = (prm.nkv + heads - 1) / heads;
+    prm.groups = prm.q_groups + 2 * kv_groups;
+    // the vector kernel's, dealt evenly: 25 heads as 7, 7, 7, 4 rather than 8, 8,
+    // 8, 1 (4096 tokens of 9 heads of 128: 4.3 us, and 6.1 as 8 and 1)
+    prm.q_per = prm.q_groups ? (prm.q_heads + prm.q_groups - 1) / prm.q_groups : 0;
+    prm.kv_per = kv_groups ? (prm.nkv + kv_groups - 1) / kv_groups : 0;
     fast_div(prm.units, &prm.unit_m, &prm.unit_s);
     fast_div(prm.groups, &prm.group_m, &prm.group_s);
     const int64_t most = (int64_t(1) << 30) / ((int64_t)units * prm.groups);   // a grid row's tokens
