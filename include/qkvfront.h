@@ -66,7 +66,7 @@ extern "C" {
 #define QKVF_STATUS_BAD_POSITION 2u  /* a position outside [0, cos_sin_rows): its q/k heads and insert skipped */
 #define QKVF_STATUS_WAIT_TIMEOUT 4u  /* a bounded wait in the kernel gave up: outputs of that call are invalid */
 #define QKVF_STATUS_BAD_REQUEST 8u   /* attn2: a request with L < 8, L beyond its table, or a page outside the cache: its rows skipped;
-                                        prefix_attn: a length beyond its table or a page outside the cache: its rows skipped */
+                                        prefix_attn: a length beyond its table or a page outside the cache: rows skipped */
 
 /*
  * qkv_front: check the call, then launch the fused front.
@@ -489,9 +489,10 @@ const char *rope_kv_append_unsupported(const void *q, int64_t q_token_stride, in
  *   workspace    device memory, 256-byte aligned, prefix_attn_workspace_bytes
  *                bytes, overlapping no other argument, no initial contents
  *                needed; one workspace serves one stream at a time.
- * A request whose length is beyond its table, or whose table names a page
- * outside the cache, is skipped (its rows left as they were) and raises
- * QKVF_STATUS_BAD_REQUEST; a bad prefix does so for every request.  Cache
+ * A request whose length is beyond its table is skipped (its rows left as they
+ * were), and so are the rows that see a page outside the cache (with them other
+ * rows of that request, but of no other): QKVF_STATUS_BAD_REQUEST is raised.  A
+ * bad prefix does so for every request.  Cache
  * slots past a length are never used, whatever they hold.
  *   head_dim 64 or 128, q_heads 1..64 times num_kv_heads (1..64), q_len
  *   1..1024, num_reqs 0..65535, num_reqs q_len q_heads <= 2^24.

@@ -21,7 +21,8 @@
 //    share, in tiles of 16 or 64 rows with mma.sync, two to four CTAs per SM.
 //    Many short key lists want many small CTAs in flight; it starts beside the
 //    tile kernel on the SMs that one leaves (its split is chosen with that work
-//    in mind) and follows on all of them.
+//    in mind) and follows on all of them.  Long own keys of many rows a request
+//    take the tile kernel instead, one item a group.
 //  * prefix_merge_kernel: a row's partials, 1 to 16 warps a row.
 //
 // What bounds it.  A prefix of many rows is a dense product: 512 rows x 8 KV
@@ -122,6 +123,7 @@ struct PrefixParams {
     int tiles;        // 128-row tiles of a KV head's rows (the tile kernel)
     int pair;         // both groups of a CTA on one key stream
     int small, pre_rows;       // the prefix's rows are few: the rows kernel's, in a tile of pre_rows
+    int own_tile;              // the own keys are the tile kernel's too
     int own_rows, own_tiles;   // rows of one tile of a request's rows, tiles of a request
     int sp, ss;       // key splits of the prefix and of a request's own keys
     float scale_log2;
@@ -183,25 +185,54 @@ __device__ __forceinline__ int pa_own_keys(const PrefixParams &p, int L, int til
     return max(0, L - p.q_len + last + 1);
 }
 
-// The tile kernel's work in order: prefix items only.  pair: a CTA's two
-// groups take the same key blocks against the two tiles of a 256-row block (a
-// second tile that does not exist has rows <= 0); otherwise the only tile's
-// splits go to 2 gridDim.x groups.
-template <int D>
+// A request's own keys: tile `tile` of request r's rows of KV head g, split s
+template <int KB>
+__device__ __forceinline__ PaItem pa_own_item(const PrefixParams &p, int P, int L, int r, int tile, int g, int s)
+{
+    PaItem it;
+    it.pages = p.block_table + (size_t)r * p.max_blocks;
+    it.g = g;
+    it.tok0 = r * p.q_len;
+    it.row0 = tile * p.own_rows;
+    it.rows = min(p.own_rows, p.q_len * p.group - it.row0);
+    it.keys = P < 0 ? 0 : pa_own_keys(p, L, tile);
+    it.limit0 = max(L, 0) - p.q_len + 1;
+    it.step = 1;
+    it.split = p.sp + s;
+    pa_deal(it, (it.keys + KB - 1) / KB, p.ss, s);
+    return it;
+}
+
+// The tile kernel's work in order.  The prefix's, pair: a CTA's two groups take
+// the same key blocks against the two tiles of a 256-row block (a second tile
+// that does not exist has rows <= 0); otherwise the only tile's splits go to 2
+// gridDim.x groups.  The own keys': one item a group.
+template <int D, bool kOwn>
 struct PaWork {
     const PrefixParams &p;
     int P, w, idx, end, stride;
     __device__ __forceinline__ PaWork(const PrefixParams &prm, int prefix, int group) : p(prm), P(prefix), w(group)
     {
-        idx = p.pair ? blockIdx.x : 2 * blockIdx.x + w;
-        stride = p.pair ? gridDim.x : 2 * gridDim.x;
-        end = P > 0 ? (p.pair ? (p.tiles + 1) / 2 : 1) * p.nkv * p.sp : 0;
+        if (kOwn) {
+            idx = 2 * blockIdx.x + w;
+            stride = end = p.R * p.nkv * p.own_tiles * p.ss;
+        } else {
+            idx = p.pair ? blockIdx.x : 2 * blockIdx.x + w;
+            stride = p.pair ? gridDim.x : 2 * gridDim.x;
+            end = P > 0 ? (p.pair ? (p.tiles + 1) / 2 : 1) * p.nkv * p.sp : 0;
+        }
     }
     __device__ __forceinline__ bool next(PaItem &it)   // the next item with key blocks
     {
         for (; idx < end; idx += stride) {
-            const int rb = p.pair ? (p.tiles + 1) / 2 : 1, tile = p.pair ? 2 * (idx % rb) + w : 0, gs = idx / rb;
-            it = pa_prefix_item<PaShape<D>::keys>(p, P, kPaTile, tile, gs % p.nkv, gs / p.nkv);
+            if (kOwn) {
+                const int g = idx % p.nkv, rest = idx / p.nkv, r = rest % p.R, ts = rest / p.R;
+                const int L = __reduce_max_sync(0xffffffffu, p.context_lens[r]);
+                it = pa_own_item<PaShape<D>::keys>(p, P, L, r, ts % p.own_tiles, g, ts / p.own_tiles);
+            } else {
+                const int rb = p.pair ? (p.tiles + 1) / 2 : 1, tile = p.pair ? 2 * (idx % rb) + w : 0, gs = idx / rb;
+                it = pa_prefix_item<PaShape<D>::keys>(p, P, kPaTile, tile, gs % p.nkv, gs / p.nkv);
+            }
             if (it.kb1 > it.kb0) {
                 idx += stride;
                 return true;
@@ -419,9 +450,10 @@ __device__ __forceinline__ float pa_weights(const uint32_t (&s)[N], uint32_t (&p
 
 // The roles of the tile kernel's warps.  Every loop over items and blocks is
 // the same in each of them.
-template <class E, int D>
+template <class E, int D, bool kOwn>
 struct PaTile {
     using Sh = PaShape<D>;
+    using Work = PaWork<D, kOwn>;
     static constexpr int KB = Sh::keys, NS = Sh::slots, U = KB / 2;
     // Each S is loaded before the weights ahead of it are handed over: 64 rows
     // x 8 KV heads of 8 over 128K keys 129.6 us, and 135.4 without.  With blocks of
@@ -443,6 +475,9 @@ struct PaTile {
         pa_wait(sb + bar, (uint32_t)n & 1, flags(), p.wait_limit_ns);
     }
     __device__ __forceinline__ bool dead() const { return flags()[0] != 0; }
+    __device__ __forceinline__ int pair() const { return kOwn ? 0 : p.pair; }
+    // A page outside the cache, as producer w has flagged: of the prefix's it voids every row
+    __device__ __forceinline__ bool bad(int w) const { return kOwn ? flags()[1 + w] : flags()[1] | flags()[2]; }
     __device__ __forceinline__ int pages_from(const PaItem &it, int block) const   // of a block, with keys
     {
         return min(Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots - block * Sh::pages);
@@ -454,13 +489,13 @@ struct PaTile {
         if (lane == 0) tma_prefetch_map(map);
         PaItem it;
         int guess = -1, entry = 0;   // the first entries as of a full table
-        if (PaWork<D>(p, p.prefix_blocks * kPageSlots, w).next(it)) {
+        if (!kOwn && Work(p, p.prefix_blocks * kPageSlots, w).next(it)) {
             guess = it.kb0 * Sh::pages;
             if (guess + lane < p.prefix_blocks) entry = it.pages[guess + lane];
         }
-        PaWork<D> work(p, length(), w);
+        Work work(p, length(), w);
         bool ok = true;
-        PaRing<NS> ring(w, p.pair);
+        PaRing<NS> ring(w, pair());
         int mine = 0;   // steps loaded into this ring
         unsigned bad_any = 0u;
         while (ok && work.next(it)) {
@@ -477,7 +512,7 @@ struct PaTile {
                 }
                 if (__any_sync(0xffffffffu, bad)) {   // seen by the softmax before these keys' products are
                     bad_any = 1u;
-                    flags()[1] = 1;
+                    flags()[1 + w] = 1;
                     __syncwarp();
                 }
                 for (int b0 = c; b0 < min(c + 32, pg1); b0 += Sh::pages) {
@@ -512,9 +547,9 @@ struct PaTile {
     template <int W>
     __device__ __forceinline__ void multiply() const
     {
-        PaWork<D> work(p, length(), W);
+        Work work(p, length(), W);
         PaItem it;
-        PaRing<NS> ring(W, p.pair);
+        PaRing<NS> ring(W, pair());
         int items = 0, blk = 0;   // items and blocks of this group so far
         const uint64_t qd = pa_desc(sb + LY.q + W * Sh::q_bytes, 16, 1024);
         const uint64_t kd0 = pa_desc(sb + LY.ring, 16, Sh::nblk * 1024);
@@ -609,7 +644,7 @@ struct PaTile {
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
         const uint32_t aSP = Sh::tSP + w * 3 * U + lane_base, aO = Sh::tO + w * D + lane_base;
         uint8_t *sq = smem + LY.q + w * Sh::q_bytes;
-        {   // the first item's rows of q into L2
+        if (!kOwn) {   // the first item's rows of q into L2
             const int idx = p.pair ? blockIdx.x : 2 * blockIdx.x + w, rb = p.pair ? (p.tiles + 1) / 2 : 1;
             const int m = (p.pair ? 2 * (idx % rb) + w : 0) * kPaTile + row, tok = m / p.group;
             const char *q = reinterpret_cast<const char *>(static_cast<const uint16_t *>(p.q) + tok * p.q_ts +
@@ -617,9 +652,9 @@ struct PaTile {
             if (tok < p.R * p.q_len)
                 for (int c = 0; c < 2 * D; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c));
         }
-        PaWork<D> work(p, length(), w);
+        Work work(p, length(), w);
         PaItem it;
-        PaRing<NS> ring(w, p.pair);
+        PaRing<NS> ring(w, pair());
         int blk = 0, items = 0;
         const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
         while (work.next(it)) {
@@ -674,9 +709,12 @@ struct PaTile {
             const auto weigh = [&](int j) {
                 const uint32_t aOut = aSP + 2 * outer * U;
                 uint32_t po[U / 2], pm[U / 2];
-                if (keys < KB) {
-                    pa_hide(so, keys - outer * U);
-                    pa_hide(sm, keys - (outer ^ 1) * U);
+                int left = keys;   // keys of the block that the row sees
+                if (kOwn && valid) left = min(left, it.limit0 + it.step * tok - (it.kb0 + j) * KB);
+                const bool hide = kOwn ? __any_sync(0xffffffffu, left < KB) : left < KB;
+                if (hide) {
+                    pa_hide(so, left - outer * U);
+                    pa_hide(sm, left - (outer ^ 1) * U);
                 }
                 float base = -mu, sum = INFINITY;
                 for (bool again = false;; again = true) {
@@ -686,7 +724,7 @@ struct PaTile {
                         if (again || !__any_sync(0xffffffffu, !(sum < kPaMost))) break;
                         pa_load_scores<U>(aOut, so);   // not overwritten yet
                         pa_loaded(so);
-                        if (keys < KB) pa_hide(so, keys - outer * U);
+                        if (hide) pa_hide(so, left - outer * U);
                     }
                     // (only this row's own scores move it, not a neighbour's)
                     const float top = pa_max(so, pa_max(sm, -INFINITY)) * p.scale_log2;
@@ -776,7 +814,7 @@ struct PaTile {
                 }
                 tc_fence_before();
                 // a sum below zero: a page outside the cache, which voids every row
-                if (valid) __stcg(p.ws_ml + grow * (p.sp + p.ss) + it.split, make_float2(mu, flags()[1] ? -1.f : l));
+                if (valid) __stcg(p.ws_ml + grow * (p.sp + p.ss) + it.split, make_float2(mu, bad(w) ? -1.f : l));
             }
         }
     }
@@ -800,7 +838,7 @@ struct PaTile {
     }
 };
 
-template <class E, int D>
+template <class E, int D, bool kOwn>
 __global__ void __launch_bounds__(kPaThreads, 1)
     prefix_tile_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
 {
@@ -811,10 +849,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const uint32_t sb = smem_u32(smem);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
+    // The own keys' CTAs behind the prefix's: as in the rows kernel, every input
+    // is written, and only the grid as a whole must not end before that one.
+    const bool behind = kOwn && p.prefix_blocks > 0, last = blockIdx.x == gridDim.x - 1;
+    if (kOwn) {
+        if (threadIdx.x == 0) griddep_launch_dependents();
+        if (!behind) griddep_wait();
+        PaItem it;
+        const int P = pa_prefix_len(p);
+        const bool any = PaWork<D, kOwn>(p, P, 0).next(it) | PaWork<D, kOwn>(p, P, 1).next(it);
+        if (!any) {   // requests without keys
+            if (behind && last) griddep_wait();
+            return;
+        }
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * Sh::slots; ++i) {
             mbar_init(sb + LY.full + 8 * i, 1);
-            mbar_init(sb + LY.empty + 8 * i, p.pair ? 2 : 1);   // the groups that read the stage
+            mbar_init(sb + LY.empty + 8 * i, !kOwn && p.pair ? 2 : 1);   // the groups that read the stage
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(sb + LY.qready + 8 * w, 128);
@@ -826,8 +878,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             mbar_init(sb + LY.odone + 8 * w, 1);
             mbar_init(sb + LY.drain + 8 * w, 1);
         }
-        reinterpret_cast<volatile int *>(smem + LY.flags)[0] = 0;   // a wait gave up
-        reinterpret_cast<volatile int *>(smem + LY.flags)[1] = 0;   // a page outside the cache
+        // a wait gave up; a page outside the cache, by producer
+        for (int i = 0; i < 3; ++i) reinterpret_cast<volatile int *>(smem + LY.flags)[i] = 0;
         fence_barrier_init();
     }
     // all of tensor memory (one CTA per SM): it starts at column 0
@@ -835,11 +887,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    griddep_wait();   // every input comes from the kernels before this one
-    // released only now: the rows kernel behind this one reads the same inputs
-    // without a wait of its own
-    if (threadIdx.x == 0) griddep_launch_dependents();
-    const PaTile<E, D> tile{&tmKV, p, smem, sb, lane};
+    if (!kOwn) {
+        griddep_wait();   // every input comes from the kernels before this one
+        // released only now: the kernel behind this one reads the same inputs
+        // without a wait of its own
+        if (threadIdx.x == 0) griddep_launch_dependents();
+    }
+    const PaTile<E, D, kOwn> tile{&tmKV, p, smem, sb, lane};
     // a softmax thread holds a row's whole S: its groups take registers from the
     // other warpgroup (256 x 208 + 128 x 88 = 384 x 168, what the launch has)
     if (warp < 8) {
@@ -858,6 +912,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 0) a2_tmem_dealloc<Sh::cols>(0u);
+    if (behind && last) griddep_wait();
 }
 
 // ---- few rows: mma.sync over small CTAs ------------------------------------
@@ -1205,21 +1260,7 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
     int first_entry = 0;
     if (warp == 4 && split == 0 && lane < (own ? p.max_blocks : p.prefix_blocks)) first_entry = pages[lane];
     const int P = pa_prefix_len(p), L = own ? p.context_lens[r] : 0;
-    PaItem it;
-    if (own) {
-        it.pages = pages;
-        it.g = g;
-        it.keys = P < 0 ? 0 : pa_own_keys(p, L, tile);
-        it.tok0 = r * p.q_len;
-        it.row0 = tile * RTO;
-        it.rows = min(RTO, p.q_len * p.group - it.row0);
-        it.limit0 = max(L, 0) - p.q_len + 1;
-        it.step = 1;
-        it.split = p.sp + split;
-        pa_deal(it, (it.keys + kPrKeys - 1) / kPrKeys, p.ss, split);
-    } else {
-        it = pa_prefix_item<kPrKeys>(p, max(P, 0), RTP, 0, g, split);
-    }
+    const PaItem it = own ? pa_own_item<kPrKeys>(p, P, L, r, tile, g, split) : pa_prefix_item<kPrKeys>(p, max(P, 0), RTP, 0, g, split);
     if (it.kb1 > it.kb0) {
         if constexpr (RTP == RTO) {
             pr_item<E, D, RTO>(tmKV, p, it, first_entry, smem);
@@ -1276,7 +1317,8 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
     }
     const int own = pa_own_keys(p, L, ((t - r * p.q_len) * p.group + h % p.group) / p.own_rows);
     const int pkeys = p.small ? kPrKeys : PaShape<D>::keys;
-    const int np = min(p.sp, (P + pkeys - 1) / pkeys), no = p.sp + min(p.ss, (own + kPrKeys - 1) / kPrKeys);
+    const int okeys = p.own_tile ? PaShape<D>::keys : kPrKeys;
+    const int np = min(p.sp, (P + pkeys - 1) / pkeys), no = p.sp + min(p.ss, (own + okeys - 1) / okeys);
     const auto holds = [&](int s) { return s < np || (s >= p.sp && s < no); };
     float M = -INFINITY;
     bool bad = false;
@@ -1349,7 +1391,7 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
 // ---- host: splits, workspace, launch ---------------------------------------
 
 struct PaPlan {
-    int small, pre_rows, tiles, pair, own_rows, own_tiles, sp, ss, sp_max, ss_max;
+    int small, pre_rows, tiles, pair, own_tile, own_rows, own_tiles, sp, ss, sp_max, ss_max;
 };
 
 // The split (1..most) that ends soonest when `units` row tiles times the
@@ -1438,24 +1480,40 @@ PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_dim, int 
     pl.pre_rows = all <= 16 ? 16 : 64;
     pl.tiles = (int)((all + kPaTile - 1) / kPaTile);
     pl.pair = !pl.small && pl.tiles > 1;
-    pl.own_rows = q_len * group <= 16 ? 16 : 64;
+    // A request's own keys go to the tile kernel from more than half a tile of
+    // rows and 512 keys on: 16 requests x 16 tokens x 64 heads of 64 over 4K keys and up to
+    // 256 own 42.5 us in the rows kernel and 46.6 here, 1024 own 54.4 and 50.9,
+    // 4096 own 90 and 65; one request of 512 tokens over 8192 keys 281 and 107.
+    // Half a tile (8 tokens of 8 heads): 33 and 37 at 1024, 52 and 49 at 4096.
+    const bool many = all > 64 && q_len * group > 64;
+    pl.own_tile = many && max_blocks > 32;
+    pl.own_rows = pl.own_tile ? kPaTile : q_len * group <= 16 ? 16 : 64;
     pl.own_tiles = (q_len * group + pl.own_rows - 1) / pl.own_rows;
     const bool wide = pl.own_rows == 64 || (pl.small && pl.pre_rows == 64);
     const int ctas = wide ? (head_dim == 64 ? 3 : 2) : (head_dim == 64 ? 4 : 3);   // of the rows kernel, per SM
-    const int keys = pl.small ? kPrKeys : head_dim == 64 ? PaShape<64>::keys : PaShape<128>::keys, ppb = keys / kPageSlots;
-    const int64_t nb = (prefix_blocks + ppb - 1) / ppb, no = (max_blocks + kPrPages - 1) / kPrPages;
+    const int tile_pages = (head_dim == 64 ? PaShape<64>::keys : PaShape<128>::keys) / kPageSlots;
+    const int ppb = pl.small ? kPrPages : tile_pages, opb = pl.own_tile ? tile_pages : kPrPages;   // pages of a block
+    const int64_t nb = (prefix_blocks + ppb - 1) / ppb, no = (max_blocks + opb - 1) / opb;
     const int64_t units = (int64_t)(pl.pair ? (pl.tiles + 1) / 2 : 1) * nkv;
     const int64_t workers = pl.small ? ctas * sms : pl.pair ? sms : 2 * sms;
-    const int64_t own = (int64_t)num_reqs * nkv * pl.own_tiles;
-    pl.ss_max = pa_most(own, ctas * sms, no);
-    pl.ss = pa_split(own, ctas * sms, no, pl.ss_max, 6.0);
+    const int64_t own = (int64_t)num_reqs * nkv * pl.own_tiles, own_workers = pl.own_tile ? 2 * sms : ctas * sms;
+    const int ss_most = pa_most(own, own_workers, no);
+    pl.ss = pa_split(own, own_workers, no, ss_most, 6.0);
+    pl.ss_max = ss_most;
+    if (pl.own_tile) {   // (a narrower table may go to the rows kernel: one bound for both)
+        const int64_t small = (int64_t)num_reqs * nkv * ((q_len * group + 63) / 64);
+        const int m = pa_most(small, (head_dim == 64 ? 3 : 2) * (int64_t)sms, (max_blocks + kPrPages - 1) / kPrPages);
+        if (m > pl.ss_max) pl.ss_max = m;
+    }
     if (pl.small) {
         pl.sp = pa_rows_split(units, workers, nb, pa_most(units, workers, nb), max_blocks > 0 ? own * pl.ss : 0,
                               (no + pl.ss - 1) / pl.ss);
     } else {
-        const double stage = (pl.own_rows == 64 ? 2.5 : 1.0) * (head_dim == 64 ? 0.2 : 0.4);
+        // an item's start and its blocks; two of the tile kernel's run side by side
+        const double start = pl.own_tile ? 2.0 : 0.6;
+        const double stage = pl.own_tile ? 0.3 : (pl.own_rows == 64 ? 2.5 : 1.0) * (head_dim == 64 ? 0.2 : 0.4);
         pl.sp = pa_tile_split(units, nb, pa_most(units, workers, nb), sms, pl.pair, head_dim == 64 ? 1.05 : 0.84,
-                              max_blocks > 0 ? (double)own * pl.ss * 0.6 + (double)own * no * stage : 0.0,
+                              max_blocks > 0 ? (double)own * pl.ss * start + (double)own * no * stage : 0.0,
                               (double)all * nkv * head_dim * 4 / 2e6);
     }
     // (up to 64 rows a narrower prefix may go to the other kernel: one bound for both)
@@ -1475,7 +1533,8 @@ bool prepare_prefix_kernel()
 {
     static_assert(pa_smem<D>().total <= (uint32_t)kMaxSmemPerCta, "shared memory");
     constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    return cudaFuncSetAttribute((const void *)prefix_tile_kernel<E, D>, attr, (int)pa_smem<D>().total) == cudaSuccess &&
+    return cudaFuncSetAttribute((const void *)prefix_tile_kernel<E, D, false>, attr, (int)pa_smem<D>().total) == cudaSuccess &&
+           cudaFuncSetAttribute((const void *)prefix_tile_kernel<E, D, true>, attr, (int)pa_smem<D>().total) == cudaSuccess &&
            cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 16, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
            cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 64, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
            cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 64, 64>, attr, (int)PrShape<D>::smem) == cudaSuccess;
@@ -1513,13 +1572,17 @@ int launch_prefix(const CUtensorMap &map, const PrefixParams &prm, int sms, void
         int64_t grid = (int64_t)prm.nkv * prm.sp;
         grid = prm.pair ? grid * ((prm.tiles + 1) / 2) : (grid + 1) / 2;
         if (grid > sms) grid = sms;
-        rc = launch_pdl(prefix_tile_kernel<E, D>, dim3((unsigned)grid), dim3(kPaThreads), (size_t)pa_smem<D>().total,
+        rc = launch_pdl(prefix_tile_kernel<E, D, false>, dim3((unsigned)grid), dim3(kPaThreads), (size_t)pa_smem<D>().total,
                         stream, map, prm);
         if (rc != QKVF_OK) return rc;
     }
     const int64_t items = (prm.small && prm.prefix_blocks > 0 ? (int64_t)prm.nkv * prm.sp : 0) +
                           (prm.max_blocks > 0 ? (int64_t)prm.R * prm.nkv * prm.own_tiles * prm.ss : 0);
-    if (items > 0) {
+    if (items > 0 && prm.own_tile) {
+        rc = launch_pdl(prefix_tile_kernel<E, D, true>, dim3((unsigned)((items + 1) / 2)), dim3(kPaThreads),
+                        (size_t)pa_smem<D>().total, stream, map, prm);
+        if (rc != QKVF_OK) return rc;
+    } else if (items > 0) {
         rc = launch_pdl(prm.own_rows == 64                       ? prefix_rows_kernel<E, D, 64, 64>
                         : prm.small && prm.pre_rows == 64 ? prefix_rows_kernel<E, D, 64, 16>
                                                           : prefix_rows_kernel<E, D, 16, 16>,
@@ -1691,6 +1754,7 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     prm.tiles = pl.tiles;
     prm.small = pl.small;
     prm.pre_rows = pl.pre_rows;
+    prm.own_tile = pl.own_tile;
     prm.own_rows = pl.own_rows;
     prm.own_tiles = pl.own_tiles;
     prm.sp = pl.sp;

@@ -308,6 +308,38 @@ def test_any_negative_length_is_padding(dev, L):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("case", [
+    (3, 20, 2, 5, 64, 130, [700, -1, 12]), (2, 9, 1, 16, 128, 0, [1030, 600]), (5, 33, 2, 4, 128, 70, [520, 0, 33, 32, 1]),
+    (1, 300, 1, 3, 64, 2000, [5000]), (2, 130, 4, 2, 64, 16, [131, 2000]), (3, 17, 1, 64, 64, 0, [513, 17, 1024]),
+], ids=lambda c: "-".join(map(str, c[:6])))
+def test_many_own_rows(dev, case, dtype):
+    """Long own keys of many rows a request: tiles of 128 rows whose tokens see
+    one key more each, with and without a prefix."""
+    d = make(*case, dtype)
+    out, lse = attend(d, case[1])
+    check(d, case[1], out, lse)
+    assert qf.status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [0, 200])
+def test_a_bad_page_voids_its_request_alone(dev, P):
+    """Neighbouring requests share a block of threads there."""
+    d = make(4, 20, 2, 5, 64, P, [700, 640, 530, 20], BF)
+    good, good_lse = attend(d, 20)
+    check(d, 20, good, good_lse)
+    assert qf.status() == 0
+    d["block_table"][2, 3] = -5
+    out, lse = attend(d, 20)
+    assert qf.status() == 8
+    keep = torch.ones(80, dtype=torch.bool, device=out.device)
+    keep[40:60] = False
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], good_lse[keep])
+    assert torch.all(out[40:60] == 3.0) and torch.all(lse[40:60] == 5.0)
+
+
+@pytest.mark.gpu
 def test_workspace_bounds(dev):
     d = make(3, 1, 1, 8, 64, 1500, [3, 40, 100], BF, seed=6)
     n = qf.prefix_attn_workspace_bytes(3, 1, 8, 1, 64, d["prefix_pages"].shape[0], d["block_table"].shape[1])
