@@ -424,6 +424,52 @@ def test_streams_graphs_and_a_shared_workspace(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,q_len,nkv,G,D,P,own", [
+    (4, 20, 2, 5, 64, 130, 600), (70, 1, 2, 4, 128, 900, 200), (2, 1, 2, 8, 64, 500, 300), (3, 40, 1, 4, 128, 0, 700),
+])
+def test_calls_follow_the_kernels_before_them(dev, R, q_len, nkv, G, D, P, own):
+    """Launched right behind the append that writes their keys, on one stream
+    and on two at once, calls give the bits of calls with a device
+    synchronization in between: no kernel starts on keys not yet written."""
+    g = torch.Generator().manual_seed(17)
+    d = make(R, q_len, nkv, G, D, P, [own + r % 3 for r in range(R)], BF, fill=0.0)
+    steps, T = 6, R * q_len
+    table = qf.rope_table(4096, D)
+    new = [torch.randn(2, T, nkv, D, generator=g).to(BF).to(dev) for _ in range(steps)]
+    qs = [torch.randn(T, nkv * G, D, generator=g).to(BF).to(dev) for _ in range(steps)]
+    pos = torch.tensor([own + r % 3 - q_len + i for r in range(R) for i in range(q_len)], device=dev)
+    req = torch.arange(R, device=dev).repeat_interleave(q_len)
+    slots = d["block_table"][req, pos // 16].long() * 16 + pos % 16
+
+    def run(sync, e):
+        ws = workspace(d["q"], d["kv_cache"], d["prefix_pages"], d["block_table"], q_len)
+        outs = [(torch.zeros_like(q), torch.zeros(T, nkv * G, device=dev)) for q in qs]
+        turned = [torch.zeros_like(q) for q in qs]
+        for (k, v), q, t, (out, lse) in zip(new, qs, turned, outs):   # nothing else is launched in between
+            qf.rope_kv_append(q, k, v, pos, slots, table, e["kv_cache"], q_out=t)
+            if sync:
+                torch.cuda.synchronize()
+            qf.prefix_attn(t, e["kv_cache"], e["prefix_pages"], e["prefix_len"], e["block_table"], e["context_lens"],
+                           ws, q_len=q_len, out=out, lse=lse)
+            if sync:
+                torch.cuda.synchronize()
+        return outs
+    want = run(True, {n: t.clone() for n, t in d.items()})
+    torch.cuda.synchronize()
+    copies = [{n: t.clone() for n, t in d.items()} for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for s, e in zip((torch.cuda.Stream(), torch.cuda.Stream()), copies):
+        with torch.cuda.stream(s):
+            got.append(run(False, e))
+    torch.cuda.synchronize()
+    for outs in got + [run(False, {n: t.clone() for n, t in d.items()})]:
+        for a, b in zip(outs, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert qf.status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("layout,D,rot,dtype", [("interleaved", 64, 64, BF), ("half", 128, 96, HF)])
 def test_serving_chain(dev, layout, D, rot, dtype):
     """As a serving program runs them: a scaled table; the prefix's tokens
