@@ -1295,7 +1295,7 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
     const int rl = warp / kWarps, wr = warp % kWarps;   // the row of the CTA, the warp of the row
     const int row = blockIdx.x * kRows + rl;
     if (kWarps == 1 && row >= p.rows) return;   // (with more warps the CTA is one row)
-    const int t = row / p.q_heads, h = row - t * p.q_heads, r = t / p.q_len;
+    const int t = row / p.q_heads, h = row - t * p.q_heads, r = p.q_len == 1 ? t : t / p.q_len;
     const int slots = p.sp + p.ss;
     const float2 *ml = p.ws_ml + (int64_t)row * slots;
     const int first = wr * (32 / LPR) + lane / LPR, d = lane % LPR;   // this lane's first slot, its 4 columns
@@ -1315,7 +1315,7 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
         if (lane == 0 && wr == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
         return;
     }
-    const int own = pa_own_keys(p, L, ((t - r * p.q_len) * p.group + h % p.group) / p.own_rows);
+    const int own = pa_own_keys(p, L, p.own_tiles == 1 ? 0 : ((t - r * p.q_len) * p.group + h % p.group) / p.own_rows);
     const int pkeys = p.small ? kPrKeys : PaShape<D>::keys;
     const int okeys = p.own_tile ? PaShape<D>::keys : kPrKeys;
     const int np = min(p.sp, (P + pkeys - 1) / pkeys), no = p.sp + min(p.ss, (own + okeys - 1) / okeys);
