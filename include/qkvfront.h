@@ -520,6 +520,17 @@ const char *prefix_attn_unsupported(const void *q, int64_t q_token_stride, int64
 size_t prefix_attn_workspace_bytes(int num_reqs, int q_len, int q_heads, int num_kv_heads, int head_dim,
                                    int prefix_blocks, int max_blocks);
 
+/*
+ * Packed calls: the same four calls with their arguments up to the stream as an
+ * array of 64-bit words, in order (pointers and integers as they are, floats
+ * and doubles as a double's bits), for bindings that pay per argument.  An
+ * integer that does not fit its parameter is refused with QKVF_ERR_SIZES.
+ */
+int rope_table_packed(const int64_t *args, void *stream);       /* 11 words */
+int rope_packed(const int64_t *args, void *stream);             /* 16 words */
+int rope_kv_append_packed(const int64_t *args, void *stream);   /* 25 words */
+int prefix_attn_packed(const int64_t *args, void *stream);      /* 22 words */
+
 
 /* Static text of a QKVF_* return code. */
 const char *qkv_front_strerror(int code);

@@ -1770,4 +1770,16 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
                           : qkvf::launch_prefix<qkvf::Fp16, 128>(map, prm, d->sms, stream);
 }
 
+int prefix_attn_packed(const int64_t *args, void *stream)
+{
+    if (!args) return QKVF_ERR_NULL;
+    qkvf::Words w(args);
+    const int prefix_blocks = w.i(6), max_blocks = w.i(9), R = w.i(11), q_len = w.i(12), q_heads = w.i(13), nkv = w.i(14),
+              dim = w.i(15), dtype = w.i(17);
+    if (!w.ok) return QKVF_ERR_SIZES;
+    return prefix_attn(w.p<void>(0), args[1], args[2], w.p<void>(3), args[4], w.p<int32_t>(5), prefix_blocks, w.p<int32_t>(7),
+                       w.p<int32_t>(8), max_blocks, w.p<int32_t>(10), R, q_len, q_heads, nkv, dim, (float)w.d(16), dtype,
+                       w.p<void>(18), w.p<float>(19), w.p<void>(20), (size_t)args[21], stream);
+}
+
 }  // extern "C"

@@ -607,6 +607,26 @@ int launch_rope(RopeParams &prm, bool half_layout, int sms, void *stream)
                       (int)half_layout);
 }
 
+// A packed call's arguments, one 64-bit word each
+struct Words {
+    const int64_t *a;
+    bool ok;   // every int so far fits one
+    explicit Words(const int64_t *words) : a(words), ok(true) {}
+    int i(int k)
+    {
+        ok &= a[k] == (int64_t)(int)a[k];
+        return (int)a[k];
+    }
+    double d(int k) const
+    {
+        double v;
+        memcpy(&v, a + k, 8);
+        return v;
+    }
+    template <class T>
+    T *p(int k) const { return reinterpret_cast<T *>((uintptr_t)a[k]); }
+};
+
 }  // namespace qkvf
 
 extern "C" {
@@ -708,6 +728,26 @@ int rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, const int
     return dtype == QKVF_DTYPE_BF16   ? qkvf::launch_rope<qkvf::Bf16>(prm, half, d->sms, stream)
            : dtype == QKVF_DTYPE_FP16 ? qkvf::launch_rope<qkvf::Fp16>(prm, half, d->sms, stream)
                                       : qkvf::launch_rope<qkvf::Fp32>(prm, half, d->sms, stream);
+}
+
+int rope_table_packed(const int64_t *args, void *stream)
+{
+    if (!args) return QKVF_ERR_NULL;
+    qkvf::Words w(args);
+    const int rot_dim = w.i(3), scaling = w.i(5);
+    if (!w.ok) return QKVF_ERR_SIZES;
+    return rope_table(w.p<float>(0), args[1], args[2], rot_dim, w.d(4), scaling, w.d(6), args[7], w.d(8), w.d(9),
+                      w.d(10), stream);
+}
+
+int rope_packed(const int64_t *args, void *stream)
+{
+    if (!args) return QKVF_ERR_NULL;
+    qkvf::Words w(args);
+    const int T = w.i(9), heads = w.i(10), dim = w.i(11), rot = w.i(12), layout = w.i(13), inverse = w.i(14), dtype = w.i(15);
+    if (!w.ok) return QKVF_ERR_SIZES;
+    return rope(w.p<void>(0), args[1], args[2], w.p<int64_t>(3), w.p<float>(4), args[5], w.p<void>(6), args[7], args[8],
+                T, heads, dim, rot, layout, inverse, dtype, stream);
 }
 
 }  // extern "C"

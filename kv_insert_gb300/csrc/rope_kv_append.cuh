@@ -137,4 +137,15 @@ int rope_kv_append(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                                     : qkvf::launch_rope<qkvf::Fp16>(prm, half, d->sms, stream);
 }
 
+int rope_kv_append_packed(const int64_t *args, void *stream)
+{
+    if (!args) return QKVF_ERR_NULL;
+    qkvf::Words w(args);
+    const int T = w.i(18), q_heads = w.i(19), nkv = w.i(20), dim = w.i(21), rot = w.i(22), layout = w.i(23), dtype = w.i(24);
+    if (!w.ok) return QKVF_ERR_SIZES;
+    return rope_kv_append(w.p<void>(0), args[1], args[2], w.p<void>(3), args[4], args[5], w.p<void>(6), args[7], args[8],
+                          w.p<int64_t>(9), w.p<int64_t>(10), w.p<float>(11), args[12], w.p<void>(13), args[14], args[15],
+                          w.p<void>(16), args[17], T, q_heads, nkv, dim, rot, layout, dtype, stream);
+}
+
 }  // extern "C"

@@ -18,6 +18,7 @@ import ctypes
 import math
 import os
 import re
+import struct
 import threading
 
 import torch
@@ -130,6 +131,8 @@ def load() -> ctypes.CDLL:
                            ("prefix_attn", prefix)):
             getattr(lib, name).argtypes = args + [vp]
             getattr(lib, name).restype = i32
+            getattr(lib, name + "_packed").argtypes = [ctypes.c_char_p, vp]
+            getattr(lib, name + "_packed").restype = i32
             getattr(lib, name + "_unsupported").argtypes = args
             getattr(lib, name + "_unsupported").restype = ctypes.c_char_p
         lib.prefix_attn_workspace_bytes.argtypes = [i32] * 7
@@ -607,22 +610,32 @@ def attn2_split_kv(qkv, kv_cache, block_table, context_lens, workspace, out=None
 
 # ---- rotary positions, rotated cache append, shared-prefix attention --------
 
-def _raw_stream(stream, index: int) -> int:
-    """The cudaStream_t of a call on device `index` (None: its current stream)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+# the words of the packed calls (ctypes converts 25 arguments in about 2 us)
+_PACK = {"rope_table": struct.Struct("4qdqdq3d").pack, "rope": struct.Struct("16q").pack,
+         "rope_kv_append": struct.Struct("25q").pack, "prefix_attn": struct.Struct("16qd5q").pack}
+
+
+_CALLS = {}
+
+
+def _bind(name: str):
+    _CALLS[name] = _PACK[name], getattr(load(), name + "_packed")
+    return _CALLS[name]
+
+
+def _raw_stream(stream) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _run(name: str, index: int, args: tuple, stream) -> None:
     """Call the library's `name` on device `index`; a refusal carries its reason."""
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _run(name, index, args, stream)
-    lib = _lib or load()
-    code = getattr(lib, name)(*args, _raw_stream(stream, index))
+    pack, call = _CALLS.get(name) or _bind(name)
+    code = call(pack(*args), torch._C._cuda_getCurrentRawStream(index) if stream is None else _raw_stream(stream))
     if code != 0:
-        why = getattr(lib, name + "_unsupported")(*args)
+        why = getattr(load(), name + "_unsupported")(*args)
         raise QkvFrontError(code, why.decode() if why else strerror(code))
 
 
@@ -658,7 +671,7 @@ def _heads(t, name: str, index: int, dtypes, shape=None):
     if len(dims) != 3 or (shape is not None and dims != shape):
         raise ValueError(f"{name} must be [tokens, heads, head_dim]"
                          + ("" if shape is None else f" = {tuple(shape)}") + f", not {tuple(dims)}")
-    if dims[0] > _MOST or dims[1] > _MOST or dims[2] > _MOST:
+    if shape is None and (dims[0] > _MOST or dims[1] > _MOST or dims[2] > _MOST):
         raise ValueError(f"{name} is too large: {tuple(dims)}")
     ts, hs, es = t.stride()
     if es != 1 and dims[2] > 1:
@@ -784,14 +797,15 @@ def _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout):
     if cache_heads != nkv:
         raise ValueError(f"{nkv} k heads for a cache of {cache_heads} KV heads")
     pt, rows, rot = _table(cos_sin, dim, index)
-    pq = po = None
-    q_heads = qt = qh = ot = oh = 0
+    pq = po = q_heads = qt = qh = ot = oh = 0
     if q is not None and q.dim() == 3 and q.shape[1] == 0:
         q = None
     if q is not None:
         q_heads = q.shape[1] if q.dim() == 3 else 0
         pq, qt, qh = _heads(q, "q", index, (dtype,), (T, q_heads, dim))
         po, ot, oh = _heads(q_out, "q_out", index, (dtype,), (T, q_heads, dim))
+        if q_heads > _MOST:
+            raise ValueError(f"q has too many heads: {q_heads}")
     return (pq, qt, qh, pk, kt, kh, pv, vt, vh, _index(positions, "positions", torch.int64, (T,), index),
             _index(slots, "slots", torch.int64, (T,), index), pt, rows, po, ot, oh, pc, pages, T, q_heads,
             nkv, dim, rot, _layout(layout), DTYPES[dtype])
@@ -836,8 +850,7 @@ def _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_len
         raise ValueError(f"{T} q rows are not whole requests of {q_len} tokens")
     R = T // q_len
     pc, pages, nkv = _cache(kv_cache, dim, dtype, index)
-    pp = pl = pb = ps = None
-    nb = mb = 0
+    pp = pl = pb = ps = nb = mb = 0
     if prefix_pages is not None and prefix_pages.numel():
         nb = prefix_pages.shape[0]
         pp = _index(prefix_pages, "prefix_pages", torch.int32, (nb,), index)

@@ -65,6 +65,26 @@ def test_page_counts_past_64_bits(lib):
     assert call(lib, pages=1 << 62, nkv=4) == 7 and call(lib, pages=(1 << 63) - 1, nkv=8) == 7
 
 
+def test_packed_calls(lib):
+    """The packed calls refuse as the plain ones do, and an integer that would
+    not fit its parameter instead of cutting it."""
+    a = dict(q=Q, qt=512, qh=64, c=C, pages=64, pp=PP, nb=8, pl=PL, bt=BT, mb=4, cl=CL, R=3, ql=1, H=8,
+             nkv=2, D=64, sc=0.125, dt=0, o=O, lse=LSE, ws=WS, n=1 << 40)
+
+    def packed(**kw):
+        return lib.prefix_attn_packed(qf._PACK["prefix_attn"](*{**a, **kw}.values()), None)
+    for kw in (dict(R=-1), dict(D=96), dict(H=9), dict(dt=2), dict(nb=-1), dict(sc=-1.0), dict(q=0), dict(ws=WS + 128),
+               dict(o=Q), dict(R=0)):
+        assert packed(**kw) == call(lib, **kw), kw
+    for name in ("nb", "mb", "R", "ql", "H", "nkv", "D", "dt"):
+        assert packed(**{name: a[name] + (1 << 32)}) == 7, name
+    assert lib.rope_packed(qf._PACK["rope"](*[1 << 42, 64, 64, 2 << 42, 3 << 42, 8, 4 << 42, 64, 64, 4 + (1 << 32), 1, 64,
+                                              64, 0, 0, 0]), None) == 7
+    assert lib.rope_table_packed(qf._PACK["rope_table"](1 << 42, 0, 8, 63, 1e4, 0, 1.0, 0, 1.0, 32.0, 1.0), None) == 10
+    for name in qf._PACK:
+        assert getattr(lib, name + "_packed")(None, None) == 3, name
+
+
 def test_binding_refusals():
     q = torch.zeros(4, 8, 64, dtype=BF)
     with pytest.raises(ValueError, match="CUDA"):
