@@ -1394,6 +1394,12 @@ struct PaPlan {
     int small, pre_rows, tiles, pair, own_tile, own_rows, own_tiles, sp, ss, sp_max, ss_max;
 };
 
+// What the tables have room for may be far more than the requests' keys: for
+// the sake of the own keys, the prefix never takes more than this times its own
+// shortest time (64 rows x 8 KV heads over 32K, up to 1K own keys, in tables of 32K:
+// 56.5 us, and 247 without this bound).
+constexpr double kPaWithin = 1.35;
+
 // The split (1..most) that ends soonest when `units` row tiles times the
 // splits run in waves of `workers`, each taking blocks / split steps and about
 // `over` steps of start and end.
@@ -1417,14 +1423,17 @@ int pa_split(int64_t units, int64_t workers, int64_t blocks, int most, double ov
 // dealt to all workers and the own keys' 8 CTAs in a wave of their own.)
 int pa_rows_split(int64_t units, int64_t workers, int64_t blocks, int most, int64_t others, int64_t other_blocks)
 {
+    const double over = 6.0, other = (double)other_blocks + over;
+    const auto each = [&](int s) { return (double)((blocks + s - 1) / s) + over; };
+    const auto waves = [&](int s) { return (units * s + workers - 1) / workers; };
+    double shortest = 1e300;
+    for (int s = 1; s <= most; ++s) shortest = waves(s) * each(s) < shortest ? waves(s) * each(s) : shortest;
     int best = 1;
     double least = 1e300;
-    const double over = 6.0, other = (double)other_blocks + over;
     for (int s = 1; s <= most; ++s) {
-        const int64_t n = units * s, waves = (n + workers - 1) / workers;
-        const double each = (double)((blocks + s - 1) / s) + over;
-        const int64_t left = others - (int64_t)((double)(waves * workers - n) * (each < other ? 1.0 : each / other));
-        const double cost = (double)waves * each + (left > 0 ? (double)((left + workers - 1) / workers) * other : 0.0);
+        if (waves(s) * each(s) > kPaWithin * shortest) continue;
+        const int64_t left = others - (int64_t)((double)(waves(s) * workers - units * s) * (each(s) < other ? 1.0 : each(s) / other));
+        const double cost = waves(s) * each(s) + (left > 0 ? (double)((left + workers - 1) / workers) * other : 0.0);
         if (cost < least * 0.999) {
             least = cost;
             best = s;
@@ -1445,17 +1454,23 @@ int pa_most(int64_t units, int64_t workers, int64_t blocks)
 // (`rest`, SM microseconds) on the SMs it leaves free meanwhile and behind it,
 // and `merge` us a split to write and join.  With 64 rows x 8 KV heads over 32K
 // and up to 1K own keys each, 9 splits (144 CTAs) take 60.8 us and 7 (112) 59.7
-// to 61.4; with 33 rows x 4 KV heads of 128 over 16K, 38 splits 30.5 and 18 26.1.
+// to 61.4; with 33 rows x 4 KV heads of 128 over 16K, 38 splits 30.5 and 18
+// 26.1.
 int pa_tile_split(int64_t units, int64_t blocks, int most, int sms, bool pair, double step, double rest, double merge)
 {
+    const auto ctas = [&](int s) { return pair ? units * s : (units * s + 1) / 2; };
+    const auto tile = [&](int s) {
+        return (double)((ctas(s) + sms - 1) / sms) * ((double)((blocks + s - 1) / s) * step + 5.0);
+    };
+    double shortest = 1e300;
+    for (int s = 1; s <= most; ++s) shortest = tile(s) < shortest ? tile(s) : shortest;
     int best = 1;
     double least = 1e300;
     for (int s = 1; s <= most; ++s) {
-        const int64_t ctas = pair ? units * s : (units * s + 1) / 2, waves = (ctas + sms - 1) / sms;
-        const double tile = (double)waves * ((double)((blocks + s - 1) / s) * step + 5.0);
-        double left = rest - (ctas < sms ? (double)(sms - ctas) * tile : 0.0);
+        if (tile(s) > kPaWithin * shortest) continue;
+        double left = rest - (ctas(s) < sms ? (double)(sms - ctas(s)) * tile(s) : 0.0);
         if (left < 0.0) left = 0.0;
-        const double cost = tile + left / sms + (rest > 0.0 ? 5.0 * left / rest : 0.0) + merge * s;
+        const double cost = tile(s) + left / sms + (rest > 0.0 ? 5.0 * left / rest : 0.0) + merge * s;
         if (cost < least * 0.999) {
             least = cost;
             best = s;
