@@ -145,7 +145,7 @@ struct PaItem {
 __device__ __forceinline__ int pa_prefix_len(const PrefixParams &p)
 {
     if (p.prefix_blocks == 0) return 0;
-    const int P = *p.prefix_len;
+    const int P = __ldcg(p.prefix_len);
     return P > p.prefix_blocks * kPageSlots ? -1 : P;
 }
 
@@ -227,7 +227,7 @@ struct PaWork {
         for (; idx < end; idx += stride) {
             if (kOwn) {
                 const int g = idx % p.nkv, rest = idx / p.nkv, r = rest % p.R, ts = rest / p.R;
-                const int L = __reduce_max_sync(0xffffffffu, p.context_lens[r]);
+                const int L = __reduce_max_sync(0xffffffffu, __ldcg(p.context_lens + r));
                 it = pa_own_item<PaShape<D>::keys>(p, P, L, r, ts % p.own_tiles, g, ts / p.own_tiles);
             } else {
                 const int rb = p.pair ? (p.tiles + 1) / 2 : 1, tile = p.pair ? 2 * (idx % rb) + w : 0, gs = idx / rb;
@@ -491,7 +491,7 @@ struct PaTile {
         int guess = -1, entry = 0;   // the first entries as of a full table
         if (!kOwn && Work(p, p.prefix_blocks * kPageSlots, w).next(it)) {
             guess = it.kb0 * Sh::pages;
-            if (guess + lane < p.prefix_blocks) entry = it.pages[guess + lane];
+            if (guess + lane < p.prefix_blocks) entry = __ldcg(it.pages + guess + lane);
         }
         Work work(p, length(), w);
         bool ok = true;
@@ -501,10 +501,10 @@ struct PaTile {
         while (ok && work.next(it)) {
             const int pg0 = it.kb0 * Sh::pages;
             const int pg1 = min(it.kb1 * Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots);
-            int next = pg0 + lane < pg1 ? (pg0 == guess ? entry : it.pages[pg0 + lane]) : 0;
+            int next = pg0 + lane < pg1 ? (pg0 == guess ? entry : __ldcg(it.pages + pg0 + lane)) : 0;
             for (int c = pg0; c < pg1 && ok; c += 32) {
                 int page = next;
-                if (c + 32 + lane < pg1) next = it.pages[c + 32 + lane];
+                if (c + 32 + lane < pg1) next = __ldcg(it.pages + c + 32 + lane);
                 bool bad = false;
                 if (c + lane < pg1 && (page < 0 || page >= p.num_pages)) {   // flagged, page 0 in its place
                     bad = true;
@@ -671,7 +671,7 @@ struct PaTile {
                     static_cast<const uint16_t *>(p.q) + (it.tok0 + tok) * p.q_ts + head * p.q_hs);
                 uint4 v[D / 8];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < D / 8; ++c) v[c] = valid ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
                     *reinterpret_cast<uint4 *>(sq + (c / 8) * (kPaTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
@@ -850,7 +850,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     // The own keys' CTAs behind the prefix's: as in the rows kernel, every input
-    // is written, and only the grid as a whole must not end before that one.
+    // is in L2 and read past L1, and only the grid as a whole must not end before
+    // that one.
     const bool behind = kOwn && p.prefix_blocks > 0, last = blockIdx.x == gridDim.x - 1;
     if (kOwn) {
         if (threadIdx.x == 0) griddep_launch_dependents();
@@ -988,10 +989,10 @@ __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixPar
         unsigned bad_any = 0u;
         bool stop = false;
         int j = 0;
-        int next = pg0 + lane < pg1 ? (pg0 == 0 ? first_entry : pages[pg0 + lane]) : 0;
+        int next = pg0 + lane < pg1 ? (pg0 == 0 ? first_entry : __ldcg(pages + pg0 + lane)) : 0;
         for (int c = pg0; c < pg1 && !stop; c += 32) {
             int page = next;
-            if (c + 32 + lane < pg1) next = pages[c + 32 + lane];
+            if (c + 32 + lane < pg1) next = __ldcg(pages + c + 32 + lane);
             bool wrong = false;
             if (c + lane < pg1 && (page < 0 || page >= p.num_pages)) {   // flagged, page 0 in its place
                 wrong = true;
@@ -1036,10 +1037,10 @@ __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixPar
             const uint16_t *pb = qp + (it.tok0 + tb) * p.q_ts + (g * p.group + mb - tb * p.group) * p.q_hs + 2 * t;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                qa[k][0] = va ? *reinterpret_cast<const uint32_t *>(pa + 16 * k) : 0u;
-                qa[k][1] = vb ? *reinterpret_cast<const uint32_t *>(pb + 16 * k) : 0u;
-                qa[k][2] = va ? *reinterpret_cast<const uint32_t *>(pa + 16 * k + 8) : 0u;
-                qa[k][3] = vb ? *reinterpret_cast<const uint32_t *>(pb + 16 * k + 8) : 0u;
+                qa[k][0] = va ? __ldcg(reinterpret_cast<const uint32_t *>(pa + 16 * k)) : 0u;
+                qa[k][1] = vb ? __ldcg(reinterpret_cast<const uint32_t *>(pb + 16 * k)) : 0u;
+                qa[k][2] = va ? __ldcg(reinterpret_cast<const uint32_t *>(pa + 16 * k + 8)) : 0u;
+                qa[k][3] = vb ? __ldcg(reinterpret_cast<const uint32_t *>(pb + 16 * k + 8)) : 0u;
             }
         }
 #pragma unroll
@@ -1242,9 +1243,12 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
         griddep_launch_dependents();
     }
     __syncthreads();
-    // Behind the tile kernel every input is already written (that kernel has
-    // waited for it before this one could start), and only the grid as a whole
-    // must not end before it: the last CTA waits, at its end.
+    // Behind the tile kernel every input is already in L2 (that kernel has
+    // waited for the kernels that write it before this one could start), and
+    // only the grid as a whole must not end before it: the last CTA waits, at
+    // its end.  A CTA without a wait of its own may find an older copy of a line
+    // in its SM's L1, so q, the lengths and the tables are read past it (keys
+    // come by TMA, from L2).
     const bool behind = !p.small && p.prefix_blocks > 0;
     if (!behind) griddep_wait();
 
@@ -1258,8 +1262,8 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
     const int32_t *pages = own ? p.block_table + (size_t)r * p.max_blocks : p.prefix_pages;
     // the first split starts at page 0: its entries need not wait for a length
     int first_entry = 0;
-    if (warp == 4 && split == 0 && lane < (own ? p.max_blocks : p.prefix_blocks)) first_entry = pages[lane];
-    const int P = pa_prefix_len(p), L = own ? p.context_lens[r] : 0;
+    if (warp == 4 && split == 0 && lane < (own ? p.max_blocks : p.prefix_blocks)) first_entry = __ldcg(pages + lane);
+    const int P = pa_prefix_len(p), L = own ? __ldcg(p.context_lens + r) : 0;
     const PaItem it = own ? pa_own_item<kPrKeys>(p, P, L, r, tile, g, split) : pa_prefix_item<kPrKeys>(p, max(P, 0), RTP, 0, g, split);
     if (it.kb1 > it.kb0) {
         if constexpr (RTP == RTO) {
@@ -1301,7 +1305,7 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
     const int first = wr * (32 / LPR) + lane / LPR, d = lane % LPR;   // this lane's first slot, its 4 columns
     const float4 *src = reinterpret_cast<const float4 *>(p.ws_o + (int64_t)row * D) + d;
     const int64_t step = (int64_t)p.rows * (D / 4);
-    const int P = pa_prefix_len(p), L = p.context_lens[r];
+    const int P = pa_prefix_len(p), L = __ldcg(p.context_lens + r);
     float2 v[2 * kPaMaxSplits / 32];
 #pragma unroll
     for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i)

@@ -490,6 +490,66 @@ def test_calls_follow_the_kernels_before_them(dev, R, q_len, nkv, G, D, P, own):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,q_len,nkv,G,D,P,own", [
+    (4, 20, 2, 5, 64, 900, 640), (70, 1, 2, 4, 128, 900, 200), (16, 8, 2, 8, 64, 1500, 300), (3, 40, 1, 4, 128, 0, 700),
+    (2, 1, 2, 8, 64, 500, 300),
+])
+def test_calls_follow_inputs_rewritten_in_place(dev, R, q_len, nkv, G, D, P, own):
+    """A decode loop's buffers: q, the lengths, the tables and the prefix's
+    length get new contents at the same addresses right before every call, by
+    the kernels just ahead of it.  The bits are those of calls with a device
+    synchronization in between: no CTA works on what an earlier call found
+    there."""
+    g = torch.Generator().manual_seed(23)
+    steps, T, H = 24, R * q_len, nkv * G
+    nb, mb = (P + 15) // 16, (own + 15) // 16
+    pages = nb + R * mb
+    cache = torch.randn(pages, nkv, 16, 2 * D, generator=g).to(BF).to(dev)
+    table = qf.rope_table(4096, D)
+    pos = torch.randint(0, 4096, (T,), generator=g).to(dev)
+    none = torch.full((T,), -1, dtype=torch.int64, device=dev)       # no slot is written
+    kv = torch.zeros(T, nkv, D, dtype=BF, device=dev)
+    per_step = [dict(q=torch.randn(T, H, D, generator=g).to(BF).to(dev),
+                     prefix_pages=torch.randperm(pages, generator=g)[:nb].to(torch.int32).to(dev),
+                     prefix_len=torch.tensor([P - (i * 37) % (P // 2 + 1)], dtype=torch.int32, device=dev),
+                     block_table=torch.randint(0, pages, (R, mb), generator=g).to(torch.int32).to(dev),
+                     context_lens=torch.randint(0, own + 1, (R,), generator=g).to(torch.int32).to(dev))
+                for i in range(steps)]
+
+    def run(sync):
+        b = {n: t.clone() for n, t in per_step[0].items()}
+        turned = torch.zeros_like(b["q"])
+        ws = workspace(turned, cache, b["prefix_pages"], b["block_table"], q_len)
+        outs = [(torch.zeros_like(turned), torch.zeros(T, H, device=dev)) for _ in range(steps)]
+        torch.cuda.synchronize()
+        for i, (step, (out, lse)) in enumerate(zip(per_step, outs)):
+            names = ["prefix_pages", "prefix_len", "block_table", "context_lens"]
+            for n in names[i % 4:] + names[:i % 4]:
+                b[n].copy_(step[n])
+                if i % 2 == 0 and n == names[i % 4]:
+                    qf.rope_kv_append(step["q"], kv, kv, pos, none, table, cache, q_out=turned)
+            if i % 2:
+                qf.rope_kv_append(step["q"], kv, kv, pos, none, table, cache, q_out=turned)
+            if sync:
+                torch.cuda.synchronize()
+            qf.prefix_attn(turned, cache, b["prefix_pages"] if nb else None, b["prefix_len"], b["block_table"],
+                           b["context_lens"], ws, q_len=q_len, out=out, lse=lse)
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+    want = run(True)
+    for _ in range(5):
+        for i, (a, b) in enumerate(zip(run(False), want)):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), i
+    first = dict(per_step[-1], q=qf.rope(per_step[-1]["q"], pos, table), kv_cache=cache)
+    if not nb:
+        first["prefix_pages"] = first["prefix_len"] = None
+    check(first, q_len, *want[-1])
+    assert qf.status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("layout,D,rot,dtype", [("interleaved", 64, 64, BF), ("half", 128, 96, HF)])
 def test_serving_chain(dev, layout, D, rot, dtype):
     """As a serving program runs them: a scaled table; the prefix's tokens
