@@ -14,6 +14,7 @@ HEADERS = [os.path.join(ROOT, "include", "qkvfront.h"),
            os.path.join(PKG, "csrc", "attn2.cuh"),
            os.path.join(PKG, "csrc", "rope.cuh"),
            os.path.join(PKG, "csrc", "rope_kv_append.cuh"),
+           os.path.join(PKG, "csrc", "prefix_plan.h"),
            os.path.join(PKG, "csrc", "prefix_attn.cuh")]
 LIB_PATH = os.path.join(PKG, "libqkvfront.so")
 

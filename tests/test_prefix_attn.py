@@ -271,6 +271,17 @@ def test_no_prefix_and_no_tables(dev):
 
 
 @pytest.mark.gpu
+def test_a_batch_without_requests(dev):
+    """Nothing to do, and nothing written."""
+    assert 0 < qf.prefix_attn_workspace_bytes(0, 1, 8, 2, 64, 8, 4) <= qf.prefix_attn_workspace_bytes(1, 1, 8, 2, 64, 8, 4)
+    d = make(1, 1, 2, 4, 64, 40, [9], BF)
+    ws = workspace(d["q"], d["kv_cache"], d["prefix_pages"], d["block_table"], 1)
+    out = qf.prefix_attn(d["q"][:0], d["kv_cache"], d["prefix_pages"], d["prefix_len"], d["block_table"][:0],
+                         d["context_lens"][:0], ws)
+    assert out.shape == (0, 8, 64) and torch.all(ws == 0xA5) and qf.status() == 0
+
+
+@pytest.mark.gpu
 def test_strided_q(dev):
     """The q columns of packed rows, and heads-major q, as they lie."""
     d = make(4, 1, 2, 4, 64, 200, [3, 40, 0, 17], BF, seed=3)
