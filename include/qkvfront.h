@@ -493,7 +493,9 @@ const char *rope_kv_append_unsupported(const void *q, int64_t q_token_stride, in
  * were), and so are the rows that see a page outside the cache (with them other
  * rows of that request, but of no other): QKVF_STATUS_BAD_REQUEST is raised.  A
  * bad prefix does so for every request.  Cache
- * slots past a length are never used, whatever they hold.
+ * slots past a length are never used, whatever they hold, and a key reaches only
+ * the rows that see it: an infinity or NaN in K or V of a request's later token
+ * does not change its earlier tokens' rows.
  *   head_dim 64 or 128, q_heads 1..64 times num_kv_heads (1..64), q_len
  *   1..1024, num_reqs 0..65535, num_reqs q_len q_heads <= 2^24.
  * Scores, softmax statistics and sums in FP32; the weights exp(s - m) are

@@ -99,7 +99,7 @@ __host__ __device__ constexpr PaSmem pa_smem()
     L.tmem = off;
     off += 8;
     L.flags = off;
-    off += 16;
+    off += 32;
     L.total = off + 1024;
     return L;
 }
@@ -127,6 +127,7 @@ struct PrefixParams {
     int own_rows, own_tiles;   // rows of one tile of a request's rows, tiles of a request
     int sp, ss;       // key splits of the prefix and of a request's own keys
     float scale_log2;
+    const void *kv_cache;
 };
 
 // One unit of work: a tile of query rows against a range of key blocks
@@ -139,6 +140,7 @@ struct PaItem {
     int keys;        // keys that some row of the tile sees
     int limit0;      // keys that token 0 of the row set sees; later tokens see `step` more each
     int step;
+    int all;         // keys that every row of the tile sees
     int split;       // partial slot
 };
 
@@ -171,6 +173,7 @@ __device__ __forceinline__ PaItem pa_prefix_item(const PrefixParams &p, int P, i
     it.keys = P;
     it.limit0 = P;
     it.step = 0;
+    it.all = P;
     it.split = s;
     pa_deal(it, (P + KB - 1) / KB, p.sp, s);
     return it;
@@ -198,6 +201,7 @@ __device__ __forceinline__ PaItem pa_own_item(const PrefixParams &p, int P, int 
     it.keys = P < 0 ? 0 : pa_own_keys(p, L, tile);
     it.limit0 = max(L, 0) - p.q_len + 1;
     it.step = 1;
+    it.all = it.limit0 + it.row0 / p.group;
     it.split = p.sp + s;
     pa_deal(it, (it.keys + KB - 1) / KB, p.ss, s);
     return it;
@@ -448,6 +452,67 @@ __device__ __forceinline__ float pa_weights(const uint32_t (&s)[N], uint32_t (&p
     return a + b;
 }
 
+// A key that only later rows of a tile see has the weight 0 in the others, and
+// a V of it that is not finite must not meet that weight (0 x infinity is not
+// 0).  Among the keys from it.all on such values become 0 before the product,
+// and the rows that see the key have them added when the item is done.  (16
+// requests x 8 tokens x 64 heads of 64 over up to 1K own keys: 19.3 us, and 18.6
+// without looking; over 8K shared keys besides 42.3 and 41.4.)
+
+// The halves of two packed values that are infinite or NaN, as a mask
+template <class E>
+__device__ __forceinline__ uint32_t pa_not_finite(uint32_t v)
+{
+    constexpr uint32_t exponent = E::is_bf16 ? 0x7f807f80u : 0x7c007c00u;
+    return __vcmpeq2(v & exponent, exponent);
+}
+
+// By one warp: whether the V rows of keys `from` .. `to` - 1 of the pages at
+// `pages` (as TMA lays them out) hold something not finite; kDrop: which
+// becomes 0
+template <class E, int D, bool kDrop>
+__device__ __forceinline__ bool pa_find_not_finite(uint8_t *pages, int from, int to)
+{
+    constexpr int rows8 = D / 32 * 1024;   // bytes of 8 slots, K and V
+    bool found = false;
+#pragma unroll 1
+    for (int c = from * (D / 8) + (threadIdx.x & 31); c < to * (D / 8); c += 32) {
+        const int key = c / (D / 8), ch = c % (D / 8);   // (a row's 16-byte chunks in any order)
+        uint4 *at = reinterpret_cast<uint4 *>(pages + (key >> 3) * rows8 + (D / 64 + ch / 8) * 1024 + (key & 7) * 128 + (ch & 7) * 16);
+        const uint4 v = *at;
+        const uint32_t x = pa_not_finite<E>(v.x), y = pa_not_finite<E>(v.y), z = pa_not_finite<E>(v.z), u = pa_not_finite<E>(v.w);
+        if (x | y | z | u) {
+            found = true;
+            if (kDrop) *at = make_uint4(v.x & ~x, v.y & ~y, v.z & ~z, v.w & ~u);
+        }
+    }
+    found = __any_sync(0xffffffffu, found);
+    if (kDrop && found) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+    }
+    return found;
+}
+
+// V row of own key `key` of the item's KV head, past L1; null: its page is outside the cache
+template <int D>
+__device__ __forceinline__ const uint32_t *pa_value_row(const PrefixParams &p, const PaItem &it, int key)
+{
+    const int page = __ldcg(it.pages + key / kPageSlots);
+    if (page < 0 || page >= p.num_pages) return nullptr;
+    const int64_t slot = ((int64_t)page * p.nkv + it.g) * kPageSlots + key % kPageSlots;
+    return reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.kv_cache) + slot * (2 * D) + D);
+}
+
+// (a, b) += those of two packed values that are not finite
+template <class E>
+__device__ __forceinline__ void pa_add_not_finite(uint32_t v, float &a, float &b)
+{
+    const uint32_t m = pa_not_finite<E>(v);
+    if (m & 0xffffu) a += E::lo(v);
+    if (m & 0xffff0000u) b += E::hi(v);
+}
+
 // The roles of the tile kernel's warps.  Every loop over items and blocks is
 // the same in each of them.
 template <class E, int D, bool kOwn>
@@ -597,6 +662,12 @@ struct PaTile {
                 }
                 if (j > 0) {   // O += P V of block j - 1
                     const int b = j < n ? blk - 2 : blk - 1;
+                    if constexpr (kOwn) {   // while its weights are being made
+                        const int k0 = (it.kb0 + j - 1) * KB;
+                        if (it.all < min(it.keys, k0 + KB) &&
+                            pa_find_not_finite<E, D, true>(smem + LY.ring + st_prev * Sh::stage_bytes, max(it.all - k0, 0), min(it.keys - k0, KB)))
+                            flags()[3 + W] = 1;
+                    }
                     wait(LY.pready + 16 * (b & 1) + 8 * W, b >> 1);
                     __syncwarp();
                     tc_fence_after();
@@ -624,6 +695,7 @@ struct PaTile {
             }
             if (pa_elect()) umma_commit(sb + LY.odone + 8 * W);
             __syncwarp();
+            if (kOwn && lane == 0) mbar_arrive(sb + LY.odone + 8 * W);   // with the flag of values dropped
         }
         // every MMA of this warp is done before tensor memory is freed (the same
         // lane is elected each time: commits cover the MMAs of one thread)
@@ -802,11 +874,28 @@ struct PaTile {
             if (active && !__any_sync(0xffffffffu, dead())) {
                 tc_fence_after();
                 float *dst = p.ws_o + ((int64_t)it.split * p.rows + grow) * D;
+                const bool dropped = kOwn && flags()[3 + w];
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     pa_tmem_ld32(aO + c, o);
                     tmem_ld_wait();
+                    if (kOwn && dropped) {
+                        const int end = min(min(it.keys, it.kb1 * KB), valid ? it.limit0 + it.step * tok : 0);
+#pragma unroll 1
+                        for (int key = max(it.all, it.kb0 * KB); key < end; ++key) {
+                            const uint32_t *v = pa_value_row<D>(p, it, key);
+                            if (!v) continue;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float a = __uint_as_float(o[e]), b = __uint_as_float(o[e + 1]);
+                                pa_add_not_finite<E>(__ldcg(v + (c + e) / 2), a, b);
+                                o[e] = __float_as_uint(a);
+                                o[e + 1] = __float_as_uint(b);
+                            }
+                        }
+                        __syncwarp();
+                    }
                     if (valid)
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
@@ -876,11 +965,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             mbar_init(sb + LY.pready + 8 * w, 4);
             mbar_init(sb + LY.pready + 16 + 8 * w, 4);
             mbar_init(sb + LY.pvdone + 8 * w, 1);
-            mbar_init(sb + LY.odone + 8 * w, 1);
+            mbar_init(sb + LY.odone + 8 * w, kOwn ? 2 : 1);
             mbar_init(sb + LY.drain + 8 * w, 1);
         }
-        // a wait gave up; a page outside the cache, by producer
-        for (int i = 0; i < 3; ++i) reinterpret_cast<volatile int *>(smem + LY.flags)[i] = 0;
+        // a wait gave up; a page outside the cache, by producer; values not finite
+        // among keys that not every row sees, by group
+        for (int i = 0; i < (kOwn ? 5 : 3); ++i) reinterpret_cast<volatile int *>(smem + LY.flags)[i] = 0;
         fence_barrier_init();
     }
     // all of tensor memory (one CTA per SM): it starts at column 0
@@ -934,6 +1024,8 @@ struct PrShape {
     static constexpr uint32_t page_bytes = kPageSlots * 4 * D;
     static constexpr uint32_t stage_bytes = kPrPages * page_bytes;
     static constexpr uint32_t ring_bytes = slots * stage_bytes;
+    // barriers full and empty, one of values cleared, pages outside the cache by
+    // stage, two flags: a wait gave up, values were cleared
     static constexpr uint32_t smem = ring_bytes + slots * 20 + 16 + 1024;
     static constexpr int ostride = D + 4;   // floats per row of a warp's partial, over the ring
     static_assert(4 * 16 * (ostride + 2) * 4 <= ring_bytes, "the warps' partials fit the ring");
@@ -958,15 +1050,18 @@ __device__ __forceinline__ void pr_mma(float (&d)[4], const uint32_t (&a)[4], ui
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One item against its key blocks: RT = 16 or 64 rows
-template <class E, int D, int RT>
+// One item against its key blocks: RT = 16 or 64 rows.  kTokens: some rows may
+// see fewer keys than others (requests of several tokens; without the code for
+// that 64 requests' own keys take 21.2 us instead of 21.4, and with a 32K prefix
+// 54.5 instead of 55.5).
+template <class E, int D, int RT, bool kTokens>
 __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixParams &p, const PaItem &it, int first_entry,
                                         uint8_t *smem)
 {
     using Sh = PrShape<D>;
     constexpr int NS = Sh::slots, NP = RT == 16 ? 1 : kPrPages;
-    const uint32_t sb = smem_u32(smem), full0 = sb + Sh::ring_bytes, empty0 = full0 + 8 * NS;
-    volatile int *slot_bad = reinterpret_cast<volatile int *>(smem + Sh::ring_bytes + 16 * NS);
+    const uint32_t sb = smem_u32(smem), full0 = sb + Sh::ring_bytes, empty0 = full0 + 8 * NS, cleared = empty0 + 8 * NS;
+    volatile int *slot_bad = reinterpret_cast<volatile int *>(smem + Sh::ring_bytes + 16 * NS + 8);
     volatile int *flags = slot_bad + NS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const auto wait = [&](uint32_t bar, int n) {
@@ -1049,12 +1144,34 @@ __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixPar
             for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
         const int lim_a = it.limit0 + it.step * ta, lim_b = it.limit0 + it.step * tb;
         const bool rows_here = RT == 16 || 16 * warp < it.rows;
+        // the first stage with keys that some rows do not see
+        const int partly_from = kTokens && it.all < it.keys ? max(it.all, 0) / kPrKeys - it.kb0 : n;
         for (int j = 0; j < n; ++j) {
             const int st = j % NS;
             ok = __all_sync(0xffffffffu, wait(full0 + 8 * st, j / NS));
             if (!ok) break;
             bad |= slot_bad[st];
             const int left = pg1 - pg0 - j * kPrPages;   // pages from this stage on
+            if (kTokens && j >= partly_from) {
+                uint8_t *stage = smem + st * Sh::stage_bytes;
+                const int k0 = (it.kb0 + j) * kPrKeys, k1 = k0 + warp * kPageSlots;
+                // the warp's page; where the other warps read it too, all of them look through
+                // the stage, and find the same, before any changes it (two phases a stage)
+                const bool clear = RT == 16 || pa_find_not_finite<E, D, false>(stage, max(it.all - k0, 0), min(it.keys - k0, kPrKeys));
+                if (RT == 64 && clear) {
+                    if (lane == 0) mbar_arrive(cleared);
+                    ok = __all_sync(0xffffffffu, wait(cleared, 0));
+                    if (!ok) break;
+                }
+                if (clear && pa_find_not_finite<E, D, true>(stage + warp * Sh::page_bytes, max(it.all - k1, 0), min(it.keys - k1, kPageSlots)))
+                    flags[1] = 1;
+                if (RT == 64 && clear) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(cleared);
+                    ok = __all_sync(0xffffffffu, wait(cleared, 1));
+                    if (!ok) break;
+                }
+            }
             const int b_lo = RT == 16 ? warp : 0;         // the warp's pages of the stage: b_lo ..
             if (rows_here && b_lo < left) {
                 const uint32_t base = sb + st * Sh::stage_bytes + b_lo * Sh::page_bytes;
@@ -1147,6 +1264,21 @@ __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixPar
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * st);
         }
+        if (kTokens && partly_from < n && __any_sync(0xffffffffu, flags[1] != 0)) {
+            const int end = min(it.keys, it.kb1 * kPrKeys);
+#pragma unroll 1
+            for (int key = max(it.all, it.kb0 * kPrKeys); key < end; ++key) {
+                if (RT == 16 && (key / kPageSlots) % kPrPages != warp) continue;   // another warp's page
+                const uint32_t *v = pa_value_row<D>(p, it, key);
+                if (!v) continue;
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) {
+                    const uint32_t x = __ldcg(v + 4 * d + t);
+                    if (key < lim_a) pa_add_not_finite<E>(x, o[d][0], o[d][1]);
+                    if (key < lim_b) pa_add_not_finite<E>(x, o[d][2], o[d][3]);
+                }
+            }
+        }
 #pragma unroll
         for (int off = 1; off <= 2; off <<= 1) {
             l_a += __shfl_xor_sync(0xffffffffu, l_a, off);
@@ -1223,7 +1355,7 @@ __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixPar
 
 // Prefix items (where the prefix's rows are few: p.small) in tiles of RTP
 // rows, then the requests' own keys in tiles of RTO.
-template <class E, int D, int RTP, int RTO>
+template <class E, int D, int RTP, int RTO, bool kTokens>
 __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP : RTO)>())
     prefix_rows_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ PrefixParams p)
 {
@@ -1238,7 +1370,8 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
             mbar_init(full0 + 8 * i, 1);
             mbar_init(empty0 + 8 * i, 4);
         }
-        reinterpret_cast<volatile int *>(smem + Sh::ring_bytes + 16 * NS)[NS] = 0;
+        mbar_init(empty0 + 8 * NS, 4);
+        for (int i = 0; i < 2; ++i) reinterpret_cast<volatile int *>(smem + Sh::ring_bytes + 16 * NS + 8)[NS + i] = 0;
         fence_barrier_init();
         griddep_launch_dependents();
     }
@@ -1267,12 +1400,12 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
     const PaItem it = own ? pa_own_item<kPrKeys>(p, P, L, r, tile, g, split) : pa_prefix_item<kPrKeys>(p, max(P, 0), RTP, 0, g, split);
     if (it.kb1 > it.kb0) {
         if constexpr (RTP == RTO) {
-            pr_item<E, D, RTO>(tmKV, p, it, first_entry, smem);
+            pr_item<E, D, RTO, kTokens>(tmKV, p, it, first_entry, smem);
         } else {
             if (own)
-                pr_item<E, D, RTO>(tmKV, p, it, first_entry, smem);
+                pr_item<E, D, RTO, kTokens>(tmKV, p, it, first_entry, smem);
             else
-                pr_item<E, D, RTP>(tmKV, p, it, first_entry, smem);
+                pr_item<E, D, RTP, false>(tmKV, p, it, first_entry, smem);
         }
     }
     if (behind && blockIdx.x == gridDim.x - 1) griddep_wait();
@@ -1394,6 +1527,14 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
 
 // ---- host: launch (splits and workspace: prefix_plan.h) ---------------------
 
+template <class E, int D, int RTP, int RTO>
+bool prepare_rows_kernel()
+{
+    constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    return cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, RTP, RTO, false>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
+           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, RTP, RTO, true>, attr, (int)PrShape<D>::smem) == cudaSuccess;
+}
+
 template <class E, int D>
 bool prepare_prefix_kernel()
 {
@@ -1401,9 +1542,7 @@ bool prepare_prefix_kernel()
     constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     return cudaFuncSetAttribute((const void *)prefix_tile_kernel<E, D, false>, attr, (int)pa_smem<D>().total) == cudaSuccess &&
            cudaFuncSetAttribute((const void *)prefix_tile_kernel<E, D, true>, attr, (int)pa_smem<D>().total) == cudaSuccess &&
-           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 16, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
-           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 64, 16>, attr, (int)PrShape<D>::smem) == cudaSuccess &&
-           cudaFuncSetAttribute((const void *)prefix_rows_kernel<E, D, 64, 64>, attr, (int)PrShape<D>::smem) == cudaSuccess;
+           prepare_rows_kernel<E, D, 16, 16>() && prepare_rows_kernel<E, D, 64, 16>() && prepare_rows_kernel<E, D, 64, 64>();
 }
 
 bool prepare_prefix_kernels()
@@ -1449,9 +1588,14 @@ int launch_prefix(const CUtensorMap &map, const PrefixParams &prm, int sms, void
                         (size_t)pa_smem<D>().total, stream, map, prm);
         if (rc != QKVF_OK) return rc;
     } else if (items > 0) {
-        rc = launch_pdl(prm.own_rows == 64                       ? prefix_rows_kernel<E, D, 64, 64>
-                        : prm.small && prm.pre_rows == 64 ? prefix_rows_kernel<E, D, 64, 16>
-                                                          : prefix_rows_kernel<E, D, 16, 16>,
+        const bool tokens = prm.q_len > 1 && prm.max_blocks > 0;
+        const auto rows = [&](auto several) {
+            constexpr bool k = decltype(several)::value;
+            return prm.own_rows == 64                ? prefix_rows_kernel<E, D, 64, 64, k>
+                   : prm.small && prm.pre_rows == 64 ? prefix_rows_kernel<E, D, 64, 16, k>
+                                                     : prefix_rows_kernel<E, D, 16, 16, k>;
+        };
+        rc = launch_pdl(tokens ? rows(std::true_type()) : rows(std::false_type()),
                         dim3((unsigned)items), dim3(kPrThreads), (size_t)PrShape<D>::smem, stream, map, prm);
         if (rc != QKVF_OK) return rc;
     }
@@ -1599,6 +1743,7 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     if (rc != QKVF_OK) return rc;
     qkvf::PrefixParams prm = {};
     prm.q = q;
+    prm.kv_cache = kv_cache;
     prm.prefix_pages = prefix_pages;
     prm.prefix_len = prefix_len;
     prm.block_table = block_table;

@@ -42,6 +42,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "qkvfront.h"
 

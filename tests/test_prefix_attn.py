@@ -257,6 +257,51 @@ def test_rows_do_not_disturb_one_another(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("case", [   # rows of a request against its keys in tiles of 16, 64 and 128
+    (3, 4, 1, 4, 64, 0, [4, 90, 33]), (3, 5, 2, 3, 128, 70, [5, 17, 300]), (2, 8, 1, 8, 64, 300, [200, 9]),
+    (3, 8, 2, 5, 128, 0, [64, 8, 129]), (2, 33, 2, 4, 64, 200, [700, 40]), (2, 130, 1, 2, 128, 0, [600, 530]),
+    (1, 300, 1, 1, 64, 900, [1000]), (2, 20, 1, 64, 64, 3000, [520, 19]),
+], ids=lambda c: "-".join(map(str, c[:6])))
+def test_a_key_reaches_only_the_rows_that_see_it(dev, case, dtype):
+    """Infinities and NaN in V, and a NaN in K, of keys that a request's later
+    tokens see and its earlier ones do not: the earlier rows keep their bits,
+    and so do the other columns of V everywhere."""
+    R, q_len, nkv, G, D, P, lens = case
+    d = make(R, q_len, nkv, G, D, P, lens, dtype)
+    clean, lse = attend(d, q_len)
+    check(d, q_len, clean, lse)
+    e = {n: t.clone() for n, t in d.items()}
+    touched = {}                                                      # (row, KV head) -> {column: value}
+    for r, L in enumerate(lens):
+        for n, back in enumerate({0, 1, q_len // 2, q_len - 1}):      # keys from the last on
+            key, g = L - 1 - back, n % nkv
+            if key < 0:
+                continue
+            value = (math.inf, math.nan, -math.inf)[(r + n) % 3]
+            e["kv_cache"][int(e["block_table"][r, key // 16]), g, key % 16, D + 7 + 5 * n] = value
+            for i in range(q_len):
+                if key <= L - q_len + i:
+                    touched.setdefault((r * q_len + i, g), {})[7 + 5 * n] = value
+    out, lse2 = attend(e, q_len)
+    assert qf.status() == 0 and torch.equal(lse, lse2)
+    same = torch.ones_like(out, dtype=torch.bool)
+    for (t, g), columns in touched.items():
+        for c, value in columns.items():
+            got = out[t, g * G:(g + 1) * G, c].float()
+            assert torch.all(torch.isnan(got) if math.isnan(value) else got == value), (t, g, c, value)
+            same[t, g * G:(g + 1) * G, c] = False
+    assert torch.equal(out[same], clean[same])
+    e = {n: t.clone() for n, t in d.items()}
+    e["kv_cache"][int(e["block_table"][0, (lens[0] - 1) // 16]), :, (lens[0] - 1) % 16, 3] = math.nan
+    out, lse2 = attend(e, q_len)
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[q_len - 1] = False                                           # request 0's last token
+    assert torch.equal(out[same], clean[same]) and torch.isnan(out[q_len - 1].float()).all()
+    assert torch.equal(lse2[same[..., 0]], lse[same[..., 0]]) and qf.status() == 0
+
+
+@pytest.mark.gpu
 def test_no_prefix_and_no_tables(dev):
     d = make(3, 1, 2, 4, 64, 0, [5, 0, 300], HF, seed=2)
     d["prefix_pages"] = d["prefix_len"] = None
