@@ -499,7 +499,8 @@ const char *rope_kv_append_unsupported(const void *q, int64_t q_token_stride, in
  *   head_dim 64 or 128, q_heads 1..64 times num_kv_heads (1..64), q_len
  *   1..1024, num_reqs 0..65535, num_reqs q_len q_heads <= 2^24.
  * Scores, softmax statistics and sums in FP32; the weights exp(s - m) are
- * rounded to dtype for the product with V.  The lengths stay on the device,
+ * rounded to dtype for the product with V (fp16: by no more than 2^-33 of the
+ * row's largest where that is more than half a step).  The lengths stay on the device,
  * so a captured call serves every step up to its tables' widths.
  * PDL-launched; allocates nothing.
  */

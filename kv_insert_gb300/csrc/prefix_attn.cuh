@@ -45,7 +45,20 @@ constexpr int kPaMaxRequests = 65535;
 constexpr int kPaMaxQLen = 1024;
 constexpr int kPaMaxGroup = 64;          // q heads per KV head
 constexpr int kPaThreads = 384;          // 2 softmax groups of 4 warps, 2 producer warps, 2 MMA warps
-constexpr float kPaMost = 16384.f;       // a row's weights of a block may add up to this before its maximum follows
+
+// Weights are 2^(s - mu), mu some bits below the row's maximum: in fp16, whose
+// normal numbers end at 2^-14, a weight of 1 for the maximum would leave keys 14
+// bits below it fewer and fewer bits, and keys 25 below it none, while they
+// still count in the sum (one early key that takes most of the weight, in front
+// of thousands that make the output).  bf16 has the range of FP32.
+// The tile kernel: mu 8 bits below (a block of 128 equal scores stays below the
+// limit); a row's weights of a block may add up to `most` before mu follows.
+// The rows kernel, whose mu follows at once: 15 bits below.
+template <class E>
+struct PaWeight {
+    static constexpr float below = E::is_bf16 ? 0.f : 8.f, most = E::is_bf16 ? 16384.f : 61440.f;
+    static constexpr float below_rows = E::is_bf16 ? 0.f : 15.f;
+};
 
 // Shapes by head width: a block of keys is one ring stage (K and V, 32 KB)
 // and one S tile; each of the two rings holds `slots` of them.
@@ -113,7 +126,7 @@ struct PrefixParams {
     void *out;
     float *lse;
     float *ws_o;      // partial O [split][row][D], prefix splits first
-    float2 *ws_ml;    // partial (maximum in log2 units, sum) [row][split]
+    float2 *ws_ml;    // partial (mu in log2 units, sum) [row][split]
     int64_t num_pages;
     int64_t q_ts, q_hs;
     unsigned long long wait_limit_ns;
@@ -775,7 +788,7 @@ struct PaTile {
             uint32_t so[U], sm[U];
             int keys = KB, outer = 0;   // of the block; the half of the keys in the outer unit
             // The weights of block j, against the maximum so far.  Later scores
-            // may exceed it as long as a block's weights stay below 2^14 in sum
+            // may exceed it as long as a block's weights stay below a limit in sum
             // (so no maximum is taken per block); otherwise it follows and O is
             // rescaled.  An item's first block starts there.
             const auto weigh = [&](int j) {
@@ -793,14 +806,14 @@ struct PaTile {
                     if (again || j > 0) {
                         sum = pa_weights<E>(so, po, cc, base);
                         sum += pa_weights<E>(sm, pm, cc, base);
-                        if (again || !__any_sync(0xffffffffu, !(sum < kPaMost))) break;
+                        if (again || !__any_sync(0xffffffffu, !(sum < PaWeight<E>::most))) break;
                         pa_load_scores<U>(aOut, so);   // not overwritten yet
                         pa_loaded(so);
                         if (hide) pa_hide(so, left - outer * U);
                     }
                     // (only this row's own scores move it, not a neighbour's)
-                    const float top = pa_max(so, pa_max(sm, -INFINITY)) * p.scale_log2;
-                    const bool grew = top > mu && !(sum < kPaMost);
+                    const float top = fmaf(pa_max(so, pa_max(sm, -INFINITY)), p.scale_log2, -PaWeight<E>::below);
+                    const bool grew = top > mu && !(sum < PaWeight<E>::most);
                     const float al = grew ? a2_ex2(mu - top) : 1.f;
                     if (grew) mu = top;
                     base = mu == -INFINITY ? 0.f : -mu;
@@ -1212,7 +1225,8 @@ __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixPar
                     mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
                     mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
                 }
-                const float mn_a = fmaxf(m_a, mx_a * p.scale_log2), mn_b = fmaxf(m_b, mx_b * p.scale_log2);
+                const float mn_a = fmaxf(m_a, fmaf(mx_a, p.scale_log2, -PaWeight<E>::below_rows)),
+                            mn_b = fmaxf(m_b, fmaf(mx_b, p.scale_log2, -PaWeight<E>::below_rows));
                 const float base_a = mn_a == -INFINITY ? 0.f : mn_a, base_b = mn_b == -INFINITY ? 0.f : mn_b;
                 if (__any_sync(0xffffffffu, mn_a != m_a || mn_b != m_b)) {
                     const float al_a = a2_ex2(m_a - base_a), al_b = a2_ex2(m_b - base_b);

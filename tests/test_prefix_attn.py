@@ -237,6 +237,56 @@ def test_scales_and_large_scores(dev, scale, size):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bits", [14.3, 18.4, 21.5, 22.0, 26.0])
+@pytest.mark.parametrize("case", [   # prefix: tiles of 128, 16 and 64 rows; own keys: of 16, 64 and 128
+    (70, 1, 16, 2, 64, 6000, [0] * 70), (140, 1, 8, 1, 128, 9000, [1] * 140), (2, 1, 2, 8, 64, 9000, [3, 0]),
+    (8, 1, 4, 8, 64, 8000, [0] * 8), (40, 1, 4, 4, 128, 0, [900] * 40), (12, 2, 8, 16, 64, 0, [1500] * 12),
+    (4, 70, 8, 1, 64, 0, [4000] * 4), (3, 70, 8, 1, 128, 0, [3000] * 3),
+], ids=lambda c: "-".join(map(str, c[:6])))
+def test_a_dominant_key_leaves_the_others_their_bits(dev, case, bits):
+    """fp16 weights far below a row's largest: one early key with V = 0 takes
+    almost all of the weight, thousands of keys `bits` bits below it make the
+    output.  With the largest weight at 2^8 at least, weights down to 2^-22 of
+    it (2^-14) are rounded to half a step, and no weight by more than half a
+    step of a subnormal, 2^-25, or 2^-33 of the largest."""
+    R, q_len, nkv, G, D, P, lens = case
+    d = make(R, q_len, nkv, G, D, P, lens, HF)
+    low = 1.0 - bits * math.log(2.0) / 16.0
+    cache = d["kv_cache"]
+    used = torch.isfinite(cache[..., :1].float())
+    k, v = torch.zeros_like(cache[..., :D]), cache[..., D:].abs() + 0.5
+    k[..., 0] = low
+    firsts = [d["prefix_pages"][0]] if P else [d["block_table"][r, 0] for r in range(R)]
+    for page in firsts:
+        k[page.long(), :, 0, 0], v[page.long(), :, 0] = 1.0, 0.0
+    d["kv_cache"] = torch.where(used, torch.cat([k, v], -1), cache)
+    d["q"] = torch.zeros_like(d["q"])
+    d["q"][..., 0] = 16.0
+    out, lse = attend(d, q_len, scale=1.0)
+    assert qf.status() == 0
+    half_step = torch.finfo(HF).eps / 2
+    rows = d["kv_cache"].double().permute(0, 2, 1, 3)                     # [pages, 16, nkv, 2 D]
+
+    def keys(entries, n):
+        return rows[entries[:(n + 15) // 16].long()].reshape(-1, nkv, 2 * D)[:n]
+    for r in range(R):
+        for i in range(q_len):
+            kv = torch.cat([keys(d["prefix_pages"], P), keys(d["block_table"][r], max(0, lens[r] - q_len + i + 1))])
+            p = torch.softmax(16.0 * kv[..., 0], 0)[..., None]            # one row of scores a KV head
+            ref, mass = (p * kv[..., D:]).sum(0), (p * kv[..., D:].abs()).sum(0)
+            # scores are exact products (16 k), so exponents are off by their own
+            # rounding alone: 2^-18 with the exponential, the sums and the division
+            tol = half_step * (mass + ref.abs()) * (1 + half_step) + 2 * 2.0 ** -18 * mass + 2.0 ** -24
+            if bits > 22:
+                tol += 2.0 ** -33 * kv[..., D:].abs().sum(0)
+            got = out[r * q_len + i].double().view(nkv, G, D)
+            worst = ((got - ref[:, None]).abs() / tol[:, None]).max()
+            assert worst <= 1, (r, i, float(worst), float(ref.max()))
+    z = torch.logsumexp(16.0 * kv[..., 0], 0)
+    assert (lse[-1].double().view(nkv, G) - z[:, None]).abs().max() <= 2.0 ** -17
+
+
+@pytest.mark.gpu
 def test_rows_do_not_disturb_one_another(dev):
     """A NaN or infinite q row, and keys of +-inf score, stay in their rows."""
     d = make(5, 1, 1, 4, 64, 300, [20, 0, 5, 1, 200], BF, seed=9)
