@@ -53,7 +53,10 @@ constexpr int kPaThreads = 384;          // 2 softmax groups of 4 warps, 2 produ
 // of thousands that make the output).  bf16 has the range of FP32.
 // The tile kernel: mu 8 bits below (a block of 128 equal scores stays below the
 // limit); a row's weights of a block may add up to `most` before mu follows.
-// The rows kernel, whose mu follows at once: 15 bits below.
+// That leaves fp16 8 bits of growth where bf16 has 14: 64 rows x 8 KV heads over
+// 32K keys take 56 us in either for scores of a standard deviation of 1 or 2, 65
+// and 55 for one of 4, 71 and 67 for one of 8.  The rows kernel, whose mu follows
+// at once: 15 bits below.
 template <class E>
 struct PaWeight {
     static constexpr float below = E::is_bf16 ? 0.f : 8.f, most = E::is_bf16 ? 16384.f : 61440.f;
