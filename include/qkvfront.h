@@ -374,6 +374,8 @@ int attn2_split_kv_noalloc(const uint16_t *qkv, const uint16_t *kv_cache, int64_
 #define QKVF_DTYPE_BF16 0
 #define QKVF_DTYPE_FP16 1
 #define QKVF_DTYPE_FP32 2        /* rope only */
+#define QKVF_DTYPE_ZERO_SKIPPED 16  /* or'ed onto a dtype: the rows of out (q_out) that a call would leave as they
+                                       were become 0, for an output without earlier contents */
 
 #define QKVF_ROPE_INTERLEAVED 0  /* pair i: columns 2i, 2i + 1 */
 #define QKVF_ROPE_HALF 1         /* pair i: columns i, i + rot_dim / 2 */

@@ -144,6 +144,7 @@ struct PrefixParams {
     int sp, ss;       // key splits of the prefix and of a request's own keys
     float scale_log2;
     const void *kv_cache;
+    int zero;         // rows left alone have zeros in out instead
 };
 
 // One unit of work: a tile of query rows against a range of key blocks
@@ -1464,10 +1465,14 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
 #pragma unroll
     for (int i = 0; i < kPaMergeAhead; ++i)
         if (first + i * PAR < slots) x[i] = __ldcg(src + (first + i * PAR) * step);
-    if (L < 0 && P >= 0) return;   // a padding request
+    const auto skip = [&]() {
+        if (p.zero && wr == 0 && lane < LPR)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + (int64_t)row * D + 4 * d) = make_uint2(0u, 0u);
+    };
+    if (L < 0 && P >= 0) return skip();   // a padding request
     if (P < 0 || L > p.max_blocks * kPageSlots) {
         if (lane == 0 && wr == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
-        return;
+        return skip();
     }
     const int own = pa_own_keys(p, L, p.own_tiles == 1 ? 0 : ((t - r * p.q_len) * p.group + h % p.group) / p.own_rows);
     const int pkeys = p.small ? kPrKeys : PaShape<D>::keys;
@@ -1485,7 +1490,7 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
         }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    if (__any_sync(0xffffffffu, bad)) return;   // a page outside the cache
+    if (__any_sync(0xffffffffu, bad)) return skip();   // a page outside the cache
     const float base = M == -INFINITY ? 0.f : M;
     float l = 0.f;
 #pragma unroll
@@ -1660,6 +1665,7 @@ const char *check_prefix_args(const void *q, int64_t q_ts, int64_t q_hs, const v
                               int dtype, const void *out, const float *lse, const void *workspace,
                               size_t workspace_bytes, int *code)
 {
+    dtype = dtype_of(dtype);
     if (const char *why = check_prefix_shape(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks,
                                              max_blocks, code))
         return why;
@@ -1754,13 +1760,14 @@ int prefix_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     if (rc != QKVF_OK) return rc;
     const qkvf::PaPlan pl = qkvf::pa_plan(num_reqs, q_len, q_heads, num_kv_heads, head_dim, prefix_blocks, max_blocks, d->sms);
     if (workspace_bytes < qkvf::pa_workspace(pl, (int64_t)num_reqs * q_len * q_heads, head_dim)) return QKVF_ERR_SIZES;
-    const bool bf16 = dtype == QKVF_DTYPE_BF16;
+    const bool bf16 = qkvf::dtype_of(dtype) == QKVF_DTYPE_BF16;
     CUtensorMap map;
     rc = qkvf::encode_prefix_map(kv_cache, num_pages, num_kv_heads, head_dim, bf16, &map);
     if (rc != QKVF_OK) return rc;
     qkvf::PrefixParams prm = {};
     prm.q = q;
     prm.kv_cache = kv_cache;
+    prm.zero = qkvf::zero_skipped(dtype);
     prm.prefix_pages = prefix_pages;
     prm.prefix_len = prefix_len;
     prm.block_table = block_table;

@@ -15,6 +15,7 @@ const char *check_append_args(const void *q, int64_t q_ts, int64_t q_hs, const v
                               int64_t num_pages, int T, int q_heads, int num_kv_heads, int head_dim, int rot_dim,
                               int layout, int dtype, int *code)
 {
+    dtype = dtype_of(dtype);
     *code = QKVF_ERR_TOKENS;
     if (T < 0 || T > kRopeMaxTokens) return "T must be 0..16777216 tokens";
     *code = QKVF_ERR_LAYOUT;
@@ -131,6 +132,8 @@ int rope_kv_append(const void *q, int64_t q_token_stride, int64_t q_head_stride,
     prm.dim = head_dim;
     prm.rot = rot_dim;
     prm.in_place = q == q_out;
+    prm.zero = qkvf::zero_skipped(dtype);
+    dtype = qkvf::dtype_of(dtype);
     prm.sign = 1.f;
     const bool half = layout == QKVF_ROPE_HALF;
     return dtype == QKVF_DTYPE_BF16 ? qkvf::launch_rope<qkvf::Bf16>(prm, half, d->sms, stream)

@@ -33,6 +33,7 @@ SLOT_WIDTH = 128
 MAX_TOKENS = 16
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+DTYPE_ZERO_SKIPPED = 16
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 
@@ -743,14 +744,14 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: str = "n
     return out
 
 
-def _rope_args(x, positions, cos_sin, out, layout, inverse):
+def _rope_args(x, positions, cos_sin, out, layout, inverse, flags=0):
     index, shape = x.get_device(), x.shape
     px, xt, xh = _heads(x, "x", index, DTYPES)
     T, heads, dim = shape
     po, ot, oh = _heads(out, "out", index, (x.dtype,), shape)
     pt, rows, rot = _table(cos_sin, dim, index)
     return (px, xt, xh, _index(positions, "positions", torch.int64, (T,), index), pt, rows, po, ot, oh, T,
-            heads, dim, rot, _layout(layout), inverse, DTYPES[x.dtype])
+            heads, dim, rot, _layout(layout), inverse, DTYPES[x.dtype] | flags)
 
 
 def rope_unsupported(x, positions, cos_sin, out, layout: str = "interleaved") -> str | None:
@@ -763,9 +764,10 @@ def rope_unsupported(x, positions, cos_sin, out, layout: str = "interleaved") ->
 
 
 def _rope(x, positions, cos_sin, out, layout, inverse, stream):
+    flags = 0
     if out is None:
-        out = _new(x.shape, x.dtype, x.device, stream)
-    args = _rope_args(x, positions, cos_sin, out, layout, inverse)
+        out, flags = _new(x.shape, x.dtype, x.device, stream), DTYPE_ZERO_SKIPPED
+    args = _rope_args(x, positions, cos_sin, out, layout, inverse, flags)
     _run("rope", x.get_device(), args, stream)
     return out
 
@@ -775,7 +777,8 @@ def rope(x, positions, cos_sin, out=None, layout: str = "interleaved", stream=No
     dimension contiguous) with the first cos_sin.shape[1] columns of every head
     rotated by row positions[t] of cos_sin; the other columns are copied.
     layout: pairs (2i, 2i + 1) "interleaved" or (i, i + rot_dim / 2) "half".
-    out=x rotates in place.  Returns out."""
+    out=x rotates in place.  A token whose position is no row of cos_sin keeps
+    what out held, or gets zeros in an out made by the call.  Returns out."""
     return _rope(x, positions, cos_sin, out, layout, 0, stream)
 
 
@@ -788,7 +791,7 @@ def rope_backward(grad_out, positions, cos_sin, out=None, layout: str = "interle
 _HALF_TYPES = (torch.bfloat16, torch.float16)
 
 
-def _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout):
+def _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout, flags=0):
     index, dtype, shape = k.get_device(), k.dtype, k.shape
     pk, kt, kh = _heads(k, "k", index, _HALF_TYPES)
     T, nkv, dim = shape
@@ -808,7 +811,7 @@ def _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout):
             raise ValueError(f"q has too many heads: {q_heads}")
     return (pq, qt, qh, pk, kt, kh, pv, vt, vh, _index(positions, "positions", torch.int64, (T,), index),
             _index(slots, "slots", torch.int64, (T,), index), pt, rows, po, ot, oh, pc, pages, T, q_heads,
-            nkv, dim, rot, _layout(layout), DTYPES[dtype])
+            nkv, dim, rot, _layout(layout), DTYPES[dtype] | flags)
 
 
 def rope_kv_append_unsupported(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
@@ -826,10 +829,13 @@ def rope_kv_append(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
     """Rotate q [tokens, q_heads, head_dim] into q_out (q_out=q: in place; None:
     a new tensor) and write the rotated k and v [tokens, num_kv_heads, head_dim]
     into kv_cache [pages, num_kv_heads, 16, 2 head_dim] at each token's slot.
-    q=None appends only.  bf16 or fp16, any strides.  Returns q_out."""
+    q=None appends only.  bf16 or fp16, any strides.  A token whose position is
+    no row of cos_sin keeps what q_out held, or gets zeros in a q_out made by the
+    call.  Returns q_out."""
+    flags = 0
     if q is not None and q_out is None:
-        q_out = _new(q.shape, q.dtype, q.device, stream)
-    args = _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout)
+        q_out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED
+    args = _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout, flags)
     _run("rope_kv_append", k.get_device(), args, stream)
     return q_out
 
@@ -842,7 +848,7 @@ def prefix_attn_workspace_bytes(num_reqs: int, q_len: int, q_heads: int, num_kv_
 
 
 def _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace, q_len,
-                 scale, out, lse):
+                 scale, out, lse, flags=0):
     index, dtype, shape = q.get_device(), q.dtype, q.shape
     pq, qt, qh = _heads(q, "q", index, _HALF_TYPES)
     T, heads, dim = shape
@@ -865,7 +871,7 @@ def _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_len
         raise ValueError("workspace must be a contiguous uint8 CUDA tensor on q's device")
     return (pq, qt, qh, pc, pages, pp, nb, pl, pb, mb,
             _index(context_lens, "context_lens", torch.int32, (R,), index), R, q_len, heads, nkv, dim,
-            dim ** -0.5 if scale is None else scale, DTYPES[dtype], po, ps, workspace.data_ptr(),
+            dim ** -0.5 if scale is None else scale, DTYPES[dtype] | flags, po, ps, workspace.data_ptr(),
             workspace.numel())
 
 
@@ -890,11 +896,14 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens
     own keys, its q_len current tokens among them (a negative length: a padding
     request, left alone); workspace: uint8, prefix_attn_workspace_bytes long.
     scale: None for head_dim^-1/2.  lse: fp32 [num_reqs q_len, q_heads], filled
-    with the rows' ln sum exp when given.  Returns out."""
+    with the rows' ln sum exp when given.  Rows of padding or refused requests
+    keep what out held, or become zeros in an out made by the call.  Returns
+    out."""
+    flags = 0
     if out is None:
-        out = _new(q.shape, q.dtype, q.device, stream)
+        out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED
     args = _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace, q_len,
-                        scale, out, lse)
+                        scale, out, lse, flags)
     _run("prefix_attn", q.get_device(), args, stream)
     return out
 

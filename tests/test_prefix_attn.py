@@ -422,6 +422,33 @@ def test_bad_requests_are_skipped(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", [(6, 2, 2, 4, 64, 150, [30, 10, 64, 20, 2, 300]), (4, 20, 2, 5, 128, 0, [700, 640, 530, 20]),
+                                  (6, 1, 1, 1, 64, 20000, [5, 1, 9, 70, 2, 40])], ids=lambda c: "-".join(map(str, c[:6])))
+def test_skipped_rows_of_a_new_output_are_zero(dev, case):
+    """An output that the call makes holds nothing before: rows of padding, of a
+    length beyond its table and of a bad page must not show what lay there;
+    nor any row behind a bad prefix."""
+    R, q_len, nkv, G, D, P, lens = case
+    d = make(*case, BF)
+    good, _ = attend(d, q_len)
+    ws = workspace(d["q"], d["kv_cache"], d["prefix_pages"], d["block_table"], q_len)
+
+    def new():
+        torch.full_like(d["q"], 3.0)                                  # its memory is the next output's
+        return qf.prefix_attn(d["q"], d["kv_cache"], d["prefix_pages"], d["prefix_len"], d["block_table"],
+                              d["context_lens"], ws, q_len=q_len)
+    assert torch.equal(new(), good) and qf.status() == 0
+    d["context_lens"][0] = -4
+    d["context_lens"][1] = 16 * d["block_table"].shape[1] + 1
+    d["block_table"][2, 0] = d["kv_cache"].shape[0]
+    out = new()
+    assert qf.status() == qf.STATUS_BAD_REQUEST
+    assert torch.all(out[:3 * q_len] == 0) and torch.equal(out[3 * q_len:], good[3 * q_len:])
+    d["prefix_len"][0] = -1
+    assert torch.all(new() == 0) and qf.status() == qf.STATUS_BAD_REQUEST
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("L", [-1, -9, -(2 ** 31) + 3, -(2 ** 31)])
 def test_any_negative_length_is_padding(dev, L):
     """Also where a request's rows are two tiles, whose first ends before the

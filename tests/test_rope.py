@@ -116,6 +116,16 @@ def test_rope_kv_append_refusals(lib):
         assert append_call(lib, **dict(packed, k=X + 1022)) == 9   # k starts inside the last q head
 
 
+def test_zero_skipped_flag(lib):
+    """The flag goes with every type an operator takes, and makes no other type of one."""
+    z = qf.DTYPE_ZERO_SKIPPED
+    for call, types in ((rope_call, (0, 1, 2)), (append_call, (0, 1))):
+        for dt in range(-1, 6):
+            for flag in (z, 2 * z, 3 * z):
+                code = call(lib, dt=dt + flag, T=0)
+                assert code == (0 if dt in types and flag == z else 10), (dt, flag, code)
+
+
 def test_binding_refusals():
     x = torch.zeros(4, 2, 64, dtype=BF)
     with pytest.raises(ValueError, match="CUDA"):
@@ -318,6 +328,35 @@ def test_rope_bad_positions_and_zero_tokens(dev):
     assert qf.rope(x[:0], pos[:0], cs).shape == (0, 2, 64)
     assert qf.rope_unsupported(x, pos, cs, out) is None
     assert "overlap" in qf.rope_unsupported(x[1:], pos[1:], cs, x[:-1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", [BF, FL])
+@pytest.mark.parametrize("shape", [(40, 9, 64, 64), (40, 2, 96, 96), (33, 17, 128, 82), (20, 5, 33, 20), (70, 1, 256, 250)], ids=str)
+def test_skipped_tokens_of_a_new_output_are_zero(dev, shape, dtype, layout):
+    """An output that the call makes holds nothing before: where memory is used
+    again, a token with a bad position must not show what lay there."""
+    x, pos, cs = inputs(*shape, dtype)
+    good = qf.rope(x, pos, cs, layout=layout), qf.rope_backward(x, pos, cs, layout=layout)
+    pos[3], pos[7], pos[-1] = -1, cs.shape[0], 1 << 40
+    keep = torch.ones(shape[0], dtype=torch.bool, device=dev)
+    keep[[3, 7, -1]] = False
+    for f, ref in zip((qf.rope, qf.rope_backward), good):
+        torch.full_like(x, 3.0)                                    # its memory is the next output's
+        out = f(x, pos, cs, layout=layout)
+        assert torch.equal(out[keep], ref[keep]) and torch.all(out[~keep] == 0)
+        assert qf.status() == qf.STATUS_BAD_POSITION
+    if dtype == BF and shape[2] % 8 == 0:
+        nkv, D = 1, shape[2]
+        cache = torch.zeros(8, nkv, 16, 2 * D, dtype=dtype, device=dev)
+        slots = torch.arange(shape[0], device=dev)
+        torch.full_like(x, 3.0)
+        out = qf.rope_kv_append(x, x[:, :1], x[:, :1], pos, slots, cs, cache, layout=layout)
+        assert torch.equal(out[keep], good[0][keep]) and torch.all(out[~keep] == 0)
+        rows = cache.permute(0, 2, 1, 3).reshape(128, 2 * D)
+        assert torch.all(rows[:shape[0]][~keep] == 0) and torch.equal(rows[:shape[0], D:][keep], x[keep, 0])
+        assert qf.status() == qf.STATUS_BAD_POSITION
 
 
 def append_inputs(T, nkv, G, D, rot, dtype, pages, seed=0):
