@@ -736,6 +736,8 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: str = "n
     elif (not out.is_cuda or out.dtype != torch.float32 or tuple(out.shape) != (rows, rot_dim)
           or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous fp32 CUDA tensor [{rows}, {rot_dim}]")
+    elif _Rotation.used and not out.is_inference():
+        torch.autograd.graph.increment_version(out)   # a graph that rope saved the old table for must not use this one
     if magnitude is None:
         magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "ramp" and factor > 0 else 1.0
     _run("rope_table", out.device.index,
@@ -763,7 +765,48 @@ def rope_unsupported(x, positions, cos_sin, out, layout: str = "interleaved") ->
     return _why("rope", x.get_device(), args)
 
 
+class _Rotation(torch.autograd.Function):
+    """rope as a node of the autograd graph: its gradient is the rotation back
+    (which is a node in turn, where a graph of the gradient is asked for)."""
+
+    used = False   # whether a graph may hold a table
+
+    @staticmethod
+    def forward(ctx, x, positions, cos_sin, layout, inverse):
+        _Rotation.used = True
+        ctx.save_for_backward(positions, cos_sin)
+        ctx.turn = layout, inverse
+        return _rope(x, positions, cos_sin, None, layout, inverse, None)
+
+    @staticmethod
+    def backward(ctx, grad):
+        positions, cos_sin = ctx.saved_tensors
+        layout, inverse = ctx.turn
+        if grad.stride(-1) != 1:   # the gradient of a sum, say: one value, expanded
+            grad = grad.contiguous()
+        return _rope(grad, positions, cos_sin, None, layout, 1 - inverse, None), None, None, None, None
+
+
+def _rope_with_grad(x, positions, cos_sin, out, layout, inverse, stream):
+    if cos_sin.requires_grad:
+        raise ValueError("no gradient is formed with respect to cos_sin: detach it")
+    if out is not None:
+        raise ValueError("a call into out is not part of the autograd graph, but x requires a gradient: "
+                         "leave out None, or call under torch.no_grad() (its gradient is rope_backward)")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+    with torch.cuda.device(x.device), torch.cuda.stream(stream):   # backward runs where forward did
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured call is not part of the autograd graph, but x requires a gradient: "
+                             "capture rope and rope_backward under torch.no_grad()")
+        return _Rotation.apply(x, positions, cos_sin, layout, inverse)
+
+
 def _rope(x, positions, cos_sin, out, layout, inverse, stream):
+    if torch.is_grad_enabled() and (x.requires_grad or cos_sin.requires_grad):
+        return _rope_with_grad(x, positions, cos_sin, out, layout, inverse, stream)
     flags = 0
     if out is None:
         out, flags = _new(x.shape, x.dtype, x.device, stream), DTYPE_ZERO_SKIPPED
@@ -778,7 +821,8 @@ def rope(x, positions, cos_sin, out=None, layout: str = "interleaved", stream=No
     rotated by row positions[t] of cos_sin; the other columns are copied.
     layout: pairs (2i, 2i + 1) "interleaved" or (i, i + rot_dim / 2) "half".
     out=x rotates in place.  A token whose position is no row of cos_sin keeps
-    what out held, or gets zeros in an out made by the call.  Returns out."""
+    what out held, or gets zeros in an out made by the call.  Without out the
+    result is part of x's autograd graph.  Returns out."""
     return _rope(x, positions, cos_sin, out, layout, 0, stream)
 
 
@@ -831,7 +875,7 @@ def rope_kv_append(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
     into kv_cache [pages, num_kv_heads, 16, 2 head_dim] at each token's slot.
     q=None appends only.  bf16 or fp16, any strides.  A token whose position is
     no row of cos_sin keeps what q_out held, or gets zeros in a q_out made by the
-    call.  Returns q_out."""
+    call.  For serving: no part of an autograd graph.  Returns q_out."""
     flags = 0
     if q is not None and q_out is None:
         q_out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED
@@ -897,8 +941,8 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens
     request, left alone); workspace: uint8, prefix_attn_workspace_bytes long.
     scale: None for head_dim^-1/2.  lse: fp32 [num_reqs q_len, q_heads], filled
     with the rows' ln sum exp when given.  Rows of padding or refused requests
-    keep what out held, or become zeros in an out made by the call.  Returns
-    out."""
+    keep what out held, or become zeros in an out made by the call.  For
+    serving: no part of an autograd graph.  Returns out."""
     flags = 0
     if out is None:
         out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED

@@ -268,6 +268,93 @@ def test_rope_backward_is_the_gradient(dev, layout):
 @pytest.mark.gpu
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("dtype", [BF, FL])
+def test_rope_in_an_autograd_graph(dev, layout, dtype):
+    """The result belongs to x's graph: its gradient is rope_backward's, through
+    views, expanded gradients, a broadcast x and a graph of the gradient."""
+    x, pos, cs = inputs(6, 3, 40, 24, dtype)
+    g = torch.randn(6, 3, 40, generator=torch.Generator().manual_seed(6)).to(dtype).to(dev)
+    leaf = x.clone().requires_grad_()
+    y = qf.rope(leaf, pos, cs, layout=layout)
+    assert y.requires_grad and torch.equal(y, qf.rope(x, pos, cs, layout=layout))
+    y.backward(g)
+    assert torch.equal(leaf.grad, qf.rope_backward(g, pos, cs, layout=layout))
+    leaf.grad = None
+    qf.rope(leaf, pos, cs, layout=layout).sum().backward()            # a gradient with strides of 0
+    assert torch.equal(leaf.grad, qf.rope_backward(torch.ones_like(x), pos, cs, layout=layout))
+    leaf.grad = None
+    qf.rope(leaf, pos, cs, layout=layout).backward(g.transpose(1, 2).contiguous().transpose(1, 2))
+    assert torch.equal(leaf.grad, qf.rope_backward(g, pos, cs, layout=layout))
+    packed = torch.randn(6, 5 * 40, generator=torch.Generator().manual_seed(7)).to(dtype).to(dev).requires_grad_()
+    qf.rope(packed[:, 40:160].view(6, 3, 40), pos, cs, layout=layout).backward(g)
+    assert torch.equal(packed.grad[:, 40:160].reshape(6, 3, 40), qf.rope_backward(g, pos, cs, layout=layout))
+    assert torch.all(packed.grad[:, :40] == 0) and torch.all(packed.grad[:, 160:] == 0)
+    one = x[:, :1].detach().clone().requires_grad_()
+    qf.rope(one.expand(6, 3, 40), pos, cs, layout=layout).backward(g)   # one head shared by three
+    ref, slack = turned(g, cs[pos], layout, True)
+    # three gradients, each within its bound of the formula, and two sums of them
+    tol = (slack + torch.finfo(dtype).eps / 2 * (ref.abs() + slack)).sum(1) + torch.finfo(dtype).eps * 1.01 * ref.abs().sum(1)
+    assert ((one.grad[:, 0].double() - ref.sum(1)).abs() <= tol).all()
+    pos[2] = -1                                                       # a skipped token takes no part
+    leaf.grad = None
+    qf.rope(leaf, pos, cs, layout=layout).backward(g)
+    assert torch.all(leaf.grad[2] == 0) and torch.equal(leaf.grad[3], qf.rope_backward(g[3:4], pos[3:4], cs, layout=layout)[0])
+    assert qf.status() == qf.STATUS_BAD_POSITION
+    pos[2] = 5
+    if dtype == FL:
+        w = torch.randn_like(x, requires_grad=True)
+        y = qf.rope(leaf, pos, cs, layout=layout)
+        grad, = torch.autograd.grad(y, leaf, w, create_graph=True)
+        grad.backward(g)                                              # linear in w: turned forth again
+        assert torch.equal(w.grad, qf.rope(g, pos, cs, layout=layout))
+    table = cs.clone()
+    y = qf.rope(leaf, pos, table, layout=layout)
+    qf.rope_table(cs.shape[0], cs.shape[1], first_position=9, out=table)   # the graph's table is gone
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward(g)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    leaf.grad = None
+    y = qf.rope(leaf, pos, cs, layout=layout, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    y.backward(g)
+    torch.cuda.synchronize()
+    assert torch.equal(leaf.grad, qf.rope_backward(g, pos, cs, layout=layout))
+
+
+@pytest.mark.gpu
+def test_rope_refuses_a_lost_gradient(dev):
+    """Where the result cannot belong to the graph, no gradient is lost in
+    silence; without gradients asked for, the same calls run."""
+    x, pos, cs = inputs(4, 2, 64, 64, BF)
+    leaf = x.clone().requires_grad_()
+    out = torch.empty_like(x)
+    for f in (qf.rope, qf.rope_backward):
+        with pytest.raises(ValueError, match="no_grad"):
+            f(leaf, pos, cs, out=out)
+        with pytest.raises(ValueError, match="cos_sin"):
+            f(x, pos, cs.clone().requires_grad_())
+        with torch.no_grad():
+            ref = f(x, pos, cs)
+            assert f(leaf, pos, cs, out=out) is out and torch.equal(out, ref)
+            assert not f(leaf, pos, cs).requires_grad
+    keep = qf.rope(leaf, pos, cs)                                      # a graph of the leaf that lives on
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="captured"):
+            qf.rope(leaf, pos, cs)
+        with torch.no_grad():
+            y = qf.rope(leaf, pos, cs)
+            dx = qf.rope_backward(y, pos, cs)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, keep) and torch.equal(dx, qf.rope_backward(keep.detach(), pos, cs))
+    keep.backward(x)
+    assert torch.equal(leaf.grad, qf.rope_backward(x, pos, cs)) and qf.status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", [BF, FL])
 def test_rope_strided_views(dev, layout, dtype):
     """q and k columns of packed rows in place, a transposed [heads, tokens]
     buffer, a misaligned start, a broadcast input."""
