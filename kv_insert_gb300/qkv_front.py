@@ -732,6 +732,8 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: str = "n
         raise ValueError("first_position and original_len must be 0..2^40")
     if out is None:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"the table is made on a CUDA device, not on {device}")
         out = _new((rows, rot_dim), torch.float32, device, stream)
     elif (not out.is_cuda or out.dtype != torch.float32 or tuple(out.shape) != (rows, rot_dim)
           or not out.is_contiguous()):

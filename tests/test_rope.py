@@ -116,6 +116,13 @@ def test_rope_kv_append_refusals(lib):
         assert append_call(lib, **dict(packed, k=X + 1022)) == 9   # k starts inside the last q head
 
 
+def test_table_on_the_host_is_refused():
+    with pytest.raises(ValueError, match="CUDA"):
+        qf.rope_table(8, 64, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        qf.rope_table(8, 64, out=torch.zeros(8, 64))
+
+
 def test_zero_skipped_flag(lib):
     """The flag goes with every type an operator takes, and makes no other type of one."""
     z = qf.DTYPE_ZERO_SKIPPED
