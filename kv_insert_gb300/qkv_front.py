@@ -681,7 +681,7 @@ def _heads(t, name: str, index: int, dtypes, shape=None):
 
 
 def _index(t, name: str, dtype, shape, index: int):
-    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {shape}, on the other tensors' device")
     return t.data_ptr()
 
@@ -862,8 +862,11 @@ def _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout, fl
 
 def rope_kv_append_unsupported(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
                                layout: str = "interleaved") -> str | None:
-    """Why rope_kv_append would refuse this call (into q_out), or None."""
+    """Why rope_kv_append would refuse this call (into q_out; None: a new
+    tensor), or None."""
     try:
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         args = _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout)
     except ValueError as e:
         return str(e)
@@ -913,7 +916,7 @@ def _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_len
     po = _index(out, "out", dtype, shape, index)
     if lse is not None:
         ps = _index(lse, "lse", torch.float32, (T, heads), index)
-    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index:
+    if workspace is None or workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError("workspace must be a contiguous uint8 CUDA tensor on q's device")
     return (pq, qt, qh, pc, pages, pp, nb, pl, pb, mb,
             _index(context_lens, "context_lens", torch.int32, (R,), index), R, q_len, heads, nkv, dim,

@@ -123,6 +123,29 @@ def test_table_on_the_host_is_refused():
         qf.rope_table(8, 64, out=torch.zeros(8, 64))
 
 
+@pytest.mark.gpu
+def test_reasons_for_new_outputs_and_missing_tensors(dev):
+    """The reason functions take what the calls take: an output left to the call,
+    a tensor that is missing."""
+    q, k, v, pos, slots, cs, cache = append_inputs(5, 2, 3, 64, 64, BF, 3)
+    assert qf.rope_kv_append_unsupported(q, k, v, pos, slots, cs, cache) is None
+    assert qf.rope_kv_append_unsupported(None, k, v, pos, slots, cs, cache) is None
+    assert "slots" in qf.rope_kv_append_unsupported(q, k, v, pos, slots[:4], cs, cache)
+    assert "positions" in qf.rope_kv_append_unsupported(q, k, v, None, slots, cs, cache)
+    assert "q" in qf.rope_kv_append_unsupported(q.cpu(), k, v, pos, slots, cs, cache)
+    out, pages = torch.empty_like(q), torch.zeros(2, dtype=torch.int32, device=dev)
+    lens = torch.zeros(5, dtype=torch.int32, device=dev)
+    ws = torch.empty(qf.prefix_attn_workspace_bytes(5, 1, 6, 2, 64, 2, 0), dtype=torch.uint8, device=dev)
+    assert qf.prefix_attn_unsupported(q, cache, pages, lens[:1], None, lens, ws, out) is None
+    for change, name in ((dict(prefix_len=None), "prefix_len"), (dict(context_lens=None), "context_lens"),
+                         (dict(workspace=None), "workspace"), (dict(out=None), "out")):
+        a = dict(dict(prefix_len=lens[:1], context_lens=lens, workspace=ws, out=out), **change)
+        assert name in qf.prefix_attn_unsupported(q, cache, pages, a["prefix_len"], None, a["context_lens"],
+                                                  a["workspace"], a["out"])
+    with pytest.raises(ValueError, match="prefix_len"):
+        qf.prefix_attn(q, cache, pages, None, None, lens, ws)
+
+
 def test_zero_skipped_flag(lib):
     """The flag goes with every type an operator takes, and makes no other type of one."""
     z = qf.DTYPE_ZERO_SKIPPED
