@@ -392,8 +392,9 @@ int attn2_split_kv_noalloc(const uint16_t *qkv, const uint16_t *kv_cache, int64_
  *   table[r][i] = magnitude cos(p f_i), table[r][rot_dim / 2 + i] = magnitude sin(p f_i), p = first + r,
  * with the pairs' frequencies f_i scaled for long contexts as named above
  * (factor >= 1; original_len, slow and fast are read by QKVF_ROPE_RAMP only).
- * Angles are kept modulo one turn in 64-bit fixed point: their error is that
- * of the 64-bit frequency, not of a 32-bit product, at any position.
+ * Angles are kept modulo one turn in 64-bit fixed point: what grows with the
+ * position is the error of the frequency as a double (about position f 2^-51
+ * radians), not that of a 32-bit product; cos and sin add 2^-22 or so.
  *   table    [rows, rot_dim] fp32, device memory, 16-byte aligned
  *   rows 0..2^32 (0: no launch), first 0..2^40, rot_dim even 2..512,
  *   base in (1, 1e30], magnitude in (0, 1e6].

@@ -115,10 +115,11 @@ bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
 constexpr int kRtMaxPairs = kRopeMaxDim / 2;
 
-// Each pair's frequency in turns per position as a 64-bit fraction: a
-// position's angle is the low 64 bits of position * rate, exact modulo one
-// turn however far the position (a 32-bit product of both would lose the
-// angle beyond 2^24 / f positions).
+// Each pair's frequency in turns per position as a 64-bit fraction, from a
+// double: a position's angle is the low 64 bits of position * rate.  The product
+// loses nothing however far the position, so the angle is off by the
+// frequency's own error alone, about position f 2^-51 radians (a 32-bit
+// product would lose the angle beyond 2^24 / f positions).
 struct RopeTableParams {
     float *table;
     int64_t first;
@@ -129,7 +130,8 @@ struct RopeTableParams {
 };
 
 // A thread keeps one pair and walks the rows: the next row's phase is a 64-bit
-// sum.  The phase's top 32 bits, signed, are its angle in 2^-31 half turns.
+// sum.  The phase's top 32 bits, signed, are its angle in 2^-31 half turns, and
+// rounded to fp32 for the sine and cosine (2^-25 half turns at most).
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ RopeTableParams p)
 {
     if (threadIdx.x == 0) griddep_launch_dependents();

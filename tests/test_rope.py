@@ -1,6 +1,7 @@
 """rope_table, rope / rope_backward and rope_kv_append: refusals on the host
 (no GPU needed), then values against plain 64-bit formulas at the layouts,
 widths, strides, types and indices where they can go wrong."""
+import decimal
 import math
 
 import pytest
@@ -206,6 +207,29 @@ def test_rope_table(dev, rows, rot, first, kw):
     # (2^-24 each), the 64-bit angle itself is good to 1e-9 here
     tol = mag * (math.pi * 2.0 ** -24 + 2.0 ** -23 + 2 * 2.0 ** -24 + 1e-9)
     assert (got - ref).abs().max() <= tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [0, (1 << 24) + 3, (1 << 31) - 1, (1 << 36) + 77, 1 << 40])
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("linear", 8.0)])
+def test_rope_table_at_far_positions(dev, first, scaling, factor):
+    """Against angles to 60 digits.  The fixed-point product loses nothing, so
+    what a position multiplies is the error of the frequency as a double: a
+    power (1 ulp, 2^-52), one or two divisions and the constant of a turn
+    (2^-53 each), and the 64-bit rate's 2^-64 turns."""
+    rows, rot, base = 3, 32, 10000.0
+    got = qf.rope_table(rows, rot, base=base, scaling=scaling, factor=factor, first_position=first, device=dev).cpu().double()
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        turn = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+        for i in range(rot // 2):
+            f = (decimal.Decimal(base).ln() * decimal.Decimal(-2 * i) / rot).exp() / decimal.Decimal(factor)
+            for r in range(rows):
+                p = first + r
+                angle = 2 * math.pi * float((p * f / turn) % 1)
+                tol = math.pi * 2.0 ** -24 + 2.0 ** -23 + 2.0 ** -24 + p * float(f) * 2.0 ** -50 + 2 * math.pi * p * 2.0 ** -64
+                assert abs(float(got[r, i]) - math.cos(angle)) <= tol and \
+                    abs(float(got[r, rot // 2 + i]) - math.sin(angle)) <= tol, (p, i)
 
 
 @pytest.mark.gpu
