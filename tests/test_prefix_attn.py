@@ -493,6 +493,60 @@ def test_a_bad_page_voids_its_request_alone(dev, P):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,q_len,nkv,G,D,blocks,dtype", [
+    (70, 1, 2, 2, 64, 1200, BF), (70, 1, 1, 4, 128, 600, HF), (300, 1, 1, 1, 64, 2048, HF),   # pairs of tiles
+    (100, 1, 2, 1, 64, 512, BF), (40, 1, 3, 1, 64, 1100, HF), (5, 4, 1, 2, 128, 700, BF),     # one tile
+    (9, 8, 1, 1, 64, 1500, BF), (4, 40, 1, 2, 64, 900, BF),                                   # own keys of 16 and 128 rows
+])
+def test_short_prefix_in_a_wide_table(dev, R, q_len, nkv, G, D, blocks, dtype):
+    """A captured call with room for a long prefix serves every shorter one:
+    splits, groups and blocks of threads without keys, a first page that is not
+    the one fetched ahead, partials that nothing wrote.  The entries behind the
+    length name no page, the workspace holds NaN."""
+    own = [q_len + r % 20 for r in range(R)] if q_len < 40 else [600 + r for r in range(R)]
+    lengths = [0, 1, 127, 129, 1000, 16 * blocks - 5]
+    calls = [make(R, q_len, nkv, G, D, P, own, dtype, seed=3) for P in lengths]
+    pages = max(c["kv_cache"].shape[0] for c in calls)
+    buf = {n: torch.zeros_like(t) for n, t in calls[0].items()}
+    buf["kv_cache"] = torch.zeros(pages, nkv, 16, 2 * D, dtype=dtype, device=dev)
+    buf["prefix_pages"] = torch.full((blocks,), 1 << 30, dtype=torch.int32, device=dev)
+    buf["block_table"] = torch.full((R, max(c["block_table"].shape[1] for c in calls)), -9, dtype=torch.int32, device=dev)
+    ws = workspace(buf["q"], buf["kv_cache"], buf["prefix_pages"], buf["block_table"], q_len)
+    out = torch.zeros_like(buf["q"])
+    lse = torch.zeros(out.shape[:2], device=dev)
+
+    def fill(c):
+        for n in ("q", "context_lens", "prefix_len"):
+            buf[n].copy_(c[n])
+        buf["kv_cache"].fill_(math.nan)
+        buf["kv_cache"][:c["kv_cache"].shape[0]] = c["kv_cache"]
+        buf["prefix_pages"].fill_(1 << 30)
+        n = min(blocks, c["prefix_pages"].shape[0] - 1)
+        buf["prefix_pages"][:n] = c["prefix_pages"][:n]
+        buf["block_table"].fill_(-9)
+        buf["block_table"][:, :c["block_table"].shape[1]] = c["block_table"]
+        ws.fill_(0xFF)
+
+    def call():
+        qf.prefix_attn(buf["q"], buf["kv_cache"], buf["prefix_pages"], buf["prefix_len"], buf["block_table"],
+                       buf["context_lens"], ws, q_len=q_len, out=out, lse=lse)
+    fill(calls[0])
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i, (P, c) in enumerate(zip(lengths + lengths[::-1], calls + calls[::-1])):
+        fill(c)
+        out.fill_(3.0)
+        lse.fill_(5.0)
+        call() if i % 2 else graph.replay()
+        torch.cuda.synchronize()
+        check(buf, q_len, out, lse)
+    assert qf.status() == 0
+
+
+@pytest.mark.gpu
 def test_workspace_bounds(dev):
     d = make(3, 1, 1, 8, 64, 1500, [3, 40, 100], BF, seed=6)
     n = qf.prefix_attn_workspace_bytes(3, 1, 8, 1, 64, d["prefix_pages"].shape[0], d["block_table"].shape[1])
