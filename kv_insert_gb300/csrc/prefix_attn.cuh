@@ -37,6 +37,8 @@
 // rows the keys' bytes bound it: 8 rows x 8 KV heads of 128 over 128K keys take
 // 82.6 us, 80.3 at the copy rate.  Short calls are two launches: 5.8 us.
 
+#include <type_traits>
+
 #include "prefix_plan.h"
 
 namespace qkvf {
@@ -362,12 +364,6 @@ __device__ __forceinline__ void pa_issue_scores(uint32_t addr, uint32_t *s, uint
         pa_tmem_ld32(addr + c, s + c);
         pa_tmem_ld32(addr2 + c, s2 + c);
     }
-}
-template <int N>
-__device__ __forceinline__ void pa_load_scores(uint32_t addr, uint32_t *s, uint32_t addr2, uint32_t *s2)
-{
-    pa_issue_scores<N>(addr, s, addr2, s2);
-    tmem_ld_wait();
 }
 
 // Behind the wait for a load: no use of its registers moves ahead of here

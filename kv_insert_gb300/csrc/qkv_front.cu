@@ -42,7 +42,6 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <type_traits>
 
 #include "qkvfront.h"
 
