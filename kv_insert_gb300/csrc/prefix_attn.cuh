@@ -53,16 +53,14 @@ constexpr int kPaThreads = 384;          // 2 softmax groups of 4 warps, 2 produ
 // bits below it fewer and fewer bits, and keys 25 below it none, while they
 // still count in the sum (one early key that takes most of the weight, in front
 // of thousands that make the output).  bf16 has the range of FP32.
-// The tile kernel: mu 8 bits below (a block of 128 equal scores stays below the
-// limit); a row's weights of a block may add up to `most` before mu follows.
-// That leaves fp16 8 bits of growth where bf16 has 14: 64 rows x 8 KV heads over
+// 8 bits: in the tile kernel a row's weights of a block may add up to `most`
+// before mu follows, and a block of 128 equal scores stays below that.  It leaves
+// fp16 8 bits of growth where bf16 has 14: 64 rows x 8 KV heads over
 // 32K keys take 56 us in either for scores of a standard deviation of 1 or 2, 65
-// and 55 for one of 4, 71 and 67 for one of 8.  The rows kernel, whose mu follows
-// at once: 15 bits below.
+// and 55 for one of 4, 71 and 67 for one of 8.
 template <class E>
 struct PaWeight {
     static constexpr float below = E::is_bf16 ? 0.f : 8.f, most = E::is_bf16 ? 16384.f : 61440.f;
-    static constexpr float below_rows = E::is_bf16 ? 0.f : 15.f;
 };
 
 // Shapes by head width: a block of keys is one ring stage (K and V, 32 KB)
@@ -1225,8 +1223,8 @@ __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixPar
                     mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
                     mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
                 }
-                const float mn_a = fmaxf(m_a, fmaf(mx_a, p.scale_log2, -PaWeight<E>::below_rows)),
-                            mn_b = fmaxf(m_b, fmaf(mx_b, p.scale_log2, -PaWeight<E>::below_rows));
+                const float mn_a = fmaxf(m_a, fmaf(mx_a, p.scale_log2, -PaWeight<E>::below)),
+                            mn_b = fmaxf(m_b, fmaf(mx_b, p.scale_log2, -PaWeight<E>::below));
                 const float base_a = mn_a == -INFINITY ? 0.f : mn_a, base_b = mn_b == -INFINITY ? 0.f : mn_b;
                 if (__any_sync(0xffffffffu, mn_a != m_a || mn_b != m_b)) {
                     const float al_a = a2_ex2(m_a - base_a), al_b = a2_ex2(m_b - base_b);
