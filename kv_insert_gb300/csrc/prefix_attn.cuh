@@ -161,10 +161,16 @@ struct PaItem {
     int split;       // partial slot
 };
 
-__device__ __forceinline__ int pa_prefix_len(const PrefixParams &p)
+// past: past L1, in a kernel that starts without a wait of its own (elsewhere
+// L1 is worth having: 64 requests' own keys without a prefix 20.3 us and 21.2, 33
+// rows x 4 KV heads of 128 over 16K 21.6 and 22.6)
+template <class T>
+__device__ __forceinline__ T pa_load(const T *ptr, bool past) { return past ? __ldcg(ptr) : *ptr; }
+
+__device__ __forceinline__ int pa_prefix_len(const PrefixParams &p, bool past)
 {
     if (p.prefix_blocks == 0) return 0;
-    const int P = __ldcg(p.prefix_len);
+    const int P = pa_load(p.prefix_len, past);
     return P > p.prefix_blocks * kPageSlots ? -1 : P;
 }
 
@@ -544,7 +550,7 @@ struct PaTile {
 
     // The prefix's length, the same register for the whole warp.  What a role's
     // first item needs besides is fetched beside it.
-    __device__ __forceinline__ int length() const { return __reduce_max_sync(0xffffffffu, pa_prefix_len(p)); }
+    __device__ __forceinline__ int length() const { return __reduce_max_sync(0xffffffffu, pa_prefix_len(p, kOwn)); }
     __device__ __forceinline__ volatile int *flags() const { return reinterpret_cast<volatile int *>(smem + LY.flags); }
     __device__ __forceinline__ void wait(uint32_t bar, int n) const   // until phase n of bar is complete
     {
@@ -567,7 +573,7 @@ struct PaTile {
         int guess = -1, entry = 0;   // the first entries as of a full table
         if (!kOwn && Work(p, p.prefix_blocks * kPageSlots, w).next(it)) {
             guess = it.kb0 * Sh::pages;
-            if (guess + lane < p.prefix_blocks) entry = __ldcg(it.pages + guess + lane);
+            if (guess + lane < p.prefix_blocks) entry = pa_load(it.pages + guess + lane, kOwn);
         }
         Work work(p, length(), w);
         bool ok = true;
@@ -577,10 +583,10 @@ struct PaTile {
         while (ok && work.next(it)) {
             const int pg0 = it.kb0 * Sh::pages;
             const int pg1 = min(it.kb1 * Sh::pages, (it.keys + kPageSlots - 1) / kPageSlots);
-            int next = pg0 + lane < pg1 ? (pg0 == guess ? entry : __ldcg(it.pages + pg0 + lane)) : 0;
+            int next = pg0 + lane < pg1 ? (pg0 == guess ? entry : pa_load(it.pages + pg0 + lane, kOwn)) : 0;
             for (int c = pg0; c < pg1 && ok; c += 32) {
                 int page = next;
-                if (c + 32 + lane < pg1) next = __ldcg(it.pages + c + 32 + lane);
+                if (c + 32 + lane < pg1) next = pa_load(it.pages + c + 32 + lane, kOwn);
                 bool bad = false;
                 if (c + lane < pg1 && (page < 0 || page >= p.num_pages)) {   // flagged, page 0 in its place
                     bad = true;
@@ -754,7 +760,7 @@ struct PaTile {
                     static_cast<const uint16_t *>(p.q) + (it.tok0 + tok) * p.q_ts + head * p.q_hs);
                 uint4 v[D / 8];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = valid ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < D / 8; ++c) v[c] = valid ? pa_load(src + c, kOwn) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
                     *reinterpret_cast<uint4 *>(sq + (c / 8) * (kPaTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
@@ -957,7 +963,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (threadIdx.x == 0) griddep_launch_dependents();
         if (!behind) griddep_wait();
         PaItem it;
-        const int P = pa_prefix_len(p);
+        const int P = pa_prefix_len(p, kOwn);
         const bool any = PaWork<D, kOwn>(p, P, 0).next(it) | PaWork<D, kOwn>(p, P, 1).next(it);
         if (!any) {   // requests without keys
             if (behind && last) griddep_wait();
@@ -1061,6 +1067,9 @@ __device__ __forceinline__ void pr_mma(float (&d)[4], const uint32_t (&a)[4], ui
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Whether the tile kernel runs in front of the rows kernel
+__device__ __forceinline__ bool pr_behind(const PrefixParams &p) { return !p.small && p.prefix_blocks > 0; }
+
 // One item against its key blocks: RT = 16 or 64 rows.  kTokens: some rows may
 // see fewer keys than others (requests of several tokens; without the code for
 // that 64 requests' own keys take 21.2 us instead of 21.4, and with a 32K prefix
@@ -1137,16 +1146,17 @@ __device__ __forceinline__ void pr_item(const CUtensorMap &tmKV, const PrefixPar
         const int ma = it.row0 + row_a, mb = it.row0 + row_b, ta = ma / p.group, tb = mb / p.group;
         const bool va = row_a < it.rows, vb = row_b < it.rows;
         uint32_t qa[D / 16][4];
+        const bool past = pr_behind(p);
         {
             const uint16_t *qp = static_cast<const uint16_t *>(p.q);
             const uint16_t *pa = qp + (it.tok0 + ta) * p.q_ts + (g * p.group + ma - ta * p.group) * p.q_hs + 2 * t;
             const uint16_t *pb = qp + (it.tok0 + tb) * p.q_ts + (g * p.group + mb - tb * p.group) * p.q_hs + 2 * t;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                qa[k][0] = va ? __ldcg(reinterpret_cast<const uint32_t *>(pa + 16 * k)) : 0u;
-                qa[k][1] = vb ? __ldcg(reinterpret_cast<const uint32_t *>(pb + 16 * k)) : 0u;
-                qa[k][2] = va ? __ldcg(reinterpret_cast<const uint32_t *>(pa + 16 * k + 8)) : 0u;
-                qa[k][3] = vb ? __ldcg(reinterpret_cast<const uint32_t *>(pb + 16 * k + 8)) : 0u;
+                qa[k][0] = va ? pa_load(reinterpret_cast<const uint32_t *>(pa + 16 * k), past) : 0u;
+                qa[k][1] = vb ? pa_load(reinterpret_cast<const uint32_t *>(pb + 16 * k), past) : 0u;
+                qa[k][2] = va ? pa_load(reinterpret_cast<const uint32_t *>(pa + 16 * k + 8), past) : 0u;
+                qa[k][3] = vb ? pa_load(reinterpret_cast<const uint32_t *>(pb + 16 * k + 8), past) : 0u;
             }
         }
 #pragma unroll
@@ -1394,7 +1404,7 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
     // its end.  A CTA without a wait of its own may find an older copy of a line
     // in its SM's L1, so q, the lengths and the tables are read past it (keys
     // come by TMA, from L2).
-    const bool behind = !p.small && p.prefix_blocks > 0;
+    const bool behind = pr_behind(p);
     if (!behind) griddep_wait();
 
     int idx = blockIdx.x;
@@ -1408,7 +1418,7 @@ __global__ void __launch_bounds__(kPrThreads, pr_ctas_per_sm<D, (RTP > RTO ? RTP
     // the first split starts at page 0: its entries need not wait for a length
     int first_entry = 0;
     if (warp == 4 && split == 0 && lane < (own ? p.max_blocks : p.prefix_blocks)) first_entry = __ldcg(pages + lane);
-    const int P = pa_prefix_len(p), L = own ? __ldcg(p.context_lens + r) : 0;
+    const int P = pa_prefix_len(p, true), L = own ? __ldcg(p.context_lens + r) : 0;
     const PaItem it = own ? pa_own_item<kPrKeys>(p, P, L, r, tile, g, split) : pa_prefix_item<kPrKeys>(p, max(P, 0), RTP, 0, g, split);
     if (it.kb1 > it.kb0) {
         if constexpr (RTP == RTO) {
@@ -1450,7 +1460,7 @@ __global__ void __launch_bounds__(pa_merge_threads(kWarps)) prefix_merge_kernel(
     const int first = wr * (32 / LPR) + lane / LPR, d = lane % LPR;   // this lane's first slot, its 4 columns
     const float4 *src = reinterpret_cast<const float4 *>(p.ws_o + (int64_t)row * D) + d;
     const int64_t step = (int64_t)p.rows * (D / 4);
-    const int P = pa_prefix_len(p), L = __ldcg(p.context_lens + r);
+    const int P = pa_prefix_len(p, false), L = p.context_lens[r];
     float2 v[2 * kPaMaxSplits / 32];
 #pragma unroll
     for (int i = 0; i < 2 * kPaMaxSplits / 32; ++i)
