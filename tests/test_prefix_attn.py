@@ -589,6 +589,45 @@ def test_far_pages(dev):
 
 
 @pytest.mark.gpu
+def test_the_most_rows(dev):
+    """65535 requests and nearly 2^24 rows: offsets of out, q and the partials
+    pass 2^31 bytes, and the last of them are right."""
+    R, nkv, G, D, P = 65535, 4, 64, 64, 200
+    d = make(4, 1, nkv, G, D, P, [0, 5, 33, 1], BF, seed=12)
+    want, want_lse = attend(d, 1)
+    check(d, 1, want, want_lse)
+    rows = torch.arange(R, device=dev) % 4
+    big = dict(d, q=d["q"][rows], block_table=d["block_table"][rows].contiguous(),
+               context_lens=d["context_lens"][rows].contiguous())
+    out, lse = attend(big, 1)
+    assert qf.status() == 0
+    half_step = torch.finfo(BF).eps / 2
+    for r in range(4):   # the split may differ from the small call's: each within its own bound of the formula
+        tol = 2 * half_step * (1 + half_step) * (2 * want[r].abs().amax().float() + 4)
+        assert ((out[r::4].float() - want[r].float()).abs() <= tol).all()
+        assert torch.equal(out[r::4], out[r].expand_as(out[r::4])) and torch.equal(lse[r::4], lse[r].expand_as(lse[r::4]))
+    last = {n: big[n][-4:].contiguous() for n in ("q", "block_table", "context_lens")}
+    check(dict(d, **last), 1, out[-4:], lse[-4:])
+
+
+@pytest.mark.gpu
+def test_without_programmatic_launches(dev):
+    """Every kernel behind the whole of the one before it: the same bits."""
+    calls = [(make(70, 1, 2, 4, 64, 900, [20 + r % 9 for r in range(70)], BF), 1),
+             (make(3, 20, 2, 5, 128, 130, [700, -1, 12], HF), 20), (make(2, 3, 2, 8, 64, 500, [3, 90], BF), 3)]
+    want = [attend(d, q_len) for d, q_len in calls]
+    qf.set_pdl(False)
+    try:
+        got = [attend(d, q_len) for d, q_len in calls]
+        torch.cuda.synchronize()
+    finally:
+        qf.set_pdl(True)
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert qf.status() == 0
+
+
+@pytest.mark.gpu
 def test_streams_graphs_and_a_shared_workspace(dev):
     """Side streams with a workspace each give the direct call's bits; a
     captured call follows the lengths; two captured graphs may share one

@@ -457,6 +457,31 @@ def test_rope_special_values_stay_in_their_pairs(dev, layout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,D,rot,dtype,layout", [
+    (1 << 24, 1, 8, 8, BF, "half"), (1 << 24, 1, 6, 2, HF, "interleaved"), (1 << 24, 3, 16, 10, BF, "half"),
+    (1 << 24, 1, 512, 16, FL, "half"), (4099, 4096, 128, 128, BF, "interleaved"),
+], ids=str)
+def test_rope_largest_calls(dev, T, H, D, rot, dtype, layout):
+    """As many tokens and heads as a call takes, up to more than 2^30 threads
+    and offsets past 2^32 bytes: the first, the last and some rows in between,
+    in place."""
+    g = torch.Generator().manual_seed(T + H)
+    ang = torch.arange(97, dtype=torch.float64)[:, None] * frequencies(rot)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float().to(dev)
+    pattern = torch.randn(101, H, D, generator=g).to(dtype).to(dev)         # token t holds row t % 101
+    x = torch.empty(T, H, D, dtype=dtype, device=dev)
+    whole = T // 101 * 101
+    x[:whole].view(-1, 101, H, D).copy_(pattern.expand(whole // 101, 101, H, D))
+    x[whole:] = pattern[:T - whole]
+    pos = torch.arange(T, device=dev) % 97
+    qf.rope(x, pos, cs, out=x, layout=layout)
+    assert qf.status() == 0
+    some = torch.cat([torch.arange(200), torch.randint(0, T, (2000,), generator=g), torch.arange(T - 200, T)]).unique().to(dev)
+    for t in some.split(64):
+        close(x[t], *turned(pattern[t % 101], cs[pos[t]], layout, False), dtype)
+
+
+@pytest.mark.gpu
 def test_rope_bad_positions_and_zero_tokens(dev):
     x, pos, cs = inputs(6, 2, 64, 64, BF)
     good = qf.rope(x, pos, cs)
