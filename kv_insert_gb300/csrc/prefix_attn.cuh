@@ -650,6 +650,8 @@ struct PaTile {
             }
             wait(LY.qready + 8 * W, items++);
             int st_prev = 0, pages_prev = 0;
+            // the first block with keys that some rows do not see
+            const int partly_from = kOwn && it.all < it.keys ? max(it.all, 0) / KB - it.kb0 : n;
             for (int j = 0; j <= n; ++j) {
                 int st = 0, pages = 0;
                 if (j < n) {   // S of block j
@@ -679,10 +681,9 @@ struct PaTile {
                 }
                 if (j > 0) {   // O += P V of block j - 1
                     const int b = j < n ? blk - 2 : blk - 1;
-                    if constexpr (kOwn) {   // while its weights are being made
+                    if (kOwn && j > partly_from) {   // while its weights are being made
                         const int k0 = (it.kb0 + j - 1) * KB;
-                        if (it.all < min(it.keys, k0 + KB) &&
-                            pa_find_not_finite<E, D, true>(smem + LY.ring + st_prev * Sh::stage_bytes, max(it.all - k0, 0), min(it.keys - k0, KB)))
+                        if (pa_find_not_finite<E, D, true>(smem + LY.ring + st_prev * Sh::stage_bytes, max(it.all - k0, 0), min(it.keys - k0, KB)))
                             flags()[3 + W] = 1;
                     }
                     wait(LY.pready + 16 * (b & 1) + 8 * W, b >> 1);
