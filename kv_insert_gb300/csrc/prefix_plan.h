@@ -124,10 +124,15 @@ inline PaPlan pa_plan(int num_reqs, int q_len, int q_heads, int nkv, int head_di
     pl.tiles = (int)((all + kPaTile - 1) / kPaTile);
     pl.pair = !pl.small && pl.tiles > 1;
     // A request's own keys go to the tile kernel from more than half a tile of
-    // rows and 512 keys on: 16 requests x 16 tokens x 64 heads of 64 over 4K keys and up to
-    // 256 own 42.5 us in the rows kernel and 46.6 here, 1024 own 54.4 and 50.9,
-    // 4096 own 90 and 65; one request of 512 tokens over 8192 keys 281 and 107.
-    // Half a tile (8 tokens of 8 heads): 33 and 37 at 1024, 52 and 49 at 4096.
+    // rows and 512 keys on: 16 requests x 16 tokens x 64 heads of 64 over 4K keys
+    // and up to 256 own 42.5 us in the rows kernel and 44.1 here, 1024 own 54.4
+    // and 50.7, 4096 own 90 and 64.7; one request of 512 tokens over 8192 keys 281
+    // and 110.  Half a tile or less stays with the rows kernel, although lengths
+    // of 2K and more would be better off here (16 requests x 8 tokens, lengths of
+    // half the table's width to all of it: 43.9 us and 34.7 at 4096, 77 and 53 at
+    // 8192): short ones are not (16.3 and 18.6 at 600; 4 requests over a 4K prefix
+    // 19.3 and 25.7), and the rule knows the table's width only, which serving
+    // programs set by the longest request they take.
     const bool many = all > 64 && q_len * group > 64;
     pl.own_tile = many && max_blocks > 32;
     pl.own_rows = pl.own_tile ? kPaTile : q_len * group <= 16 ? 16 : 64;
