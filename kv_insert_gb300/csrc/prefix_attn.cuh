@@ -6,7 +6,7 @@
 // under one softmax:
 //   s = scale q . k;  out = sum exp(s - m) v / sum exp(s - m);  lse = ln sum exp(s).
 // Both key ranges are split; every split leaves a partial (m, sum exp(s - m),
-// sum exp(s - m) v) per row in the workspace, in FP32, and a merge joins them:
+// sum exp(s - m) v), m near its own maximum, per row in the workspace, in FP32, and a merge joins them:
 //   out = sum_k e^(m_k - M) o_k / sum_k e^(m_k - M) l_k,  M = max_k m_k.
 //
 // Three kernels, the second and third PDL-launched behind the first:
@@ -32,10 +32,10 @@
 // exponentials need (8 a clock and scheduler), 1050 the tensor pipe's work
 // beside them, and the rest the hand-overs between softmax and MMA warps
 // (160 - 275 clocks each), which the two groups' warps on a scheduler spend
-// at the same time.  64 x 64 heads of 64 over 128K keys run in 125.5 us (1100
-// TFLOP/s); the 32K call with up to 1K own keys per request in 58 us.  With few
+// at the same time.  64 x 64 heads of 64 over 128K keys run in 123 us (1120
+// TFLOP/s); the 32K call with up to 1K own keys per request in 56.4 us.  With few
 // rows the keys' bytes bound it: 8 rows x 8 KV heads of 128 over 128K keys take
-// 82.6 us, 80.3 at the copy rate.  Short calls are two launches: 5.8 us.
+// 83 us, 80.3 at the copy rate.  Short calls are two launches: 5.8 us.
 
 #include <type_traits>
 

@@ -8,9 +8,9 @@
 // gradient of a rotation is the turn by -p f_i: the same kernel with s negated.
 //
 // Bound by bytes: 16384 tokens x 32 heads of 128 (bf16) take 41.4 us, the
-// copy rate; 4096 tokens of 8 KV heads of 64 into the cache 16.2 us (12.7 at
-// the copy rate); a table of 131072 x 128 13.2 us (10.0; its sines and cosines
-// are the rest); 4099 x 25 heads of 80 (fp16, 32 columns rotated) 8.3 us, of
+// copy rate; 4096 tokens of 8 KV heads of 64 into the cache 15.4 us (12.7 at
+// the copy rate); a table of 131072 x 128 13.3 us (10.0; its sines and cosines
+// are the rest); 4099 x 25 heads of 80 (fp16, 32 columns rotated) 8.5 us, of
 // which 5.0 are bytes and ~2.4 the launch's start and first loads, as in every
 // call of a few tokens.
 
