@@ -824,7 +824,8 @@ def rope(x, positions, cos_sin, out=None, layout: str = "interleaved", stream=No
     layout: pairs (2i, 2i + 1) "interleaved" or (i, i + rot_dim / 2) "half".
     out=x rotates in place.  A token whose position is no row of cos_sin keeps
     what out held, or gets zeros in an out made by the call.  Without out the
-    result is part of x's autograd graph.  Returns out."""
+    result is part of x's autograd graph; with out, or captured, a call is refused
+    where x requires a gradient (under torch.no_grad() it is not).  Returns out."""
     return _rope(x, positions, cos_sin, out, layout, 0, stream)
 
 
