@@ -527,7 +527,212 @@ size_t prefix_attn_workspace_bytes(int num_reqs, int q_len, int q_heads, int num
                                    int prefix_blocks, int max_blocks);
 
 /*
- * Packed calls: the same four calls with their arguments up to the stream as an
+ * norm_rope: the RMS norm of every head, times a weight, then its rotation,
+ * in one pass over x:
+ *   y = R(position) (w * x r),  r = (mean of the head's head_dim squares + eps)^(-1/2),
+ * R as in rope: the first rot_dim columns turned, the others (normed and
+ * weighted like them) not.
+ *   x, out, positions, cos_sin, T, heads, head_dim, rot_dim, layout, dtype as
+ *            for rope (out may be x itself); a bad position leaves its token's
+ *            heads of out as they were and raises QKVF_STATUS_BAD_POSITION.
+ *   weight   [head_dim] of weight_dtype (dtype's type or fp32), or NULL for 1.
+ *   eps in [0, 1].
+ * Squares, products and sums in FP32, one rounding to dtype.  PDL-launched;
+ * allocates nothing.
+ */
+int norm_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, const void *weight, int weight_dtype,
+              const int64_t *positions, const float *cos_sin, int64_t cos_sin_rows, void *out,
+              int64_t out_token_stride, int64_t out_head_stride, int T, int heads, int head_dim, int rot_dim,
+              int layout, float eps, int dtype, void *stream);
+
+const char *norm_rope_unsupported(const void *x, int64_t x_token_stride, int64_t x_head_stride, const void *weight,
+                                  int weight_dtype, const int64_t *positions, const float *cos_sin,
+                                  int64_t cos_sin_rows, void *out, int64_t out_token_stride, int64_t out_head_stride,
+                                  int T, int heads, int head_dim, int rot_dim, int layout, float eps, int dtype);
+
+/*
+ * norm_rope_backward: the gradients of norm_rope, from the gradient of its
+ * output and its input x.  With g' = R(-position) grad and u = w * g':
+ *   grad_x = r u - x r^3 mean(u * x),   grad_weight = sum over tokens and heads of g' * x r.
+ *   grad_out, x, grad_x  [T, heads, head_dim] of dtype, strided; grad_x may be
+ *            grad_out itself (same pointer and strides), otherwise it overlaps
+ *            neither.  A head stride of 0 broadcasts.
+ *   grad_weight [head_dim] of grad_weight_dtype (dtype's type or fp32), written,
+ *            not added to; NULL: not formed.  NULL where weight is NULL.
+ *   workspace device memory, 256-byte aligned, norm_rope_backward_workspace_bytes
+ *            bytes, overlapping no other argument, no initial contents needed;
+ *            one workspace serves one stream at a time.  Unused (may be NULL)
+ *            without grad_weight.
+ * A token of a bad position has its grad_x left as it was and adds nothing to
+ * grad_weight; QKVF_STATUS_BAD_POSITION is raised.  All sums in FP32 and in a
+ * fixed order.  PDL-launched; allocates nothing.
+ */
+int norm_rope_backward(const void *grad_out, int64_t grad_token_stride, int64_t grad_head_stride, const void *x,
+                       int64_t x_token_stride, int64_t x_head_stride, const void *weight, int weight_dtype,
+                       const int64_t *positions, const float *cos_sin, int64_t cos_sin_rows, void *grad_x,
+                       int64_t grad_x_token_stride, int64_t grad_x_head_stride, void *grad_weight,
+                       int grad_weight_dtype, int T, int heads, int head_dim, int rot_dim, int layout, float eps,
+                       int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+const char *norm_rope_backward_unsupported(const void *grad_out, int64_t grad_token_stride, int64_t grad_head_stride,
+                                           const void *x, int64_t x_token_stride, int64_t x_head_stride,
+                                           const void *weight, int weight_dtype, const int64_t *positions,
+                                           const float *cos_sin, int64_t cos_sin_rows, void *grad_x,
+                                           int64_t grad_x_token_stride, int64_t grad_x_head_stride, void *grad_weight,
+                                           int grad_weight_dtype, int T, int heads, int head_dim, int rot_dim,
+                                           int layout, float eps, int dtype, const void *workspace,
+                                           size_t workspace_bytes);
+
+/* Workspace bytes norm_rope_backward needs on the current device (0 on bad
+ * input, or without tokens). */
+size_t norm_rope_backward_workspace_bytes(int T, int heads, int head_dim);
+
+/*
+ * norm_rope_kv_append: rope_kv_append with the heads of q and k normed and
+ * weighted before they are turned (norm_rope), v as it is.
+ *   q_weight, k_weight [head_dim] of weight_dtype (dtype's type or fp32), each
+ *            may be NULL for 1; eps in [0, 1]; the rest as for rope_kv_append.
+ */
+int norm_rope_kv_append(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+                        int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                        int64_t v_head_stride, const void *q_weight, const void *k_weight, int weight_dtype,
+                        const int64_t *positions, const int64_t *slots, const float *cos_sin, int64_t cos_sin_rows,
+                        void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void *kv_cache,
+                        int64_t num_pages, int T, int q_heads, int num_kv_heads, int head_dim, int rot_dim,
+                        int layout, float eps, int dtype, void *stream);
+
+const char *norm_rope_kv_append_unsupported(
+    const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
+    int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride, const void *q_weight,
+    const void *k_weight, int weight_dtype, const int64_t *positions, const int64_t *slots, const float *cos_sin,
+    int64_t cos_sin_rows, void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void *kv_cache,
+    int64_t num_pages, int T, int q_heads, int num_kv_heads, int head_dim, int rot_dim, int layout, float eps,
+    int dtype);
+
+/*
+ * chunk_attn: attention of each request's new tokens, any number of them a
+ * request, over its paged keys: prefill chunks and decode steps in one call.
+ * Request r brings the n = starts[r + 1] - starts[r] rows from starts[r] on and
+ * has L = context_lens[r] keys, its new tokens' (the last n) among them.  Its
+ * token i sees keys j <= L - n + i (none where that is negative):
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = ln sum_j exp(s_j),  s_j = scale q . k_j.
+ * A row that sees no key gives out = 0 and lse = -infinity.
+ *   q            [T, q_heads, head_dim] of dtype (bf16 or fp16), 16-byte
+ *                aligned, strides multiples of 8; head h reads KV head
+ *                h / (q_heads / num_kv_heads).
+ *   kv_cache     [num_pages, num_kv_heads, 16, 2 head_dim] of dtype.
+ *   starts       [num_reqs + 1] int32, not decreasing, 0 .. T.  Rows of no
+ *                request (before starts[0], from starts[num_reqs] on) are left
+ *                as they were.
+ *   block_table  [num_reqs, max_blocks] int32: key j of a request is slot j % 16
+ *                of page block_table[r][j / 16]; entries past a length are not
+ *                used, whatever they hold.
+ *   context_lens [num_reqs] int32, 0 .. 16 max_blocks.  Negative: a padding
+ *                request, its rows of out and lse left as they were.
+ *   out          [T, q_heads, head_dim] of dtype, contiguous; lse [T, q_heads]
+ *                fp32, or NULL.
+ *   workspace    device memory, 256-byte aligned, chunk_attn_workspace_bytes
+ *                bytes, overlapping no other argument, no initial contents
+ *                needed; one workspace serves one stream at a time.
+ * A request whose length is beyond its table, whose starts decrease or leave
+ * 0 .. T, or that sees a page outside the cache is skipped (its rows left as
+ * they were; where only some of its rows see that page, others may be
+ * computed): QKVF_STATUS_BAD_REQUEST is raised.  Cache slots past a length are
+ * never used, whatever they hold, and a key reaches only the rows that see it.
+ *   head_dim 64 or 128, q_heads 1..64 times num_kv_heads (1..64), num_reqs
+ *   0..65535, T 0..2^24, T q_heads <= 2^30, max_blocks 1..2^20.
+ * Scores, softmax statistics and sums in FP32; the weights exp(s - m) are
+ * rounded to dtype for the product with V.  Starts and lengths stay on the
+ * device, so a captured call serves every step of its sizes.
+ * PDL-launched; allocates nothing.
+ */
+int chunk_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *kv_cache, int64_t num_pages,
+               const int32_t *starts, const int32_t *block_table, int max_blocks, const int32_t *context_lens, int T,
+               int num_reqs, int q_heads, int num_kv_heads, int head_dim, float scale, int dtype, void *out,
+               float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+const char *chunk_attn_unsupported(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *kv_cache,
+                                   int64_t num_pages, const int32_t *starts, const int32_t *block_table,
+                                   int max_blocks, const int32_t *context_lens, int T, int num_reqs, int q_heads,
+                                   int num_kv_heads, int head_dim, float scale, int dtype, void *out, float *lse,
+                                   const void *workspace, size_t workspace_bytes);
+
+/* Workspace bytes chunk_attn needs on the current device (0 on bad input). */
+size_t chunk_attn_workspace_bytes(int T, int num_reqs, int q_heads, int num_kv_heads, int head_dim, int max_blocks);
+
+/*
+ * key_weights: the attention weight that each cached key received from the
+ * step's rows, kept from step to step:
+ *   out[r][g][j] = decay weights[r][g][j] + sum of exp(scale q . k_j - lse)
+ * over the request's tokens that see key j (its last `window` tokens only, 0:
+ * all) and the q heads of KV head g.  q, starts, block_table, context_lens, the
+ * cache and the limits as for chunk_attn; lse [T, q_heads] as it gave it (a row
+ * of lse -infinity adds nothing).
+ *   weights, out [num_reqs, num_kv_heads, 16 max_blocks] fp32; out may be
+ *            weights itself, otherwise it must not overlap it.  Keys below a
+ *            length are written, others left as they were.  decay in [0, 1];
+ *            0: weights is not read (may be NULL).
+ *   workspace as for chunk_attn, key_weights_workspace_bytes bytes.
+ * A request that chunk_attn would skip has its weights left as they were (of
+ * a page outside the cache, at least those keys'), QKVF_STATUS_BAD_REQUEST as
+ * there.  Sums in FP32 and in a fixed order.  PDL-launched; allocates nothing.
+ */
+int key_weights(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *kv_cache, int64_t num_pages,
+                const float *lse, const int32_t *starts, const int32_t *block_table, int max_blocks,
+                const int32_t *context_lens, int T, int num_reqs, int q_heads, int num_kv_heads, int head_dim,
+                int window, float decay, float scale, int dtype, const float *weights, float *out, void *workspace,
+                size_t workspace_bytes, void *stream);
+
+const char *key_weights_unsupported(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *kv_cache,
+                                    int64_t num_pages, const float *lse, const int32_t *starts,
+                                    const int32_t *block_table, int max_blocks, const int32_t *context_lens, int T,
+                                    int num_reqs, int q_heads, int num_kv_heads, int head_dim, int window, float decay,
+                                    float scale, int dtype, const float *weights, float *out, const void *workspace,
+                                    size_t workspace_bytes);
+
+/* Workspace bytes key_weights needs on the current device (0 on bad input). */
+size_t key_weights_workspace_bytes(int T, int num_reqs, int q_heads, int num_kv_heads, int head_dim, int max_blocks);
+
+/*
+ * kv_evict: drop the keys of least weight.  Of each request's L keys, for each
+ * KV head on its own, the last `recent` are kept and of the others the
+ * keep - recent of largest weight (the lower index among equals; a NaN above
+ * every number); with L <= keep all of them.  The kept keys, in their order,
+ * become keys 0 .. min(L, keep) - 1:
+ *   kept[r][g][i]  the index that key i had (-1 from min(L, keep) on);
+ *   K and V of key kept[r][g][i] go to key i of out_table's pages;
+ *   out_weights[r][g][i] = weights[r][g][kept[r][g][i]], and 0 behind them (as
+ *            far as weights had keys, in place; otherwise to the row's end);
+ *   out_lens[r] = min(L, keep).
+ *   kv_cache     [num_pages, num_kv_heads, 16, 2 head_dim] of a 16-bit type.
+ *   weights      [num_reqs, num_kv_heads, 16 max_blocks] fp32.
+ *   block_table  [num_reqs, max_blocks], context_lens [num_reqs] as for
+ *                chunk_attn (negative: a padding request, left alone).
+ *   out_table    [num_reqs, out_blocks], out_weights [num_reqs, num_kv_heads, 16
+ *                out_blocks], out_lens [num_reqs]: all three the inputs
+ *                themselves (in place), or none of them; then 16 out_blocks >=
+ *                keep, and no page that out_table names for a kept key may be a
+ *                page of another key of this call.  A page that several
+ *                requests share is not evicted in place.
+ *   kept         [num_reqs, num_kv_heads, keep] int32.
+ * A request whose length is beyond its table, or that needs a page outside the
+ * cache, is left alone (its row of kept becomes -1): QKVF_STATUS_BAD_REQUEST.
+ *   head_dim a multiple of 8 up to 512, num_kv_heads 1..1024, num_reqs 0..65535,
+ *   max_blocks and out_blocks 1..2^20, keep 1..2^24, recent 0..keep.
+ * PDL-launched; allocates nothing.
+ */
+int kv_evict(void *kv_cache, int64_t num_pages, const float *weights, const int32_t *block_table, int max_blocks,
+             const int32_t *context_lens, int num_reqs, int num_kv_heads, int head_dim, int keep, int recent,
+             const int32_t *out_table, int out_blocks, float *out_weights, int32_t *out_lens, int32_t *kept,
+             void *stream);
+
+const char *kv_evict_unsupported(void *kv_cache, int64_t num_pages, const float *weights, const int32_t *block_table,
+                                 int max_blocks, const int32_t *context_lens, int num_reqs, int num_kv_heads,
+                                 int head_dim, int keep, int recent, const int32_t *out_table, int out_blocks,
+                                 float *out_weights, int32_t *out_lens, int32_t *kept);
+
+/*
+ * Packed calls: the same calls with their arguments up to the stream as an
  * array of 64-bit words, in order (pointers and integers as they are, floats
  * and doubles as a double's bits), for bindings that pay per argument.  An
  * integer that does not fit its parameter is refused with QKVF_ERR_SIZES.
@@ -536,6 +741,12 @@ int rope_table_packed(const int64_t *args, void *stream);       /* 11 words */
 int rope_packed(const int64_t *args, void *stream);             /* 16 words */
 int rope_kv_append_packed(const int64_t *args, void *stream);   /* 25 words */
 int prefix_attn_packed(const int64_t *args, void *stream);      /* 22 words */
+int norm_rope_packed(const int64_t *args, void *stream);            /* 18 words */
+int norm_rope_backward_packed(const int64_t *args, void *stream);   /* 25 words */
+int norm_rope_kv_append_packed(const int64_t *args, void *stream);  /* 29 words */
+int chunk_attn_packed(const int64_t *args, void *stream);           /* 20 words */
+int key_weights_packed(const int64_t *args, void *stream);          /* 23 words */
+int kv_evict_packed(const int64_t *args, void *stream);             /* 16 words */
 
 
 /* Static text of a QKVF_* return code. */

@@ -1450,6 +1450,9 @@ int launch_front(const uint16_t *x, const uint16_t *W, const int64_t *positions,
 #include "rope.cuh"
 #include "rope_kv_append.cuh"
 #include "prefix_attn.cuh"
+#include "norm_rope.cuh"
+#include "chunk_attn.cuh"
+#include "kv_evict.cuh"
 
 using namespace qkvf;
 

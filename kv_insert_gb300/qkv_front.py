@@ -128,8 +128,19 @@ def load() -> ctypes.CDLL:
         append = [vp, i64, i64] * 3 + [vp, vp, vp, i64, vp, i64, i64, vp, i64] + [i32] * 7
         prefix = ([vp, i64, i64, vp, i64, vp, i32, vp, vp, i32, vp] + [i32] * 5
                   + [ctypes.c_float, i32, vp, vp, vp, size])
+        f32 = ctypes.c_float
+        norm = [vp, i64, i64, vp, i32, vp, vp, i64, vp, i64, i64] + [i32] * 5 + [f32, i32]
+        norm_back = ([vp, i64, i64] * 2 + [vp, i32, vp, vp, i64, vp, i64, i64, vp] + [i32] * 6
+                     + [f32, i32, vp, size])
+        norm_append = ([vp, i64, i64] * 3 + [vp, vp, i32, vp, vp, vp, i64, vp, i64, i64, vp, i64] + [i32] * 6
+                       + [f32, i32])
+        chunk = [vp, i64, i64, vp, i64, vp, vp, i32, vp] + [i32] * 5 + [f32, i32, vp, vp, vp, size]
+        key_weights = [vp, i64, i64, vp, i64, vp, vp, vp, i32, vp] + [i32] * 6 + [f32, f32, i32, vp, vp, vp, size]
+        evict = [vp, i64, vp, vp, i32, vp] + [i32] * 5 + [vp, i32, vp, vp, vp]
         for name, args in (("rope_table", table), ("rope", rope_args), ("rope_kv_append", append),
-                           ("prefix_attn", prefix)):
+                           ("prefix_attn", prefix), ("norm_rope", norm), ("norm_rope_backward", norm_back),
+                           ("norm_rope_kv_append", norm_append), ("chunk_attn", chunk),
+                           ("key_weights", key_weights), ("kv_evict", evict)):
             getattr(lib, name).argtypes = args + [vp]
             getattr(lib, name).restype = i32
             getattr(lib, name + "_packed").argtypes = [ctypes.c_char_p, vp]
@@ -138,6 +149,9 @@ def load() -> ctypes.CDLL:
             getattr(lib, name + "_unsupported").restype = ctypes.c_char_p
         lib.prefix_attn_workspace_bytes.argtypes = [i32] * 7
         lib.prefix_attn_workspace_bytes.restype = size
+        for name, n in (("norm_rope_backward", 3), ("chunk_attn", 6), ("key_weights", 6)):
+            getattr(lib, name + "_workspace_bytes").argtypes = [i32] * n
+            getattr(lib, name + "_workspace_bytes").restype = size
         lib.qkv_front_set_pdl.argtypes = [i32]
         lib.qkv_front_set_pdl.restype = i32
         _lib = lib
@@ -149,7 +163,8 @@ def header_functions() -> list[str]:
     text = open(HEADER).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(
-        r"\b((?:qkv_front|qknorm_rope_kv_insert|layer_front|attn2|rope|prefix_attn)\w*)\s*\(", text)))
+        r"\b((?:qkv_front|qknorm_rope_kv_insert|layer_front|attn2|rope|prefix_attn|norm_rope|chunk_attn"
+        r"|key_weights|kv_evict)\w*)\s*\(", text)))
 
 
 def strerror(code: int) -> str:
@@ -613,7 +628,10 @@ def attn2_split_kv(qkv, kv_cache, block_table, context_lens, workspace, out=None
 
 # the words of the packed calls (ctypes converts 25 arguments in about 2 us)
 _PACK = {"rope_table": struct.Struct("4qdqdq3d").pack, "rope": struct.Struct("16q").pack,
-         "rope_kv_append": struct.Struct("25q").pack, "prefix_attn": struct.Struct("16qd5q").pack}
+         "rope_kv_append": struct.Struct("25q").pack, "prefix_attn": struct.Struct("16qd5q").pack,
+         "norm_rope": struct.Struct("16qdq").pack, "norm_rope_backward": struct.Struct("21qd3q").pack,
+         "norm_rope_kv_append": struct.Struct("27qdq").pack, "chunk_attn": struct.Struct("14qd5q").pack,
+         "key_weights": struct.Struct("16q2d5q").pack, "kv_evict": struct.Struct("16q").pack}
 
 
 _CALLS = {}
@@ -956,6 +974,371 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens
                         scale, out, lse, flags)
     _run("prefix_attn", q.get_device(), args, stream)
     return out
+
+
+# ---- normed rotation, ragged chunks over the cache, eviction -----------------
+
+def _weight(w, name: str, head_dim: int, dtype, index: int):
+    """(pointer, dtype code) of a norm weight; None: no weight, 1 in its place."""
+    if w is None:
+        return 0, DTYPES[dtype]
+    if w.dtype not in (dtype, torch.float32):
+        raise ValueError(f"{name} must be {dtype} or torch.float32, not {w.dtype}")
+    return _index(w, name, w.dtype, (head_dim,), index), DTYPES[w.dtype]
+
+
+def _workspace(workspace, index: int):
+    if (workspace is None or workspace.dtype is not torch.uint8 or not workspace.is_contiguous()
+            or workspace.get_device() != index):
+        raise ValueError("workspace must be a contiguous uint8 CUDA tensor on the other tensors' device")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _norm_args(x, weight, positions, cos_sin, out, eps, layout, flags=0):
+    index, shape, dtype = x.get_device(), x.shape, x.dtype
+    px, xt, xh = _heads(x, "x", index, DTYPES)
+    T, heads, dim = shape
+    po, ot, oh = _heads(out, "out", index, (dtype,), shape)
+    pt, rows, rot = _table(cos_sin, dim, index)
+    pw, wd = _weight(weight, "weight", dim, dtype, index)
+    return (px, xt, xh, pw, wd, _index(positions, "positions", torch.int64, (T,), index), pt, rows, po, ot, oh,
+            T, heads, dim, rot, _layout(layout), eps, DTYPES[dtype] | flags)
+
+
+def norm_rope_unsupported(x, weight, positions, cos_sin, out, eps: float = 1e-6,
+                          layout: str = "interleaved") -> str | None:
+    """Why norm_rope would refuse this call, or None."""
+    try:
+        args = _norm_args(x, weight, positions, cos_sin, out, eps, layout)
+    except ValueError as e:
+        return str(e)
+    return _why("norm_rope", x.get_device(), args)
+
+
+class _NormRotation(torch.autograd.Function):
+    """norm_rope as a node of the autograd graph (its gradient is formed once:
+    no graph of the gradient)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, positions, cos_sin, eps, layout):
+        _Rotation.used = True
+        ctx.save_for_backward(x, weight, positions, cos_sin)
+        ctx.how = eps, layout
+        return _norm_rope(x, weight, positions, cos_sin, None, eps, layout, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        x, weight, positions, cos_sin = ctx.saved_tensors
+        with torch.cuda.device(x.device):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("the backward pass of an autograd graph is not captured: capture "
+                                 "norm_rope_backward under torch.no_grad()")
+        if grad.stride(-1) != 1:   # the gradient of a sum, say: one value, expanded
+            grad = grad.contiguous()
+        eps, layout = ctx.how
+        form = weight is not None and ctx.needs_input_grad[1]
+        dw = torch.empty_like(weight) if form else None
+        dx, dw = norm_rope_backward(grad, x, weight, positions, cos_sin, eps=eps, layout=layout, grad_weight=dw)
+        return dx, dw if form else None, None, None, None, None
+
+
+def _norm_rope_with_grad(x, weight, positions, cos_sin, out, eps, layout, stream):
+    if cos_sin.requires_grad:
+        raise ValueError("no gradient is formed with respect to cos_sin: detach it")
+    if out is not None:
+        raise ValueError("a call into out is not part of the autograd graph, but x or weight requires a gradient: "
+                         "leave out None, or call under torch.no_grad() (its gradient is norm_rope_backward)")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+    with torch.cuda.device(x.device), torch.cuda.stream(stream):   # backward runs where forward did
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured call is not part of the autograd graph, but x or weight requires a "
+                             "gradient: capture norm_rope and norm_rope_backward under torch.no_grad()")
+        return _NormRotation.apply(x, weight, positions, cos_sin, eps, layout)
+
+
+def _norm_rope(x, weight, positions, cos_sin, out, eps, layout, stream):
+    if torch.is_grad_enabled() and (x.requires_grad or cos_sin.requires_grad
+                                    or (weight is not None and weight.requires_grad)):
+        return _norm_rope_with_grad(x, weight, positions, cos_sin, out, eps, layout, stream)
+    flags = 0
+    if out is None:
+        out, flags = _new(x.shape, x.dtype, x.device, stream), DTYPE_ZERO_SKIPPED
+    _run("norm_rope", x.get_device(), _norm_args(x, weight, positions, cos_sin, out, eps, layout, flags), stream)
+    return out
+
+
+def norm_rope(x, weight, positions, cos_sin, out=None, eps: float = 1e-6, layout: str = "interleaved",
+              stream=None):
+    """The RMS norm of every head of x [tokens, heads, head_dim] (bf16, fp16 or
+    fp32, any strides, last dimension contiguous), times weight [head_dim] (x's
+    dtype or fp32; None: 1), then the rotation of rope, in one pass:
+    rope(weight * x / sqrt(mean(x^2) + eps)).  out=x works in place.  A token
+    whose position is no row of cos_sin keeps what out held, or gets zeros in an
+    out made by the call.  Without out the result is part of the autograd graph
+    of x and weight; with out, or captured, a call is refused where one of them
+    requires a gradient (under torch.no_grad() it is not).  Returns out."""
+    return _norm_rope(x, weight, positions, cos_sin, out, eps, layout, stream)
+
+
+def norm_rope_backward_workspace_bytes(tokens: int, heads: int, head_dim: int) -> int:
+    """Workspace bytes of norm_rope_backward on the current device (0: bad sizes, or no tokens)."""
+    return int((_lib or load()).norm_rope_backward_workspace_bytes(tokens, heads, head_dim))
+
+
+def _norm_back_args(grad_out, x, weight, positions, cos_sin, grad_x, grad_weight, workspace, eps, layout, flags=0):
+    index, shape, dtype = x.get_device(), x.shape, x.dtype
+    px, xt, xh = _heads(x, "x", index, DTYPES)
+    T, heads, dim = shape
+    pg, gt, gh = _heads(grad_out, "grad_out", index, (dtype,), shape)
+    pd, dt, dh = _heads(grad_x, "grad_x", index, (dtype,), shape)
+    pt, rows, rot = _table(cos_sin, dim, index)
+    pw, wd = _weight(weight, "weight", dim, dtype, index)
+    pdw, dwd = _weight(grad_weight, "grad_weight", dim, dtype, index)
+    ws, size = (0, 0) if workspace is None else _workspace(workspace, index)
+    return (pg, gt, gh, px, xt, xh, pw, wd, _index(positions, "positions", torch.int64, (T,), index), pt, rows,
+            pd, dt, dh, pdw, dwd, T, heads, dim, rot, _layout(layout), eps, DTYPES[dtype] | flags, ws, size)
+
+
+def norm_rope_backward_unsupported(grad_out, x, weight, positions, cos_sin, grad_x, grad_weight=None,
+                                   workspace=None, eps: float = 1e-6, layout: str = "interleaved") -> str | None:
+    """Why norm_rope_backward would refuse this call into grad_x and grad_weight, or None."""
+    try:
+        args = _norm_back_args(grad_out, x, weight, positions, cos_sin, grad_x, grad_weight, workspace, eps, layout)
+    except ValueError as e:
+        return str(e)
+    return _why("norm_rope_backward", x.get_device(), args)
+
+
+def norm_rope_backward(grad_out, x, weight, positions, cos_sin, eps: float = 1e-6, layout: str = "interleaved",
+                       grad_x=None, grad_weight=None, workspace=None, stream=None):
+    """The gradients of norm_rope with respect to x and weight, from the gradient
+    of its output and its x.  grad_x=grad_out writes it in place; None: a new
+    tensor.  grad_weight [head_dim] (fp32 or x's dtype) is written, not added to;
+    None: a new fp32 tensor (no gradient where weight is None).  workspace:
+    uint8, norm_rope_backward_workspace_bytes long; None: made by the call.  A
+    token whose position is no row of cos_sin keeps what grad_x held (zeros in
+    one made by the call) and adds nothing to grad_weight.  Returns
+    (grad_x, grad_weight)."""
+    flags = 0
+    if grad_x is None:
+        grad_x, flags = _new(x.shape, x.dtype, x.device, stream), DTYPE_ZERO_SKIPPED
+    if weight is not None:
+        if grad_weight is None:
+            grad_weight = _new(weight.shape, torch.float32, x.device, stream)
+        if workspace is None and x.is_cuda and x.dim() == 3:
+            with torch.cuda.device(x.device):
+                n = norm_rope_backward_workspace_bytes(*(min(d, _MOST) for d in x.shape))
+            workspace = _new((n,), torch.uint8, x.device, stream)
+    args = _norm_back_args(grad_out, x, weight, positions, cos_sin, grad_x, grad_weight, workspace, eps, layout, flags)
+    _run("norm_rope_backward", x.get_device(), args, stream)
+    return grad_x, grad_weight
+
+
+def _norm_append_args(q, k, v, q_weight, k_weight, positions, slots, cos_sin, kv_cache, q_out, eps, layout, flags=0):
+    a = _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout, flags)
+    index, dtype, dim = k.get_device(), k.dtype, k.shape[2]
+    pq, qd = _weight(q_weight, "q_weight", dim, dtype, index)
+    pk, kd = _weight(k_weight, "k_weight", dim, dtype, index)
+    if q_weight is not None and k_weight is not None and qd != kd:
+        raise ValueError(f"q_weight and k_weight must be of one dtype, not {q_weight.dtype} and {k_weight.dtype}")
+    return a[:9] + (pq, pk, kd if q_weight is None else qd) + a[9:-1] + (eps, a[-1])
+
+
+def norm_rope_kv_append_unsupported(q, k, v, q_weight, k_weight, positions, slots, cos_sin, kv_cache, q_out=None,
+                                    eps: float = 1e-6, layout: str = "interleaved") -> str | None:
+    """Why norm_rope_kv_append would refuse this call (into q_out; None: a new
+    tensor), or None."""
+    try:
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        args = _norm_append_args(q, k, v, q_weight, k_weight, positions, slots, cos_sin, kv_cache, q_out, eps, layout)
+    except ValueError as e:
+        return str(e)
+    return _why("norm_rope_kv_append", k.get_device(), args)
+
+
+def norm_rope_kv_append(q, k, v, q_weight, k_weight, positions, slots, cos_sin, kv_cache, q_out=None,
+                        eps: float = 1e-6, layout: str = "interleaved", stream=None):
+    """rope_kv_append with every head of q and k normed and weighted first, as in
+    norm_rope: q_weight and k_weight [head_dim] (k's dtype or fp32, both the same;
+    None: 1).  v is written as it is.  Returns q_out."""
+    flags = 0
+    if q is not None and q_out is None:
+        q_out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED
+    args = _norm_append_args(q, k, v, q_weight, k_weight, positions, slots, cos_sin, kv_cache, q_out, eps, layout, flags)
+    _run("norm_rope_kv_append", k.get_device(), args, stream)
+    return q_out
+
+
+def chunk_attn_workspace_bytes(tokens: int, num_reqs: int, q_heads: int, num_kv_heads: int, head_dim: int,
+                               max_blocks: int) -> int:
+    """Workspace bytes of chunk_attn on the current device (0: bad sizes)."""
+    return int((_lib or load()).chunk_attn_workspace_bytes(tokens, num_reqs, q_heads, num_kv_heads, head_dim,
+                                                           max_blocks))
+
+
+def key_weights_workspace_bytes(tokens: int, num_reqs: int, q_heads: int, num_kv_heads: int, head_dim: int,
+                                max_blocks: int) -> int:
+    """Workspace bytes of key_weights on the current device (0: bad sizes)."""
+    return int((_lib or load()).key_weights_workspace_bytes(tokens, num_reqs, q_heads, num_kv_heads, head_dim,
+                                                            max_blocks))
+
+
+def _ragged_args(q, kv_cache, starts, block_table, context_lens, workspace, scale):
+    """What chunk_attn and key_weights share, checked: pointers and sizes by name."""
+    index, dtype = q.get_device(), q.dtype
+    pq, qt, qh = _heads(q, "q", index, _HALF_TYPES)
+    T, heads, dim = q.shape
+    pc, pages, nkv = _cache(kv_cache, dim, dtype, index)
+    if block_table.dim() != 2 or max(block_table.shape) > _MOST:
+        raise ValueError("block_table must be [num_reqs, max_blocks]")
+    R, mb = block_table.shape
+    ws, size = _workspace(workspace, index)
+    return {"q": (pq, qt, qh, pc, pages), "starts": _index(starts, "starts", torch.int32, (R + 1,), index),
+            "table": (_index(block_table, "block_table", torch.int32, (R, mb), index), mb,
+                      _index(context_lens, "context_lens", torch.int32, (R,), index)),
+            "sizes": (T, R, heads, nkv, dim), "scale": dim ** -0.5 if scale is None else scale,
+            "dtype": DTYPES[dtype], "workspace": (ws, size), "index": index}
+
+
+def _chunk_args(q, kv_cache, starts, block_table, context_lens, workspace, scale, out, lse, flags=0):
+    a = _ragged_args(q, kv_cache, starts, block_table, context_lens, workspace, scale)
+    po = _index(out, "out", q.dtype, q.shape, a["index"])
+    pl = 0 if lse is None else _index(lse, "lse", torch.float32, q.shape[:2], a["index"])
+    return (*a["q"], a["starts"], *a["table"], *a["sizes"], a["scale"], a["dtype"] | flags, po, pl, *a["workspace"])
+
+
+def chunk_attn_unsupported(q, kv_cache, starts, block_table, context_lens, workspace, out, scale=None,
+                           lse=None) -> str | None:
+    """Why chunk_attn would refuse this call into `out`, or None."""
+    try:
+        args = _chunk_args(q, kv_cache, starts, block_table, context_lens, workspace, scale, out, lse)
+    except ValueError as e:
+        return str(e)
+    return _why("chunk_attn", q.get_device(), args)
+
+
+def chunk_attn(q, kv_cache, starts, block_table, context_lens, workspace, scale=None, out=None, lse=None,
+               stream=None):
+    """Causal attention of each request's new tokens, any number of them a
+    request, over its paged keys: prefill chunks and decode steps in one call.
+    q [tokens, q_heads, head_dim] (bf16 or fp16), request r's rows starts[r] ..
+    starts[r + 1] - 1 (int32 [num_reqs + 1]); kv_cache [pages, num_kv_heads, 16,
+    2 head_dim]; block_table int32 [num_reqs, max_blocks] and context_lens int32
+    [num_reqs]: each request's keys, its new tokens' the last of them (a negative
+    length: a padding request, left alone); workspace: uint8,
+    chunk_attn_workspace_bytes long.  scale: None for head_dim^-1/2.  lse: fp32
+    [tokens, q_heads], filled with the rows' ln sum exp when given.  Rows of no
+    request, of padding or of refused requests keep what out held, or become
+    zeros in an out made by the call.  For serving: no part of an autograd graph.
+    Returns out."""
+    flags = 0
+    if out is None:
+        out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED
+    args = _chunk_args(q, kv_cache, starts, block_table, context_lens, workspace, scale, out, lse, flags)
+    _run("chunk_attn", q.get_device(), args, stream)
+    return out
+
+
+def _key_weights_args(q, kv_cache, lse, starts, block_table, context_lens, weights, workspace, window, decay, scale,
+                      out):
+    a = _ragged_args(q, kv_cache, starts, block_table, context_lens, workspace, scale)
+    _, R, _, nkv, _ = a["sizes"]
+    shape = (R, nkv, block_table.shape[1] * PAGE_SLOTS)
+    pw = 0 if weights is None else _index(weights, "weights", torch.float32, shape, a["index"])
+    return (*a["q"], _index(lse, "lse", torch.float32, q.shape[:2], a["index"]), a["starts"], *a["table"],
+            *a["sizes"], window, decay, a["scale"], a["dtype"], pw,
+            _index(out, "out", torch.float32, shape, a["index"]), *a["workspace"])
+
+
+def key_weights_unsupported(q, kv_cache, lse, starts, block_table, context_lens, weights, workspace,
+                            window: int = 0, decay: float = 1.0, scale=None, out=None) -> str | None:
+    """Why key_weights would refuse this call, or None."""
+    try:
+        args = _key_weights_args(q, kv_cache, lse, starts, block_table, context_lens, weights, workspace, window,
+                                 decay, scale, weights if out is None else out)
+    except ValueError as e:
+        return str(e)
+    return _why("key_weights", q.get_device(), args)
+
+
+def key_weights(q, kv_cache, lse, starts, block_table, context_lens, weights, workspace, window: int = 0,
+                decay: float = 1.0, scale=None, out=None, stream=None):
+    """The attention weight that every cached key received from this step's rows,
+    added to what it had: out[r, g, j] = decay weights[r, g, j] + the sum of
+    exp(scale q . k_j - lse) over the request's tokens that see key j (its last
+    `window` tokens only, 0: all) and the q heads of KV head g.  q, kv_cache,
+    starts, block_table, context_lens, scale as for chunk_attn, lse as it gave it;
+    weights fp32 [num_reqs, num_kv_heads, 16 max_blocks]; out None: in place.
+    Only keys below a request's length are written.  decay 0 starts anew and does
+    not read weights (which may be None where out is given).  workspace: uint8,
+    key_weights_workspace_bytes long.  Returns out."""
+    out = weights if out is None else out
+    args = _key_weights_args(q, kv_cache, lse, starts, block_table, context_lens, weights, workspace, window, decay,
+                             scale, out)
+    _run("key_weights", q.get_device(), args, stream)
+    return out
+
+
+def _evict_args(kv_cache, weights, block_table, context_lens, keep, recent, out_table, out_weights, out_lens, kept):
+    given = [t is not None for t in (out_table, out_weights, out_lens)]
+    if any(given) != all(given):
+        raise ValueError("out_table, out_weights and out_lens must all be given, or none of them (in place)")
+    if not any(given):
+        out_table, out_weights, out_lens = block_table, weights, context_lens
+    index, dims = kv_cache.get_device(), kv_cache.shape
+    if kv_cache.dtype not in _HALF_TYPES or kv_cache.dim() != 4 or dims[3] % 2:
+        raise ValueError(f"kv_cache must be {' or '.join(map(str, _HALF_TYPES))} "
+                         f"[pages, num_kv_heads, {PAGE_SLOTS}, 2 head_dim]")
+    pc, pages, nkv = _cache(kv_cache, dims[3] // 2, kv_cache.dtype, index)
+    for name, t in (("block_table", block_table), ("out_table", out_table)):
+        if t.dim() != 2 or max(t.shape) > _MOST:
+            raise ValueError(f"{name} must be [num_reqs, blocks]")
+    R, mb = block_table.shape
+    ob = out_table.shape[1]
+    return (pc, pages, _index(weights, "weights", torch.float32, (R, nkv, mb * PAGE_SLOTS), index),
+            _index(block_table, "block_table", torch.int32, (R, mb), index), mb,
+            _index(context_lens, "context_lens", torch.int32, (R,), index), R, nkv, dims[3] // 2, keep, recent,
+            _index(out_table, "out_table", torch.int32, (R, ob), index), ob,
+            _index(out_weights, "out_weights", torch.float32, (R, nkv, ob * PAGE_SLOTS), index),
+            _index(out_lens, "out_lens", torch.int32, (R,), index),
+            _index(kept, "kept", torch.int32, (R, nkv, keep), index))
+
+
+def kv_evict_unsupported(kv_cache, weights, block_table, context_lens, keep: int, kept, recent: int = 0,
+                         out_table=None, out_weights=None, out_lens=None) -> str | None:
+    """Why kv_evict would refuse this call into `kept`, or None."""
+    try:
+        args = _evict_args(kv_cache, weights, block_table, context_lens, keep, recent, out_table, out_weights,
+                           out_lens, kept)
+    except ValueError as e:
+        return str(e)
+    return _why("kv_evict", kv_cache.get_device(), args)
+
+
+def kv_evict(kv_cache, weights, block_table, context_lens, keep: int, recent: int = 0, out_table=None,
+             out_weights=None, out_lens=None, kept=None, stream=None):
+    """Keep `keep` keys of every request and KV head: its last `recent`, and of the
+    others those of largest weight (the lower index among equals), moved together
+    in their order; a request of no more keys keeps all.  kv_cache [pages,
+    num_kv_heads, 16, 2 head_dim] (bf16 or fp16); weights fp32 [num_reqs,
+    num_kv_heads, 16 max_blocks], as key_weights keeps them; block_table and
+    context_lens as for chunk_attn.  In place (the cache's pages, weights and
+    context_lens change), or, with out_table int32 [num_reqs, blocks],
+    out_weights and out_lens given, into other pages, which no request of the call
+    may use.  Weights behind the kept keys become 0.  kept: int32 [num_reqs,
+    num_kv_heads, keep], None: a new tensor; the index that every kept key had, -1
+    behind them.  Returns kept."""
+    if kept is None:
+        kept = _new((block_table.shape[0], kv_cache.shape[1], max(keep, 0)), torch.int32, kv_cache.device, stream)
+    args = _evict_args(kv_cache, weights, block_table, context_lens, keep, recent, out_table, out_weights, out_lens,
+                       kept)
+    _run("kv_evict", kv_cache.get_device(), args, stream)
+    return kept
 
 
 def selftest_wait(timeout_ns: int, stream=None) -> None:
