@@ -17,6 +17,7 @@ HEADERS = [os.path.join(ROOT, "include", "qkvfront.h"),
            os.path.join(PKG, "csrc", "prefix_plan.h"),
            os.path.join(PKG, "csrc", "prefix_attn.cuh"),
            os.path.join(PKG, "csrc", "norm_rope.cuh"),
+           os.path.join(PKG, "csrc", "chunk_plan.h"),
            os.path.join(PKG, "csrc", "chunk_attn.cuh"),
            os.path.join(PKG, "csrc", "kv_evict.cuh")]
 LIB_PATH = os.path.join(PKG, "libqkvfront.so")

@@ -5,8 +5,31 @@
 // Request r brings the rows starts[r] .. starts[r + 1] - 1 of q, n of them, and
 // has L keys, its new tokens' among them.  Its token i sees keys j <= L - n + i:
 //   s = scale q . k;  out = sum exp(s - m) v / sum exp(s - m);  lse = ln sum exp(s).
-// key_weights: w[j] = decay w[j] + sum over tokens and the KV head's q heads of
-// exp(s - lse).
+//
+// chunk_tile_kernel, one CTA per SM.  A request's rows (token, q head of a KV
+// head) are cut into blocks of 256, two tensor-memory tiles, each the work of a
+// group of four softmax warps (a thread per row) and an MMA warp; both tiles
+// take the same keys, 128 a step, from one ring that a producer warp fills (TMA,
+// a swizzled box for K and one for V of every page).  A block of 128 rows or
+// fewer (decode) is one tile whose even steps are the first group's and whose
+// odd ones the second's, joined at its end.  Lengths are on the device:
+// chunk_plan_kernel, one CTA, adds the requests' costs up and cuts the line of
+// work into equal parts (chunk_plan.h), a CTA's each, which start and end in the
+// middle of a block's keys too.  A block that several CTAs share leaves partials (m, sum exp(s - m),
+// sum exp(s - m) v) in the workspace, at most two a CTA, and chunk_merge_kernel
+// joins them in order.
+//
+// S = Q K^T goes to tensor memory and the weights back over it, as the A operand
+// of O += P V.  With heads of 64 the weights take the outer half of S's columns
+// and the next S the other ones, made meanwhile; with heads of 128 S, O and the
+// weights fill tensor memory, and the next S follows the product.
+//
+// A checker warp looks at V before its product where a step ends behind the keys
+// or holds keys that not every row of the block sees: slots behind the keys
+// become 0, and so do infinities and NaN among the others (0 x infinity is not
+// 0), which are added at the block's end for the rows that see them.
+
+#include "chunk_plan.h"
 
 namespace qkvf {
 
@@ -22,31 +45,36 @@ struct RaggedParams {
     float *out_weights;
     int64_t num_pages;
     int64_t q_ts, q_hs;
+    float *ws_o;            // chunk_attn: partial O [2 parts][256][D]
+    float2 *ws_ml;          // (maximum in log2 units, sum; below 0: void) [2 parts][256]
+    ChPos *ws_pos;          // [parts + 1]: where every part starts
+    unsigned long long wait_limit_ns;
     int T, R, max_blocks, q_heads, nkv, group;
+    int parts;
     int window;
     float decay;
     float scale_log2;
     int zero;
 };
 
-// A request's rows and keys; n < 0: left alone
-struct RaggedRequest {
-    int row0, n, L;
-};
-
-__device__ __forceinline__ RaggedRequest ragged_request(const RaggedParams &p, int r)
+// Request r, n <= 0 where it has no rows or is left alone; flag: raise the
+// status bit of a bad one
+__device__ __forceinline__ ChRequest ragged_request(const RaggedParams &p, int b, int e, int L, bool flag)
 {
-    RaggedRequest q;
-    const int b = p.starts[r], e = p.starts[r + 1];
-    q.L = p.context_lens[r];
+    ChRequest q;
     q.row0 = b;
     q.n = e - b;
-    const bool bad = b < 0 || e < b || e > p.T || q.L > p.max_blocks * kPageSlots;
-    if (bad || q.L < 0) {
-        if (bad) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
+    q.L = L;
+    const bool bad = b < 0 || e < b || e > p.T || L > p.max_blocks * kPageSlots;
+    if (bad || L < 0) {
+        if (bad && flag) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
         q.n = -1;
     }
     return q;
+}
+__device__ __forceinline__ ChRequest ragged_request(const RaggedParams &p, int r, bool flag)
+{
+    return ragged_request(p, p.starts[r], p.starts[r + 1], p.context_lens[r], flag);
 }
 
 template <class E, int D>
@@ -60,61 +88,923 @@ __device__ __forceinline__ float ragged_dot(const uint16_t *k, const float *q, i
     return s;
 }
 
+// ---- shapes -----------------------------------------------------------------
+
+constexpr int kChThreads = 384;   // 2 softmax groups of 4 warps, a producer, a checker, 2 MMA warps
+constexpr int kChPages = kChKeys / kPageSlots;
+constexpr int kChSeq = 16;        // items whose flags are kept: more than the ring runs ahead
+static_assert(kChTile == kPaTile, "tiles as in prefix_attn");
+
+// A unit of the ring is K or V of one step
+template <int D>
+struct ChShape {
+    static constexpr int nb = D / 64;                          // 64-column blocks of K or V
+    static constexpr uint32_t page_bytes = kPageSlots * 2 * D; // one box
+    static constexpr uint32_t unit_bytes = kChPages * page_bytes;
+    static constexpr int units = D == 64 ? 12 : 5;
+    static constexpr uint32_t q_bytes = kChTile * 2 * D;
+    // tensor memory: a group's S and weights (three units of 64 columns, or S
+    // alone with the weights over it), then both groups' O
+    static constexpr bool over = D == 128;
+    static constexpr uint32_t sp_cols = over ? kChKeys : 3 * kChKeys / 2;
+    static constexpr uint32_t tO = 2 * sp_cols, cols = 512;
+    static_assert(tO + 2 * D <= cols, "tensor memory");
+};
+
+struct ChSmem {   // offsets from the 1024-byte aligned base
+    uint32_t q, ring, full, empty, vready, qready, sfull, sfree, pready, pvdone, odone, drain, tmem, dead, bad, dropped, pos, join, total;
+};
+
+template <int D>
+__host__ __device__ constexpr ChSmem ch_smem()
+{
+    using Sh = ChShape<D>;
+    ChSmem L = {};
+    uint32_t off = 0;
+    L.q = off;
+    off += 2 * Sh::q_bytes;
+    L.ring = off;
+    off += Sh::units * Sh::unit_bytes;
+    L.full = off;
+    off += Sh::units * 8;
+    L.empty = off;
+    off += Sh::units * 8;
+    L.vready = off;
+    off += Sh::units * 8;
+    L.qready = off;
+    off += 16;
+    L.sfull = off;
+    off += 16;
+    L.sfree = off;
+    off += 16;
+    L.pready = off;   // [block % 2][group]
+    off += 32;
+    L.pvdone = off;
+    off += 16;
+    L.odone = off;
+    off += 16;
+    L.drain = off;
+    off += 16;
+    L.tmem = off;
+    off += 8;
+    L.dead = off;
+    off += 8;
+    L.bad = off;       // [item % kChSeq]: the item, where it sees a page outside the cache
+    off += 4 * kChSeq;
+    L.dropped = off;   // the same: where values of V were left out
+    off += 4 * kChSeq;
+    L.pos = off;       // the part's start and end, every warp's place
+    off += (2 + kChThreads / 32) * sizeof(ChPos);
+    L.join = off;      // the second group's maxima and sums
+    off += 8 * kChTile;
+    L.total = off + 1024;
+    return L;
+}
+
+// ---- the items of a part, the same for every warp ----------------------------
+
+// A warp's place in the part is in shared memory (where[0], the part's end in
+// end[0]): registers hold the item alone
+struct ChWork {
+    const RaggedParams &p;
+    ChPos *where;
+    const ChPos *end;
+    int seq = 0;   // items with steps so far
+    // the item
+    ChRequest q;
+    ChPiece piece;
+    int rows, single, keys, all;   // keys: that some row sees; all: that every row sees
+
+    __device__ __forceinline__ ChWork(const RaggedParams &prm, ChPos *warp_pos, const ChPos *part_end) : p(prm), where(warp_pos), end(part_end) {}
+    __device__ __forceinline__ bool next()
+    {
+        ChPos at = *where;
+        bool found = false;
+        while (!found && !ch_reached(at, *end)) {
+            q = ragged_request(p, at.r, false);
+            if (q.n <= 0)
+                at = {at.r + 1, 0, 0, 0};
+            else
+                found = ch_take(q, p.group, p.nkv, at, *end, piece);
+        }
+        __syncwarp();
+        *where = at;
+        __syncwarp();
+        if (!found) return false;
+        rows = ch_rows(q.n, p.group, piece.at.b);
+        single = rows <= kChTile;
+        keys = ch_keys(q, p.group, piece.at.b);
+        all = q.L - q.n + piece.at.b * kChRows / p.group + 1;
+        if (piece.steps) ++seq;
+        return true;
+    }
+    __device__ __forceinline__ int steps() const { return piece.k1 - piece.at.k; }
+    __device__ __forceinline__ bool mine(int step, int w) const { return !single || (step & 1) == w; }   // (step from the piece's first)
+    __device__ __forceinline__ int pages(int step) const   // of a step, with keys
+    {
+        return min(kChPages, (keys + kPageSlots - 1) / kPageSlots - (piece.at.k + step) * kChPages);
+    }
+    // whether a step's V goes past the checker's eyes: an end behind the keys, or keys that some rows do not see
+    __device__ __forceinline__ bool partly(int step) const { return min(all, keys) < (piece.at.k + step + 1) * kChKeys; }
+    __device__ __forceinline__ bool whole() const { return piece.at.k == 0 && piece.k1 == piece.steps; }
+};
+
+__device__ __forceinline__ void ch_load_page(uint32_t dst, const CUtensorMap *m, uint32_t bar, int block, int c4)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %5, %3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(c4), "r"(block)
+        : "memory");
+}
+
+// Tensor memory into registers.  The wait stands in the same statement as the
+// loads: they write their registers behind the compiler's back, and what it put
+// in between (a register spilled or moved) would take or lose a value.
+#define CH_REGS16(a, i) PA_REGS8(a, i), PA_REGS8(a, i + 8)
+#define CH_REGS64(a) CH_REGS16(a, 0), CH_REGS16(a, 16), CH_REGS16(a, 32), CH_REGS16(a, 48)
+
+// 64 columns from addr and from addr2 on
+__device__ __forceinline__ void ch_load_scores(uint32_t addr, uint32_t (&a)[64], uint32_t addr2, uint32_t (&b)[64])
+{
+    asm volatile(
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
+        "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
+        "%60, %61, %62, %63}, [%128];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, "
+        "%78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, "
+        "%100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, "
+        "%118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        "}\n"
+        : CH_REGS64(a), CH_REGS64(b)
+        : "r"(addr), "r"(addr2)
+        : "memory");
+}
+
+__device__ __forceinline__ void ch_load64(uint32_t addr, uint32_t (&a)[64])
+{
+    asm volatile(
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
+        "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
+        "%60, %61, %62, %63}, [%64];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        "}\n"
+        : CH_REGS64(a)
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void ch_load32(uint32_t addr, uint32_t (&a)[32])
+{
+    asm volatile(
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        "}\n"
+        : CH_REGS16(a, 0), CH_REGS16(a, 16)
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void ch_load16(uint32_t addr, uint32_t (&a)[16])
+{
+    asm volatile(
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        "}\n"
+        : CH_REGS16(a, 0)
+        : "r"(addr)
+        : "memory");
+}
+
+// 1 / x and log2 x on the special-function unit, within 2^-22: functions with
+// a slow path are subroutine calls there
+__device__ __forceinline__ float ch_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float ch_lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Both softmax groups (named barrier 1)
+__device__ __forceinline__ void ch_groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// V row of key j of a request; null: its page is outside the cache
+template <int D>
+__device__ __forceinline__ const uint32_t *ch_value_row(const RaggedParams &p, int r, int g, int j)
+{
+    const int page = p.block_table[(int64_t)r * p.max_blocks + j / kPageSlots];
+    if (page < 0 || page >= p.num_pages) return nullptr;
+    const int64_t slot = ((int64_t)page * p.nkv + g) * kPageSlots + j % kPageSlots;
+    return reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.kv_cache) + slot * (2 * D) + D);
+}
+
 template <class E, int D>
-__global__ void __launch_bounds__(128) chunk_rows_kernel(const __grid_constant__ RaggedParams p)
+struct ChTile {
+    using Sh = ChShape<D>;
+    static constexpr int NU = Sh::units, U = kChKeys / 2;
+    static constexpr ChSmem LY = ch_smem<D>();
+    const CUtensorMap *map;
+    const RaggedParams &p;
+    uint8_t *smem;
+    uint32_t sb;
+    int lane;
+
+    __device__ __forceinline__ volatile int *dead_flag() const { return reinterpret_cast<volatile int *>(smem + LY.dead); }
+    __device__ __forceinline__ bool dead() const { return dead_flag()[0] != 0; }
+    __device__ __forceinline__ void wait(uint32_t bar, int n) const   // until phase n of bar is complete
+    {
+        pa_wait(sb + bar, (uint32_t)n & 1, dead_flag(), p.wait_limit_ns);
+    }
+    __device__ __forceinline__ volatile int *mark(uint32_t which, int seq) const
+    {
+        return reinterpret_cast<volatile int *>(smem + which) + seq % kChSeq;
+    }
+    __device__ __forceinline__ ChWork work() const
+    {
+        ChPos *pos = reinterpret_cast<ChPos *>(smem + LY.pos), *mine = pos + 2 + (threadIdx.x >> 5);
+        if (lane == 0) *mine = pos[0];
+        __syncwarp();
+        return ChWork(p, mine, pos + 1);
+    }
+    // V unit u, checked.  (An odd number of units holds K and V in turns in each
+    // place: only every other use of it passes the checker.)
+    __device__ __forceinline__ void wait_value(int u) const { wait(LY.vready + 8 * (u % NU), NU % 2 ? u / NU / 2 : u / NU); }
+    __device__ __forceinline__ uint32_t unit(int u) const { return LY.ring + (u % NU) * Sh::unit_bytes; }
+
+    // ---- produce: K, then V of every step ----
+    __device__ __forceinline__ void produce() const
+    {
+        if (lane == 0) tma_prefetch_map(map);
+        ChWork it = work();
+        int u = 0;
+        bool ok = true, bad_any = false;
+        while (ok && it.next()) {
+            const int32_t *table = p.block_table + (int64_t)it.piece.at.r * p.max_blocks;
+            const int pg0 = it.piece.at.k * kChPages, pg1 = min(it.piece.k1 * kChPages, (it.keys + kPageSlots - 1) / kPageSlots);
+            int next = pg0 + lane < pg1 ? table[pg0 + lane] : 0;
+            for (int c = pg0; c < pg1 && ok; c += 32) {
+                int page = next;
+                if (c + 32 + lane < pg1) next = table[c + 32 + lane];
+                bool bad = false;
+                if (c + lane < pg1 && (page < 0 || page >= p.num_pages)) {   // flagged, page 0 in its place
+                    bad = true;
+                    page = 0;
+                }
+                if (__any_sync(0xffffffffu, bad)) {   // seen by the softmax before the item's end
+                    bad_any = true;
+                    *mark(LY.bad, it.seq) = it.seq;
+                    __syncwarp();
+                }
+                for (int s0 = c; s0 < min(c + 32, pg1) && ok; s0 += kChPages) {
+                    const int n = min(kChPages, pg1 - s0), i = c + lane - s0;
+                    for (int v = 0; v < 2; ++v, ++u) {
+                        if (u >= NU) wait(LY.empty + 8 * (u % NU), u / NU - 1);
+                        __syncwarp();
+                        ok = !__any_sync(0xffffffffu, dead());
+                        if (!ok) break;
+                        const uint32_t bar = sb + LY.full + 8 * (u % NU);
+                        if (lane == 0) mbar_expect_tx(bar, (uint32_t)n * Sh::page_bytes);
+                        __syncwarp();
+                        if (i >= 0 && i < n)
+                            ch_load_page(sb + unit(u) + i * Sh::page_bytes, map, bar, v * Sh::nb, page * p.nkv + it.piece.at.g);
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
+            if (dead())   // our copies land before the CTA leaves
+                for (int k = max(0, u - NU); k < u; ++k)
+                    pa_wait(sb + LY.full + 8 * (k % NU), (uint32_t)((k / NU) & 1), dead_flag(), p.wait_limit_ns, false);
+        }
+        __syncwarp();
+    }
+
+    // ---- check: every V unit, before its product ----
+    __device__ __forceinline__ void check() const
+    {
+        ChWork it = work();
+        int u = 1;
+        while (it.next())
+            for (int s = 0; s < it.steps(); ++s, u += 2) {
+                wait(LY.full + 8 * (u % NU), u / NU);
+                __syncwarp();
+                if (it.partly(s) && look<true>(it, s, smem + unit(u))) *mark(LY.dropped, it.seq) = it.seq;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb + LY.vready + 8 * (u % NU));
+            }
+    }
+    // The V rows of a step: 0 behind the keys; not finite, among those that some
+    // row does not see: 0, and true
+    template <bool kDrop>
+    __device__ __forceinline__ bool look(const ChWork &it, int step, uint8_t *at) const
+    {
+        const int k0 = (it.piece.at.k + step) * kChKeys, from = max(min(it.all, it.keys) - k0, 0), keys = min(it.keys - k0, kChKeys);
+        const int to = (keys + kPageSlots - 1) / kPageSlots * kPageSlots;
+        bool found = false, wrote = false;
+#pragma unroll 4
+        for (int c = from * (D / 8) + lane; c < to * (D / 8); c += 32) {
+            const int key = c / (D / 8), ch = c % (D / 8);   // (a row's 16-byte chunks in any order)
+            uint4 *x = reinterpret_cast<uint4 *>(at + (key >> 3) * (Sh::nb * 1024) + (ch / 8) * 1024 + (key & 7) * 128 + (ch & 7) * 16);
+            const uint4 v = *x;
+            uint4 m = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (key < keys) {
+                m = make_uint4(pa_not_finite<E>(v.x), pa_not_finite<E>(v.y), pa_not_finite<E>(v.z), pa_not_finite<E>(v.w));
+                found |= (m.x | m.y | m.z | m.w) != 0;
+            }
+            if (m.x | m.y | m.z | m.w) {
+                wrote = true;
+                *x = make_uint4(v.x & ~m.x, v.y & ~m.y, v.z & ~m.z, v.w & ~m.w);
+            }
+        }
+        if (__any_sync(0xffffffffu, wrote)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        return __any_sync(0xffffffffu, found);
+    }
+
+    // ---- multiply: group W's S = Q K^T and O += P V ----
+    template <int W>
+    __device__ __forceinline__ void multiply() const
+    {
+        ChWork it = work();
+        int u0 = 0, items = 0, blk = 0;   // units before the item; items and steps of this group
+        const uint64_t qd = pa_desc(sb + LY.q + W * Sh::q_bytes, 16, 1024);
+        const uint64_t kd0 = pa_desc(sb + LY.ring, 16, Sh::nb * 1024);
+        const uint64_t vd0 = pa_desc(sb + LY.ring, 1024, Sh::nb * 1024);
+        constexpr uint32_t dSP = W * Sh::sp_cols, dO = Sh::tO + W * D;
+        // S of the step whose K is unit u, the item's `nth` of this group
+        const auto scores = [&](int u, int nth) {
+            wait(LY.full + 8 * (u % NU), u / NU);
+            // the columns S takes: the weights before (one, or two steps ago) are
+            // multiplied (an item's end has waited for all of its products), and
+            // the last S is read
+            if (Sh::over) {
+                if (blk > 0) wait(LY.pvdone + 8 * W, blk - 1);
+            } else {
+                if (nth > 1) wait(LY.pvdone + 8 * W, blk - 2);
+                if (blk > 0) wait(LY.sfree + 8 * W, blk - 1);
+            }
+            __syncwarp();
+            tc_fence_after();
+            const uint64_t kd = kd0 + (uint32_t)(u % NU) * (Sh::unit_bytes / 16);
+            const uint32_t dS = dSP + (Sh::over ? 0 : (blk & 1) * U);
+            if (pa_elect()) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    umma_bf16(dS, qd + (i / 4) * (kChTile * 8) + (i % 4) * 2, kd + (i / 4) * 64 + (i % 4) * 2,
+                              pa_idesc<E>(kChKeys, false), i != 0);
+                umma_commit(sb + LY.sfull + 8 * W);
+                umma_commit(sb + LY.empty + 8 * (u % NU));
+            }
+            __syncwarp();
+            ++blk;
+        };
+        const auto values = [&](int b, int u, int pages, uint32_t acc) {   // O += P V of step b, its V unit u
+            wait_value(u);
+            wait(LY.pready + 16 * (b & 1) + 8 * W, b >> 1);
+            __syncwarp();
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint32_t)(u % NU) * (Sh::unit_bytes / 16);
+            const uint32_t dP = dSP + (Sh::over ? 0 : (b & 1) * 2 * U);
+            if (pa_elect()) {
+                if (pages == kChPages) {
+#pragma unroll
+                    for (int i = 0; i < kChPages; ++i)
+                        pa_umma_ts(dO, dP + 8 * i, vd + i * (Sh::page_bytes / 16), pa_idesc<E>(D, true), i > 0 ? 1u : acc);
+                } else {
+                    for (int i = 0; i < pages; ++i)
+                        pa_umma_ts(dO, dP + 8 * i, vd + i * (Sh::page_bytes / 16), pa_idesc<E>(D, true), i > 0 ? 1u : acc);
+                }
+                umma_commit(sb + LY.pvdone + 8 * W);
+                umma_commit(sb + LY.empty + 8 * (u % NU));
+            }
+            __syncwarp();
+        };
+        // The other group's step: its units pass here too, in order, so that no
+        // phase of a barrier is missed
+        const auto pass = [&](int u) {
+            wait(LY.full + 8 * (u % NU), u / NU);
+            wait_value(u + 1);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(sb + LY.empty + 8 * (u % NU));
+                mbar_arrive(sb + LY.empty + 8 * ((u + 1) % NU));
+            }
+        };
+        while (it.next()) {
+            const int n = it.steps();
+            int before = -1, nth = 0;   // the step whose product is due
+            for (int s = 0; s < n; ++s) {
+                if (!it.mine(s, W)) {
+                    pass(u0 + 2 * s);
+                    continue;
+                }
+                if (nth == 0) wait(LY.qready + 8 * W, items++);
+                if (Sh::over && nth > 0) values(blk - 1, u0 + 2 * before + 1, kChPages, nth > 1);
+                scores(u0 + 2 * s, nth);
+                if (!Sh::over && nth > 0) values(blk - 2, u0 + 2 * before + 1, kChPages, nth > 1);
+                before = s;
+                ++nth;
+            }
+            if (nth > 0) {
+                values(blk - 1, u0 + 2 * before + 1, it.pages(before), nth > 1);
+                if (pa_elect()) umma_commit(sb + LY.odone + 8 * W);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb + LY.odone + 8 * W);   // with the flags of bad pages and values left out
+            }
+            u0 += 2 * n;
+        }
+        // every MMA of this warp is done before tensor memory is freed (the same
+        // lane is elected each time: commits cover the MMAs of one thread)
+        if (pa_elect()) umma_commit(sb + LY.drain + 8 * W);
+        __syncwarp();
+        if (lane == 0) pa_wait(sb + LY.drain + 8 * W, 0, dead_flag(), p.wait_limit_ns, false);
+        __syncwarp();
+    }
+
+    // ---- softmax: thread = row of group w's tile ----
+    __device__ __forceinline__ void softmax(int w, int wq) const
+    {
+        const int row = 32 * wq + lane;
+        const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+        const uint32_t aSP = w * Sh::sp_cols + lane_base, aO = Sh::tO + w * D + lane_base;
+        uint8_t *sq = smem + LY.q + w * Sh::q_bytes;
+        ChWork it = work();
+        int blk = 0, items = 0;
+        const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
+        while (it.next()) {
+            const int n = it.steps(), by = it.single ? 2 : 1, first = it.single ? w : 0;
+            const int m = (it.single ? 0 : w * kChTile) + row;   // the thread's row of the block
+            const bool active = 32 * wq + (it.single ? 0 : w * kChTile) < it.rows;
+            const int mr = it.piece.at.b * kChRows + m, tok = mr / p.group, head = it.piece.at.g * p.group + mr - tok * p.group;
+            const int64_t grow = ((int64_t)it.q.row0 + tok) * p.q_heads + head;   // output row
+            const bool valid = m < it.rows;
+            const int limit = valid ? it.q.L - it.q.n + tok + 1 : 0;              // keys that the row sees
+            if (n == 0) {   // rows that see no key
+                if (valid && (!it.single || w == 0)) put_none(grow, true);
+                continue;
+            }
+            float mu = -INFINITY, l = 0.f;
+            if (first < n) {
+                if (active) {   // the previous item is done: its Q is no longer read
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
+                                                                       ((int64_t)it.q.row0 + tok) * p.q_ts + head * p.q_hs);
+                    uint4 v[D / 8];
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) v[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint4 *>(sq + (c / 8) * (kChTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                mbar_arrive(sb + LY.qready + 8 * w);
+                uint32_t so[U], sm[U];
+                int outer = 0;   // the half of the keys in S's outer unit
+                const auto arrive = [&](uint32_t bar) {   // for this warp, which has left tensor memory
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sb + bar);
+                };
+                // (two barriers in turn: S of step b says that the weights of step
+                // b - 2 have been multiplied, so that phase has been seen)
+                const auto pready = [&](int b) { return LY.pready + 16 * (b & 1) + 8 * w; };
+                // The weights of step s, against the maximum so far.  Later scores
+                // may exceed it as long as a step's weights stay below a limit in sum
+                // (so no maximum is taken per step); otherwise it follows and O is
+                // rescaled.  An item's first step starts there.
+                const auto weigh = [&](int s) {
+                    const uint32_t aOut = aSP + 2 * outer * U;
+                    uint32_t po[U / 2], pm[U / 2];
+                    const int left = limit - (it.piece.at.k + s) * kChKeys;   // keys of the step that the row sees
+                    const bool hide = __any_sync(0xffffffffu, valid && left < kChKeys);
+                    if (hide) {
+                        pa_hide(so, left - outer * U);
+                        pa_hide(sm, left - (outer ^ 1) * U);
+                    }
+                    float base = -mu, sum = INFINITY;
+                    for (bool again = false;; again = true) {
+                        if (again || s != first) {
+                            sum = pa_weights<E>(so, po, cc, base);
+                            sum += pa_weights<E>(sm, pm, cc, base);
+                            if (again || !__any_sync(0xffffffffu, !(sum < PaWeight<E>::most))) break;
+                            ch_load64(aOut, so);   // not overwritten yet
+                            if (hide) pa_hide(so, left - outer * U);
+                        }
+                        // (only this row's own scores move it, not a neighbour's)
+                        const float top = fmaf(pa_max(so, pa_max(sm, -INFINITY)), p.scale_log2, -PaWeight<E>::below);
+                        const bool grew = top > mu && !(sum < PaWeight<E>::most);
+                        const float al = grew ? a2_ex2(mu - top) : 1.f;
+                        if (grew) mu = top;
+                        base = mu == -INFINITY ? 0.f : -mu;
+                        l *= al;
+                        if (s != first) {
+                            wait(LY.pvdone + 8 * w, blk - 1);
+                            __syncwarp();
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                ch_load16(aO + c, o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                pa_tmem_st16(aO + c, o);
+                            }
+                        }
+                    }
+                    l += sum;
+                    pa_tmem_st<U / 2>(aOut + outer * (U / 2), po);
+                    pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pm);
+                };
+                for (int s = first; s < n; s += by, ++blk) {
+                    wait(LY.sfull + 8 * w, blk);
+                    __syncwarp();
+                    if (active) {
+                        tc_fence_after();
+                        outer = Sh::over ? 0 : blk & 1;
+                        ch_load_scores(aSP + 2 * outer * U, so, aSP + U, sm);
+                        if (!Sh::over) arrive(LY.sfree + 8 * w);
+                        weigh(s);
+                        pa_tmem_st_wait();
+                    } else if (!Sh::over) {
+                        arrive(LY.sfree + 8 * w);
+                    }
+                    arrive(pready(blk));
+                }
+                wait(LY.odone + 8 * w, items++);
+                __syncwarp();
+                tc_fence_after();
+            }
+            finish(it, w, row, m, active, valid, grow, limit, mu, l, aO);
+            tc_fence_before();
+        }
+    }
+
+    // A row without keys, or of a skipped request
+    __device__ __forceinline__ void put_none(int64_t grow, bool seen) const
+    {
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + grow * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) out[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (seen && p.lse) p.lse[grow] = -INFINITY;
+    }
+
+    // The item's rows: joined if the groups shared them, then the output, or a partial
+    __device__ __forceinline__ void finish(const ChWork &it, int w, int row, int m, bool active, bool valid, int64_t grow, int limit,
+                                           float mu, float l, uint32_t aO) const
+    {
+        const bool joined = it.single && it.steps() > 1;
+        float4 *shared = reinterpret_cast<float4 *>(smem + LY.q);      // [D / 4][128]: the whole Q area, whose products are done
+        float2 *shared_ml = reinterpret_cast<float2 *>(smem + LY.join);
+        if (it.single && w == 1) {
+            if (!joined) return;
+            ch_groups_sync();   // both groups' products are done
+            if (active) {
+                shared_ml[row] = make_float2(mu, l);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    ch_load32(aO + c, o);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        shared[(c + e) / 4 * kChTile + row] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                                         __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                }
+            }
+            ch_groups_sync();   // written
+            ch_groups_sync();   // and read
+            return;
+        }
+        float al0 = 1.f, al1 = 0.f;
+        if (joined) {
+            ch_groups_sync();
+            ch_groups_sync();
+            if (active) {
+                const float2 other = shared_ml[row];
+                const float top = fmaxf(mu, other.x), base = top == -INFINITY ? 0.f : top;
+                al0 = a2_ex2(mu - base);
+                al1 = a2_ex2(other.x - base);
+                l = l * al0 + other.y * al1;
+                mu = top;
+            }
+        }
+        if (active && !__any_sync(0xffffffffu, dead())) {
+            const bool dropped = *mark(LY.dropped, it.seq) == it.seq, bad = *mark(LY.bad, it.seq) == it.seq;
+            const bool whole = it.whole();
+            const int part = 2 * blockIdx.x + (it.piece.at.k == 0);
+            float *po = p.ws_o + ((int64_t)part * kChRows + m) * D;
+            const float inv = ch_rcp(l);   // (a sum of a row that sees a key is far above the subnormals)
+            uint16_t *out = static_cast<uint16_t *>(p.out) + grow * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                ch_load32(aO + c, o);
+                if (joined) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 y = shared[(c + e) / 4 * kChTile + row];
+                        o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), al0, y.x * al1));
+                        o[e + 1] = __float_as_uint(fmaf(__uint_as_float(o[e + 1]), al0, y.y * al1));
+                        o[e + 2] = __float_as_uint(fmaf(__uint_as_float(o[e + 2]), al0, y.z * al1));
+                        o[e + 3] = __float_as_uint(fmaf(__uint_as_float(o[e + 3]), al0, y.w * al1));
+                    }
+                }
+                if (dropped) {
+                    const int to = min(min(it.keys, it.piece.k1 * kChKeys), limit);
+#pragma unroll 1
+                    for (int key = max(it.all, it.piece.at.k * kChKeys); key < to; ++key) {
+                        const uint32_t *v = ch_value_row<D>(p, it.piece.at.r, it.piece.at.g, key);
+                        if (!v) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a = __uint_as_float(o[e]), b = __uint_as_float(o[e + 1]);
+                            pa_add_not_finite<E>(v[(c + e) / 2], a, b);
+                            o[e] = __float_as_uint(a);
+                            o[e + 1] = __float_as_uint(b);
+                        }
+                    }
+                }
+                if (valid && !whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(po + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if (valid && !bad) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            y[i] = l == 0.f ? 0u : E::pack(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+            if (valid && !whole)
+                p.ws_ml[(int64_t)part * kChRows + m] = make_float2(mu, bad ? -1.f : l);
+            else if (valid && bad && p.zero)
+                put_none(grow, false);
+            else if (valid && !bad && p.lse)
+                p.lse[grow] = l == 0.f ? -INFINITY : (mu + ch_lg2(l)) * 0.6931471805599453f;
+        }
+        if (joined) ch_groups_sync();   // the Q area is the next item's
+    }
+};
+
+// Where every part of the line of work starts: the requests' costs added up (a
+// thread's run of requests each), then a part a thread.
+constexpr int kChPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kChPlanThreads) chunk_plan_kernel(const __grid_constant__ RaggedParams p)
+{
+    __shared__ int64_t before[kChPlanThreads + 1], warps[32];
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.R + kChPlanThreads - 1) / kChPlanThreads, r0 = tid * per, r1 = min(p.R, r0 + per);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) mine += p.nkv * ch_request_cost(ragged_request(p, r, true), p.group);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) warps[warp] = upto;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t v = warps[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        warps[lane] = v;
+    }
+    __syncthreads();
+    if (warp > 0) upto += warps[warp - 1];
+    before[tid + 1] = upto;
+    if (tid == 0) before[0] = 0;
+    __syncthreads();
+    const int64_t total = before[kChPlanThreads];
+    for (int c = tid; c <= p.parts; c += kChPlanThreads) {
+        ChPos at = {p.R, 0, 0, 0};
+        int64_t off = ch_part(total, p.parts, c);
+        if (off < total) {
+            int lo = 0, hi = kChPlanThreads - 1;   // the last thread whose run starts at or before it
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (before[mid] <= off) lo = mid;
+                else hi = mid - 1;
+            }
+            off -= before[lo];
+            for (int r = lo * per; r < min(p.R, lo * per + per); ++r) {
+                const ChRequest q = ragged_request(p, r, false);
+                const int64_t cost = p.nkv * ch_request_cost(q, p.group);
+                if (off < cost) {
+                    at = ch_locate(q, p.group, r, off);
+                    break;
+                }
+                off -= cost;
+            }
+        }
+        p.ws_pos[c] = at;
+    }
+}
+
+template <class E, int D>
+__global__ void __launch_bounds__(kChThreads, 1)
+    chunk_tile_kernel(const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ RaggedParams p)
+{
+    using Sh = ChShape<D>;
+    constexpr ChSmem LY = ch_smem<D>();
+    extern __shared__ uint8_t ch_smem_dyn[];
+    uint8_t *smem = ch_smem_dyn + ((1024u - (smem_u32(ch_smem_dyn) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    ChPos *pos = reinterpret_cast<ChPos *>(smem + LY.pos);
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();   // every input comes from the kernels before this one
+    const ChPos begin = p.ws_pos[blockIdx.x], end = p.ws_pos[blockIdx.x + 1];
+    if (ch_reached(begin, end)) return;   // no work is left for this part
+    if (threadIdx.x == 0) {
+        pos[0] = begin;
+        pos[1] = end;
+        for (int i = 0; i < Sh::units; ++i) {
+            mbar_init(sb + LY.full + 8 * i, 1);
+            mbar_init(sb + LY.empty + 8 * i, 2);
+            mbar_init(sb + LY.vready + 8 * i, 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(sb + LY.qready + 8 * w, 128);
+            mbar_init(sb + LY.sfull + 8 * w, 1);
+            mbar_init(sb + LY.sfree + 8 * w, 4);
+            mbar_init(sb + LY.pready + 8 * w, 4);
+            mbar_init(sb + LY.pready + 16 + 8 * w, 4);
+            mbar_init(sb + LY.pvdone + 8 * w, 1);
+            mbar_init(sb + LY.odone + 8 * w, 2);
+            mbar_init(sb + LY.drain + 8 * w, 1);
+        }
+        *reinterpret_cast<volatile int *>(smem + LY.dead) = 0;
+        for (int i = 0; i < 2 * kChSeq; ++i) reinterpret_cast<volatile int *>(smem + LY.bad)[i] = 0;   // (and dropped)
+        fence_barrier_init();
+    }
+    // all of tensor memory (one CTA per SM): it starts at column 0
+    if (warp == 0) a2_tmem_alloc<Sh::cols>(sb + LY.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const ChTile<E, D> tile{&tmKV, p, smem, sb, lane};
+    // a softmax thread holds a row's whole S: its groups take registers from the
+    // other warpgroup (256 x 216 + 128 x 72 = 384 x 168, what the launch has)
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        tile.softmax(warp >> 2, warp & 3);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8)
+            tile.produce();
+        else if (warp == 9)
+            tile.check();
+        else if (warp == 10)
+            tile.template multiply<0>();
+        else
+            tile.template multiply<1>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) a2_tmem_dealloc<Sh::cols>(0u);
+}
+
+// Joins the partials of the item that part blockIdx.x leaves to the next ones,
+// a warp per row, the parts in order; and clears the rows of an output without
+// earlier contents that no request has.
+constexpr int kChMergeThreads = 256, kChMergeY = 8;   // 32 rows a CTA
+
+template <class E, int D>
+__global__ void __launch_bounds__(kChMergeThreads) chunk_merge_kernel(const __grid_constant__ RaggedParams p)
 {
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (int64_t)p.T * p.q_heads) return;
-    const int t = (int)(row / p.q_heads), h = (int)(row % p.q_heads), g = h / p.group;
-    uint16_t *out = static_cast<uint16_t *>(p.out) + row * D;
-    int lo = 0, hi = p.R;   // the last request that starts at or before t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (p.starts[mid] <= t) lo = mid;
-        else hi = mid - 1;
-    }
-    bool ok = lo < p.R && p.starts[lo] <= t && t < p.starts[lo + 1];
-    RaggedRequest q = {0, -1, 0};
-    if (ok) q = ragged_request(p, lo);
-    ok = q.n >= 0;
-    if (blockIdx.x == 0)   // each request's starts and length, flagged once
-        for (int r = threadIdx.x; r < p.R; r += 128) ragged_request(p, r);
-    float acc[D / 32] = {}, m = -INFINITY, l = 0.f, part = 0.f, qv[D / 32];   // part: of up to 64 keys
-    if (ok) {
-        const uint16_t *qp = static_cast<const uint16_t *>(p.q) + t * p.q_ts + h * p.q_hs;
-        for (int i = 0; i < D / 32; ++i) qv[i] = E::get(qp[lane + 32 * i]);
-        const int end = q.L - q.n + (t - q.row0) + 1;
-        for (int j = 0; j < end; ++j) {
-            const int page = p.block_table[(int64_t)lo * p.max_blocks + j / kPageSlots];
-            if (page < 0 || page >= p.num_pages) {
-                ok = false;
-                atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
-                break;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    using V = typename std::conditional<D == 128, float4, float2>::type;   // a lane's columns
+    if (p.zero)
+        for (int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; t < p.T; t += (int64_t)gridDim.x * gridDim.y * 8) {
+            int lo = 0, hi = p.R;   // the last request that starts at or before t
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (p.starts[mid] <= t) lo = mid;
+                else hi = mid - 1;
             }
-            const uint16_t *k = static_cast<const uint16_t *>(p.kv_cache) +
-                                (((int64_t)page * p.nkv + g) * kPageSlots + j % kPageSlots) * (2 * D);
-            const float s = ragged_dot<E, D>(k, qv, lane) * p.scale_log2, mn = fmaxf(m, s);
-            const float al = exp2f(m - mn), w = exp2f(s - mn);
-            m = mn;
-            part = part * al + w;
-            l *= al;
-            if (j % 64 == 63) {
-                l += part;
-                part = 0.f;
-            }
-            for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(w, E::get(k[D + lane + 32 * i]), acc[i] * al);
+            if (lo < p.R && p.starts[lo] <= t && t < p.starts[lo + 1] && ragged_request(p, lo, false).n > 0) continue;
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + t * p.q_heads * D);
+            for (int64_t i = lane; i < (int64_t)p.q_heads * D / 8; i += 32) out[i] = make_uint4(0u, 0u, 0u, 0u);
         }
+    const int c = blockIdx.x;
+    const ChPos here = p.ws_pos[c], next = p.ws_pos[c + 1];
+    if (next.k == 0 || (ch_same_item(here, next) && here.k > 0)) return;   // none, or an earlier part's
+    const ChRequest q = ragged_request(p, next.r, false);
+    int last = c + 1;   // the part that ends it
+    while (ch_same_item(p.ws_pos[last + 1], next)) ++last;
+    const int rows = ch_rows(q.n, p.group, next.b);
+    for (int m = blockIdx.y * 8 + warp; m < rows; m += gridDim.y * 8) {
+        const auto slot = [&](int part) { return ((int64_t)2 * part + (part == c)) * kChRows + m; };
+        float top = -INFINITY;
+        bool bad = false;
+        for (int i = c + lane; i <= last; i += 32) {   // (a part without a step of it left nothing)
+            if (i > c && i < last && p.ws_pos[i].k == p.ws_pos[i + 1].k) continue;
+            const float2 ml = p.ws_ml[slot(i)];
+            bad |= ml.y < 0.f;
+            top = fmaxf(top, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        bad = __any_sync(0xffffffffu, bad);
+        const int mr = next.b * kChRows + m, tok = mr / p.group;
+        const int64_t grow = ((int64_t)q.row0 + tok) * p.q_heads + next.g * p.group + mr - tok * p.group;
+        uint16_t *out = static_cast<uint16_t *>(p.out) + grow * D + lane * (D / 32);
+        if (bad) {
+            for (int e = 0; p.zero && e < D / 32; ++e) out[e] = 0;
+            continue;
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+        float o[D / 32] = {}, l = 0.f;
+#pragma unroll 4
+        for (int i = c; i <= last; ++i) {
+            if (i > c && i < last && p.ws_pos[i].k == p.ws_pos[i + 1].k) continue;
+            const float2 ml = p.ws_ml[slot(i)];
+            const V y = *reinterpret_cast<const V *>(p.ws_o + slot(i) * D + lane * (D / 32));
+            const float al = a2_ex2(ml.x - base);
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;   // no key of it seen
+            l = fmaf(ml.y, al, l);
+            o[0] = fmaf(y.x, al, o[0]);
+            o[1] = fmaf(y.y, al, o[1]);
+            if constexpr (D == 128) {
+                o[2] = fmaf(y.z, al, o[2]);
+                o[3] = fmaf(y.w, al, o[3]);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < D / 32; e += 2)
+            *reinterpret_cast<uint32_t *>(out + e) = l == 0.f ? 0u : E::pack(o[e] * inv, o[e + 1] * inv);
+        if (p.lse && lane == 0) p.lse[grow] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
     }
-    if (!ok) {
-        for (int i = 0; p.zero && i < D / 32; ++i) out[lane + 32 * i] = 0;
-        return;
-    }
-    l += part;
-    for (int i = 0; i < D / 32; ++i) out[lane + 32 * i] = E::put(l == 0.f ? 0.f : acc[i] / l);
-    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <class E, int D>
+bool prepare_chunk_kernel()
+{
+    static_assert(ch_smem<D>().total <= (uint32_t)kMaxSmemPerCta, "shared memory");
+    return cudaFuncSetAttribute((const void *)chunk_tile_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)ch_smem<D>().total) == cudaSuccess;
+}
+
+bool prepare_chunk_kernels()
+{
+    return prepare_chunk_kernel<Bf16, 64>() && prepare_chunk_kernel<Bf16, 128>() && prepare_chunk_kernel<Fp16, 64>() &&
+           prepare_chunk_kernel<Fp16, 128>();
+}
+
+// The cache as in encode_prefix_map, in boxes of K or V of one page of one KV
+// head: 8-slot groups of its 64-column blocks, 1 KB each
+int encode_chunk_map(const void *kv_cache, int64_t num_pages, int nkv, int head_dim, bool bf16, CUtensorMap *m)
+{
+    const cuuint64_t slot = (cuuint64_t)head_dim * 4;   // bytes of a slot
+    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)head_dim / 32, 2, (cuuint64_t)num_pages * nkv};
+    const cuuint64_t strides[4] = {slot, 128, 8 * slot, kPageSlots * slot};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)head_dim / 64, 2, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, (void *)kv_cache,
+                    dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QKVF_OK
+               : QKVF_ERR_CUDA;
+}
+
+template <class E, int D>
+int launch_chunk(const CUtensorMap &map, const RaggedParams &prm, void *stream)
+{
+    int rc = launch_pdl(chunk_plan_kernel, dim3(1), dim3(kChPlanThreads), 0, stream, prm);
+    if (rc != QKVF_OK) return rc;
+    rc = launch_pdl(chunk_tile_kernel<E, D>, dim3((unsigned)prm.parts), dim3(kChThreads), (size_t)ch_smem<D>().total,
+                              stream, map, prm);
+    if (rc != QKVF_OK) return rc;
+    return launch_pdl(chunk_merge_kernel<E, D>, dim3((unsigned)prm.parts, kChMergeY), dim3(kChMergeThreads), 0, stream, prm);
 }
 
 template <class E, int D>
@@ -124,7 +1014,7 @@ __global__ void __launch_bounds__(128) key_rows_kernel(const __grid_constant__ R
     griddep_wait();
     const int lane = threadIdx.x & 31, r = blockIdx.z, g = blockIdx.y;
     const int j = blockIdx.x * 4 + (threadIdx.x >> 5);
-    const RaggedRequest q = ragged_request(p, r);
+    const ChRequest q = ragged_request(p, r, threadIdx.x == 0 && blockIdx.x == 0);
     if (q.n < 0 || j >= q.L) return;
     const int page = p.block_table[(int64_t)r * p.max_blocks + j / kPageSlots];
     if (page < 0 || page >= p.num_pages) {
@@ -294,7 +1184,12 @@ RaggedParams ragged_params(const void *q, int64_t q_ts, int64_t q_hs, const void
     return p;
 }
 
-size_t chunk_workspace(int head_dim, int sms) { return 512; }
+// Two partials a part, their maxima and sums, the parts' starts
+size_t chunk_workspace(int head_dim, int sms)
+{
+    const size_t slots = (size_t)2 * sms;
+    return slots * kChRows * (head_dim * 4 + 8) + ((size_t)(sms + 1) * sizeof(ChPos) + 255) / 256 * 256;
+}
 size_t key_weights_workspace(int head_dim, int sms) { return 512; }
 
 }  // namespace qkvf
@@ -345,10 +1240,19 @@ int chunk_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, con
     if (rc != QKVF_OK) return rc;
     if (workspace_bytes < qkvf::chunk_workspace(head_dim, d->sms)) return QKVF_ERR_SIZES;
     const bool bf16 = qkvf::dtype_of(dtype) == QKVF_DTYPE_BF16;
-    const dim3 grid((unsigned)(((int64_t)T * q_heads + 3) / 4));
-    return qkvf::launch_pdl(bf16 ? head_dim == 64 ? qkvf::chunk_rows_kernel<qkvf::Bf16, 64> : qkvf::chunk_rows_kernel<qkvf::Bf16, 128>
-                                 : head_dim == 64 ? qkvf::chunk_rows_kernel<qkvf::Fp16, 64> : qkvf::chunk_rows_kernel<qkvf::Fp16, 128>,
-                            grid, dim3(128), 0, stream, prm);
+    CUtensorMap map;
+    const int mrc = qkvf::encode_chunk_map(kv_cache, num_pages, num_kv_heads, head_dim, bf16, &map);
+    if (mrc != QKVF_OK) return mrc;
+    prm.wait_limit_ns = qkvf::g_wait_limit_ns;
+    prm.parts = d->sms;
+    prm.ws_o = static_cast<float *>(workspace);
+    prm.ws_ml = reinterpret_cast<float2 *>(prm.ws_o + (size_t)2 * d->sms * qkvf::kChRows * head_dim);
+    prm.ws_pos = reinterpret_cast<qkvf::ChPos *>(prm.ws_ml + (size_t)2 * d->sms * qkvf::kChRows);
+    if (bf16)
+        return head_dim == 64 ? qkvf::launch_chunk<qkvf::Bf16, 64>(map, prm, stream)
+                              : qkvf::launch_chunk<qkvf::Bf16, 128>(map, prm, stream);
+    return head_dim == 64 ? qkvf::launch_chunk<qkvf::Fp16, 64>(map, prm, stream)
+                          : qkvf::launch_chunk<qkvf::Fp16, 128>(map, prm, stream);
 }
 
 size_t key_weights_workspace_bytes(int T, int num_reqs, int q_heads, int num_kv_heads, int head_dim, int max_blocks)

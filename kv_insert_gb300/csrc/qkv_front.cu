@@ -1169,6 +1169,7 @@ constexpr bool kDefaultTC = false;     // consumer: tcgen05 (true) or mma.sync
 bool prepare_epi_kernel();
 bool prepare_attn2_kernel();
 bool prepare_prefix_kernels();
+bool prepare_chunk_kernels();
 
 int probe_device(DeviceState **out)
 {
@@ -1211,7 +1212,8 @@ int probe_device(DeviceState **out)
             if (cudaFuncSetAttribute(res[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)res_smem_bytes(i ? 16 : 8)) != cudaSuccess)
                 return QKVF_ERR_CUDA;
-        if (!prepare_epi_kernel() || !prepare_attn2_kernel() || !prepare_prefix_kernels()) return QKVF_ERR_CUDA;
+        if (!prepare_epi_kernel() || !prepare_attn2_kernel() || !prepare_prefix_kernels() || !prepare_chunk_kernels())
+            return QKVF_ERR_CUDA;
         d.prepared = true;
     }
     *out = &d;

@@ -1,0 +1,124 @@
+"""The dealing of a chunk_attn call's work (chunk_plan.h), on the host under
+the undefined-behaviour sanitizer: every key step of every item is taken once,
+in order, by parts of nearly equal cost, for drawn and extreme batches."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+CHECK = r"""
+#include "chunk_plan.h"
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include <vector>
+using namespace qkvf;
+#define NEED(c) do { if (!(c)) { printf("failed: %s (group %d parts %d)\n", #c, group, parts); exit(1); } } while (0)
+
+// One batch: the parts' pieces in order against the list of all items
+static void check(const std::vector<ChRequest> &reqs, int nkv, int group, int parts)
+{
+    const int R = (int)reqs.size();
+    std::vector<int64_t> before(R + 1, 0);
+    for (int r = 0; r < R; ++r) {
+        int64_t sum = 0;
+        const int blocks = ch_blocks(reqs[r].n, group);
+        for (int b = 0; b < blocks; ++b) {
+            if (b < 2000 || b == blocks - 1) NEED(ch_before(reqs[r], group, b) == sum || b >= 2000);
+            sum += ch_cost(reqs[r], group, b);
+        }
+        NEED(blocks == 0 || sum == ch_request_cost(reqs[r], group));
+        before[r + 1] = before[r] + nkv * ch_request_cost(reqs[r], group);
+    }
+    const int64_t total = before[R];
+    NEED(total >= 0 && total < (int64_t(1) << 60));
+    std::vector<ChPos> pos;
+    for (int c = 0; c <= parts; ++c) {
+        const int64_t u = ch_part(total, parts, c);
+        NEED(u >= 0 && u <= total && (c < parts || u == total));
+        ChPos at = {R, 0, 0, 0};
+        for (int r = 0; r < R; ++r)
+            if (u >= before[r] && u < before[r + 1]) at = ch_locate(reqs[r], group, r, u - before[r]);
+        if (at.r < R) {
+            NEED(at.g >= 0 && at.g < nkv && at.b >= 0 && at.b < ch_blocks(reqs[at.r].n, group));
+            const int steps = ch_steps(ch_keys(reqs[at.r], group, at.b));
+            NEED(at.k >= 0 && (steps == 0 ? at.k == 0 : at.k < steps));
+        }
+        NEED(c == 0 || ch_reached(at, pos.back()));
+        pos.push_back(at);
+    }
+    ChPos want = {0, 0, 0, 0};   // the next step that nobody has taken
+    const auto settle = [&] { while (want.r < R && reqs[want.r].n <= 0) want = {want.r + 1, 0, 0, 0}; };
+    settle();
+    for (int c = 0; c < parts; ++c) {
+        ChPos at = pos[c];
+        int first = 0, last = 0, count = 0;
+        while (!ch_reached(at, pos[c + 1])) {
+            if (reqs[at.r].n <= 0) {
+                at = {at.r + 1, 0, 0, 0};
+                continue;
+            }
+            ChPiece p;
+            const ChRequest &q = reqs[at.r];
+            if (!ch_take(q, group, nkv, at, pos[c + 1], p)) continue;
+            NEED(ch_same_item(p.at, want) && p.at.k == want.k);
+            NEED(p.k1 <= p.steps && p.k1 >= p.at.k);
+            first += p.at.k > 0;
+            last += p.at.k == 0 && p.k1 < p.steps;
+            NEED(p.at.k == 0 || count == 0);   // only a part's first piece continues an item
+            ++count;
+            want.k = p.k1;
+            if (p.k1 == p.steps) {
+                want.k = 0;
+                if (++want.b == ch_blocks(q.n, group)) {
+                    want.b = 0;
+                    if (++want.g == nkv) want = {want.r + 1, 0, 0, 0};
+                }
+                settle();
+            }
+        }
+        NEED(first <= 1 && last <= 1);
+    }
+    NEED(want.r == R);
+}
+
+int main()
+{
+    std::mt19937 rng(7);
+    const auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+    for (int i = 0; i < 3000; ++i) {
+        std::vector<ChRequest> reqs;
+        const int R = pick(0, 12), most = 1 << pick(0, 12);
+        for (int r = 0; r < R; ++r) {
+            const int n = pick(0, 3) ? pick(0, most) : 1;
+            reqs.push_back({0, n, pick(0, 5) ? n + pick(0, 1 << pick(0, 17)) : pick(0, n)});
+        }
+        check(reqs, pick(1, 9), pick(1, 64), pick(0, 1) ? 152 : pick(1, 300));
+    }
+    const int far = 1 << 24;
+    check({{0, far, far}}, 1, 1, 152);
+    check({{0, far, far}}, 64, 1, 152);
+    check({{0, 1 << 18, far}}, 4, 64, 152);
+    check({{0, 1, far}}, 64, 64, 152);
+    check({{0, 1, 1}}, 1, 1, 152);
+    check({{0, far, 0}}, 2, 3, 152);
+    check({{0, far, 1 << 10}}, 1, 5, 7);
+    check(std::vector<ChRequest>(65535, ChRequest{0, 1, far}), 64, 64, 152);
+    check(std::vector<ChRequest>(65535, ChRequest{0, 1, 1}), 1, 1, 152);
+    puts("ok");
+}
+"""
+
+
+@pytest.mark.skipif(not shutil.which("g++"), reason="no g++")
+def test_plan_on_the_host(tmp_path):
+    src = tmp_path / "check.cpp"
+    src.write_text(CHECK)
+    exe = tmp_path / "check"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I",
+                    os.path.join(ROOT, "kv_insert_gb300", "csrc"), "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=600)
+    assert out.returncode == 0 and out.stdout.strip().endswith("ok"), out.stdout + out.stderr
