@@ -90,9 +90,10 @@ __device__ __forceinline__ float ragged_dot(const uint16_t *k, const float *q, i
 
 // ---- shapes -----------------------------------------------------------------
 
-constexpr int kChThreads = 384;   // 2 softmax groups of 4 warps, a producer, a checker, 2 MMA warps
+constexpr int kChThreads = 384;   // 2 softmax groups of 4 warps, producers of K and of V, 2 MMA warps
 constexpr int kChPages = kChKeys / kPageSlots;
-constexpr int kChSeq = 16;        // items whose flags are kept: more than the ring runs ahead
+constexpr int kChLooks = 8;       // barriers of looked-at V in turn: more than the ring holds steps
+constexpr int kChSeq = 16;         // items whose flags are kept: more than the ring runs ahead
 static_assert(kChTile == kPaTile, "tiles as in prefix_attn");
 
 // A unit of the ring is K or V of one step
@@ -130,7 +131,7 @@ __host__ __device__ constexpr ChSmem ch_smem()
     L.empty = off;
     off += Sh::units * 8;
     L.vready = off;
-    off += Sh::units * 8;
+    off += kChLooks * 8;
     L.qready = off;
     off += 16;
     L.sfull = off;
@@ -163,13 +164,17 @@ __host__ __device__ constexpr ChSmem ch_smem()
 
 // ---- the items of a part, the same for every warp ----------------------------
 
+__device__ __forceinline__ int ch_uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 // A warp's place in the part is in shared memory (where[0], the part's end in
 // end[0]): registers hold the item alone
 struct ChWork {
     const RaggedParams &p;
     ChPos *where;
     const ChPos *end;
-    int seq = 0;   // items with steps so far
+    int seq = 0;     // items with steps so far
+    int looks = 0;   // steps before the item whose V is looked at
+    int due = 0;     // such steps of the item, its last ones
     // the item
     ChRequest q;
     ChPiece piece;
@@ -191,10 +196,19 @@ struct ChWork {
         *where = at;
         __syncwarp();
         if (!found) return false;
+        // (known to the compiler as one value a warp: what follows from them stays
+        // in uniform registers, which the operands of products and copies need)
+        piece.at.k = ch_uniform(piece.at.k);
+        piece.at.b = ch_uniform(piece.at.b);
+        piece.k1 = ch_uniform(piece.k1);
+        q.n = ch_uniform(q.n);
+        q.L = ch_uniform(q.L);
         rows = ch_rows(q.n, p.group, piece.at.b);
         single = rows <= kChTile;
         keys = ch_keys(q, p.group, piece.at.b);
         all = q.L - q.n + piece.at.b * kChRows / p.group + 1;
+        looks += due;
+        due = max(0, min(steps(), piece.k1 - max(min(all, keys), 0) / kChKeys));
         if (piece.steps) ++seq;
         return true;
     }
@@ -204,8 +218,9 @@ struct ChWork {
     {
         return min(kChPages, (keys + kPageSlots - 1) / kPageSlots - (piece.at.k + step) * kChPages);
     }
-    // whether a step's V goes past the checker's eyes: an end behind the keys, or keys that some rows do not see
-    __device__ __forceinline__ bool partly(int step) const { return min(all, keys) < (piece.at.k + step + 1) * kChKeys; }
+    // whether a step's V is looked at: it ends behind the keys, or some rows do not see all of it
+    __device__ __forceinline__ bool partly(int step) const { return step >= steps() - due; }
+    __device__ __forceinline__ int look(int step) const { return looks + step - (steps() - due); }   // which look that is
     __device__ __forceinline__ bool whole() const { return piece.at.k == 0 && piece.k1 == piece.steps; }
 };
 
@@ -224,26 +239,6 @@ __device__ __forceinline__ void ch_load_page(uint32_t dst, const CUtensorMap *m,
 #define CH_REGS16(a, i) PA_REGS8(a, i), PA_REGS8(a, i + 8)
 #define CH_REGS64(a) CH_REGS16(a, 0), CH_REGS16(a, 16), CH_REGS16(a, 32), CH_REGS16(a, 48)
 
-// 64 columns from addr and from addr2 on
-__device__ __forceinline__ void ch_load_scores(uint32_t addr, uint32_t (&a)[64], uint32_t addr2, uint32_t (&b)[64])
-{
-    asm volatile(
-        "{\n"
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
-        "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
-        "%60, %61, %62, %63}, [%128];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, "
-        "%78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, "
-        "%100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, "
-        "%118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        "}\n"
-        : CH_REGS64(a), CH_REGS64(b)
-        : "r"(addr), "r"(addr2)
-        : "memory");
-}
-
 __device__ __forceinline__ void ch_load64(uint32_t addr, uint32_t (&a)[64])
 {
     asm volatile(
@@ -259,19 +254,6 @@ __device__ __forceinline__ void ch_load64(uint32_t addr, uint32_t (&a)[64])
         : "memory");
 }
 
-__device__ __forceinline__ void ch_load32(uint32_t addr, uint32_t (&a)[32])
-{
-    asm volatile(
-        "{\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        "}\n"
-        : CH_REGS16(a, 0), CH_REGS16(a, 16)
-        : "r"(addr)
-        : "memory");
-}
-
 __device__ __forceinline__ void ch_load16(uint32_t addr, uint32_t (&a)[16])
 {
     asm volatile(
@@ -283,6 +265,24 @@ __device__ __forceinline__ void ch_load16(uint32_t addr, uint32_t (&a)[16])
         : CH_REGS16(a, 0)
         : "r"(addr)
         : "memory");
+}
+
+// pa_wait in few instructions: the kernel's code has to stay in the instruction
+// cache (below)
+__device__ __forceinline__ void ch_wait(uint32_t bar, uint32_t parity, volatile int *dead, unsigned long long limit_ns, bool honour)
+{
+    unsigned long long start = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        const unsigned long long now = global_ns();
+        if (start == 0) start = now;
+        if (now - start > limit_ns) {
+            *dead = 1;
+            atomicOr(&g_status, QKVF_STATUS_WAIT_TIMEOUT);
+            return;
+        }
+        if (honour && *dead) return;
+    }
 }
 
 // 1 / x and log2 x on the special-function unit, within 2^-22: functions with
@@ -305,12 +305,12 @@ __device__ __forceinline__ void ch_groups_sync() { asm volatile("bar.sync 1, 256
 
 // V row of key j of a request; null: its page is outside the cache
 template <int D>
-__device__ __forceinline__ const uint32_t *ch_value_row(const RaggedParams &p, int r, int g, int j)
+__device__ __forceinline__ const uint16_t *ch_value_row(const RaggedParams &p, int r, int g, int j)
 {
     const int page = p.block_table[(int64_t)r * p.max_blocks + j / kPageSlots];
     if (page < 0 || page >= p.num_pages) return nullptr;
     const int64_t slot = ((int64_t)page * p.nkv + g) * kPageSlots + j % kPageSlots;
-    return reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.kv_cache) + slot * (2 * D) + D);
+    return static_cast<const uint16_t *>(p.kv_cache) + slot * (2 * D) + D;
 }
 
 template <class E, int D>
@@ -328,7 +328,7 @@ struct ChTile {
     __device__ __forceinline__ bool dead() const { return dead_flag()[0] != 0; }
     __device__ __forceinline__ void wait(uint32_t bar, int n) const   // until phase n of bar is complete
     {
-        pa_wait(sb + bar, (uint32_t)n & 1, dead_flag(), p.wait_limit_ns);
+        ch_wait(sb + bar, (uint32_t)n & 1, dead_flag(), p.wait_limit_ns, true);
     }
     __device__ __forceinline__ volatile int *mark(uint32_t which, int seq) const
     {
@@ -341,17 +341,24 @@ struct ChTile {
         __syncwarp();
         return ChWork(p, mine, pos + 1);
     }
-    // V unit u, checked.  (An odd number of units holds K and V in turns in each
-    // place: only every other use of it passes the checker.)
-    __device__ __forceinline__ void wait_value(int u) const { wait(LY.vready + 8 * (u % NU), NU % 2 ? u / NU / 2 : u / NU); }
+    // V unit u of a step
+    __device__ __forceinline__ void wait_value(const ChWork &it, int step, int u) const
+    {
+        if (it.partly(step)) {
+            const int n = it.look(step);
+            wait(LY.vready + 8 * (n % kChLooks), n / kChLooks);
+        } else {
+            wait(LY.full + 8 * (u % NU), u / NU);
+        }
+    }
     __device__ __forceinline__ uint32_t unit(int u) const { return LY.ring + (u % NU) * Sh::unit_bytes; }
 
-    // ---- produce: K, then V of every step ----
-    __device__ __forceinline__ void produce() const
+    // ---- produce: K (kV = 0) or V (1) of every step, and look at V where that is due ----
+    __device__ __forceinline__ void produce(int kV) const
     {
         if (lane == 0) tma_prefetch_map(map);
         ChWork it = work();
-        int u = 0;
+        int u = kV;
         bool ok = true, bad_any = false;
         while (ok && it.next()) {
             const int32_t *table = p.block_table + (int64_t)it.piece.at.r * p.max_blocks;
@@ -370,18 +377,29 @@ struct ChTile {
                     *mark(LY.bad, it.seq) = it.seq;
                     __syncwarp();
                 }
-                for (int s0 = c; s0 < min(c + 32, pg1) && ok; s0 += kChPages) {
-                    const int n = min(kChPages, pg1 - s0), i = c + lane - s0;
-                    for (int v = 0; v < 2; ++v, ++u) {
-                        if (u >= NU) wait(LY.empty + 8 * (u % NU), u / NU - 1);
+                const int box = page * p.nkv + it.piece.at.g;
+                for (int s0 = c; s0 < min(c + 32, pg1); s0 += kChPages, u += 2) {
+                    const int n = min(kChPages, pg1 - s0);
+                    if (u >= NU) wait(LY.empty + 8 * (u % NU), u / NU - 1);
+                    __syncwarp();
+                    ok = !__any_sync(0xffffffffu, dead());
+                    if (!ok) break;
+                    const uint32_t bar = sb + LY.full + 8 * (u % NU), dst = sb + unit(u);
+                    if (pa_elect()) mbar_expect_tx(bar, (uint32_t)n * Sh::page_bytes);
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i) {   // page i: its box is lane s0 - c + i's
+                        const int c4 = ch_uniform(lane == s0 - c + i ? box : INT_MIN);
+                        if (pa_elect()) ch_load_page(dst + i * Sh::page_bytes, map, bar, kV * Sh::nb, c4);
+                    }
+                    __syncwarp();
+                    const int step = (s0 - pg0) / kChPages;
+                    if (kV && it.partly(step)) {
+                        wait(LY.full + 8 * (u % NU), u / NU);
                         __syncwarp();
-                        ok = !__any_sync(0xffffffffu, dead());
-                        if (!ok) break;
-                        const uint32_t bar = sb + LY.full + 8 * (u % NU);
-                        if (lane == 0) mbar_expect_tx(bar, (uint32_t)n * Sh::page_bytes);
+                        if (look(it, step, smem + unit(u))) *mark(LY.dropped, it.seq) = it.seq;
                         __syncwarp();
-                        if (i >= 0 && i < n)
-                            ch_load_page(sb + unit(u) + i * Sh::page_bytes, map, bar, v * Sh::nb, page * p.nkv + it.piece.at.g);
+                        if (lane == 0) mbar_arrive(sb + LY.vready + 8 * (it.look(step) % kChLooks));
                     }
                 }
             }
@@ -389,35 +407,19 @@ struct ChTile {
         if (lane == 0) {
             if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
             if (dead())   // our copies land before the CTA leaves
-                for (int k = max(0, u - NU); k < u; ++k)
-                    pa_wait(sb + LY.full + 8 * (k % NU), (uint32_t)((k / NU) & 1), dead_flag(), p.wait_limit_ns, false);
+                for (int k = max(kV, u - 2 * NU); k < u; k += 2)
+                    if (k >= u - NU) ch_wait(sb + LY.full + 8 * (k % NU), (uint32_t)((k / NU) & 1), dead_flag(), p.wait_limit_ns, false);
         }
         __syncwarp();
     }
-
-    // ---- check: every V unit, before its product ----
-    __device__ __forceinline__ void check() const
-    {
-        ChWork it = work();
-        int u = 1;
-        while (it.next())
-            for (int s = 0; s < it.steps(); ++s, u += 2) {
-                wait(LY.full + 8 * (u % NU), u / NU);
-                __syncwarp();
-                if (it.partly(s) && look<true>(it, s, smem + unit(u))) *mark(LY.dropped, it.seq) = it.seq;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb + LY.vready + 8 * (u % NU));
-            }
-    }
     // The V rows of a step: 0 behind the keys; not finite, among those that some
     // row does not see: 0, and true
-    template <bool kDrop>
     __device__ __forceinline__ bool look(const ChWork &it, int step, uint8_t *at) const
     {
         const int k0 = (it.piece.at.k + step) * kChKeys, from = max(min(it.all, it.keys) - k0, 0), keys = min(it.keys - k0, kChKeys);
         const int to = (keys + kPageSlots - 1) / kPageSlots * kPageSlots;
         bool found = false, wrote = false;
-#pragma unroll 4
+#pragma unroll 2
         for (int c = from * (D / 8) + lane; c < to * (D / 8); c += 32) {
             const int key = c / (D / 8), ch = c % (D / 8);   // (a row's 16-byte chunks in any order)
             uint4 *x = reinterpret_cast<uint4 *>(at + (key >> 3) * (Sh::nb * 1024) + (ch / 8) * 1024 + (key & 7) * 128 + (ch & 7) * 16);
@@ -436,25 +438,24 @@ struct ChTile {
         return __any_sync(0xffffffffu, found);
     }
 
-    // ---- multiply: group W's S = Q K^T and O += P V ----
-    template <int W>
-    __device__ __forceinline__ void multiply() const
+    // ---- multiply: group w's S = Q K^T and O += P V ----
+    __device__ __forceinline__ void multiply(int W) const
     {
         ChWork it = work();
         int u0 = 0, items = 0, blk = 0;   // units before the item; items and steps of this group
         const uint64_t qd = pa_desc(sb + LY.q + W * Sh::q_bytes, 16, 1024);
         const uint64_t kd0 = pa_desc(sb + LY.ring, 16, Sh::nb * 1024);
         const uint64_t vd0 = pa_desc(sb + LY.ring, 1024, Sh::nb * 1024);
-        constexpr uint32_t dSP = W * Sh::sp_cols, dO = Sh::tO + W * D;
+        const uint32_t dSP = W * Sh::sp_cols, dO = Sh::tO + W * D;
         // S of the step whose K is unit u, the item's `nth` of this group
         const auto scores = [&](int u, int nth) {
             wait(LY.full + 8 * (u % NU), u / NU);
             // the columns S takes: the weights before (one, or two steps ago) are
             // multiplied (an item's end has waited for all of its products), and
             // the last S is read
-            if (Sh::over) {
-                if (blk > 0) wait(LY.pvdone + 8 * W, blk - 1);
-            } else {
+            // (over: S follows the product of the weights it overwrites in the order
+            // of this thread's products, which the tensor pipe keeps)
+            if (!Sh::over) {
                 if (nth > 1) wait(LY.pvdone + 8 * W, blk - 2);
                 if (blk > 0) wait(LY.sfree + 8 * W, blk - 1);
             }
@@ -473,22 +474,19 @@ struct ChTile {
             __syncwarp();
             ++blk;
         };
-        const auto values = [&](int b, int u, int pages, uint32_t acc) {   // O += P V of step b, its V unit u
-            wait_value(u);
+        const auto values = [&](int b, int step, uint32_t acc) {   // O += P V of this group's step b
+            const int u = u0 + 2 * step + 1, pages = it.pages(step);
+            wait_value(it, step, u);
             wait(LY.pready + 16 * (b & 1) + 8 * W, b >> 1);
             __syncwarp();
             tc_fence_after();
             const uint64_t vd = vd0 + (uint32_t)(u % NU) * (Sh::unit_bytes / 16);
             const uint32_t dP = dSP + (Sh::over ? 0 : (b & 1) * 2 * U);
             if (pa_elect()) {
-                if (pages == kChPages) {
 #pragma unroll
-                    for (int i = 0; i < kChPages; ++i)
+                for (int i = 0; i < kChPages; ++i)
+                    if (i < pages)
                         pa_umma_ts(dO, dP + 8 * i, vd + i * (Sh::page_bytes / 16), pa_idesc<E>(D, true), i > 0 ? 1u : acc);
-                } else {
-                    for (int i = 0; i < pages; ++i)
-                        pa_umma_ts(dO, dP + 8 * i, vd + i * (Sh::page_bytes / 16), pa_idesc<E>(D, true), i > 0 ? 1u : acc);
-                }
                 umma_commit(sb + LY.pvdone + 8 * W);
                 umma_commit(sb + LY.empty + 8 * (u % NU));
             }
@@ -496,9 +494,10 @@ struct ChTile {
         };
         // The other group's step: its units pass here too, in order, so that no
         // phase of a barrier is missed
-        const auto pass = [&](int u) {
+        const auto pass = [&](int step) {
+            const int u = u0 + 2 * step;
             wait(LY.full + 8 * (u % NU), u / NU);
-            wait_value(u + 1);
+            wait_value(it, step, u + 1);
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(sb + LY.empty + 8 * (u % NU));
@@ -508,20 +507,20 @@ struct ChTile {
         while (it.next()) {
             const int n = it.steps();
             int before = -1, nth = 0;   // the step whose product is due
-            for (int s = 0; s < n; ++s) {
-                if (!it.mine(s, W)) {
-                    pass(u0 + 2 * s);
+            for (int s = 0; s <= n; ++s) {   // (n: the last product)
+                if (s < n && !it.mine(s, W)) {
+                    pass(s);
                     continue;
                 }
+                if (s == n && nth == 0) break;   // no step was this group's
                 if (nth == 0) wait(LY.qready + 8 * W, items++);
-                if (Sh::over && nth > 0) values(blk - 1, u0 + 2 * before + 1, kChPages, nth > 1);
-                scores(u0 + 2 * s, nth);
-                if (!Sh::over && nth > 0) values(blk - 2, u0 + 2 * before + 1, kChPages, nth > 1);
+                if (!Sh::over && s < n) scores(u0 + 2 * s, nth);
+                if (nth > 0) values(s < n && !Sh::over ? blk - 2 : blk - 1, before, nth > 1);
+                if (Sh::over && s < n) scores(u0 + 2 * s, nth);
                 before = s;
                 ++nth;
             }
             if (nth > 0) {
-                values(blk - 1, u0 + 2 * before + 1, it.pages(before), nth > 1);
                 if (pa_elect()) umma_commit(sb + LY.odone + 8 * W);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sb + LY.odone + 8 * W);   // with the flags of bad pages and values left out
@@ -532,7 +531,7 @@ struct ChTile {
         // lane is elected each time: commits cover the MMAs of one thread)
         if (pa_elect()) umma_commit(sb + LY.drain + 8 * W);
         __syncwarp();
-        if (lane == 0) pa_wait(sb + LY.drain + 8 * W, 0, dead_flag(), p.wait_limit_ns, false);
+        if (lane == 0) ch_wait(sb + LY.drain + 8 * W, 0, dead_flag(), p.wait_limit_ns, false);
         __syncwarp();
     }
 
@@ -563,17 +562,18 @@ struct ChTile {
                 if (active) {   // the previous item is done: its Q is no longer read
                     const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
                                                                        ((int64_t)it.q.row0 + tok) * p.q_ts + head * p.q_hs);
-                    uint4 v[D / 8];
+#pragma unroll 1
+                    for (int b = 0; b < Sh::nb; ++b) {
+                        uint4 v[8];
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) v[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                        for (int c = 0; c < 8; ++c) v[c] = valid ? src[8 * b + c] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        *reinterpret_cast<uint4 *>(sq + (c / 8) * (kChTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4 *>(sq + b * (kChTile * 128) + row * 128 + ((c ^ (row & 7)) << 4)) = v[c];
+                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 mbar_arrive(sb + LY.qready + 8 * w);
-                uint32_t so[U], sm[U];
-                int outer = 0;   // the half of the keys in S's outer unit
                 const auto arrive = [&](uint32_t bar) {   // for this warp, which has left tensor memory
                     tc_fence_before();
                     __syncwarp();
@@ -582,62 +582,45 @@ struct ChTile {
                 // (two barriers in turn: S of step b says that the weights of step
                 // b - 2 have been multiplied, so that phase has been seen)
                 const auto pready = [&](int b) { return LY.pready + 16 * (b & 1) + 8 * w; };
-                // The weights of step s, against the maximum so far.  Later scores
-                // may exceed it as long as a step's weights stay below a limit in sum
-                // (so no maximum is taken per step); otherwise it follows and O is
-                // rescaled.  An item's first step starts there.
-                const auto weigh = [&](int s) {
-                    const uint32_t aOut = aSP + 2 * outer * U;
-                    uint32_t po[U / 2], pm[U / 2];
-                    const int left = limit - (it.piece.at.k + s) * kChKeys;   // keys of the step that the row sees
-                    const bool hide = __any_sync(0xffffffffu, valid && left < kChKeys);
-                    if (hide) {
-                        pa_hide(so, left - outer * U);
-                        pa_hide(sm, left - (outer ^ 1) * U);
-                    }
-                    float base = -mu, sum = INFINITY;
-                    for (bool again = false;; again = true) {
-                        if (again || s != first) {
-                            sum = pa_weights<E>(so, po, cc, base);
-                            sum += pa_weights<E>(sm, pm, cc, base);
-                            if (again || !__any_sync(0xffffffffu, !(sum < PaWeight<E>::most))) break;
-                            ch_load64(aOut, so);   // not overwritten yet
-                            if (hide) pa_hide(so, left - outer * U);
-                        }
-                        // (only this row's own scores move it, not a neighbour's)
-                        const float top = fmaf(pa_max(so, pa_max(sm, -INFINITY)), p.scale_log2, -PaWeight<E>::below);
-                        const bool grew = top > mu && !(sum < PaWeight<E>::most);
-                        const float al = grew ? a2_ex2(mu - top) : 1.f;
-                        if (grew) mu = top;
-                        base = mu == -INFINITY ? 0.f : -mu;
-                        l *= al;
-                        if (s != first) {
-                            wait(LY.pvdone + 8 * w, blk - 1);
-                            __syncwarp();
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o[16];
-                                ch_load16(aO + c, o);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                pa_tmem_st16(aO + c, o);
-                            }
-                        }
-                    }
-                    l += sum;
-                    pa_tmem_st<U / 2>(aOut + outer * (U / 2), po);
-                    pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pm);
-                };
+                // The weights of a step, against the maximum so far.  Later scores may
+                // exceed it as long as a step's weights stay below a limit in sum (so
+                // no maximum is taken per step); otherwise it follows, O is rescaled
+                // and the weights are formed again.  An item's first step starts there.
                 for (int s = first; s < n; s += by, ++blk) {
                     wait(LY.sfull + 8 * w, blk);
                     __syncwarp();
                     if (active) {
                         tc_fence_after();
-                        outer = Sh::over ? 0 : blk & 1;
-                        ch_load_scores(aSP + 2 * outer * U, so, aSP + U, sm);
-                        if (!Sh::over) arrive(LY.sfree + 8 * w);
-                        weigh(s);
+                        const int outer = Sh::over ? 0 : blk & 1;   // the half of the keys in S's outer unit
+                        const uint32_t aOut = aSP + 2 * outer * U;
+                        uint32_t so[U], sm[U], po[U / 2], pm[U / 2];
+                        const int left = limit - (it.piece.at.k + s) * kChKeys;   // keys of the step that the row sees
+                        if (__any_sync(0xffffffffu, valid && left < kChKeys)) hide(aSP + (Sh::over ? 0 : outer * U), left);
+                        bool follow = s == first;
+                        float sum = INFINITY;
+                        ch_load64(aSP + U, sm);
+#pragma unroll 1
+                        for (bool again = false;; again = true) {
+                            ch_load64(aOut, so);   // (not overwritten yet)
+                            if (!Sh::over && !again) arrive(LY.sfree + 8 * w);
+                            if (follow) {
+                                // (only this row's own scores move it, not a neighbour's)
+                                const float top = fmaf(pa_max(so, pa_max(sm, -INFINITY)), p.scale_log2, -PaWeight<E>::below);
+                                const bool grew = top > mu && !(sum < PaWeight<E>::most);
+                                const float al = grew ? a2_ex2(mu - top) : 1.f;
+                                if (grew) mu = top;
+                                l *= al;
+                                if (s != first) rescale(w, blk - 1, aO, al);
+                            }
+                            const float base = mu == -INFINITY ? 0.f : -mu;
+                            sum = pa_weights<E>(so, po, cc, base);
+                            sum += pa_weights<E>(sm, pm, cc, base);
+                            if (follow || !__any_sync(0xffffffffu, !(sum < PaWeight<E>::most))) break;
+                            follow = true;
+                        }
+                        l += sum;
+                        pa_tmem_st<U / 2>(aOut + outer * (U / 2), po);
+                        pa_tmem_st<U / 2>(aOut + (outer ^ 1) * (U / 2), pm);
                         pa_tmem_st_wait();
                     } else if (!Sh::over) {
                         arrive(LY.sfree + 8 * w);
@@ -650,6 +633,38 @@ struct ChTile {
             }
             finish(it, w, row, m, active, valid, grow, limit, mu, l, aO);
             tc_fence_before();
+        }
+    }
+
+    // The scores from column `left` on become -infinity, whatever their slots
+    // hold (in a loop over tensor memory: steps that need it are few)
+    __device__ __forceinline__ void hide(uint32_t aS, int left) const
+    {
+#pragma unroll 1
+        for (int c = 0; c < kChKeys; c += 16) {
+            uint32_t t[16];
+            ch_load16(aS + c, t);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (c + e >= left) t[e] = 0xff800000u;
+            pa_tmem_st16(aS + c, t);
+        }
+        pa_tmem_st_wait();
+    }
+
+    // O times al, behind the product of step b
+    __device__ __forceinline__ void rescale(int w, int b, uint32_t aO, float al) const
+    {
+        wait(LY.pvdone + 8 * w, b);
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            ch_load16(aO + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+            pa_tmem_st16(aO + c, o);
         }
     }
 
@@ -674,12 +689,12 @@ struct ChTile {
             ch_groups_sync();   // both groups' products are done
             if (active) {
                 shared_ml[row] = make_float2(mu, l);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    ch_load16(aO + c, o);
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    ch_load32(aO + c, o);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
+                    for (int e = 0; e < 16; e += 4)
                         shared[(c + e) / 4 * kChTile + row] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
                                                                          __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                 }
@@ -708,14 +723,14 @@ struct ChTile {
             float *po = p.ws_o + ((int64_t)part * kChRows + m) * D;
             const float inv = ch_rcp(l);   // (a sum of a row that sees a key is far above the subnormals)
             uint16_t *out = static_cast<uint16_t *>(p.out) + grow * D;
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
                 __syncwarp();
-                ch_load32(aO + c, o);
+                ch_load16(aO + c, o);
                 if (joined) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
+                    for (int e = 0; e < 16; e += 4) {
                         const float4 y = shared[(c + e) / 4 * kChTile + row];
                         o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), al0, y.x * al1));
                         o[e + 1] = __float_as_uint(fmaf(__uint_as_float(o[e + 1]), al0, y.y * al1));
@@ -723,34 +738,34 @@ struct ChTile {
                         o[e + 3] = __float_as_uint(fmaf(__uint_as_float(o[e + 3]), al0, y.w * al1));
                     }
                 }
-                if (dropped) {
-                    const int to = min(min(it.keys, it.piece.k1 * kChKeys), limit);
-#pragma unroll 1
-                    for (int key = max(it.all, it.piece.at.k * kChKeys); key < to; ++key) {
-                        const uint32_t *v = ch_value_row<D>(p, it.piece.at.r, it.piece.at.g, key);
-                        if (!v) continue;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float a = __uint_as_float(o[e]), b = __uint_as_float(o[e + 1]);
-                            pa_add_not_finite<E>(v[(c + e) / 2], a, b);
-                            o[e] = __float_as_uint(a);
-                            o[e + 1] = __float_as_uint(b);
-                        }
-                    }
-                }
                 if (valid && !whole) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
+                    for (int e = 0; e < 16; e += 4)
                         *reinterpret_cast<uint4 *>(po + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 } else if (valid && !bad) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
+                    for (int e = 0; e < 16; e += 8) {
                         uint32_t y[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             y[i] = l == 0.f ? 0u : E::pack(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv);
                         *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
+                }
+            }
+            if (dropped && valid && !bad) {   // what is not finite, to the rows that see it
+                const int to = min(min(it.keys, it.piece.k1 * kChKeys), limit);
+#pragma unroll 1
+                for (int key = max(it.all, it.piece.at.k * kChKeys); key < to; ++key) {
+                    const uint16_t *v = ch_value_row<D>(p, it.piece.at.r, it.piece.at.g, key);
+#pragma unroll 1
+                    for (int d = 0; v && d < D; ++d)
+                        if (pa_not_finite<E>(v[d])) {
+                            if (whole)
+                                out[d] = E::put(E::get(out[d]) + E::get(v[d]));
+                            else
+                                po[d] += E::get(v[d]);
+                        }
                 }
             }
             if (valid && !whole)
@@ -846,8 +861,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
         for (int i = 0; i < Sh::units; ++i) {
             mbar_init(sb + LY.full + 8 * i, 1);
             mbar_init(sb + LY.empty + 8 * i, 2);
-            mbar_init(sb + LY.vready + 8 * i, 1);
         }
+        for (int i = 0; i < kChLooks; ++i) mbar_init(sb + LY.vready + 8 * i, 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(sb + LY.qready + 8 * w, 128);
             mbar_init(sb + LY.sfull + 8 * w, 1);
@@ -875,14 +890,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
         tile.softmax(warp >> 2, warp & 3);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8)
-            tile.produce();
-        else if (warp == 9)
-            tile.check();
-        else if (warp == 10)
-            tile.template multiply<0>();
+        if (warp < 10)
+            tile.produce(ch_uniform(warp - 8));
         else
-            tile.template multiply<1>();
+            tile.multiply(ch_uniform(warp - 10));
     }
     tc_fence_before();
     __syncthreads();
