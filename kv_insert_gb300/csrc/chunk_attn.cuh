@@ -93,7 +93,7 @@ __device__ __forceinline__ float ragged_dot(const uint16_t *k, const float *q, i
 constexpr int kChThreads = 384;   // 2 softmax groups of 4 warps, producers of K and of V, 2 MMA warps
 constexpr int kChPages = kChKeys / kPageSlots;
 constexpr int kChLooks = 8;       // barriers of looked-at V in turn: more than the ring holds steps
-constexpr int kChSeq = 16;         // items whose flags are kept: more than the ring runs ahead
+constexpr int kChItems = 4;       // items handed out and not done with
 static_assert(kChTile == kPaTile, "tiles as in prefix_attn");
 
 // A unit of the ring is K or V of one step
@@ -112,8 +112,68 @@ struct ChShape {
     static_assert(tO + 2 * D <= cols, "tensor memory");
 };
 
+// ---- the items of a part ------------------------------------------------------
+
+// (Known to the compiler as one value a warp: what follows from such values stays
+// in uniform registers, which the operands of products and copies need.)
+__device__ __forceinline__ int ch_uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// Steps of one block's keys, as the producer of K hands them to the other warps
+struct ChItem {
+    int r, g, b, k;          // request, KV head, block, first step
+    int n;                   // steps here (0: rows that see no key; -1: the part's end)
+    int of;                  // the block's steps in all
+    int rows;                // of the block
+    int keys, all;           // keys that some row sees, and that every row sees
+    int row0, tokens, L;     // the request's
+    int look_from, look0;    // V is looked at from that step on; look0 + step: which look it is
+    int bad, dropped;        // a page outside the cache; values of V left out
+    __device__ __forceinline__ bool single() const { return rows <= kChTile; }
+    __device__ __forceinline__ bool mine(int step, int w) const { return !single() || (step & 1) == w; }
+    __device__ __forceinline__ int pages(int step) const   // of a step, with keys
+    {
+        return min(kChPages, (keys + kPageSlots - 1) / kPageSlots - (k + step) * kChPages);
+    }
+    __device__ __forceinline__ bool whole() const { return n == of; }
+};
+static_assert(sizeof(ChItem) == 64, "four 16-byte words");
+
+// The next item of a part (by one warp); looks: steps before it whose V is looked at
+__device__ __forceinline__ ChItem ch_next(const RaggedParams &p, ChPos &at, const ChPos &end, int &looks)
+{
+    ChItem it = {};
+    it.n = -1;
+    while (!ch_reached(at, end)) {
+        const ChRequest q = ragged_request(p, ch_uniform(p.starts[at.r]), ch_uniform(p.starts[at.r + 1]), ch_uniform(p.context_lens[at.r]), false);
+        if (q.n <= 0) {
+            at = {at.r + 1, 0, 0, 0};
+            continue;
+        }
+        ChPiece piece;
+        if (!ch_take(q, p.group, p.nkv, at, end, piece)) continue;
+        it.r = piece.at.r;
+        it.g = piece.at.g;
+        it.b = piece.at.b;
+        it.k = piece.at.k;
+        it.n = piece.k1 - piece.at.k;
+        it.of = piece.steps;
+        it.rows = ch_rows(q.n, p.group, it.b);
+        it.keys = ch_keys(q, p.group, it.b);
+        it.all = q.L - q.n + it.b * kChRows / p.group + 1;
+        it.row0 = q.row0;
+        it.tokens = q.n;
+        it.L = q.L;
+        // a step's V is looked at if it ends behind the keys, or some rows do not see all of it
+        it.look_from = max(0, min(it.n, max(min(it.all, it.keys), 0) / kChKeys - it.k));
+        it.look0 = looks - it.look_from;
+        looks += it.n - it.look_from;
+        break;
+    }
+    return it;
+}
+
 struct ChSmem {   // offsets from the 1024-byte aligned base
-    uint32_t q, ring, full, empty, vready, qready, sfull, sfree, pready, pvdone, odone, drain, tmem, dead, bad, dropped, pos, join, total;
+    uint32_t q, ring, full, empty, vready, qready, sfull, sfree, pready, pvdone, odone, drain, tmem, dead, ifull, iempty, items, join, total;
 };
 
 template <int D>
@@ -150,79 +210,18 @@ __host__ __device__ constexpr ChSmem ch_smem()
     off += 8;
     L.dead = off;
     off += 8;
-    L.bad = off;       // [item % kChSeq]: the item, where it sees a page outside the cache
-    off += 4 * kChSeq;
-    L.dropped = off;   // the same: where values of V were left out
-    off += 4 * kChSeq;
-    L.pos = off;       // the part's start and end, every warp's place
-    off += (2 + kChThreads / 32) * sizeof(ChPos);
+    L.ifull = off;
+    off += kChItems * 8;
+    L.iempty = off;
+    off += kChItems * 8;
+    off = (off + 15) / 16 * 16;
+    L.items = off;
+    off += kChItems * sizeof(ChItem);
     L.join = off;      // the second group's maxima and sums
     off += 8 * kChTile;
     L.total = off + 1024;
     return L;
 }
-
-// ---- the items of a part, the same for every warp ----------------------------
-
-__device__ __forceinline__ int ch_uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
-
-// A warp's place in the part is in shared memory (where[0], the part's end in
-// end[0]): registers hold the item alone
-struct ChWork {
-    const RaggedParams &p;
-    ChPos *where;
-    const ChPos *end;
-    int seq = 0;     // items with steps so far
-    int looks = 0;   // steps before the item whose V is looked at
-    int due = 0;     // such steps of the item, its last ones
-    // the item
-    ChRequest q;
-    ChPiece piece;
-    int rows, single, keys, all;   // keys: that some row sees; all: that every row sees
-
-    __device__ __forceinline__ ChWork(const RaggedParams &prm, ChPos *warp_pos, const ChPos *part_end) : p(prm), where(warp_pos), end(part_end) {}
-    __device__ __forceinline__ bool next()
-    {
-        ChPos at = *where;
-        bool found = false;
-        while (!found && !ch_reached(at, *end)) {
-            q = ragged_request(p, at.r, false);
-            if (q.n <= 0)
-                at = {at.r + 1, 0, 0, 0};
-            else
-                found = ch_take(q, p.group, p.nkv, at, *end, piece);
-        }
-        __syncwarp();
-        *where = at;
-        __syncwarp();
-        if (!found) return false;
-        // (known to the compiler as one value a warp: what follows from them stays
-        // in uniform registers, which the operands of products and copies need)
-        piece.at.k = ch_uniform(piece.at.k);
-        piece.at.b = ch_uniform(piece.at.b);
-        piece.k1 = ch_uniform(piece.k1);
-        q.n = ch_uniform(q.n);
-        q.L = ch_uniform(q.L);
-        rows = ch_rows(q.n, p.group, piece.at.b);
-        single = rows <= kChTile;
-        keys = ch_keys(q, p.group, piece.at.b);
-        all = q.L - q.n + piece.at.b * kChRows / p.group + 1;
-        looks += due;
-        due = max(0, min(steps(), piece.k1 - max(min(all, keys), 0) / kChKeys));
-        if (piece.steps) ++seq;
-        return true;
-    }
-    __device__ __forceinline__ int steps() const { return piece.k1 - piece.at.k; }
-    __device__ __forceinline__ bool mine(int step, int w) const { return !single || (step & 1) == w; }   // (step from the piece's first)
-    __device__ __forceinline__ int pages(int step) const   // of a step, with keys
-    {
-        return min(kChPages, (keys + kPageSlots - 1) / kPageSlots - (piece.at.k + step) * kChPages);
-    }
-    // whether a step's V is looked at: it ends behind the keys, or some rows do not see all of it
-    __device__ __forceinline__ bool partly(int step) const { return step >= steps() - due; }
-    __device__ __forceinline__ int look(int step) const { return looks + step - (steps() - due); }   // which look that is
-    __device__ __forceinline__ bool whole() const { return piece.at.k == 0 && piece.k1 == piece.steps; }
-};
 
 __device__ __forceinline__ void ch_load_page(uint32_t dst, const CUtensorMap *m, uint32_t bar, int block, int c4)
 {
@@ -330,22 +329,41 @@ struct ChTile {
     {
         ch_wait(sb + bar, (uint32_t)n & 1, dead_flag(), p.wait_limit_ns, true);
     }
-    __device__ __forceinline__ volatile int *mark(uint32_t which, int seq) const
+    // Item `seq`: its place, and by its values (at the part's end n is -1).  Items
+    // come and go whether or not a wait gave up: every warp sees all of them.
+    __device__ __forceinline__ ChItem *place(int seq) const { return reinterpret_cast<ChItem *>(smem + LY.items) + seq % kChItems; }
+    __device__ __forceinline__ ChItem item(int seq) const
     {
-        return reinterpret_cast<volatile int *>(smem + which) + seq % kChSeq;
-    }
-    __device__ __forceinline__ ChWork work() const
-    {
-        ChPos *pos = reinterpret_cast<ChPos *>(smem + LY.pos), *mine = pos + 2 + (threadIdx.x >> 5);
-        if (lane == 0) *mine = pos[0];
+        ch_wait(sb + LY.ifull + 8 * (seq % kChItems), (uint32_t)(seq / kChItems) & 1, dead_flag(), p.wait_limit_ns, false);
         __syncwarp();
-        return ChWork(p, mine, pos + 1);
+        const int *x = reinterpret_cast<const int *>(place(seq));
+        ChItem it = {};
+        it.r = ch_uniform(x[0]);
+        it.g = ch_uniform(x[1]);
+        it.b = ch_uniform(x[2]);
+        it.k = ch_uniform(x[3]);
+        it.n = ch_uniform(x[4]);
+        it.of = ch_uniform(x[5]);
+        it.rows = ch_uniform(x[6]);
+        it.keys = ch_uniform(x[7]);
+        it.all = ch_uniform(x[8]);
+        it.row0 = ch_uniform(x[9]);
+        it.tokens = ch_uniform(x[10]);
+        it.L = ch_uniform(x[11]);
+        it.look_from = ch_uniform(x[12]);
+        it.look0 = ch_uniform(x[13]);
+        return it;
+    }
+    __device__ __forceinline__ void done(int seq) const   // this warp is, with item seq
+    {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sb + LY.iempty + 8 * (seq % kChItems));
     }
     // V unit u of a step
-    __device__ __forceinline__ void wait_value(const ChWork &it, int step, int u) const
+    __device__ __forceinline__ void wait_value(const ChItem &it, int step, int u) const
     {
-        if (it.partly(step)) {
-            const int n = it.look(step);
+        if (step >= it.look_from) {
+            const int n = it.look0 + step;
             wait(LY.vready + 8 * (n % kChLooks), n / kChLooks);
         } else {
             wait(LY.full + 8 * (u % NU), u / NU);
@@ -353,17 +371,35 @@ struct ChTile {
     }
     __device__ __forceinline__ uint32_t unit(int u) const { return LY.ring + (u % NU) * Sh::unit_bytes; }
 
-    // ---- produce: K (kV = 0) or V (1) of every step, and look at V where that is due ----
-    __device__ __forceinline__ void produce(int kV) const
+    // ---- produce: K (kV = 0) or V (1) of every step; K's warp hands out the
+    // items, V's looks at V where that is due ----
+    __device__ __forceinline__ void produce(int kV, ChPos at, const ChPos &end) const
     {
         if (lane == 0) tma_prefetch_map(map);
-        ChWork it = work();
-        int u = kV;
+        int u = kV, looks = 0;
         bool ok = true, bad_any = false;
-        while (ok && it.next()) {
-            const int32_t *table = p.block_table + (int64_t)it.piece.at.r * p.max_blocks;
-            const int pg0 = it.piece.at.k * kChPages, pg1 = min(it.piece.k1 * kChPages, (it.keys + kPageSlots - 1) / kPageSlots);
+#pragma unroll 1
+        for (int seq = 0;; ++seq) {
+            ChItem it;
+            if (kV) {
+                it = item(seq);
+                if (it.n > 0) fetch(it);
+            } else {
+                it = ch_next(p, at, end, looks);
+                if (seq >= kChItems)
+                    ch_wait(sb + LY.iempty + 8 * (seq % kChItems), (uint32_t)(seq / kChItems - 1) & 1, dead_flag(), p.wait_limit_ns, false);
+                __syncwarp();
+                if (lane == 0) {
+                    *place(seq) = it;
+                    mbar_arrive(sb + LY.ifull + 8 * (seq % kChItems));
+                }
+                __syncwarp();
+            }
+            if (it.n < 0) break;
+            const int32_t *table = p.block_table + (int64_t)it.r * p.max_blocks;
+            const int pg0 = it.k * kChPages, pg1 = min((it.k + it.n) * kChPages, (it.keys + kPageSlots - 1) / kPageSlots);
             int next = pg0 + lane < pg1 ? table[pg0 + lane] : 0;
+#pragma unroll 1
             for (int c = pg0; c < pg1 && ok; c += 32) {
                 int page = next;
                 if (c + 32 + lane < pg1) next = table[c + 32 + lane];
@@ -374,10 +410,11 @@ struct ChTile {
                 }
                 if (__any_sync(0xffffffffu, bad)) {   // seen by the softmax before the item's end
                     bad_any = true;
-                    *mark(LY.bad, it.seq) = it.seq;
+                    *reinterpret_cast<volatile int *>(&place(seq)->bad) = 1;
                     __syncwarp();
                 }
-                const int box = page * p.nkv + it.piece.at.g;
+                const int box = page * p.nkv + it.g;
+#pragma unroll 1
                 for (int s0 = c; s0 < min(c + 32, pg1); s0 += kChPages, u += 2) {
                     const int n = min(kChPages, pg1 - s0);
                     if (u >= NU) wait(LY.empty + 8 * (u % NU), u / NU - 1);
@@ -394,15 +431,16 @@ struct ChTile {
                     }
                     __syncwarp();
                     const int step = (s0 - pg0) / kChPages;
-                    if (kV && it.partly(step)) {
+                    if (kV && step >= it.look_from) {
                         wait(LY.full + 8 * (u % NU), u / NU);
                         __syncwarp();
-                        if (look(it, step, smem + unit(u))) *mark(LY.dropped, it.seq) = it.seq;
+                        if (look(it, step, smem + unit(u))) *reinterpret_cast<volatile int *>(&place(seq)->dropped) = 1;
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(sb + LY.vready + 8 * (it.look(step) % kChLooks));
+                        if (lane == 0) mbar_arrive(sb + LY.vready + 8 * ((it.look0 + step) % kChLooks));
                     }
                 }
             }
+            if (kV) done(seq);
         }
         if (lane == 0) {
             if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
@@ -412,11 +450,21 @@ struct ChTile {
         }
         __syncwarp();
     }
+    // The item's rows of q into L2, some steps before they are loaded
+    __device__ __forceinline__ void fetch(const ChItem &it) const
+    {
+#pragma unroll 1
+        for (int i = lane; i < it.rows * Sh::nb; i += 32) {
+            const int mr = it.b * kChRows + i / Sh::nb, tok = mr / p.group, head = it.g * p.group + mr - tok * p.group;
+            const uint16_t *row = static_cast<const uint16_t *>(p.q) + ((int64_t)it.row0 + tok) * p.q_ts + head * p.q_hs;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + i % Sh::nb * 64));
+        }
+    }
     // The V rows of a step: 0 behind the keys; not finite, among those that some
     // row does not see: 0, and true
-    __device__ __forceinline__ bool look(const ChWork &it, int step, uint8_t *at) const
+    __device__ __forceinline__ bool look(const ChItem &it, int step, uint8_t *at) const
     {
-        const int k0 = (it.piece.at.k + step) * kChKeys, from = max(min(it.all, it.keys) - k0, 0), keys = min(it.keys - k0, kChKeys);
+        const int k0 = (it.k + step) * kChKeys, from = max(min(it.all, it.keys) - k0, 0), keys = min(it.keys - k0, kChKeys);
         const int to = (keys + kPageSlots - 1) / kPageSlots * kPageSlots;
         bool found = false, wrote = false;
 #pragma unroll 2
@@ -441,7 +489,7 @@ struct ChTile {
     // ---- multiply: group w's S = Q K^T and O += P V ----
     __device__ __forceinline__ void multiply(int W) const
     {
-        ChWork it = work();
+        ChItem it;
         int u0 = 0, items = 0, blk = 0;   // units before the item; items and steps of this group
         const uint64_t qd = pa_desc(sb + LY.q + W * Sh::q_bytes, 16, 1024);
         const uint64_t kd0 = pa_desc(sb + LY.ring, 16, Sh::nb * 1024);
@@ -504,9 +552,13 @@ struct ChTile {
                 mbar_arrive(sb + LY.empty + 8 * ((u + 1) % NU));
             }
         };
-        while (it.next()) {
-            const int n = it.steps();
+#pragma unroll 1
+        for (int seq = 0;; ++seq) {
+            it = item(seq);
+            if (it.n < 0) break;
+            const int n = it.n;
             int before = -1, nth = 0;   // the step whose product is due
+#pragma unroll 1
             for (int s = 0; s <= n; ++s) {   // (n: the last product)
                 if (s < n && !it.mine(s, W)) {
                     pass(s);
@@ -526,6 +578,7 @@ struct ChTile {
                 if (lane == 0) mbar_arrive(sb + LY.odone + 8 * W);   // with the flags of bad pages and values left out
             }
             u0 += 2 * n;
+            done(seq);
         }
         // every MMA of this warp is done before tensor memory is freed (the same
         // lane is elected each time: commits cover the MMAs of one thread)
@@ -535,6 +588,14 @@ struct ChTile {
         __syncwarp();
     }
 
+    // A warp's 32 rows of Q or the output in accesses of whole rows
+    static constexpr int kRowsAtOnce = 32 / (D / 8), kRowTurns = 32 / kRowsAtOnce;
+    // 16-byte chunk c of a row of a Q tile
+    static __device__ __forceinline__ uint4 *chunk(uint8_t *tile, int row, int c)
+    {
+        return reinterpret_cast<uint4 *>(tile + (c / 8) * (kChTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+    }
+
     // ---- softmax: thread = row of group w's tile ----
     __device__ __forceinline__ void softmax(int w, int wq) const
     {
@@ -542,34 +603,34 @@ struct ChTile {
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
         const uint32_t aSP = w * Sh::sp_cols + lane_base, aO = Sh::tO + w * D + lane_base;
         uint8_t *sq = smem + LY.q + w * Sh::q_bytes;
-        ChWork it = work();
         int blk = 0, items = 0;
         const uint64_t cc = f2_pack(p.scale_log2, p.scale_log2);
-        while (it.next()) {
-            const int n = it.steps(), by = it.single ? 2 : 1, first = it.single ? w : 0;
-            const int m = (it.single ? 0 : w * kChTile) + row;   // the thread's row of the block
-            const bool active = 32 * wq + (it.single ? 0 : w * kChTile) < it.rows;
-            const int mr = it.piece.at.b * kChRows + m, tok = mr / p.group, head = it.piece.at.g * p.group + mr - tok * p.group;
-            const int64_t grow = ((int64_t)it.q.row0 + tok) * p.q_heads + head;   // output row
-            const bool valid = m < it.rows;
-            const int limit = valid ? it.q.L - it.q.n + tok + 1 : 0;              // keys that the row sees
+#pragma unroll 1
+        for (int seq = 0;; ++seq) {
+            const ChItem it = item(seq);
+            if (it.n < 0) break;
+            const bool single = it.single();
+            const int n = it.n, by = single ? 2 : 1, first = single ? w : 0;
+            const int m = (single ? 0 : w * kChTile) + row;   // the thread's row of the block
+            const bool active = 32 * wq + (single ? 0 : w * kChTile) < it.rows, valid = m < it.rows;
+            const int mr = it.b * kChRows + m, tok = mr / p.group, head = it.g * p.group + mr - tok * p.group;
+            const int64_t grow = ((int64_t)it.row0 + tok) * p.q_heads + head;   // output row
+            const int limit = valid ? it.L - it.tokens + tok + 1 : 0;           // keys that the row sees
             if (n == 0) {   // rows that see no key
-                if (valid && (!it.single || w == 0)) put_none(grow, true);
+                if (valid && (!single || w == 0)) put_none(grow, true);
+                done(seq);
                 continue;
             }
             float mu = -INFINITY, l = 0.f;
             if (first < n) {
                 if (active) {   // the previous item is done: its Q is no longer read
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
-                                                                       ((int64_t)it.q.row0 + tok) * p.q_ts + head * p.q_hs);
-#pragma unroll 1
-                    for (int b = 0; b < Sh::nb; ++b) {
-                        uint4 v[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] = valid ? src[8 * b + c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            *reinterpret_cast<uint4 *>(sq + b * (kChTile * 128) + row * 128 + ((c ^ (row & 7)) << 4)) = v[c];
+                    const uint16_t *src = valid ? static_cast<const uint16_t *>(p.q) + ((int64_t)it.row0 + tok) * p.q_ts + head * p.q_hs
+                                                : nullptr;
+#pragma unroll 8
+                    for (int i = 0; i < kRowTurns; ++i) {   // whole rows: few lines an access
+                        const int r = i * kRowsAtOnce + lane / (D / 8), c = lane % (D / 8);
+                        const uint4 *x = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, (unsigned long long)src, r));
+                        *chunk(sq, 32 * wq + r, c) = x ? x[c] : make_uint4(0u, 0u, 0u, 0u);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
@@ -586,6 +647,7 @@ struct ChTile {
                 // exceed it as long as a step's weights stay below a limit in sum (so
                 // no maximum is taken per step); otherwise it follows, O is rescaled
                 // and the weights are formed again.  An item's first step starts there.
+#pragma unroll 1
                 for (int s = first; s < n; s += by, ++blk) {
                     wait(LY.sfull + 8 * w, blk);
                     __syncwarp();
@@ -594,7 +656,7 @@ struct ChTile {
                         const int outer = Sh::over ? 0 : blk & 1;   // the half of the keys in S's outer unit
                         const uint32_t aOut = aSP + 2 * outer * U;
                         uint32_t so[U], sm[U], po[U / 2], pm[U / 2];
-                        const int left = limit - (it.piece.at.k + s) * kChKeys;   // keys of the step that the row sees
+                        const int left = limit - (it.k + s) * kChKeys;   // keys of the step that the row sees
                         if (__any_sync(0xffffffffu, valid && left < kChKeys)) hide(aSP + (Sh::over ? 0 : outer * U), left);
                         bool follow = s == first;
                         float sum = INFINITY;
@@ -631,8 +693,9 @@ struct ChTile {
                 __syncwarp();
                 tc_fence_after();
             }
-            finish(it, w, row, m, active, valid, grow, limit, mu, l, aO);
+            finish(it, seq, w, row, m, active, valid, grow, limit, mu, l, aO);
             tc_fence_before();
+            done(seq);
         }
     }
 
@@ -678,13 +741,13 @@ struct ChTile {
     }
 
     // The item's rows: joined if the groups shared them, then the output, or a partial
-    __device__ __forceinline__ void finish(const ChWork &it, int w, int row, int m, bool active, bool valid, int64_t grow, int limit,
+    __device__ __forceinline__ void finish(const ChItem &it, int seq, int w, int row, int m, bool active, bool valid, int64_t grow, int limit,
                                            float mu, float l, uint32_t aO) const
     {
-        const bool joined = it.single && it.steps() > 1;
+        const bool joined = it.single() && it.n > 1;
         float4 *shared = reinterpret_cast<float4 *>(smem + LY.q);      // [D / 4][128]: the whole Q area, whose products are done
         float2 *shared_ml = reinterpret_cast<float2 *>(smem + LY.join);
-        if (it.single && w == 1) {
+        if (it.single() && w == 1) {
             if (!joined) return;
             ch_groups_sync();   // both groups' products are done
             if (active) {
@@ -716,10 +779,12 @@ struct ChTile {
                 mu = top;
             }
         }
+        uint8_t *sq = smem + LY.q + w * Sh::q_bytes;
         if (active && !__any_sync(0xffffffffu, dead())) {
-            const bool dropped = *mark(LY.dropped, it.seq) == it.seq, bad = *mark(LY.bad, it.seq) == it.seq;
+            const volatile ChItem *flags = place(seq);
+            const bool dropped = flags->dropped, bad = flags->bad;
             const bool whole = it.whole();
-            const int part = 2 * blockIdx.x + (it.piece.at.k == 0);
+            const int part = 2 * blockIdx.x + (it.k == 0);
             float *po = p.ws_o + ((int64_t)part * kChRows + m) * D;
             const float inv = ch_rcp(l);   // (a sum of a row that sees a key is far above the subnormals)
             uint16_t *out = static_cast<uint16_t *>(p.out) + grow * D;
@@ -749,15 +814,27 @@ struct ChTile {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             y[i] = l == 0.f ? 0u : E::pack(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        uint4 *dst = joined ? reinterpret_cast<uint4 *>(out + c + e) : chunk(sq, row, (c + e) / 8);
+                        *dst = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
             }
+            if (whole && !joined) {   // by way of the Q tile: whole rows an access
+                __syncwarp();
+                const unsigned long long mine = (unsigned long long)(valid && !bad ? out : nullptr);
+#pragma unroll 4
+                for (int i = 0; i < kRowTurns; ++i) {
+                    const int r = i * kRowsAtOnce + lane / (D / 8), c = lane % (D / 8);
+                    uint4 *y = reinterpret_cast<uint4 *>(__shfl_sync(0xffffffffu, mine, r));
+                    if (y) y[c] = *chunk(sq, (row & ~31) + r, c);
+                }
+                __syncwarp();
+            }
             if (dropped && valid && !bad) {   // what is not finite, to the rows that see it
-                const int to = min(min(it.keys, it.piece.k1 * kChKeys), limit);
+                const int to = min(min(it.keys, (it.k + it.n) * kChKeys), limit);
 #pragma unroll 1
-                for (int key = max(it.all, it.piece.at.k * kChKeys); key < to; ++key) {
-                    const uint16_t *v = ch_value_row<D>(p, it.piece.at.r, it.piece.at.g, key);
+                for (int key = max(it.all, it.k * kChKeys); key < to; ++key) {
+                    const uint16_t *v = ch_value_row<D>(p, it.r, it.g, key);
 #pragma unroll 1
                     for (int d = 0; v && d < D; ++d)
                         if (pa_not_finite<E>(v[d])) {
@@ -850,14 +927,16 @@ __global__ void __launch_bounds__(kChThreads, 1)
     uint8_t *smem = ch_smem_dyn + ((1024u - (smem_u32(ch_smem_dyn) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    ChPos *pos = reinterpret_cast<ChPos *>(smem + LY.pos);
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();   // every input comes from the kernels before this one
-    const ChPos begin = p.ws_pos[blockIdx.x], end = p.ws_pos[blockIdx.x + 1];
+    ChPos begin, end;   // (as in ChItem: one value a warp)
+    {
+        const int *x = reinterpret_cast<const int *>(p.ws_pos + blockIdx.x);
+        begin = {ch_uniform(x[0]), ch_uniform(x[1]), ch_uniform(x[2]), ch_uniform(x[3])};
+        end = {ch_uniform(x[4]), ch_uniform(x[5]), ch_uniform(x[6]), ch_uniform(x[7])};
+    }
     if (ch_reached(begin, end)) return;   // no work is left for this part
     if (threadIdx.x == 0) {
-        pos[0] = begin;
-        pos[1] = end;
         for (int i = 0; i < Sh::units; ++i) {
             mbar_init(sb + LY.full + 8 * i, 1);
             mbar_init(sb + LY.empty + 8 * i, 2);
@@ -874,7 +953,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
             mbar_init(sb + LY.drain + 8 * w, 1);
         }
         *reinterpret_cast<volatile int *>(smem + LY.dead) = 0;
-        for (int i = 0; i < 2 * kChSeq; ++i) reinterpret_cast<volatile int *>(smem + LY.bad)[i] = 0;   // (and dropped)
+        for (int i = 0; i < kChItems; ++i) {
+            mbar_init(sb + LY.ifull + 8 * i, 1);
+            mbar_init(sb + LY.iempty + 8 * i, 11);   // all warps but the one that hands them out
+        }
         fence_barrier_init();
     }
     // all of tensor memory (one CTA per SM): it starts at column 0
@@ -891,7 +973,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp < 10)
-            tile.produce(ch_uniform(warp - 8));
+            tile.produce(ch_uniform(warp - 8), begin, end);
         else
             tile.multiply(ch_uniform(warp - 10));
     }

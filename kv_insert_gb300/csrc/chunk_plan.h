@@ -23,7 +23,7 @@ constexpr int kChTile = 128;     // rows of one tile; a block of no more has one
 // end, in keys x q heads (so that a block's own 256 rows are 256 of them).  A
 // block of one tile shares its keys between the two groups of warps that
 // otherwise take a tile each: 3 of 4 of a whole block's cost a key.
-constexpr int kChOver = 192;
+constexpr int kChOver = 704;
 constexpr int kChWhole = 4, kChHalf = 3;
 
 struct ChRequest {
