@@ -19,6 +19,7 @@ HEADERS = [os.path.join(ROOT, "include", "qkvfront.h"),
            os.path.join(PKG, "csrc", "norm_rope.cuh"),
            os.path.join(PKG, "csrc", "chunk_plan.h"),
            os.path.join(PKG, "csrc", "chunk_attn.cuh"),
+           os.path.join(PKG, "csrc", "key_weights.cuh"),
            os.path.join(PKG, "csrc", "kv_evict.cuh")]
 LIB_PATH = os.path.join(PKG, "libqkvfront.so")
 

@@ -1,6 +1,5 @@
-// chunk_attn: attention of each request's new tokens over its paged keys, and
-// key_weights: what each key received of it (included by qkv_front.cu after
-// norm_rope.cuh: one translation unit).
+// chunk_attn: attention of each request's new tokens over its paged keys
+// (included by qkv_front.cu after norm_rope.cuh: one translation unit).
 //
 // Request r brings the rows starts[r] .. starts[r + 1] - 1 of q, n of them, and
 // has L keys, its new tokens' among them.  Its token i sees keys j <= L - n + i:
@@ -75,17 +74,6 @@ __device__ __forceinline__ ChRequest ragged_request(const RaggedParams &p, int b
 __device__ __forceinline__ ChRequest ragged_request(const RaggedParams &p, int r, bool flag)
 {
     return ragged_request(p, p.starts[r], p.starts[r + 1], p.context_lens[r], flag);
-}
-
-template <class E, int D>
-__device__ __forceinline__ float ragged_dot(const uint16_t *k, const float *q, int lane)
-{
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) s = fmaf(q[i], E::get(k[lane + 32 * i]), s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
 }
 
 // ---- shapes -----------------------------------------------------------------
@@ -860,16 +848,17 @@ struct ChTile {
 // thread's run of requests each), then a part a thread.
 constexpr int kChPlanThreads = 1024;
 
-__global__ void __launch_bounds__(kChPlanThreads) chunk_plan_kernel(const __grid_constant__ RaggedParams p)
+// cost(r, flag, request): request r's cost (flag: raise the status bit of a bad
+// one) and what locate needs; locate(request, r, off): the place that far into it
+template <class Cost, class Locate>
+__device__ __forceinline__ void ch_plan(const RaggedParams &p, Cost cost, Locate locate)
 {
     __shared__ int64_t before[kChPlanThreads + 1], warps[32];
-    if (threadIdx.x == 0) griddep_launch_dependents();
-    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.R + kChPlanThreads - 1) / kChPlanThreads, r0 = tid * per, r1 = min(p.R, r0 + per);
-    int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += p.nkv * ch_request_cost(ragged_request(p, r, true), p.group);
-    int64_t upto = mine;
+    ChRequest q;
+    int64_t upto = 0;
+    for (int r = r0; r < r1; ++r) upto += cost(r, true, q);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -904,17 +893,27 @@ __global__ void __launch_bounds__(kChPlanThreads) chunk_plan_kernel(const __grid
             }
             off -= before[lo];
             for (int r = lo * per; r < min(p.R, lo * per + per); ++r) {
-                const ChRequest q = ragged_request(p, r, false);
-                const int64_t cost = p.nkv * ch_request_cost(q, p.group);
-                if (off < cost) {
-                    at = ch_locate(q, p.group, r, off);
+                const int64_t own = cost(r, false, q);
+                if (off < own) {
+                    at = locate(q, r, off);
                     break;
                 }
-                off -= cost;
+                off -= own;
             }
         }
         p.ws_pos[c] = at;
     }
+}
+
+__global__ void __launch_bounds__(kChPlanThreads) chunk_plan_kernel(const __grid_constant__ RaggedParams p)
+{
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();
+    const auto cost = [&](int r, bool flag, ChRequest &q) {
+        q = ragged_request(p, r, flag);
+        return p.nkv * ch_request_cost(q, p.group);
+    };
+    ch_plan(p, cost, [&](const ChRequest &q, int r, int64_t off) { return ch_locate(q, p.group, r, off); });
 }
 
 template <class E, int D>
@@ -1100,41 +1099,6 @@ int launch_chunk(const CUtensorMap &map, const RaggedParams &prm, void *stream)
     return launch_pdl(chunk_merge_kernel<E, D>, dim3((unsigned)prm.parts, kChMergeY), dim3(kChMergeThreads), 0, stream, prm);
 }
 
-template <class E, int D>
-__global__ void __launch_bounds__(128) key_rows_kernel(const __grid_constant__ RaggedParams p)
-{
-    if (threadIdx.x == 0) griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31, r = blockIdx.z, g = blockIdx.y;
-    const int j = blockIdx.x * 4 + (threadIdx.x >> 5);
-    const ChRequest q = ragged_request(p, r, threadIdx.x == 0 && blockIdx.x == 0);
-    if (q.n < 0 || j >= q.L) return;
-    const int page = p.block_table[(int64_t)r * p.max_blocks + j / kPageSlots];
-    if (page < 0 || page >= p.num_pages) {
-        atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
-        return;
-    }
-    const uint16_t *k = static_cast<const uint16_t *>(p.kv_cache) +
-                        (((int64_t)page * p.nkv + g) * kPageSlots + j % kPageSlots) * (2 * D);
-    float sum = 0.f;
-    const int n = p.window ? min(q.n, p.window) : q.n;
-    for (int i = max(q.n - n, j - (q.L - q.n)); i < q.n; ++i) {
-        const int t = q.row0 + i;
-        for (int h = g * p.group; h < (g + 1) * p.group; ++h) {
-            float qv[D / 32];
-            for (int d = 0; d < D / 32; ++d)
-                qv[d] = E::get((static_cast<const uint16_t *>(p.q) + t * p.q_ts + h * p.q_hs)[lane + 32 * d]);
-            const float lse = p.lse[(int64_t)t * p.q_heads + h];
-            const float s = ragged_dot<E, D>(k, qv, lane);
-            if (lse > -INFINITY) sum += exp2f(fmaf(s, p.scale_log2, -lse * 1.4426950408889634f));
-        }
-    }
-    if (lane == 0) {
-        const int64_t at = ((int64_t)r * p.nkv + g) * p.max_blocks * kPageSlots + j;
-        p.out_weights[at] = p.decay == 0.f ? sum : fmaf(p.decay, p.weights[at], sum);
-    }
-}
-
 // ---- host -------------------------------------------------------------------
 
 const char *check_ragged_shape(int T, int num_reqs, int q_heads, int num_kv_heads, int head_dim, int max_blocks, int *code)
@@ -1223,36 +1187,6 @@ const char *check_chunk_args(const RaggedParams &p, int head_dim, float scale, i
     return nullptr;
 }
 
-const char *check_key_weights_args(const RaggedParams &p, int head_dim, float scale, int dtype, const void *workspace,
-                                   size_t workspace_bytes, int *code)
-{
-    if (const char *why = check_ragged_args(p.q, p.q_ts, p.q_hs, p.kv_cache, p.num_pages, p.starts, p.block_table,
-                                            p.max_blocks, p.context_lens, p.T, p.R, p.q_heads, p.nkv, head_dim, scale,
-                                            dtype, workspace, code))
-        return why;
-    *code = QKVF_ERR_ARG;
-    if (p.window < 0) return "window must be 0 (every token) or more";
-    if (!(p.decay >= 0.f) || !(p.decay <= 1.f)) return "decay must be in [0, 1]";
-    *code = QKVF_OK;
-    if (p.R == 0) return nullptr;
-    *code = QKVF_ERR_NULL;
-    if ((p.T > 0 && !p.lse) || !p.out_weights || (p.decay != 0.f && !p.weights)) return "a required pointer is NULL";
-    *code = QKVF_ERR_ALIGN;
-    if (!aligned(p.lse, 4) || !aligned(p.weights, 4) || !aligned(p.out_weights, 4))
-        return "lse and the weights must be 4-byte aligned";
-    *code = QKVF_ERR_ARG;
-    const size_t w_bytes = (size_t)p.R * p.nkv * p.max_blocks * kPageSlots * 4, rows = (size_t)p.T * p.q_heads;
-    if (p.weights && p.weights != p.out_weights && overlap(p.weights, w_bytes, p.out_weights, w_bytes))
-        return "out overlaps weights without being weights";
-    if (p.weights && workspace_bytes && overlap(p.weights, w_bytes, workspace, workspace_bytes))
-        return "out or the workspace overlaps another argument";
-    const void *outs[] = {p.out_weights, workspace};
-    const size_t sizes[] = {w_bytes, workspace_bytes};
-    if (ragged_overlap(p, head_dim, outs, sizes, 2, p.lse, rows * 4)) return "out or the workspace overlaps another argument";
-    *code = QKVF_OK;
-    return nullptr;
-}
-
 RaggedParams ragged_params(const void *q, int64_t q_ts, int64_t q_hs, const void *kv_cache, int64_t num_pages,
                            const int32_t *starts, const int32_t *block_table, int max_blocks, const int32_t *context_lens,
                            int T, int num_reqs, int q_heads, int num_kv_heads, float scale, int dtype)
@@ -1283,7 +1217,6 @@ size_t chunk_workspace(int head_dim, int sms)
     const size_t slots = (size_t)2 * sms;
     return slots * kChRows * (head_dim * 4 + 8) + ((size_t)(sms + 1) * sizeof(ChPos) + 255) / 256 * 256;
 }
-size_t key_weights_workspace(int head_dim, int sms) { return 512; }
 
 }  // namespace qkvf
 
@@ -1348,63 +1281,6 @@ int chunk_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, con
                           : qkvf::launch_chunk<qkvf::Fp16, 128>(map, prm, stream);
 }
 
-size_t key_weights_workspace_bytes(int T, int num_reqs, int q_heads, int num_kv_heads, int head_dim, int max_blocks)
-{
-    int code;
-    if (qkvf::check_ragged_shape(T, num_reqs, q_heads, num_kv_heads, head_dim, max_blocks, &code)) return 0;
-    qkvf::DeviceState *d;
-    return qkvf::probe_device(&d) == QKVF_OK ? qkvf::key_weights_workspace(head_dim, d->sms) : 0;
-}
-
-const char *key_weights_unsupported(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *kv_cache,
-                                    int64_t num_pages, const float *lse, const int32_t *starts, const int32_t *block_table,
-                                    int max_blocks, const int32_t *context_lens, int T, int num_reqs, int q_heads,
-                                    int num_kv_heads, int head_dim, int window, float decay, float scale, int dtype,
-                                    const float *weights, float *out, const void *workspace, size_t workspace_bytes)
-{
-    qkvf::RaggedParams prm = qkvf::ragged_params(q, q_token_stride, q_head_stride, kv_cache, num_pages, starts, block_table,
-                                                 max_blocks, context_lens, T, num_reqs, q_heads, num_kv_heads, scale, dtype);
-    prm.lse = const_cast<float *>(lse);
-    prm.weights = weights;
-    prm.out_weights = out;
-    prm.window = window;
-    prm.decay = decay;
-    int code;
-    const char *why = qkvf::check_key_weights_args(prm, head_dim, scale, dtype, workspace, workspace_bytes, &code);
-    if (why) return why;
-    qkvf::DeviceState *d;
-    const int rc = qkvf::probe_device(&d);
-    if (rc != QKVF_OK) return qkv_front_strerror(rc);
-    return num_reqs > 0 && workspace_bytes < qkvf::key_weights_workspace(head_dim, d->sms) ? "the workspace is too small" : nullptr;
-}
-
-int key_weights(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *kv_cache, int64_t num_pages,
-                const float *lse, const int32_t *starts, const int32_t *block_table, int max_blocks,
-                const int32_t *context_lens, int T, int num_reqs, int q_heads, int num_kv_heads, int head_dim, int window,
-                float decay, float scale, int dtype, const float *weights, float *out, void *workspace,
-                size_t workspace_bytes, void *stream)
-{
-    qkvf::RaggedParams prm = qkvf::ragged_params(q, q_token_stride, q_head_stride, kv_cache, num_pages, starts, block_table,
-                                                 max_blocks, context_lens, T, num_reqs, q_heads, num_kv_heads, scale, dtype);
-    prm.lse = const_cast<float *>(lse);
-    prm.weights = weights;
-    prm.out_weights = out;
-    prm.window = window;
-    prm.decay = decay;
-    int code;
-    if (qkvf::check_key_weights_args(prm, head_dim, scale, dtype, workspace, workspace_bytes, &code)) return code;
-    if (num_reqs == 0) return QKVF_OK;
-    qkvf::DeviceState *d;
-    const int rc = qkvf::probe_device(&d);
-    if (rc != QKVF_OK) return rc;
-    if (workspace_bytes < qkvf::key_weights_workspace(head_dim, d->sms)) return QKVF_ERR_SIZES;
-    const bool bf16 = qkvf::dtype_of(dtype) == QKVF_DTYPE_BF16;
-    const dim3 grid((unsigned)(max_blocks * qkvf::kPageSlots / 4), (unsigned)num_kv_heads, (unsigned)num_reqs);
-    return qkvf::launch_pdl(bf16 ? head_dim == 64 ? qkvf::key_rows_kernel<qkvf::Bf16, 64> : qkvf::key_rows_kernel<qkvf::Bf16, 128>
-                                 : head_dim == 64 ? qkvf::key_rows_kernel<qkvf::Fp16, 64> : qkvf::key_rows_kernel<qkvf::Fp16, 128>,
-                            grid, dim3(128), 0, stream, prm);
-}
-
 int chunk_attn_packed(const int64_t *args, void *stream)
 {
     if (!args) return QKVF_ERR_NULL;
@@ -1414,18 +1290,6 @@ int chunk_attn_packed(const int64_t *args, void *stream)
     return chunk_attn(w.p<void>(0), args[1], args[2], w.p<void>(3), args[4], w.p<int32_t>(5), w.p<int32_t>(6), mb,
                       w.p<int32_t>(8), T, R, q_heads, nkv, dim, (float)w.d(14), dtype, w.p<void>(16), w.p<float>(17),
                       w.p<void>(18), (size_t)args[19], stream);
-}
-
-int key_weights_packed(const int64_t *args, void *stream)
-{
-    if (!args) return QKVF_ERR_NULL;
-    qkvf::Words w(args);
-    const int mb = w.i(8), T = w.i(10), R = w.i(11), q_heads = w.i(12), nkv = w.i(13), dim = w.i(14), window = w.i(15),
-              dtype = w.i(18);
-    if (!w.ok) return QKVF_ERR_SIZES;
-    return key_weights(w.p<void>(0), args[1], args[2], w.p<void>(3), args[4], w.p<float>(5), w.p<int32_t>(6), w.p<int32_t>(7),
-                       mb, w.p<int32_t>(9), T, R, q_heads, nkv, dim, window, (float)w.d(16), (float)w.d(17), dtype,
-                       w.p<float>(19), w.p<float>(20), w.p<void>(21), (size_t)args[22], stream);
 }
 
 }  // extern "C"

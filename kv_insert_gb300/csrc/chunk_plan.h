@@ -141,4 +141,67 @@ CH_HD bool ch_take(const ChRequest &q, int group, int nkv, ChPos &at, const ChPo
     return piece.k1 > piece.at.k || (piece.steps == 0 && !ends);
 }
 
+// ---- key_weights: blocks of keys against the rows that see them ---------------
+
+constexpr int kKwKeys = 256;   // keys of a block: two tensor-memory tiles
+
+// A request's tokens that count (the last n) and its keys; `tokens` of a step.
+// Block b's keys are seen by tokens from L - 256 b or n from the end on; it costs
+// those, and `over` tokens' worth of loading the keys.
+CH_HD int kw_blocks(const ChRequest &q) { return (int)(((int64_t)q.L + kKwKeys - 1) / kKwKeys); }
+CH_HD int kw_seen(const ChRequest &q, int b) { return q.n < q.L - b * kKwKeys ? q.n : q.L - b * kKwKeys; }
+CH_HD int kw_steps(const ChRequest &q, int b, int tokens) { return (kw_seen(q, b) + tokens - 1) / tokens; }
+
+CH_HD int64_t kw_before(const ChRequest &q, int b, int over)   // the first b blocks' cost
+{
+    const int64_t flat = q.L > q.n ? (q.L - q.n) / kKwKeys + 1 : 1;   // blocks that all n see
+    const int64_t f = b < flat ? b : flat, m = b - f;
+    const int64_t ends = (int64_t)q.L * m - kKwKeys / 2 * ((int64_t)b * (b - 1) - f * (f - 1));
+    return (int64_t)over * b + (q.n < q.L ? q.n : q.L) * f + (m > 0 ? ends : 0);
+}
+CH_HD int64_t kw_cost(const ChRequest &q, int b, int over) { return (int64_t)over + kw_seen(q, b); }
+CH_HD int64_t kw_request_cost(const ChRequest &q, int over) { return q.n < 0 || q.L <= 0 ? 0 : kw_before(q, kw_blocks(q), over); }
+
+CH_HD ChPos kw_locate(const ChRequest &q, int r, int64_t off, int tokens, int over)
+{
+    ChPos at;
+    const int64_t per = kw_request_cost(q, over);
+    const int last = kw_blocks(q) - 1;
+    at.r = r;
+    at.g = (int)(off / per);
+    off -= at.g * per;
+    // bisection: 25 steps at most
+    int lo = 0, hi = last;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (kw_before(q, mid, over) <= off) lo = mid;
+        else hi = mid - 1;
+    }
+    at.b = lo;
+    at.k = (int)((off - kw_before(q, at.b, over)) * kw_steps(q, at.b, tokens) / kw_cost(q, at.b, over));
+    return at;
+}
+
+// As ch_take, of one request's blocks of keys
+CH_HD bool kw_take(const ChRequest &q, int tokens, int nkv, ChPos &at, const ChPos &end, ChPiece &piece)
+{
+    piece.at = at;
+    piece.steps = kw_steps(q, at.b, tokens);
+    const bool ends = ch_same_item(at, end);
+    piece.k1 = ends ? end.k : piece.steps;
+    if (ends) {
+        at = end;
+    } else {
+        at.k = 0;
+        if (++at.b == kw_blocks(q)) {
+            at.b = 0;
+            if (++at.g == nkv) {
+                at.g = 0;
+                ++at.r;
+            }
+        }
+    }
+    return piece.k1 > piece.at.k || (piece.steps == 0 && !ends);
+}
+
 }  // namespace qkvf

@@ -1171,6 +1171,7 @@ bool prepare_epi_kernel();
 bool prepare_attn2_kernel();
 bool prepare_prefix_kernels();
 bool prepare_chunk_kernels();
+bool prepare_key_kernels();
 
 int probe_device(DeviceState **out)
 {
@@ -1213,7 +1214,8 @@ int probe_device(DeviceState **out)
             if (cudaFuncSetAttribute(res[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)res_smem_bytes(i ? 16 : 8)) != cudaSuccess)
                 return QKVF_ERR_CUDA;
-        if (!prepare_epi_kernel() || !prepare_attn2_kernel() || !prepare_prefix_kernels() || !prepare_chunk_kernels())
+        if (!prepare_epi_kernel() || !prepare_attn2_kernel() || !prepare_prefix_kernels() || !prepare_chunk_kernels() ||
+            !prepare_key_kernels())
             return QKVF_ERR_CUDA;
         d.prepared = true;
     }
@@ -1455,6 +1457,7 @@ int launch_front(const uint16_t *x, const uint16_t *W, const int64_t *positions,
 #include "prefix_attn.cuh"
 #include "norm_rope.cuh"
 #include "chunk_attn.cuh"
+#include "key_weights.cuh"
 #include "kv_evict.cuh"
 
 using namespace qkvf;

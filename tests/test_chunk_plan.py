@@ -1,4 +1,4 @@
-"""The dealing of a chunk_attn call's work (chunk_plan.h), on the host under
+"""The dealing of chunk_attn's and key_weights' work (chunk_plan.h), on the host under
 the undefined-behaviour sanitizer: every key step of every item is taken once,
 in order, by parts of nearly equal cost, for drawn and extreme batches."""
 import os
@@ -85,6 +85,71 @@ static void check(const std::vector<ChRequest> &reqs, int nkv, int group, int pa
     NEED(want.r == R);
 }
 
+// The same for key_weights' blocks of keys
+static void check_keys(const std::vector<ChRequest> &reqs, int nkv, int group, int parts)
+{
+    const int R = (int)reqs.size(), tokens = 128 / group > 0 ? 128 / group : 1, over = 3 * tokens;
+    std::vector<int64_t> before(R + 1, 0);
+    for (int r = 0; r < R; ++r) {
+        int64_t sum = 0;
+        if (reqs[r].n >= 0 && reqs[r].L > 0) {
+            const int blocks = kw_blocks(reqs[r]);
+            for (int b = 0; b < blocks; ++b) {
+                if (b < 2000 || b == blocks - 1) NEED(kw_before(reqs[r], b, over) == sum);
+                NEED(kw_seen(reqs[r], b) >= 0 && kw_seen(reqs[r], b) <= reqs[r].n);
+                sum += kw_cost(reqs[r], b, over);
+            }
+        }
+        NEED(sum == kw_request_cost(reqs[r], over));
+        before[r + 1] = before[r] + nkv * sum;
+    }
+    const int64_t total = before[R];
+    std::vector<ChPos> pos;
+    for (int c = 0; c <= parts; ++c) {
+        const int64_t u = ch_part(total, parts, c);
+        ChPos at = {R, 0, 0, 0};
+        for (int r = 0; r < R; ++r)
+            if (u >= before[r] && u < before[r + 1]) at = kw_locate(reqs[r], r, u - before[r], tokens, over);
+        if (at.r < R) {
+            NEED(at.g >= 0 && at.g < nkv && at.b >= 0 && at.b < kw_blocks(reqs[at.r]));
+            const int steps = kw_steps(reqs[at.r], at.b, tokens);
+            NEED(at.k >= 0 && (steps == 0 ? at.k == 0 : at.k < steps));
+        }
+        NEED(c == 0 || ch_reached(at, pos.back()));
+        pos.push_back(at);
+    }
+    ChPos want = {0, 0, 0, 0};
+    const auto none = [&](int r) { return reqs[r].n < 0 || reqs[r].L <= 0; };
+    const auto settle = [&] { while (want.r < R && none(want.r)) want = {want.r + 1, 0, 0, 0}; };
+    settle();
+    for (int c = 0; c < parts; ++c) {
+        ChPos at = pos[c];
+        int count = 0;
+        while (!ch_reached(at, pos[c + 1])) {
+            if (none(at.r)) {
+                at = {at.r + 1, 0, 0, 0};
+                continue;
+            }
+            ChPiece p;
+            const ChRequest &q = reqs[at.r];
+            if (!kw_take(q, tokens, nkv, at, pos[c + 1], p)) continue;
+            NEED(ch_same_item(p.at, want) && p.at.k == want.k && p.k1 <= p.steps);
+            NEED(p.at.k == 0 || count == 0);
+            ++count;
+            want.k = p.k1;
+            if (p.k1 == p.steps) {
+                want.k = 0;
+                if (++want.b == kw_blocks(q)) {
+                    want.b = 0;
+                    if (++want.g == nkv) want = {want.r + 1, 0, 0, 0};
+                }
+                settle();
+            }
+        }
+    }
+    NEED(want.r == R);
+}
+
 int main()
 {
     std::mt19937 rng(7);
@@ -97,6 +162,9 @@ int main()
             reqs.push_back({0, n, pick(0, 5) ? n + pick(0, 1 << pick(0, 17)) : pick(0, n)});
         }
         check(reqs, pick(1, 9), pick(1, 64), pick(0, 1) ? 152 : pick(1, 300));
+        for (auto &q : reqs)
+            if (!pick(0, 5)) q.n = pick(-1, 0);
+        check_keys(reqs, pick(1, 9), pick(1, 64), pick(0, 1) ? 152 : pick(1, 300));
     }
     const int far = 1 << 24;
     check({{0, far, far}}, 1, 1, 152);
@@ -108,6 +176,10 @@ int main()
     check({{0, far, 1 << 10}}, 1, 5, 7);
     check(std::vector<ChRequest>(65535, ChRequest{0, 1, far}), 64, 64, 152);
     check(std::vector<ChRequest>(65535, ChRequest{0, 1, 1}), 1, 1, 152);
+    check_keys({{0, far, far}}, 64, 1, 152);
+    check_keys({{0, 1, far}}, 64, 64, 152);
+    check_keys({{0, 0, far}, {0, 1 << 18, far}}, 1, 64, 152);
+    check_keys({{0, far, 300}, {0, 256, 512}, {0, 0, 256}}, 1, 1, 152);
     puts("ok");
 }
 """
