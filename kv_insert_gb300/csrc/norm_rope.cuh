@@ -10,12 +10,12 @@
 // r is formed again from x, which dx and dw need anyway: nothing is kept
 // between the two directions.
 //
-// A group of P lanes takes a head (P a power of two, P * units-a-lane covers
-// the head's 16-byte chunks), with the chunks' weights in registers; the sums
-// over a head are shuffles within the group.  In the half layout a unit is a
-// chunk and its partner, so no column crosses lanes.  Rows off the 16-byte
-// grid, and half pairs whose distance is no whole chunk, take a warp per head
-// element by element.
+// A group of P lanes takes a head, a unit of two 16-byte chunks a lane (two
+// units for the widest), with the chunks' weights in registers; the sums over a
+// head are shuffles within the group.  A unit's chunks are neighbours, or in the
+// half layout a chunk and its partner, so no column crosses lanes; half pairs
+// whose distance is no whole chunk go through shared memory.  Rows off the
+// 16-byte grid take a warp per head element by element.
 
 namespace qkvf {
 
@@ -31,7 +31,7 @@ struct NormParams {
     float *part;              // [ctas][dim] sums of g' * x r (null: no weight gradient)
 };
 
-// Weights of `n` columns from c on (1 without a weight)
+// Weights of a 16-byte chunk's columns from c on (1 without a weight)
 template <class E, int n>
 __device__ __forceinline__ void norm_weights(const void *w, int fp32, int c, float (&out)[n])
 {
@@ -60,7 +60,7 @@ template <int pairs>
 __device__ __forceinline__ void norm_angles(const float *row, int rot, int i0, float sign, float (&c)[pairs], float (&s)[pairs])
 {
     const int half = rot >> 1;
-    if (pairs % 4 == 0 && rot % 8 == 0) {   // both halves of the row on 16 bytes
+    if (pairs % 4 == 0 && rot % 8 == 0 && i0 + pairs <= half) {   // both halves of the row on 16 bytes
 #pragma unroll
         for (int i = 0; i + 4 <= pairs; i += 4) {
             *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(row + i0 + i);
@@ -78,37 +78,62 @@ __device__ __forceinline__ void norm_angles(const float *row, int rot, int i0, f
     for (int i = 0; i < pairs; ++i) s[i] *= sign;
 }
 
-// A lane's unit u of a head: chunk `a` and, in the half layout, the chunk with
-// its pairs' other columns
-template <class E, bool kHalf>
+// Pairs (2i, 2i + 1); pairs (i, i + rot / 2) whose distance is whole chunks; the
+// same at any distance, by way of shared memory
+enum NormPairs { kNormInterleaved = 0, kNormHalf = 1, kNormStaged = 2 };
+
+// A lane's unit u of a head: two chunks, at columns a and b (the second may not
+// exist), whose pairs are within the unit but for kNormStaged
+template <class E, int kPairs>
 struct NormUnit {
-    static constexpr int vec = RopeChunk<E>::vec, pairs = kHalf ? vec : vec / 2;
+    static constexpr int vec = RopeChunk<E>::vec;
     int a, b;        // first columns
     int i0, whole;   // first pair, pairs turned
     bool in, two;    // the unit exists; it has a second chunk
     __device__ __forceinline__ NormUnit(const RopeParams &p, int u)
     {
-        const int half = p.rot >> 1;
+        const int half = p.rot >> 1, h = kPairs == kNormHalf ? half / vec : 0;   // units of two chunks that turn together
         in = u < p.units;
-        two = kHalf && u < half / vec;
-        a = (kHalf && !two ? half / vec + u : u) * vec;
-        b = a + half;
-        i0 = u * pairs;
-        whole = kHalf ? (two ? pairs : 0) : max(0, min(pairs, half - i0));
+        if (u < h) {
+            a = u * vec;
+            b = a + half;
+        } else {
+            a = 2 * (h + (u - h)) * vec;
+            b = a + vec;
+        }
+        two = b < p.dim;
+        i0 = u * vec;
+        whole = kPairs == kNormHalf ? (u < h ? vec : 0) : max(0, min(vec, half - i0));
     }
 };
 
 // Turn a unit's values in place
-template <class E, bool kHalf, int vec>
+template <class E, int kPairs, int vec>
 __device__ __forceinline__ void norm_turn(float (&a)[vec], float (&b)[vec], const float *c, const float *s, int whole)
 {
-    constexpr int pairs = kHalf ? vec : vec / 2;
 #pragma unroll
-    for (int k = 0; k < pairs; ++k)
+    for (int k = 0; k < vec; ++k)
         if (k < whole) {
-            float &va = kHalf ? a[k] : a[2 * k], &vb = kHalf ? b[k] : a[2 * k + 1];
-            rope_pair(va, vb, c[k], s[k], va, vb);
+            if (kPairs == kNormHalf)
+                rope_pair(a[k], b[k], c[k], s[k], a[k], b[k]);
+            else if (k < vec / 2)
+                rope_pair(a[2 * k], a[2 * k + 1], c[k], s[k], a[2 * k], a[2 * k + 1]);
+            else
+                rope_pair(b[2 * k - vec], b[2 * k + 1 - vec], c[k], s[k], b[2 * k - vec], b[2 * k + 1 - vec]);
         }
+}
+
+// kNormStaged: column c of a head whose values are in `row`, turned.  `own` is
+// its value, w the partner's weight (times r).
+template <class E>
+__device__ __forceinline__ float norm_turn_staged(const typename E::store *row, const float *angles, int half, float sign, int c, float own,
+                                                  const void *weight, int fp32, float r)
+{
+    if (c >= 2 * half) return own;
+    const bool second = c >= half;
+    const int i = second ? c - half : c, q = second ? i : c + half;
+    const float other = E::get(row[q]) * r * norm_weight<E>(weight, fp32, q), sn = sign * angles[half + i];
+    return fmaf(own, angles[i], second ? other * sn : -(other * sn));
 }
 
 __device__ __forceinline__ float norm_sum(float v, int lanes)
@@ -117,14 +142,17 @@ __device__ __forceinline__ float norm_sum(float v, int lanes)
     return v;
 }
 
-// One group of lanes takes kHeads neighbouring heads of a token
-template <class E, bool kHalf, int kHeads, int kUnits>
-__global__ void __launch_bounds__(256) norm_vec_kernel(const __grid_constant__ NormParams p)
+// One group of lanes takes kHeads neighbouring heads of a token.  Three CTAs an
+// SM: with two heads a lane 48 KB are in flight on it (8192 tokens of 32 heads of
+// 128: @@FWD@@).
+template <class E, int kPairs, int kHeads, int kUnits>
+__global__ void __launch_bounds__(256, kPairs == kNormStaged ? 2 : 3) norm_vec_kernel(const __grid_constant__ NormParams p)
 {
     using S = typename E::store;
     using Chunk = RopeChunk<E>;
-    using Unit = NormUnit<E, kHalf>;
-    constexpr int vec = Chunk::vec, pairs = Unit::pairs, B = kHalf ? kHeads : 1;
+    using Unit = NormUnit<E, kPairs>;
+    constexpr int vec = Chunk::vec;
+    __shared__ uint4 stage[kPairs == kNormStaged ? 256 * 2 * kHeads * kUnits : 1];
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
     const RopeParams &r = p.r;
@@ -136,49 +164,57 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(const __grid_constant__ N
     const int64_t pos = mine ? r.positions[t] : -1, slot = mine && r.nkv ? r.slots[t] : -1;
     RopeHeads<S> hd(r, mine ? t : 0, mine ? grp : 0, r.q_per, r.kv_per, (r.groups - r.q_groups) >> 1);
     if (!mine) hd.n = 0;
-    Chunk x[kUnits][kHeads], y[kUnits][B];
-    float ss[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) ss[i] = 0.f;
+    Chunk x[kUnits][kHeads], y[kUnits][kHeads];
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
         const Unit un(r, sl + k * p.lanes);
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i)
+        for (int i = 0; i < kHeads; ++i) {
+            x[k][i].v = y[k][i].v = make_uint4(0u, 0u, 0u, 0u);
             if (un.in && i < hd.n) {
                 x[k][i].v = *reinterpret_cast<const uint4 *>(hd.src + i * hd.src_step + un.a);
-                if (kHalf && un.two) y[k][kHalf ? i : 0].v = *reinterpret_cast<const uint4 *>(hd.src + i * hd.src_step + un.b);
+                if (un.two) y[k][i].v = *reinterpret_cast<const uint4 *>(hd.src + i * hd.src_step + un.b);
             }
+        }
     }
     const RopeToken tok = mine ? rope_token(r, pos, slot, sl == 0 && grp == 0) : RopeToken{nullptr, -1};
     const bool put = mine && hd.place(r, tok);
+    float rs[kHeads];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        const Unit un(r, sl + k * p.lanes);
+    for (int i = 0; i < kHeads; ++i) {
+        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i)
-            if (un.in && i < hd.n) {
+        for (int k = 0; k < kUnits; ++k)
 #pragma unroll
-                for (int e = 0; e < vec; ++e) {
-                    const float a = E::get(x[k][i].e[e]);
-                    ss[i] = fmaf(a, a, ss[i]);
-                    if (kHalf && un.two) {
-                        const float b = E::get(y[k][kHalf ? i : 0].e[e]);
-                        ss[i] = fmaf(b, b, ss[i]);
-                    }
-                }
+            for (int e = 0; e < vec; ++e) {
+                const float a = E::get(x[k][i].e[e]), b = E::get(y[k][i].e[e]);
+                ss = fmaf(b, b, fmaf(a, a, ss));
             }
+        rs[i] = rsqrtf(fmaf(norm_sum(ss, p.lanes), 1.f / (float)r.dim, p.eps));   // every lane of the warp is here
     }
+    const void *w = hd.is_q ? p.qw : p.kw;
+    const int wf = hd.is_q ? p.qw_fp32 : p.kw_fp32;
+    S *rows = reinterpret_cast<S *>(stage) + (size_t)(threadIdx.x >> p.lane_shift) * kHeads * r.dim;   // the group's heads
+    if (kPairs == kNormStaged) {
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) ss[i] = norm_sum(ss[i], p.lanes);   // every lane of the warp is here
-    const float inv_dim = 1.f / (float)r.dim;
+        for (int k = 0; k < kUnits; ++k) {
+            const Unit un(r, sl + k * p.lanes);
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i)
+                if (un.in) {
+                    *reinterpret_cast<uint4 *>(rows + i * r.dim + un.a) = x[k][i].v;
+                    if (un.two) *reinterpret_cast<uint4 *>(rows + i * r.dim + un.b) = y[k][i].v;
+                }
+        }
+        __syncwarp();   // (a group is within a warp)
+    }
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
         const Unit un(r, sl + k * p.lanes);
         if (!un.in || !mine) continue;
         if (!put) {
             hd.clear(r, un.a);
-            if (kHalf && un.two) hd.clear(r, un.b);
+            if (un.two) hd.clear(r, un.b);
             continue;
         }
         if (hd.is_v) {
@@ -186,30 +222,38 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(const __grid_constant__ N
             for (int i = 0; i < kHeads; ++i)
                 if (i < hd.n) {
                     *reinterpret_cast<uint4 *>(hd.dst + i * hd.dst_step + un.a) = x[k][i].v;
-                    if (kHalf && un.two) *reinterpret_cast<uint4 *>(hd.dst + i * hd.dst_step + un.b) = y[k][kHalf ? i : 0].v;
+                    if (un.two) *reinterpret_cast<uint4 *>(hd.dst + i * hd.dst_step + un.b) = y[k][i].v;
                 }
             continue;
         }
-        float wa[vec], wb[vec], c[pairs], s[pairs];
-        norm_weights<E>(hd.is_q ? p.qw : p.kw, hd.is_q ? p.qw_fp32 : p.kw_fp32, un.a, wa);
-        if (kHalf && un.two) norm_weights<E>(hd.is_q ? p.qw : p.kw, hd.is_q ? p.qw_fp32 : p.kw_fp32, un.b, wb);
-        if (un.whole > 0) norm_angles<pairs>(tok.row, r.rot, un.i0, 1.f, c, s);
+        float wa[vec], wb[vec], c[vec], s[vec];
+        norm_weights<E>(w, wf, un.a, wa);
+        if (un.two) norm_weights<E>(w, wf, un.b, wb);
+        if (kPairs != kNormStaged && un.whole > 0) norm_angles<vec>(tok.row, r.rot, un.i0, 1.f, c, s);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i)
             if (i < hd.n) {
-                const float rs = rsqrtf(fmaf(ss[i], inv_dim, p.eps));
                 float a[vec], b[vec];
                 Chunk o;
 #pragma unroll
                 for (int e = 0; e < vec; ++e) {
-                    a[e] = E::get(x[k][i].e[e]) * rs * wa[e];
-                    if (kHalf && un.two) b[e] = E::get(y[k][kHalf ? i : 0].e[e]) * rs * wb[e];
+                    a[e] = E::get(x[k][i].e[e]) * rs[i] * wa[e];
+                    if (un.two) b[e] = E::get(y[k][i].e[e]) * rs[i] * wb[e];
                 }
-                norm_turn<E, kHalf>(a, b, c, s, un.whole);
+                if (kPairs == kNormStaged) {
+                    const int half = r.rot >> 1;
+#pragma unroll
+                    for (int e = 0; e < vec; ++e) {
+                        a[e] = norm_turn_staged<E>(rows + i * r.dim, tok.row, half, 1.f, un.a + e, a[e], w, wf, rs[i]);
+                        if (un.two) b[e] = norm_turn_staged<E>(rows + i * r.dim, tok.row, half, 1.f, un.b + e, b[e], w, wf, rs[i]);
+                    }
+                } else {
+                    norm_turn<E, kPairs>(a, b, c, s, un.whole);
+                }
 #pragma unroll
                 for (int e = 0; e < vec; ++e) o.e[e] = E::put(a[e]);
                 *reinterpret_cast<uint4 *>(hd.dst + i * hd.dst_step + un.a) = o.v;
-                if (kHalf && un.two) {
+                if (un.two) {
 #pragma unroll
                     for (int e = 0; e < vec; ++e) o.e[e] = E::put(b[e]);
                     *reinterpret_cast<uint4 *>(hd.dst + i * hd.dst_step + un.b) = o.v;
@@ -271,119 +315,186 @@ __global__ void __launch_bounds__(256) norm_element_kernel(const __grid_constant
 // A lane keeps its unit while its group walks over the heads, so the weight's
 // gradient adds up in registers; a CTA joins its groups in shared memory in
 // order and leaves one row of sums, and norm_dw_kernel adds the CTAs' rows in
-// order: a call repeats bitwise.
+// order: a call repeats bitwise.  The next heads' chunks are on their way to
+// shared memory while one is computed (four: 128 KB an SM); two CTAs an SM (8192 tokens of 32 heads of 128: @@BACK@@).
 
-template <class E, bool kHalf, int kUnits>
-__global__ void __launch_bounds__(256) norm_back_vec_kernel(const __grid_constant__ NormParams p)
+constexpr int kNormAhead = 4;
+
+__device__ __forceinline__ void norm_fetch(uint4 *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+template <class E, int kPairs, int kUnits>
+__global__ void __launch_bounds__(256, kUnits == 1 ? 2 : 1) norm_back_vec_kernel(const __grid_constant__ NormParams p)
 {
     using S = typename E::store;
     using Chunk = RopeChunk<E>;
-    using Unit = NormUnit<E, kHalf>;
-    constexpr int vec = Chunk::vec, pairs = Unit::pairs, nb = kHalf ? kUnits : 1;
-    extern __shared__ float norm_dw[];   // [groups of the CTA][dim]
+    using Unit = NormUnit<E, kPairs>;
+    constexpr int vec = Chunk::vec;
+    extern __shared__ float norm_dw[];   // [groups of the CTA][dim]; kNormStaged: before that their heads
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
     const RopeParams &r = p.r;
     const int sl = threadIdx.x & (p.lanes - 1), sub = threadIdx.x >> p.lane_shift, subs = 256 >> p.lane_shift;
     const float inv_dim = 1.f / (float)r.dim;
-    float wa[kUnits][vec], wb[nb][vec], da[kUnits][vec], db[nb][vec];
+    float wa[kUnits][vec], wb[kUnits][vec], da[kUnits][vec], db[kUnits][vec];
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
         const Unit un(r, sl + k * p.lanes);
-        if (un.in) norm_weights<E>(p.qw, p.qw_fp32, un.a, wa[k]);
-        if (kHalf && un.in && un.two) norm_weights<E>(p.qw, p.qw_fp32, un.b, wb[kHalf ? k : 0]);
 #pragma unroll
-        for (int e = 0; e < vec; ++e) {
-            da[k][e] = 0.f;
-            if (kHalf) db[kHalf ? k : 0][e] = 0.f;
-        }
+        for (int e = 0; e < vec; ++e) wa[k][e] = wb[k][e] = da[k][e] = db[k][e] = 0.f;
+        if (un.in) norm_weights<E>(p.qw, p.qw_fp32, un.a, wa[k]);
+        if (un.in && un.two) norm_weights<E>(p.qw, p.qw_fp32, un.b, wb[k]);
     }
     const int64_t rows = (int64_t)r.T * r.q_heads, step = (int64_t)gridDim.x * subs;
+    // A lane's chunks of the next heads on their way to shared memory: [turn][chunk][thread]
+    uint4 *ahead = reinterpret_cast<uint4 *>(norm_dw + (size_t)subs * r.dim) + threadIdx.x;
+    // a walk over the group's heads (a 64-bit division a head would cost as much as its sums)
+    const int dt = (int)(step / r.q_heads), dh = (int)(step - (int64_t)dt * r.q_heads);
+    struct Walk {
+        int t, h;
+    };
+    const auto advance = [&](Walk &w) {
+        w.t += dt;
+        w.h += dh;
+        if (w.h >= r.q_heads) {
+            w.h -= r.q_heads;
+            ++w.t;
+        }
+    };
+    const int64_t row00 = (int64_t)blockIdx.x * subs + sub;
+    Walk now = {(int)(row00 / r.q_heads), (int)(row00 % r.q_heads)}, next = now;
+    const auto fetch = [&](int turn) {
+        if (next.t < r.T) {
+            const S *gp = static_cast<const S *>(r.q) + next.t * r.q_ts + next.h * r.q_hs;
+            const S *xp = static_cast<const S *>(p.x) + next.t * p.x_ts + next.h * p.x_hs;
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                const Unit un(r, sl + k * p.lanes);
+                uint4 *dst = ahead + (turn * kUnits + k) * (4 * 256);
+                if (!un.in) continue;
+                norm_fetch(dst, gp + un.a);
+                norm_fetch(dst + 512, xp + un.a);
+                if (un.two) {
+                    norm_fetch(dst + 256, gp + un.b);
+                    norm_fetch(dst + 768, xp + un.b);
+                }
+            }
+        }
+        advance(next);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < kNormAhead; ++i) fetch(i);
+    int64_t pos = now.t < r.T ? r.positions[now.t] : -1;
+    int turn = 0;
     // (the same number of rounds for every group: shuffles take whole warps)
+#pragma unroll 1
     for (int64_t row0 = (int64_t)blockIdx.x * subs; row0 < rows; row0 += step) {
-        const int64_t row = row0 + sub;
-        const bool mine = row < rows;
-        const int64_t t = mine ? row / r.q_heads : 0;
-        const int h = mine ? (int)(row - t * r.q_heads) : 0;
-        const int64_t pos = mine ? r.positions[t] : -1;
-        const S *gp = static_cast<const S *>(r.q) + t * r.q_ts + h * r.q_hs;
-        const S *xp = static_cast<const S *>(p.x) + t * p.x_ts + h * p.x_hs;
-        S *dst = static_cast<S *>(r.out) + t * r.o_ts + h * r.o_hs;
-        Chunk ga[kUnits], gb[nb], xa[kUnits], xb[nb];
+        const bool mine = now.t < r.T;
+        struct {
+            int64_t pos;
+            int t, h;
+            Chunk ga[kUnits], gb[kUnits], xa[kUnits], xb[kUnits];
+        } cur;
+        cur.t = now.t;
+        cur.h = now.h;
+        cur.pos = pos;
+        advance(now);
+        if (now.t < r.T) pos = r.positions[now.t];
+        asm volatile("cp.async.wait_group %0;" ::"n"(kNormAhead - 1) : "memory");
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const Unit un(r, sl + k * p.lanes);
-            if (!un.in || !mine) continue;
-            ga[k].v = *reinterpret_cast<const uint4 *>(gp + un.a);
-            xa[k].v = *reinterpret_cast<const uint4 *>(xp + un.a);
-            if (kHalf && un.two) {
-                gb[kHalf ? k : 0].v = *reinterpret_cast<const uint4 *>(gp + un.b);
-                xb[kHalf ? k : 0].v = *reinterpret_cast<const uint4 *>(xp + un.b);
-            }
+            const uint4 *src = ahead + (turn * kUnits + k) * (4 * 256), none = make_uint4(0u, 0u, 0u, 0u);
+            const bool one = mine && un.in, two = one && un.two;
+            cur.ga[k].v = one ? src[0] : none;
+            cur.gb[k].v = two ? src[256] : none;
+            cur.xa[k].v = one ? src[512] : none;
+            cur.xb[k].v = two ? src[768] : none;
         }
-        const RopeToken tok = mine ? rope_token(r, pos, -1, sl == 0 && h == 0) : RopeToken{nullptr, -1};
-        float g[kUnits][vec], g2[nb][vec], ss = 0.f, dot = 0.f;
+        fetch(turn);   // into the place just read
+        turn = turn == kNormAhead - 1 ? 0 : turn + 1;
+        const RopeToken tok = mine ? rope_token(r, cur.pos, -1, sl == 0 && cur.h == 0) : RopeToken{nullptr, -1};
+        S *row = reinterpret_cast<S *>(norm_dw) + (size_t)sub * r.dim;
+        if (kPairs == kNormStaged) {
+            __syncwarp();   // the head before is read
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                const Unit un(r, sl + k * p.lanes);
+                if (un.in) *reinterpret_cast<uint4 *>(row + un.a) = cur.ga[k].v;
+                if (un.in && un.two) *reinterpret_cast<uint4 *>(row + un.b) = cur.gb[k].v;
+            }
+            __syncwarp();
+        }
+        float g[kUnits][vec], g2[kUnits][vec], ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const Unit un(r, sl + k * p.lanes);
             if (!un.in || !tok.row) continue;
-            float c[pairs], s[pairs];
-            if (un.whole > 0) norm_angles<pairs>(tok.row, r.rot, un.i0, -1.f, c, s);
-            const int kb = kHalf ? k : 0;
 #pragma unroll
             for (int e = 0; e < vec; ++e) {
-                g[k][e] = E::get(ga[k].e[e]);
-                if (kHalf && un.two) g2[kb][e] = E::get(gb[kb].e[e]);
+                g[k][e] = E::get(cur.ga[k].e[e]);
+                g2[k][e] = E::get(cur.gb[k].e[e]);
             }
-            norm_turn<E, kHalf>(g[k], g2[kb], c, s, un.whole);
+            if (kPairs == kNormStaged) {
+                const int half = r.rot >> 1;
+#pragma unroll
+                for (int e = 0; e < vec; ++e) {
+                    g[k][e] = norm_turn_staged<E>(row, tok.row, half, -1.f, un.a + e, g[k][e], nullptr, 0, 1.f);
+                    if (un.two) g2[k][e] = norm_turn_staged<E>(row, tok.row, half, -1.f, un.b + e, g2[k][e], nullptr, 0, 1.f);
+                }
+            } else if (un.whole > 0) {
+                float c[vec], s[vec];
+                norm_angles<vec>(tok.row, r.rot, un.i0, -1.f, c, s);
+                norm_turn<E, kPairs>(g[k], g2[k], c, s, un.whole);
+            }
 #pragma unroll
             for (int e = 0; e < vec; ++e) {
-                const float x = E::get(xa[k].e[e]);
-                ss = fmaf(x, x, ss);
-                dot = fmaf(g[k][e] * wa[k][e], x, dot);
-                if (kHalf && un.two) {
-                    const float x2 = E::get(xb[kb].e[e]);
-                    ss = fmaf(x2, x2, ss);
-                    dot = fmaf(g2[kb][e] * wb[kb][e], x2, dot);
-                }
+                const float x = E::get(cur.xa[k].e[e]), x2 = E::get(cur.xb[k].e[e]);
+                ss = fmaf(x2, x2, fmaf(x, x, ss));
+                dot = fmaf(g2[k][e] * wb[k][e], x2, fmaf(g[k][e] * wa[k][e], x, dot));
             }
         }
         ss = norm_sum(ss, p.lanes);
         dot = norm_sum(dot, p.lanes);
         const float rs = rsqrtf(fmaf(ss, inv_dim, p.eps)), back = rs * rs * rs * (dot * inv_dim);
+        S *dst = static_cast<S *>(r.out) + cur.t * r.o_ts + cur.h * r.o_hs;
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const Unit un(r, sl + k * p.lanes);
             if (!un.in || !mine) continue;
-            const int kb = kHalf ? k : 0;
             Chunk o;
             if (!tok.row) {
                 if (r.zero) {
                     o.v = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4 *>(dst + un.a) = o.v;
-                    if (kHalf && un.two) *reinterpret_cast<uint4 *>(dst + un.b) = o.v;
+                    if (un.two) *reinterpret_cast<uint4 *>(dst + un.b) = o.v;
                 }
                 continue;
             }
 #pragma unroll
             for (int e = 0; e < vec; ++e) {
-                const float x = E::get(xa[k].e[e]);
+                const float x = E::get(cur.xa[k].e[e]);
                 da[k][e] = fmaf(g[k][e], x * rs, da[k][e]);
                 o.e[e] = E::put(fmaf(-x, back, rs * (g[k][e] * wa[k][e])));
             }
             *reinterpret_cast<uint4 *>(dst + un.a) = o.v;
-            if (kHalf && un.two) {
+            if (un.two) {
 #pragma unroll
                 for (int e = 0; e < vec; ++e) {
-                    const float x = E::get(xb[kb].e[e]);
-                    db[kb][e] = fmaf(g2[kb][e], x * rs, db[kb][e]);
-                    o.e[e] = E::put(fmaf(-x, back, rs * (g2[kb][e] * wb[kb][e])));
+                    const float x = E::get(cur.xb[k].e[e]);
+                    db[k][e] = fmaf(g2[k][e], x * rs, db[k][e]);
+                    o.e[e] = E::put(fmaf(-x, back, rs * (g2[k][e] * wb[k][e])));
                 }
                 *reinterpret_cast<uint4 *>(dst + un.b) = o.v;
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!p.part) return;
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
         const Unit un(r, sl + k * p.lanes);
@@ -391,7 +502,7 @@ __global__ void __launch_bounds__(256) norm_back_vec_kernel(const __grid_constan
 #pragma unroll
         for (int e = 0; e < vec; ++e) {
             norm_dw[sub * r.dim + un.a + e] = da[k][e];
-            if (kHalf && un.two) norm_dw[sub * r.dim + un.b + e] = db[kHalf ? k : 0][e];
+            if (un.two) norm_dw[sub * r.dim + un.b + e] = db[k][e];
         }
     }
     __syncthreads();
@@ -415,9 +526,11 @@ __global__ void __launch_bounds__(256) norm_back_element_kernel(const __grid_con
     for (int i = lane; i < r.dim; i += 32) dw[i] = 0.f;
     __syncwarp();
     const int64_t rows = (int64_t)r.T * r.q_heads, step = (int64_t)gridDim.x * 8;
-    for (int64_t row = (int64_t)blockIdx.x * 8 + warp; row < rows; row += step) {
-        const int64_t t = row / r.q_heads;
-        const int h = (int)(row - t * r.q_heads);
+    const int dt = (int)(step / r.q_heads), dh = (int)(step - (int64_t)dt * r.q_heads);
+    int64_t t = ((int64_t)blockIdx.x * 8 + warp) / r.q_heads;
+    int h = (int)(((int64_t)blockIdx.x * 8 + warp) % r.q_heads);
+    for (int64_t row = (int64_t)blockIdx.x * 8 + warp; row < rows; row += step, t += dt + (h + dh >= r.q_heads),
+                 h += dh - (h + dh >= r.q_heads ? r.q_heads : 0)) {
         const S *gp = static_cast<const S *>(r.q) + t * r.q_ts + h * r.q_hs;
         const S *xp = static_cast<const S *>(p.x) + t * p.x_ts + h * p.x_hs;
         S *dst = static_cast<S *>(r.out) + t * r.o_ts + h * r.o_hs;
@@ -469,23 +582,24 @@ __global__ void __launch_bounds__(256) norm_back_element_kernel(const __grid_con
     }
 }
 
-// The weight's gradient from the CTAs' rows: 8 warps take every eighth row of
-// 32 columns, joined in order
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float *part, int rows, int dim, void *out, int dtype)
+// The weight's gradient from the CTAs' rows: 32 warps take every 32nd row of 32
+// columns, joined in order
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, int rows, int dim, void *out, int dtype)
 {
-    __shared__ float sums[8][32];
+    __shared__ float sums[32][32];
     if (threadIdx.x == 0) griddep_launch_dependents();
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < dim)
-#pragma unroll 8
-        for (int i = warp; i < rows; i += 8) v += part[(int64_t)i * dim + c];
+#pragma unroll 4
+        for (int i = warp; i < rows; i += 32) v += part[(int64_t)i * dim + c];
     sums[warp][lane] = v;
     __syncthreads();
     if (warp > 0 || c >= dim) return;
     v = 0.f;
-    for (int i = 0; i < 8; ++i) v += sums[i][lane];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += sums[i][lane];
     if (dtype == QKVF_DTYPE_FP32)
         static_cast<float *>(out)[c] = v;
     else
@@ -494,7 +608,24 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float *part, int row
 
 // ---- host -------------------------------------------------------------------
 
-constexpr int kNormBackCtas = 4;   // per SM
+template <class E, int kPairs>
+bool prepare_norm_kernel()
+{
+    constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    constexpr int smem = 16384 + kNormAhead * 4 * 256 * 16;
+    return cudaFuncSetAttribute((const void *)norm_back_vec_kernel<E, kPairs, 1>, attr, smem) == cudaSuccess &&
+           cudaFuncSetAttribute((const void *)norm_back_vec_kernel<E, kPairs, 2>, attr, smem + kNormAhead * 4 * 256 * 16) == cudaSuccess;
+}
+
+template <class E>
+bool prepare_norm_kernel()
+{
+    return prepare_norm_kernel<E, kNormInterleaved>() && prepare_norm_kernel<E, kNormHalf>() && prepare_norm_kernel<E, kNormStaged>();
+}
+
+bool prepare_norm_kernels() { return prepare_norm_kernel<Bf16>() && prepare_norm_kernel<Fp16>() && prepare_norm_kernel<Fp32>(); }
+
+constexpr int kNormBackCtas = 2;   // per SM
 
 int64_t norm_back_ctas(int64_t rows, int sms)
 {
@@ -512,22 +643,31 @@ int norm_lanes(NormParams &prm, int units)
     return (units + prm.lanes - 1) / prm.lanes;   // units of a lane
 }
 
-// Whether the 16-byte kernels take rows: whole chunks, also between partners
+// Whether the 16-byte kernels take rows
 template <class E>
-bool norm_whole(const NormParams &prm, bool half_layout)
+bool norm_whole(const NormParams &prm)
 {
     constexpr int vec = RopeChunk<E>::vec;
     const RopeParams &r = prm.r;
     const auto whole = [&](const void *ptr, int64_t ts, int64_t hs, int heads) {
         return heads == 0 || !ptr || (aligned(ptr, 16) && (r.T == 1 || ts % vec == 0) && (heads == 1 || hs % vec == 0));
     };
-    return r.dim % vec == 0 && !(half_layout && r.rot / 2 % vec) && whole(r.q, r.q_ts, r.q_hs, r.q_heads) &&
-           whole(r.out, r.o_ts, r.o_hs, r.q_heads) && whole(r.k, r.k_ts, r.k_hs, r.nkv) &&
-           whole(r.v, r.v_ts, r.v_hs, r.nkv) && whole(prm.x, prm.x_ts, prm.x_hs, r.q_heads) && aligned(prm.qw, 16) &&
-           aligned(prm.kw, 16);
+    return r.dim % vec == 0 && whole(r.q, r.q_ts, r.q_hs, r.q_heads) && whole(r.out, r.o_ts, r.o_hs, r.q_heads) &&
+           whole(r.k, r.k_ts, r.k_hs, r.nkv) && whole(r.v, r.v_ts, r.v_hs, r.nkv) && whole(prm.x, prm.x_ts, prm.x_hs, r.q_heads) &&
+           aligned(prm.qw, 16) && aligned(prm.kw, 16);
 }
 
-template <class E, bool kHalf, int kHeads, int kUnits>
+// How pairs lie, and the units of a head (two chunks each)
+template <class E>
+int norm_pairs(const NormParams &prm, bool half_layout, int *units)
+{
+    constexpr int vec = RopeChunk<E>::vec;
+    const int chunks = prm.r.dim / vec, h = half_layout && prm.r.rot / 2 % vec == 0 ? prm.r.rot / 2 / vec : 0;
+    *units = h + (chunks - 2 * h + 1) / 2;
+    return !half_layout ? kNormInterleaved : h ? kNormHalf : kNormStaged;
+}
+
+template <class E, int kPairs, int kHeads, int kUnits>
 int launch_norm_vec(NormParams &prm, void *stream)
 {
     RopeParams &r = prm.r;
@@ -541,39 +681,37 @@ int launch_norm_vec(NormParams &prm, void *stream)
     r.tokens = (int)(r.T < most ? r.T : most);
     const int64_t threads = (int64_t)r.tokens * r.groups * prm.lanes;
     const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)((r.T + r.tokens - 1) / r.tokens));
-    return launch_pdl(norm_vec_kernel<E, kHalf, kHeads, kUnits>, grid, dim3(256), 0, stream, prm);
+    return launch_pdl(norm_vec_kernel<E, kPairs, kHeads, kUnits>, grid, dim3(256), 0, stream, prm);
 }
 
-template <class E, bool kHalf>
-int launch_norm_layout(NormParams &prm, void *stream)
+template <class E, int kPairs>
+int launch_norm_pairs(NormParams &prm, int units, void *stream)
 {
-    const int units = (kHalf ? prm.r.dim - prm.r.rot / 2 : prm.r.dim) / RopeChunk<E>::vec;
-    const int per = norm_lanes(prm, units);
-    if (per == 1) return launch_norm_vec<E, kHalf, 4, 1>(prm, stream);
-    if (per == 2) return launch_norm_vec<E, kHalf, 2, 2>(prm, stream);
-    return launch_norm_vec<E, kHalf, 1, 4>(prm, stream);
+    return norm_lanes(prm, units) == 1 ? launch_norm_vec<E, kPairs, 2, 1>(prm, stream) : launch_norm_vec<E, kPairs, 1, 2>(prm, stream);
 }
 
 template <class E>
 int launch_norm(NormParams &prm, bool half_layout, int sms, void *stream)
 {
-    if (norm_whole<E>(prm, half_layout))
-        return half_layout ? launch_norm_layout<E, true>(prm, stream) : launch_norm_layout<E, false>(prm, stream);
+    if (norm_whole<E>(prm)) {
+        int units;
+        const int pairs = norm_pairs<E>(prm, half_layout, &units);
+        return pairs == kNormInterleaved ? launch_norm_pairs<E, kNormInterleaved>(prm, units, stream)
+               : pairs == kNormHalf      ? launch_norm_pairs<E, kNormHalf>(prm, units, stream)
+                                         : launch_norm_pairs<E, kNormStaged>(prm, units, stream);
+    }
     const int64_t most = (int64_t)sms * 8;
     return launch_pdl(norm_element_kernel<E>, dim3((unsigned)(prm.r.T < most ? prm.r.T : most)), dim3(256), 0, stream, prm,
                       (int)half_layout);
 }
 
-template <class E, bool kHalf>
-int launch_norm_back_layout(NormParams &prm, int64_t ctas, void *stream)
+template <class E, int kPairs>
+int launch_norm_back_pairs(NormParams &prm, int units, int64_t ctas, void *stream)
 {
-    const int units = (kHalf ? prm.r.dim - prm.r.rot / 2 : prm.r.dim) / RopeChunk<E>::vec;
     const int per = norm_lanes(prm, units);
-    const size_t smem = prm.part ? (size_t)(256 / prm.lanes) * prm.r.dim * 4 : 0;   // 32 KB at most (fp32 chunks: 16)
-    return launch_pdl(per == 1   ? norm_back_vec_kernel<E, kHalf, 1>
-                      : per == 2 ? norm_back_vec_kernel<E, kHalf, 2>
-                                 : norm_back_vec_kernel<E, kHalf, 4>,
-                      dim3((unsigned)ctas), dim3(256), smem, stream, prm);
+    const size_t smem = (size_t)(256 / prm.lanes) * prm.r.dim * 4 + (size_t)kNormAhead * per * 4 * 256 * 16;   // 16 KB at most, and 64 a unit
+    return launch_pdl(per == 1 ? norm_back_vec_kernel<E, kPairs, 1> : norm_back_vec_kernel<E, kPairs, 2>, dim3((unsigned)ctas),
+                      dim3(256), smem, stream, prm);
 }
 
 template <class E>
@@ -581,13 +719,18 @@ int launch_norm_back(NormParams &prm, bool half_layout, int sms, void *grad_weig
 {
     const int64_t ctas = norm_back_ctas((int64_t)prm.r.T * prm.r.q_heads, sms);
     int rc;
-    if (norm_whole<E>(prm, half_layout))
-        rc = half_layout ? launch_norm_back_layout<E, true>(prm, ctas, stream) : launch_norm_back_layout<E, false>(prm, ctas, stream);
-    else
+    if (norm_whole<E>(prm)) {
+        int units;
+        const int pairs = norm_pairs<E>(prm, half_layout, &units);
+        rc = pairs == kNormInterleaved ? launch_norm_back_pairs<E, kNormInterleaved>(prm, units, ctas, stream)
+             : pairs == kNormHalf      ? launch_norm_back_pairs<E, kNormHalf>(prm, units, ctas, stream)
+                                       : launch_norm_back_pairs<E, kNormStaged>(prm, units, ctas, stream);
+    } else {
         rc = launch_pdl(norm_back_element_kernel<E>, dim3((unsigned)ctas), dim3(256), (size_t)8 * prm.r.dim * 4, stream, prm,
                         (int)half_layout);
+    }
     if (rc != QKVF_OK || !grad_weight) return rc;
-    return launch_pdl(norm_dw_kernel, dim3((unsigned)((prm.r.dim + 31) / 32)), dim3(256), 0, stream,
+    return launch_pdl(norm_dw_kernel, dim3((unsigned)((prm.r.dim + 31) / 32)), dim3(1024), 0, stream,
                       (const float *)prm.part, (int)ctas, prm.r.dim, grad_weight, grad_weight_dtype);
 }
 
@@ -800,7 +943,7 @@ int norm_rope_backward(const void *grad_out, int64_t grad_token_stride, int64_t 
     const int rc = qkvf::probe_device(&d);
     if (rc != QKVF_OK) return rc;
     if (T == 0)   // no token: a gradient of zeros
-        return qkvf::launch_pdl(qkvf::norm_dw_kernel, dim3((unsigned)((head_dim + 31) / 32)), dim3(256), 0, stream,
+        return qkvf::launch_pdl(qkvf::norm_dw_kernel, dim3((unsigned)((head_dim + 31) / 32)), dim3(1024), 0, stream,
                                 (const float *)nullptr, 0, head_dim, grad_weight, grad_weight_dtype);
     if (grad_weight && workspace_bytes < qkvf::norm_back_workspace(T, heads, head_dim, d->sms)) return QKVF_ERR_SIZES;
     qkvf::NormParams prm = {};

@@ -1172,6 +1172,7 @@ bool prepare_attn2_kernel();
 bool prepare_prefix_kernels();
 bool prepare_chunk_kernels();
 bool prepare_key_kernels();
+bool prepare_norm_kernels();
 
 int probe_device(DeviceState **out)
 {
@@ -1215,7 +1216,7 @@ int probe_device(DeviceState **out)
                                      (int)res_smem_bytes(i ? 16 : 8)) != cudaSuccess)
                 return QKVF_ERR_CUDA;
         if (!prepare_epi_kernel() || !prepare_attn2_kernel() || !prepare_prefix_kernels() || !prepare_chunk_kernels() ||
-            !prepare_key_kernels())
+            !prepare_key_kernels() || !prepare_norm_kernels())
             return QKVF_ERR_CUDA;
         d.prepared = true;
     }

@@ -1030,10 +1030,9 @@ class _NormRotation(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         x, weight, positions, cos_sin = ctx.saved_tensors
-        with torch.cuda.device(x.device):
-            if torch.cuda.is_current_stream_capturing():
-                raise ValueError("the backward pass of an autograd graph is not captured: capture "
-                                 "norm_rope_backward under torch.no_grad()")
+        if torch._C._cuda_isCurrentStreamCapturing():   # (the engine has made x's device and stream current)
+            raise ValueError("the backward pass of an autograd graph is not captured: capture "
+                             "norm_rope_backward under torch.no_grad()")
         if grad.stride(-1) != 1:   # the gradient of a sum, say: one value, expanded
             grad = grad.contiguous()
         eps, layout = ctx.how
@@ -1051,13 +1050,15 @@ def _norm_rope_with_grad(x, weight, positions, cos_sin, out, eps, layout, stream
                          "leave out None, or call under torch.no_grad() (its gradient is norm_rope_backward)")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=x.device)
-    with torch.cuda.device(x.device), torch.cuda.stream(stream):   # backward runs where forward did
-        if torch.cuda.is_current_stream_capturing():
-            raise ValueError("a captured call is not part of the autograd graph, but x or weight requires a "
-                             "gradient: capture norm_rope and norm_rope_backward under torch.no_grad()")
-        return _NormRotation.apply(x, weight, positions, cos_sin, eps, layout)
+    if stream is not None or x.get_device() != torch._C._cuda_getDevice():
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+        with torch.cuda.device(x.device), torch.cuda.stream(stream):   # backward runs where forward did
+            return _norm_rope_with_grad(x, weight, positions, cos_sin, None, eps, layout, None)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        raise ValueError("a captured call is not part of the autograd graph, but x or weight requires a "
+                         "gradient: capture norm_rope and norm_rope_backward under torch.no_grad()")
+    return _NormRotation.apply(x, weight, positions, cos_sin, eps, layout)
 
 
 def _norm_rope(x, weight, positions, cos_sin, out, eps, layout, stream):
@@ -1130,8 +1131,12 @@ def norm_rope_backward(grad_out, x, weight, positions, cos_sin, eps: float = 1e-
         if grad_weight is None:
             grad_weight = _new(weight.shape, torch.float32, x.device, stream)
         if workspace is None and x.is_cuda and x.dim() == 3:
-            with torch.cuda.device(x.device):
-                n = norm_rope_backward_workspace_bytes(*(min(d, _MOST) for d in x.shape))
+            T, heads, dim = x.shape
+            if x.get_device() == torch._C._cuda_getDevice():
+                n = norm_rope_backward_workspace_bytes(min(T, _MOST), min(heads, _MOST), min(dim, _MOST))
+            else:
+                with torch.cuda.device(x.device):
+                    n = norm_rope_backward_workspace_bytes(min(T, _MOST), min(heads, _MOST), min(dim, _MOST))
             workspace = _new((n,), torch.uint8, x.device, stream)
     args = _norm_back_args(grad_out, x, weight, positions, cos_sin, grad_x, grad_weight, workspace, eps, layout, flags)
     _run("norm_rope_backward", x.get_device(), args, stream)
