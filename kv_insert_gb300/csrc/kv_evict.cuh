@@ -6,16 +6,22 @@
 // recent of largest weight, the lower index first among equals; kept keys keep
 // their order.  Two kernels:
 //  * evict_select_kernel, a CTA per (request, KV head): the smallest kept
-//    weight by three passes over its bits (11, 11 and 10 at a time, a histogram
-//    each), then one ordered pass that numbers the kept keys and moves their
-//    weights.
+//    weight by up to four passes over its bits (8, 11, 11 and 2 at a time, a
+//    histogram each; no more once the digits found are taken whole), then one
+//    ordered pass that numbers the kept keys and moves their weights.  A row's
+//    weights are read once, into shared memory (the first 18,432 of them).
+//    What bounds it is one CTA's instructions and barriers (64 rows of 9,000 to
+//    16,384 keys, 2,048 kept: 15 us, of them 3 to load, 2.7 a pass and 4 for the
+//    numbering; the weights read from memory in every pass: 19).
 //  * evict_move_kernel copies K | V slots.  Into other pages every slot is on
 //    its own; in place a kept key only ever moves down, so a CTA takes some
 //    columns of all slots and reads each round of slots before it writes them.
 
 namespace qkvf {
 
-constexpr int kEvThreads = 1024, kEvEach = 4, kEvBins = 2048;
+constexpr int kEvThreads = 1024, kEvBins = 2048;
+constexpr int kEvFirst = 256;      // bins of the first pass, 32 copies of each
+constexpr int kEvCached = 18432;   // weights of a row kept in shared memory (72 KB beside 32 KB of bins: two CTAs an SM)
 constexpr int kEvMaxKeep = 1 << 24;
 
 struct EvictParams {
@@ -32,140 +38,207 @@ struct EvictParams {
     int in_place;
 };
 
-// Weights in the order of unsigned numbers: -0 is 0, NaN above everything
+// Weights in the order of unsigned numbers: -0 is 0 (the sum), and NaN, which a
+// sum makes 0x7fffffff, above everything
 __device__ __forceinline__ uint32_t ev_key(float w)
 {
-    const uint32_t u = __float_as_uint(w + 0.f);
-    if (w != w) return 0xffffffffu;
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+    const uint32_t u = __float_as_uint(__fadd_rn(w, 0.f));
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// Inclusive sum over the block's threads before and with this one; total: of all
-__device__ __forceinline__ uint64_t ev_scan(uint64_t v, uint64_t *warp_sums, uint64_t &total)
+// Where chunk c of four weights lies in shared memory: neither neighbours nor
+// chunks at a distance of 2 or 4 meet in a bank
+__device__ __forceinline__ int ev_chunk(int c) { return c ^ ((c >> 3) & 3); }
+
+// Sum over the warp's lanes up to this one
+__device__ __forceinline__ uint32_t ev_scan(uint32_t v)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
     }
-    __syncthreads();   // the sums of the scan before are read
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        uint64_t s = warp_sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        warp_sums[lane] = s;
-    }
-    __syncthreads();
-    total = warp_sums[31];
-    return v + (warp ? warp_sums[warp - 1] : 0);
+    return v;
 }
+
+// One more at `bin` (an address in shared memory) where `on`
+__device__ __forceinline__ void ev_count(uint32_t bin, bool on)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p red.shared.add.u32 [%0], 1;\n}" ::"r"(bin), "r"((uint32_t)on)
+                 : "memory");
+}
+
+extern __shared__ __align__(16) float ev_weights[];
 
 __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_constant__ EvictParams p)
 {
-    __shared__ uint32_t bins[kEvBins];
-    __shared__ uint64_t warp_sums[32];
-    __shared__ uint32_t found[2];   // the digit, and the keys of higher digits
-    __shared__ int bad;
+    __shared__ uint32_t bins[kEvFirst * 32];
+    __shared__ uint32_t warp_sums[2][32];   // a barrier apart: the next sums take the other row
+    __shared__ uint32_t found[2][3];        // the digit, the keys above it, whether it is taken whole
     if (threadIdx.x == 0) griddep_launch_dependents();
+    for (int i = threadIdx.x; i < kEvFirst * 32; i += kEvThreads) bins[i] = 0u;
     griddep_wait();
-    const int r = blockIdx.x / p.nkv, g = blockIdx.x % p.nkv, tid = threadIdx.x;
+    const int r = blockIdx.x / p.nkv, g = blockIdx.x % p.nkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x;
     const float *w = p.weights + row * p.max_blocks * kPageSlots;
     float *ow = p.out_weights + row * p.out_blocks * kPageSlots;
     int32_t *kept = p.kept + row * p.keep;
     const int L = p.context_lens[r], n = min(L, p.keep);
+    bool bad = L > p.max_blocks * kPageSlots;
+    const int cached = bad ? 0 : min(max(L, 0), kEvCached);
+    const uint32_t cache = smem_u32(ev_weights), bins0 = smem_u32(bins);
+    if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {   // (a row's end is a multiple of 16 bytes as well)
+        for (int c = tid; c * 4 < cached; c += kEvThreads)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(cache + ev_chunk(c) * 16), "l"(w + c * 4) : "memory");
+    } else {
+        for (int j = tid; j < cached; j += kEvThreads)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(cache + ev_chunk(j >> 2) * 16 + (j & 3) * 4), "l"(w + j)
+                         : "memory");
+    }
     // a page outside the cache leaves the request alone, in every KV head
-    if (tid == 0) bad = L > p.max_blocks * kPageSlots;
-    __syncthreads();
     if (L > 0 && !bad) {
         const int32_t *from = p.block_table + (int64_t)r * p.max_blocks, *to = p.out_table + (int64_t)r * p.out_blocks;
-        bool out = false;
-        for (int i = tid; i < (L + kPageSlots - 1) / kPageSlots; i += kEvThreads) out |= from[i] < 0 || from[i] >= p.num_pages;
-        for (int i = tid; i < (n + kPageSlots - 1) / kPageSlots; i += kEvThreads) out |= to[i] < 0 || to[i] >= p.num_pages;
-        if (out) bad = 1;
+        for (int i = tid; i < (L + kPageSlots - 1) / kPageSlots; i += kEvThreads) bad |= from[i] < 0 || from[i] >= p.num_pages;
+        for (int i = tid; i < (n + kPageSlots - 1) / kPageSlots; i += kEvThreads) bad |= to[i] < 0 || to[i] >= p.num_pages;
     }
-    __syncthreads();
-    if (bad || L < 0) {
-        if (bad && tid == 0 && g == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (__syncthreads_or(bad) || L < 0) {
+        if (L >= 0 && tid == 0 && g == 0) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
         for (int i = tid; i < p.keep; i += kEvThreads) kept[i] = -1;
         return;
     }
+    // weights 4 c .. 4 c + 3 (those from L on are anything)
+    const auto four = [&](int c, float (&v)[4]) {
+        if (c * 4 < cached) {
+            const float4 x = *reinterpret_cast<const float4 *>(ev_weights + ev_chunk(c) * 4);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = c * 4 + e < L ? w[c * 4 + e] : 0.f;
+        }
+    };
     for (int i = n + tid; i < p.keep; i += kEvThreads) kept[i] = -1;
     // the keys to choose from, and how many of them
     const int old = L - min(p.recent, L), take = n - (L - old);
     uint32_t prefix = 0u, mask = 0u;
-    int above = 0;   // keys of larger weight than `prefix` so far
-    if (take < old) {
+    int above = 0, turn = 0;   // keys of larger weight than `prefix` so far
+    if (take == 0) {           // none: more than any weight, and no equal of it taken
+        prefix = mask = 0xffffffffu;
+    } else if (take < old) {
 #pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 1024 : 2048;
-            for (int i = tid; i < width; i += kEvThreads) bins[i] = 0u;
-            __syncthreads();
-            for (int j = tid; j < old; j += kEvThreads) {
-                const uint32_t k = ev_key(w[j]);
-                if ((k & mask) == prefix) atomicAdd(&bins[(k >> shift) & (width - 1)], 1u);
+        for (int pass = 0, shift = 24; pass < 4; ++pass, turn ^= 1) {
+            // the first digit is mostly the same: a lane has its own copy of the bins (sums of one address take turns)
+            const int bits = pass == 0 ? 8 : pass < 3 ? 11 : 2, copies = pass == 0 ? 5 : 0;
+            if (pass > 0) shift -= bits;
+            const int turned = shift - copies - 2;   // to where a bin's address has the digit
+            const uint32_t bin0 = bins0 + (pass == 0 ? lane * 4 : 0), digits = ((1u << bits) - 1u) << (copies + 2);
+            for (int c = tid; c * 4 < old; c += kEvThreads) {
+                float v[4];
+                four(c, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t k = ev_key(v[e]);
+                    ev_count(bin0 + (__funnelshift_r(k, k, turned) & digits), c * 4 + e < old && (k & mask) == prefix);
+                }
             }
             __syncthreads();
-            // from the largest digit down: where the number to take is reached
-            const int per = width / kEvThreads, top = width - 1 - tid * per;
-            uint32_t c0 = bins[top], c1 = per == 2 ? bins[top - 1] : 0u;
-            uint64_t total;
-            const uint32_t upto = above + (uint32_t)ev_scan(c0 + c1, warp_sums, total), before = upto - c0 - c1;
-            if ((int)before < take && take <= (int)upto) {
-                const bool second = (int)(before + c0) < take;
-                found[0] = second ? top - 1 : top;
-                found[1] = second ? before + c0 : before;
+            // from the largest digit down, two a thread: where the number to take is reached
+            int top;
+            uint32_t c0 = 0u, c1 = 0u;
+            if (pass == 0) {   // four threads a digit, the first of them holds its count
+                top = kEvFirst - 1 - tid / 4;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t &bin = bins[top * 32 + (tid & 3) * 8 + ((i + tid / 4) & 7)];
+                    c0 += bin;
+                    bin = 0u;
+                }
+                c0 += __shfl_xor_sync(0xffffffffu, c0, 1);
+                c0 += __shfl_xor_sync(0xffffffffu, c0, 2);
+                if (tid & 3) c0 = 0u;
+            } else {
+                top = kEvBins - 1 - 2 * tid;
+                c0 = bins[top], c1 = bins[top - 1];
+                bins[top] = bins[top - 1] = 0u;
             }
-            if (take == 0 && tid == 0) {   // none of them: above every digit
-                found[0] = width - 1;
-                found[1] = 0;
+            const uint32_t all = __reduce_add_sync(0xffffffffu, c0 + c1);
+            if (lane == 0) warp_sums[turn][warp] = all;
+            __syncthreads();
+            const uint32_t lower = above + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[turn][lane] : 0u);
+            if ((int)lower < take && take <= (int)(lower + all)) {   // one warp has it
+                const uint32_t upto = lower + ev_scan(c0 + c1), before = upto - c0 - c1;
+                if ((int)before < take && take <= (int)upto) {
+                    const bool second = (int)(before + c0) < take;
+                    found[turn][0] = second ? top - 1 : top;
+                    found[turn][1] = second ? before + c0 : before;
+                    found[turn][2] = take == (int)(second ? upto : before + c0);
+                }
             }
             __syncthreads();
-            prefix |= found[0] << shift;
-            mask |= (uint32_t)(width - 1) << shift;
-            above = (int)found[1];
-            __syncthreads();
+            prefix |= found[turn][0] << shift;
+            mask |= ((1u << bits) - 1u) << shift;
+            above = (int)found[turn][1];
+            if (found[turn][2]) break;   // every key of these digits stays: the others do not matter
         }
+        turn ^= 1;
     }
-    const int ties = take - above;   // of weight `prefix` itself, in order
+    const int ties = take - above;   // of the digits of `prefix`, in order
     const bool all = take >= old;
     if (!(all && p.in_place)) {
-        uint64_t base = 0;   // kept for their weight or age in the high half, ties in the low one
-        for (int j0 = 0; j0 < L; j0 += kEvThreads * kEvEach) {
-            const int j = j0 + tid * kEvEach;
-            float v[kEvEach];
-            uint64_t mine = 0;
-            uint32_t kind[kEvEach];
+        // a thread takes neighbouring keys, up to 16 of them a round, and lists
+        // the kept ones in shared memory: written from the threads themselves,
+        // 16 stores of a few lanes each, the round took a fifth longer
+        uint16_t *list = reinterpret_cast<uint16_t *>(bins);
+        const int each = min(4, (L + kEvThreads * 4 - 1) / (kEvThreads * 4));
+        int sure = 0, equal = 0;   // kept for their weight or age, and ties, before this round
+        for (int j0 = 0; j0 < L; j0 += kEvThreads * 4 * each, turn ^= 1) {
+            const int own = tid * 4 * each, j = j0 + own;
+            uint32_t yes = 0u, maybe = 0u;
+#pragma unroll 1
+            for (int i = 0; i < each && j + i * 4 < L; ++i) {
+                float v[4];
+                four(j / 4 + i, v);
 #pragma unroll
-            for (int e = 0; e < kEvEach; ++e) {
-                v[e] = j + e < L ? w[j + e] : 0.f;
-                kind[e] = 0;
-                if (j + e < L) {
-                    const uint32_t k = ev_key(v[e]);
-                    kind[e] = all || j + e >= old || k > prefix ? 2 : k == prefix ? 1 : 0;
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t k = ev_key(v[e]) & mask, bit = 1u << e << (i * 4);
+                    if (all || j + i * 4 + e >= old || k > prefix) yes |= bit;
+                    if (k == prefix) maybe |= bit;
                 }
-                mine += kind[e] == 2 ? uint64_t(1) << 32 : kind[e];
             }
-            uint64_t total;
-            uint64_t at = base + ev_scan(mine, warp_sums, total) - mine;   // (and every weight of the round is read)
-#pragma unroll
-            for (int e = 0; e < kEvEach; ++e) {
-                const int tied = (int)(uint32_t)at;
-                const bool keep = kind[e] == 2 || (kind[e] == 1 && tied < ties);
-                if (keep) {
-                    const int dst = (int)(at >> 32) + min(tied, ties);
-                    kept[dst] = j + e;
-                    ow[dst] = v[e];
+            const uint32_t in = L - j >= 16 ? 0xffffu : (1u << max(L - j, 0)) - 1u;
+            yes &= in;
+            maybe &= in & ~yes;
+            const uint32_t mine = ((uint32_t)__popc(yes) << 16) + __popc(maybe);   // (at most 16384 of a kind in a round)
+            const uint32_t upto = ev_scan(mine);
+            if (lane == 31) warp_sums[turn][warp] = upto;
+            __syncthreads();
+            const uint32_t others = warp_sums[turn][lane];
+            const uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? others : 0u) + upto - mine;
+            const uint32_t total = __reduce_add_sync(0xffffffffu, others);
+            const int before = min(equal, ties);   // ties kept before this round
+            int t = equal + (int)(at & 0xffffu), dst = (int)(at >> 16) + min(t, ties) - before;
+            for (uint32_t m = yes | maybe; m; m &= m - 1u) {
+                const int e = __ffs(m) - 1;
+                const bool tie = maybe >> e & 1u;
+                if (!tie || t < ties) list[dst++] = (uint16_t)(own + e);
+                t += tie;
+            }
+            __syncthreads();
+            const int base = sure + before;
+            equal += (int)(total & 0xffffu);
+            sure += (int)(total >> 16);
+            const int count = sure + min(equal, ties) - base;
+            for (int i0 = 0; i0 < count; i0 += kEvThreads) {
+                const int i = i0 + tid, src = i < count ? j0 + list[i] : 0;
+                float v = 0.f;
+                if (i < count) v = src < cached ? ev_weights[ev_chunk(src >> 2) * 4 + (src & 3)] : w[src];
+                __syncthreads();   // in place a kept key only ever moves down: what is written now is read
+                if (i < count) {
+                    kept[base + i] = src;
+                    ow[base + i] = v;
                 }
-                at += kind[e] == 2 ? uint64_t(1) << 32 : kind[e];
             }
-            base += total;
         }
     } else {
         for (int i = tid; i < n; i += kEvThreads) kept[i] = i;
@@ -220,6 +293,12 @@ __global__ void __launch_bounds__(kEvMoveThreads) evict_move_kernel(const __grid
         for (int e = 0; e < kEvMoveEach; ++e)
             if (src[e] >= 0) ev_slot(p, to, g, (int)(b + e * per + i0))[c] = v[e];
     }
+}
+
+bool prepare_evict_kernel()
+{
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvCached * (int)sizeof(float)) ==
+           cudaSuccess;
 }
 
 const char *check_evict_args(const void *kv_cache, int64_t num_pages, const float *weights, const int32_t *block_table,
@@ -320,7 +399,9 @@ int kv_evict(void *kv_cache, int64_t num_pages, const float *weights, const int3
     prm.recent = recent;
     prm.in_place = out_table == block_table;
     const int64_t rows = (int64_t)num_reqs * num_kv_heads;
-    rc = qkvf::launch_pdl(qkvf::evict_select_kernel, dim3((unsigned)rows), dim3(qkvf::kEvThreads), 0, stream, prm);
+    const int64_t cached = (int64_t)max_blocks * qkvf::kPageSlots;
+    rc = qkvf::launch_pdl(qkvf::evict_select_kernel, dim3((unsigned)rows), dim3(qkvf::kEvThreads),
+                          (cached < qkvf::kEvCached ? cached : qkvf::kEvCached) * sizeof(float), stream, prm);
     if (rc != QKVF_OK) return rc;
     const int chunks = head_dim / 4, step = qkvf::kEvMoveThreads / chunks * qkvf::kEvMoveEach;
     const int x = prm.in_place ? (chunks + qkvf::kEvSlice - 1) / qkvf::kEvSlice : (keep + step - 1) / step;

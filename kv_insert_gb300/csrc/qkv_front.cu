@@ -1173,6 +1173,7 @@ bool prepare_prefix_kernels();
 bool prepare_chunk_kernels();
 bool prepare_key_kernels();
 bool prepare_norm_kernels();
+bool prepare_evict_kernel();
 
 int probe_device(DeviceState **out)
 {
@@ -1216,7 +1217,7 @@ int probe_device(DeviceState **out)
                                      (int)res_smem_bytes(i ? 16 : 8)) != cudaSuccess)
                 return QKVF_ERR_CUDA;
         if (!prepare_epi_kernel() || !prepare_attn2_kernel() || !prepare_prefix_kernels() || !prepare_chunk_kernels() ||
-            !prepare_key_kernels() || !prepare_norm_kernels())
+            !prepare_key_kernels() || !prepare_norm_kernels() || !prepare_evict_kernel())
             return QKVF_ERR_CUDA;
         d.prepared = true;
     }
