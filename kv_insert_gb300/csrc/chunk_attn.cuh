@@ -254,6 +254,19 @@ __device__ __forceinline__ void ch_load16(uint32_t addr, uint32_t (&a)[16])
         : "memory");
 }
 
+__device__ __forceinline__ void ch_load32(uint32_t addr, uint32_t (&a)[32])
+{
+    asm volatile(
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        "}\n"
+        : CH_REGS16(a, 0), CH_REGS16(a, 16)
+        : "r"(addr)
+        : "memory");
+}
+
 // pa_wait in few instructions: the kernel's code has to stay in the instruction
 // cache (below)
 __device__ __forceinline__ void ch_wait(uint32_t bar, uint32_t parity, volatile int *dead, unsigned long long limit_ns, bool honour)

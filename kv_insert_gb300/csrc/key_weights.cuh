@@ -104,13 +104,17 @@ __device__ __forceinline__ ChRequest kw_request(const RaggedParams &p, int b, in
     return q;
 }
 
-__device__ __forceinline__ KwItem kw_next(const KeyParams &kp, ChPos &at, const ChPos &end)
+// (q: the request of number qr, kept from one item to the next)
+__device__ __forceinline__ KwItem kw_next(const KeyParams &kp, ChPos &at, const ChPos &end, ChRequest &q, int &qr)
 {
     const RaggedParams &p = kp.r;
     KwItem it = {};
     it.n = -1;
     while (!ch_reached(at, end)) {
-        const ChRequest q = kw_request(p, ch_uniform(p.starts[at.r]), ch_uniform(p.starts[at.r + 1]), ch_uniform(p.context_lens[at.r]), false);
+        if (at.r != qr) {
+            qr = at.r;
+            q = kw_request(p, ch_uniform(p.starts[at.r]), ch_uniform(p.starts[at.r + 1]), ch_uniform(p.context_lens[at.r]), false);
+        }
         if (q.n < 0 || q.L <= 0) {
             at = {at.r + 1, 0, 0, 0};
             continue;
@@ -193,55 +197,72 @@ struct KwTile {
     __device__ __forceinline__ int token(const KwItem &it, int step) const { return it.first + (it.k + step) * kp.tokens; }
 
     // ---- the keys of every item, and the items ----
+    // Hands item seq out and copies its keys; false at the end
+    __device__ __forceinline__ bool copy(int seq, const KwItem &it, int pages, int page, int &t, bool &ok, bool &bad_any) const
+    {
+        const RaggedParams &p = kp.r;
+        if (seq >= kKwItems) wait(LY.iempty + 8 * (seq % kKwItems), seq / kKwItems - 1, false);
+        __syncwarp();
+        if (lane == 0) {
+            *place(seq) = it;
+            mbar_arrive(sb + LY.ifull + 8 * (seq % kKwItems));
+        }
+        __syncwarp();
+        if (it.n < 0) return false;
+        bool bad = false;
+        if (lane < pages && (page < 0 || page >= p.num_pages)) {   // flagged, page 0 in its place
+            bad = true;
+            page = 0;
+        }
+        if (__any_sync(0xffffffffu, bad)) {   // seen before the item's end
+            bad_any = true;
+            *reinterpret_cast<volatile int *>(&place(seq)->bad) = 1;
+            __syncwarp();
+        }
+        const int box = page * p.nkv + it.g;
+#pragma unroll 1
+        for (int half = 0; half * kChPages < pages; ++half, ++t) {
+            const int n = min(kChPages, pages - half * kChPages), st = t % Sh::tiles;
+            if (ok && t >= Sh::tiles) wait(LY.kempty + 8 * st, t / Sh::tiles - 1);
+            __syncwarp();
+            ok = ok && !__any_sync(0xffffffffu, dead());
+            if (!ok) break;
+            const uint32_t bar = sb + LY.kfull + 8 * st;
+            int c4[kChPages];   // (all of them first: one at a time each waits for the one before)
+#pragma unroll
+            for (int i = 0; i < kChPages; ++i) c4[i] = ch_uniform(lane == half * kChPages + i ? box : INT_MIN);
+            if (pa_elect()) {
+                mbar_expect_tx(bar, (uint32_t)n * Sh::page_bytes);
+#pragma unroll
+                for (int i = 0; i < kChPages; ++i)
+                    if (i < n) ch_load_page(sb + LY.keys + st * Sh::tile_bytes + i * Sh::page_bytes, key_map, bar, 0, c4[i]);
+            }
+            __syncwarp();
+        }
+        return true;
+    }
+
     __device__ __forceinline__ void produce_keys(ChPos at, const ChPos &end) const
     {
         const RaggedParams &p = kp.r;
         if (lane == 0) tma_prefetch_map(key_map);
         int t = 0;   // tiles so far
         bool ok = true, bad_any = false;
+        // an item and its pages are looked up while the one before is copied
+        // (a chain of two reads from memory, longer than the copy's issue)
+        ChRequest q = {};
+        int qr = -1, pages = 0, page = 0;
+        KwItem it = {};
 #pragma unroll 1
-        for (int seq = 0;; ++seq) {
-            const KwItem it = kw_next(kp, at, end);
-            if (seq >= kKwItems) wait(LY.iempty + 8 * (seq % kKwItems), seq / kKwItems - 1, false);
-            __syncwarp();
-            if (lane == 0) {
-                *place(seq) = it;
-                mbar_arrive(sb + LY.ifull + 8 * (seq % kKwItems));
-            }
-            __syncwarp();
-            if (it.n < 0) break;
-            if (it.n == 0) continue;
-            const int32_t *table = p.block_table + (int64_t)it.r * p.max_blocks;
-            const int pg0 = it.b * (kKwKeys / kPageSlots), pages = min(2 * kChPages, (it.L + kPageSlots - 1) / kPageSlots - pg0);
-            int page = lane < pages ? table[pg0 + lane] : 0;
-            bool bad = false;
-            if (lane < pages && (page < 0 || page >= p.num_pages)) {   // flagged, page 0 in its place
-                bad = true;
-                page = 0;
-            }
-            if (__any_sync(0xffffffffu, bad)) {   // seen before the item's end
-                bad_any = true;
-                *reinterpret_cast<volatile int *>(&place(seq)->bad) = 1;
-                __syncwarp();
-            }
-            const int box = page * p.nkv + it.g;
-#pragma unroll 1
-            for (int half = 0; half < 2 && half * kChPages < pages; ++half, ++t) {
-                const int n = min(kChPages, pages - half * kChPages), st = t % Sh::tiles;
-                if (ok && t >= Sh::tiles) wait(LY.kempty + 8 * st, t / Sh::tiles - 1);
-                __syncwarp();
-                ok = ok && !__any_sync(0xffffffffu, dead());
-                if (!ok) break;
-                const uint32_t bar = sb + LY.kfull + 8 * st;
-                if (pa_elect()) mbar_expect_tx(bar, (uint32_t)n * Sh::page_bytes);
-                __syncwarp();
-#pragma unroll 1
-                for (int i = 0; i < n; ++i) {
-                    const int c4 = ch_uniform(lane == half * kChPages + i ? box : INT_MIN);
-                    if (pa_elect()) ch_load_page(sb + LY.keys + st * Sh::tile_bytes + i * Sh::page_bytes, key_map, bar, 0, c4);
-                }
-                __syncwarp();
-            }
+        for (int seq = -1;; ++seq) {
+            const KwItem next = kw_next(kp, at, end, q, qr);
+            const int pg0 = next.b * (kKwKeys / kPageSlots);
+            const int next_pages = next.n > 0 ? min(2 * kChPages, (next.L + kPageSlots - 1) / kPageSlots - pg0) : 0;
+            const int next_page = lane < next_pages ? p.block_table[(int64_t)next.r * p.max_blocks + pg0 + lane] : 0;
+            if (seq >= 0 && !copy(seq, it, pages, page, t, ok, bad_any)) break;
+            it = next;
+            pages = next_pages;
+            page = next_page;
         }
         if (lane == 0) {
             if (bad_any) atomicOr(&g_status, QKVF_STATUS_BAD_REQUEST);
@@ -345,6 +366,39 @@ struct KwTile {
         __syncwarp();
     }
 
+    // The weights of rows from c on, of one key: added up (all 32 of them, or of 16 those from..rows - 1: the
+    // choice row by row costs more than the weights)
+    template <bool all>
+    __device__ __forceinline__ float weigh_rows(uint32_t aS, const float *lse, int c, int from, int rows, uint64_t scale2) const
+    {
+        const uint64_t log2e = f2_pack(1.4426950408889634f, 1.4426950408889634f);
+        constexpr int count = all ? 32 : 16;
+        uint32_t x[count];
+        if constexpr (all)
+            ch_load32(aS + c, x);
+        else
+            ch_load16(aS + c, x);
+        uint64_t acc[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < count; e += 4) {
+            const float4 z = *reinterpret_cast<const float4 *>(lse + c + e);
+            float y[4];
+            // the difference first: near 0 the weight then has all of its bits
+            f2_unpack(f2_mul(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, f2_pack(z.x, z.y)), log2e), y[0], y[1]);
+            f2_unpack(f2_mul(f2_fma(f2_pack(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), scale2, f2_pack(z.z, z.w)), log2e), y[2], y[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[i] = a2_ex2(y[i]);
+                if (!all && (c + e + i < from || c + e + i >= rows)) y[i] = 0.f;
+            }
+            acc[0] = f2_add(acc[0], f2_pack(y[0], y[1]));
+            acc[1] = f2_add(acc[1], f2_pack(y[2], y[3]));
+        }
+        float a, b;
+        f2_unpack(f2_add(acc[0], acc[1]), a, b);
+        return a + b;
+    }
+
     // ---- the weights: thread = key of half h's tile ----
     __device__ __forceinline__ void weigh(int h, int wq) const
     {
@@ -352,13 +406,17 @@ struct KwTile {
         const int key = 32 * wq + lane;
         const uint32_t aS = (uint32_t)(2 * h) * kChTile + ((uint32_t)(32 * wq) << 16);
         const float scale = p.scale_log2 * 0.6931471805599453f;
-        const uint64_t scale2 = f2_pack(scale, scale), log2e = f2_pack(1.4426950408889634f, 1.4426950408889634f);
+        const uint64_t scale2 = f2_pack(scale, scale);
         int s = 0, n = 0;
 #pragma unroll 1
         for (int seq = 0;; ++seq) {
             const KwItem it = item(seq);
             if (it.n < 0) break;
             const int keys = it.keys(h), j = it.b * kKwKeys + h * kChTile + key;   // the thread's key
+            const int64_t place_of = ((int64_t)it.r * p.nkv + it.g) * p.max_blocks * kPageSlots + j;
+            const bool whole = it.n == it.of && key < keys;
+            // (on its way while the rows are weighed)
+            const float held = p.decay != 0.f && whole ? p.weights[place_of] : 0.f;
             float total = 0.f;
 #pragma unroll 1
             for (int i = 0; i < it.n; ++i, ++s) {
@@ -374,30 +432,11 @@ struct KwTile {
                     __syncwarp();
                     tc_fence_after();
                     float sum = 0.f;
+                    int c = 0;
 #pragma unroll 1
-                    for (int c = 0; c < rows; c += 16) {
-                        uint32_t x[16];
-                        ch_load16(aS + (n & 1) * kChTile + c, x);
-                        uint64_t acc = 0;
-                        const bool all = plain && c + 16 <= rows;
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 z = *reinterpret_cast<const float4 *>(lse + c + e);
-                            float y[4];
-                            // the difference first: near 0 the weight then has all of its bits
-                            f2_unpack(f2_mul(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, f2_pack(z.x, z.y)), log2e), y[0], y[1]);
-                            f2_unpack(f2_mul(f2_fma(f2_pack(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), scale2, f2_pack(z.z, z.w)), log2e), y[2], y[3]);
-#pragma unroll
-                            for (int i4 = 0; i4 < 4; ++i4) {
-                                y[i4] = a2_ex2(y[i4]);
-                                if (!all && (c + e + i4 < from || c + e + i4 >= rows)) y[i4] = 0.f;
-                            }
-                            acc = f2_add(acc, f2_add(f2_pack(y[0], y[1]), f2_pack(y[2], y[3])));
-                        }
-                        float a, b;
-                        f2_unpack(acc, a, b);
-                        sum += a + b;
-                    }
+                    for (; plain && c + 32 <= rows; c += 32) sum += weigh_rows<true>(aS + (n & 1) * kChTile, lse, c, from, rows, scale2);
+#pragma unroll 1
+                    for (; c < rows; c += 16) sum += weigh_rows<false>(aS + (n & 1) * kChTile, lse, c, from, rows, scale2);
                     total += sum;
                     tc_fence_before();
                     __syncwarp();
@@ -414,8 +453,7 @@ struct KwTile {
                     kp.ws[(int64_t)part * kKwKeys + h * kChTile + key] = total;
                     if (h == 0 && key == 0) kp.ws_bad[part] = bad;
                 } else if (key < keys && !bad) {
-                    const int64_t at = ((int64_t)it.r * p.nkv + it.g) * p.max_blocks * kPageSlots + j;
-                    p.out_weights[at] = p.decay == 0.f ? total : fmaf(p.decay, p.weights[at], total);
+                    p.out_weights[place_of] = p.decay == 0.f ? total : fmaf(p.decay, held, total);
                 }
             }
             done(seq);
