@@ -59,7 +59,7 @@ extern "C" {
 #define QKVF_ERR_SIZES 7         /* cos_sin_rows < 1, num_pages < 1, or too large */
 #define QKVF_ERR_VARIANT 8       /* an explicit variant that this shape cannot use */
 #define QKVF_ERR_ARG 9           /* any other bad argument */
-#define QKVF_ERR_LAYOUT 10       /* head counts, head_dim, rotary width, dtype or strides (rope*, prefix_attn) */
+#define QKVF_ERR_LAYOUT 10       /* head counts, head_dim, rotary width, dtype or strides (rope*, norm_rope*, prefix_attn, chunk_attn, key_weights, kv_evict) */
 
 /* ---- device status bits (qkv_front_status) ------------------------------- */
 #define QKVF_STATUS_BAD_SLOT 1u      /* a slot >= num_pages * 16: that token's insert skipped */
@@ -665,8 +665,8 @@ size_t chunk_attn_workspace_bytes(int T, int num_reqs, int q_heads, int num_kv_h
  * step's rows, kept from step to step:
  *   out[r][g][j] = decay weights[r][g][j] + sum of exp(scale q . k_j - lse)
  * over the request's tokens that see key j (its last `window` tokens only, 0:
- * all) and the q heads of KV head g.  q, starts, block_table, context_lens, the
- * cache and the limits as for chunk_attn; lse [T, q_heads] as it gave it (a row
+ * all) and the q heads of KV head g.  q (its strides above 0), starts,
+ * block_table, context_lens, the cache and the limits as for chunk_attn; lse [T, q_heads] as it gave it (a row
  * of lse -infinity adds nothing).
  *   weights, out [num_reqs, num_kv_heads, 16 max_blocks] fp32; out may be
  *            weights itself, otherwise it must not overlap it.  Keys below a

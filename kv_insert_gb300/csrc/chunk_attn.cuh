@@ -8,8 +8,9 @@
 // chunk_tile_kernel, one CTA per SM.  A request's rows (token, q head of a KV
 // head) are cut into blocks of 256, two tensor-memory tiles, each the work of a
 // group of four softmax warps (a thread per row) and an MMA warp; both tiles
-// take the same keys, 128 a step, from one ring that a producer warp fills (TMA,
-// a swizzled box for K and one for V of every page).  A block of 128 rows or
+// take the same keys, 128 a step, from one ring that two producer warps fill, one
+// with K and one with V (TMA, a swizzled box of every page each).  The producer of
+// K also hands the CTA's items out.  A block of 128 rows or
 // fewer (decode) is one tile whose even steps are the first group's and whose
 // odd ones the second's, joined at its end.  Lengths are on the device:
 // chunk_plan_kernel, one CTA, adds the requests' costs up and cuts the line of
@@ -23,8 +24,8 @@
 // and the next S the other ones, made meanwhile; with heads of 128 S, O and the
 // weights fill tensor memory, and the next S follows the product.
 //
-// A checker warp looks at V before its product where a step ends behind the keys
-// or holds keys that not every row of the block sees: slots behind the keys
+// The producer of V looks at it before its product where a step ends behind the
+// keys or holds keys that not every row of the block sees: slots behind the keys
 // become 0, and so do infinities and NaN among the others (0 x infinity is not
 // 0), which are added at the block's end for the rows that see them.
 

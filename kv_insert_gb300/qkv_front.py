@@ -1277,8 +1277,8 @@ def key_weights(q, kv_cache, lse, starts, block_table, context_lens, weights, wo
     added to what it had: out[r, g, j] = decay weights[r, g, j] + the sum of
     exp(scale q . k_j - lse) over the request's tokens that see key j (its last
     `window` tokens only, 0: all) and the q heads of KV head g.  q, kv_cache,
-    starts, block_table, context_lens, scale as for chunk_attn, lse as it gave it;
-    weights fp32 [num_reqs, num_kv_heads, 16 max_blocks]; out None: in place.
+    starts, block_table, context_lens, scale as for chunk_attn (q's strides above
+    0: no expanded q), lse as it gave it; weights fp32 [num_reqs, num_kv_heads, 16 max_blocks]; out None: in place.
     Only keys below a request's length are written.  decay 0 starts anew and does
     not read weights (which may be None where out is given).  workspace: uint8,
     key_weights_workspace_bytes long.  Returns out."""

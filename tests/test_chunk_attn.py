@@ -82,6 +82,7 @@ def test_own_refusals(lib):
         assert weights_call(lib, dec=dec) == 9
     assert weights_call(lib, w=0) == 3 and weights_call(lib, lse=0) == 3 and weights_call(lib, w=OW + 64) == 9
     assert weights_call(lib, w=WS) == 9
+    assert weights_call(lib, qt=0) == 10 and weights_call(lib, qh=0) == 10   # (a copy's strides are above 0)
     if not torch.cuda.is_available():
         assert chunk_call(lib, lse=0) in (5, 6)
         assert weights_call(lib, w=OW) in (5, 6) and weights_call(lib, w=0, dec=0.0) in (5, 6)

@@ -158,6 +158,18 @@ def test_long(dev, weights, in_place):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("lens", [[37, 130, 2], [20001, 18432, 18433]])
+def test_weights_off_the_16_byte_grid(dev, lens, in_place):
+    c = Case(lens, 2, 64, BF, 30, seed=3)
+    room = torch.empty(c.w.numel() + 1, device="cuda")
+    w = room[1:].view(c.w.shape).copy_(c.w)
+    c.w = w
+    c.check(7, in_place)
+    assert qf.status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("seed", range(8))
 def test_drawn(dev, seed):
     rng = random.Random(seed)
