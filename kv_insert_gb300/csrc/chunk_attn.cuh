@@ -634,12 +634,16 @@ struct ChTile {
                 if (active) {   // the previous item is done: its Q is no longer read
                     const uint16_t *src = valid ? static_cast<const uint16_t *>(p.q) + ((int64_t)it.row0 + tok) * p.q_ts + head * p.q_hs
                                                 : nullptr;
-#pragma unroll 8
+#pragma unroll 4
                     for (int i = 0; i < kRowTurns; ++i) {   // whole rows: few lines an access
                         const int r = i * kRowsAtOnce + lane / (D / 8), c = lane % (D / 8);
-                        const uint4 *x = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, (unsigned long long)src, r));
-                        *chunk(sq, 32 * wq + r, c) = x ? x[c] : make_uint4(0u, 0u, 0u, 0u);
+                        const uint16_t *x = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, (unsigned long long)src, r));
+                        // (all of them on their way at once; zeros for a row of none)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(chunk(sq, 32 * wq + r, c))),
+                                     "l"(x ? x + c * 8 : static_cast<const uint16_t *>(p.q)), "r"(x ? 16 : 0)
+                                     : "memory");
                     }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 mbar_arrive(sb + LY.qready + 8 * w);
