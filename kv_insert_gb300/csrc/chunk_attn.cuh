@@ -32,8 +32,8 @@
 // What bounds it: for long rows the step of 256 x 128 (3,100 to 3,600 clocks with
 // heads of 128, of them 2,048 of products, the rest softmax and hand-overs that
 // do not overlap them): three prompts of up to 8192 tokens, 8 x 4 heads of 128,
-// 498 us, 1.1 PFLOP/s.  For single tokens bytes: 64 requests of up to 4096 keys,
-// 104 us, 5.6 TB/s.  A CTA's warps run six programs: their code has to stay in
+// 468 us, 1.2 PFLOP/s.  For single tokens bytes: 64 requests of up to 4096 keys,
+// 103 us, 5.6 TB/s.  A CTA's warps run six programs: their code has to stay in
 // the instruction cache (157 KB of it took twice the time of 55).
 
 #include "chunk_plan.h"

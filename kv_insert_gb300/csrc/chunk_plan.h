@@ -23,10 +23,10 @@ constexpr int kChTile = 128;     // rows of one tile; a block of no more has one
 // end, in keys x q heads (so that a block's own 256 rows are 256 of them).  A
 // block of one tile shares its keys between the two groups of warps that
 // otherwise take a tile each: 3 of 4 of a whole block's cost a key.  (kChOver
-// 192 / 448 / 704 / 960: 615 / 526 / 498 / 507 us for three prompts of up to 8192
-// tokens, 233 / 220 / 218 / 221 for chunks beside single tokens, 117 / 104 / 104 /
-// 105 for 64 single tokens.)
-constexpr int kChOver = 704;
+// 448 / 576 / 704: 468 / 472 / 475 us for three prompts of up to 8192 tokens, 208 /
+// 208 / 210 for chunks beside single tokens, 103 / 104 / 103 for 64 single tokens;
+// 192, with a slower start of an item, a fifth more than the best.)
+constexpr int kChOver = 448;
 constexpr int kChWhole = 4, kChHalf = 3;
 
 struct ChRequest {
