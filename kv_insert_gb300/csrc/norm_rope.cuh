@@ -6,7 +6,9 @@
 // of its first rot columns by the token's position (rope.cuh):
 //   y = R(p) (w * x r).
 // Its gradients, with g' = R(-p) g, u = w * g' and mean over the D columns:
-//   dx = r u - x r^3 mean(u * x),   dw = sum over tokens and heads of g' * x r.
+//   dx = r u - x r^3 mean(u * x),   dw = sum over tokens and heads of g' * x r,
+// the second term as (x r) (r (r mean(u * x))): r^3 by itself leaves FP32 for
+// rows of 1e13 and more, or of 1e-13 and less with a small eps, dx does not.
 // r is formed again from x, which dx and dw need anyway: nothing is kept
 // between the two directions.
 //
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(256, kUnits == 1 ? 2 : 1) norm_back_vec_kernel
         ss = norm_group_sum(ss + odd, p, sl);
         f2_unpack(dots, dot, odd);
         dot = norm_group_sum(dot + odd, p, sl);
-        const float rs = rsqrtf(fmaf(ss, inv_dim, p.eps)), back = rs * rs * rs * (dot * inv_dim);
+        const float rs = rsqrtf(fmaf(ss, inv_dim, p.eps)), back = rs * (rs * dot * inv_dim);
         S *dst = static_cast<S *>(r.out) + cur.t * r.o_ts + cur.h * r.o_hs;
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
@@ -560,9 +562,9 @@ __global__ void __launch_bounds__(256, kUnits == 1 ? 2 : 1) norm_back_vec_kernel
                 norm_unpack<E>(xs, x);
 #pragma unroll
                 for (int e = 0; e < vec; e += 2) {
-                    const uint64_t x2 = norm_two(x + e), gg = norm_two(gs + e);
-                    f2_unpack(f2_fma(gg, f2_mul(x2, r2), norm_two(ds + e)), ds[e], ds[e + 1]);
-                    f2_unpack(f2_fma(x2, back2, f2_mul(r2, f2_mul(gg, norm_two(ws + e)))), y[e], y[e + 1]);
+                    const uint64_t n2 = f2_mul(norm_two(x + e), r2), gg = norm_two(gs + e);
+                    f2_unpack(f2_fma(gg, n2, norm_two(ds + e)), ds[e], ds[e + 1]);
+                    f2_unpack(f2_fma(n2, back2, f2_mul(r2, f2_mul(gg, norm_two(ws + e)))), y[e], y[e + 1]);
                 }
             };
             half(cur.xa[k], g[k], wa[k], da[k]);
@@ -643,11 +645,11 @@ __global__ void __launch_bounds__(256) norm_back_element_kernel(const __grid_con
         ss = norm_sum(ss, 32);
         dot = norm_sum(dot, 32);   // (the whole row is read before any of it is written)
         const float inv_dim = 1.f / (float)r.dim;
-        const float rs = rsqrtf(fmaf(ss, inv_dim, p.eps)), back = rs * rs * rs * (dot * inv_dim);
+        const float rs = rsqrtf(fmaf(ss, inv_dim, p.eps)), back = rs * (rs * dot * inv_dim);
         const auto put = [&](int c, float g) {
-            const float x = E::get(xp[c]);
-            dw[c] = fmaf(g, x * rs, dw[c]);
-            dst[c] = E::put(fmaf(-x, back, rs * (g * norm_weight<E>(p.qw, p.qw_fp32, c))));
+            const float n = E::get(xp[c]) * rs;
+            dw[c] = fmaf(g, n, dw[c]);
+            dst[c] = E::put(fmaf(-n, back, rs * (g * norm_weight<E>(p.qw, p.qw_fp32, c))));
         };
         each([&](int ca, float a, int cb, float b) {
             put(ca, a);

@@ -499,3 +499,35 @@ def test_same_numbers_with_and_without_the_cache(dev):
     assert "weight" in qf.norm_rope_unsupported(x, w.double(), pos, cs, x)
     assert "workspace" in qf.norm_rope_backward_unsupported(x, x, w, pos, cs, torch.empty_like(x), w.clone(),
                                                             torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def check_scaled(dx, grad, x, w, pos, cs, layout, eps):
+    """As check_grads, without an absolute term: the gradient may be of any size."""
+    g, gm = turn(grad.double(), cs[pos], layout, -1.0)
+    X, W = x.double(), w.double()
+    r = (X.square().mean(-1, keepdim=True) + eps).rsqrt()
+    n = X * r
+    ref = r * (g * W - n * (g * W * n).mean(-1, keepdim=True))
+    mags = r * (gm * W.abs() + n.abs() * (gm * W.abs() * n.abs()).mean(-1, keepdim=True))
+    tol = torch.finfo(dx.dtype).eps / 2 * ref.abs() + 4 * ROUND * mags
+    assert dx.isfinite().all()
+    assert ((dx.double() - ref).abs() <= tol).all(), float(((dx.double() - ref).abs() / tol).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", [BF, FL])
+@pytest.mark.parametrize("size,eps", [(1e-18, 0.0), (1e-15, 0.0), (1e-15, 1e-30), (1e-13, 0.0), (1.0, 0.0), (1e13, 1e-6),
+                                      (1e16, 1e-6), (1e17, 1e-6)])
+def test_gradients_at_the_ends_of_the_range(dev, size, eps, dtype, layout):
+    """r^3 alone leaves FP32 long before the gradient does (r is 1e18 to 1e-17 here; the squares stay in range):
+    chunks of a head, half pairs through shared memory, rows off the 16-byte grid."""
+    for T, H, D, rot in ((7, 3, 64, 64), (6, 5, 24, 12), (5, 2, 130, 82)):
+        x, w, pos, cs, grad = inputs(T, H, D, rot, FL)
+        x = (size * x / x.square().mean(-1, keepdim=True).sqrt()).to(dtype)
+        w, grad = w.to(dtype), grad.to(dtype)
+        dx, dw = qf.norm_rope_backward(grad, x, w, pos, cs, eps=eps, layout=layout)
+        check_scaled(dx, grad, x, w, pos, cs, layout, eps)
+        g, gm = turn(grad.double(), cs[pos], layout, -1.0)
+        n = x.double() * (x.double().square().mean(-1, keepdim=True) + eps).rsqrt()
+        close(dw, (g * n).sum((0, 1)), (gm * n.abs()).sum((0, 1)), FL, 512 * 2.0 ** -24 + 4 * ROUND)
