@@ -667,7 +667,7 @@ size_t chunk_attn_workspace_bytes(int T, int num_reqs, int q_heads, int num_kv_h
  * over the request's tokens that see key j (its last `window` tokens only, 0:
  * all) and the q heads of KV head g.  q (its strides above 0), starts,
  * block_table, context_lens, the cache and the limits as for chunk_attn; lse [T, q_heads] as it gave it (a row
- * of lse -infinity adds nothing).
+ * of lse -infinity adds nothing, whatever its q holds).
  *   weights, out [num_reqs, num_kv_heads, 16 max_blocks] fp32; out may be
  *            weights itself, otherwise it must not overlap it.  Keys below a
  *            length are written, others left as they were.  decay in [0, 1];

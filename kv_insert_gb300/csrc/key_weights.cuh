@@ -15,7 +15,7 @@
 //
 // Rows arrive by TMA, as many whole tokens of the KV head's q heads as a step
 // has room for; lse beside them.  Rows of a step that no token of the request
-// has are not counted, whatever they hold.
+// has, and rows of lse -infinity, are not counted, whatever they hold.
 //
 // What bounds it: with many rows the exponentials' issue (64 tokens x 4 heads a
 // KV head of 128, 2 requests of up to 32K keys: 37 us, 2.0 T exponentials a second; half
@@ -57,7 +57,7 @@ struct KwItem {
 static_assert(sizeof(KwItem) == 64, "four 16-byte words");
 
 struct KwSmem {
-    uint32_t keys, rows, lse, kfull, kempty, rfull, rempty, sfull, sfree, ifull, iempty, drain, tmem, dead, items, total;
+    uint32_t keys, rows, lse, out, kfull, kempty, rfull, rempty, sfull, sfree, ifull, iempty, drain, tmem, dead, items, total;
 };
 
 template <int D>
@@ -72,6 +72,8 @@ __host__ __device__ constexpr KwSmem kw_smem()
     off += Sh::blocks * Sh::rows_bytes;
     L.lse = off;
     off += Sh::blocks * kChTile * 4;
+    L.out = off;     // whether a step has rows that are left out (lse -infinity)
+    off += Sh::blocks * 4;
     L.kfull = off;
     off += Sh::tiles * 8;
     L.kempty = off;
@@ -309,6 +311,14 @@ struct KwTile {
 #pragma unroll
                 for (int e = 0; e < kChTile / 32; ++e)   // a row that sees no key (-infinity) adds nothing to any
                     dst[32 * e + lane] = lse[e] == -INFINITY ? -INFINITY : -lse[e];
+                bool out = false;   // (here: until now the loads were on their way)
+#pragma unroll
+                for (int e = 0; e < kChTile / 32; ++e) {
+                    const int m = 32 * e + lane;
+                    out |= lse[e] == -INFINITY && m < kp.rows && t0 + m / p.group < it.tokens;
+                }
+                out = __any_sync(0xffffffffu, out);
+                if (lane == 0) reinterpret_cast<int *>(smem + LY.out)[st] = out;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar);
                 if (pa_elect()) {
@@ -374,8 +384,9 @@ struct KwTile {
     }
 
     // The weights of rows from c on, of one key: added up (all 32 of them, or of 16 those from..rows - 1: the
-    // choice row by row costs more than the weights)
-    template <bool all>
+    // choice row by row costs more than the weights; out: and without those of lse -infinity, whose scores
+    // may be NaN)
+    template <bool all, bool out>
     __device__ __forceinline__ float weigh_rows(uint32_t aS, const float *lse, int c, int from, int rows, uint64_t scale2) const
     {
         const uint64_t log2e = f2_pack(1.4426950408889634f, 1.4426950408889634f);
@@ -397,6 +408,7 @@ struct KwTile {
             for (int i = 0; i < 4; ++i) {
                 y[i] = a2_ex2(y[i]);
                 if (!all && (c + e + i < from || c + e + i >= rows)) y[i] = 0.f;
+                if (out && (i == 0 ? z.x : i == 1 ? z.y : i == 2 ? z.z : z.w) == -INFINITY) y[i] = 0.f;
             }
             acc[0] = f2_add(acc[0], f2_pack(y[0], y[1]));
             acc[1] = f2_add(acc[1], f2_pack(y[2], y[3]));
@@ -433,7 +445,8 @@ struct KwTile {
                     const int t0 = token(it, i), rows = min(kp.rows, (it.tokens - t0) * p.group);
                     // the first row that sees the key
                     const int from = (j - (it.L - it.tokens) - t0) * p.group;
-                    const bool plain = !__any_sync(0xffffffffu, from > 0);
+                    const bool out = reinterpret_cast<const volatile int *>(smem + LY.out)[s % Sh::blocks] != 0;
+                    const bool plain = !__any_sync(0xffffffffu, from > 0 || out);
                     const float *lse = reinterpret_cast<const float *>(smem + LY.lse) + (s % Sh::blocks) * kChTile;
                     wait(LY.sfull + 16 * h + 8 * (n & 1), n / 2);
                     __syncwarp();
@@ -441,9 +454,13 @@ struct KwTile {
                     float sum = 0.f;
                     int c = 0;
 #pragma unroll 1
-                    for (; plain && c + 32 <= rows; c += 32) sum += weigh_rows<true>(aS + (n & 1) * kChTile, lse, c, from, rows, scale2);
+                    for (; plain && c + 32 <= rows; c += 32)
+                        sum += weigh_rows<true, false>(aS + (n & 1) * kChTile, lse, c, from, rows, scale2);
 #pragma unroll 1
-                    for (; c < rows; c += 16) sum += weigh_rows<false>(aS + (n & 1) * kChTile, lse, c, from, rows, scale2);
+                    for (; !out && c < rows; c += 16)
+                        sum += weigh_rows<false, false>(aS + (n & 1) * kChTile, lse, c, from, rows, scale2);
+#pragma unroll 1
+                    for (; c < rows; c += 16) sum += weigh_rows<false, true>(aS + (n & 1) * kChTile, lse, c, from, rows, scale2);
                     total += sum;
                     tc_fence_before();
                     __syncwarp();

@@ -561,6 +561,25 @@ def test_weights_of_keys_with_odd_values(dev):
     assert torch.equal(got[1, :, :2], want[1, :, :2])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("D,group", [(64, 4), (128, 8), (64, 64)])
+def test_rows_of_lse_minus_infinity(dev, D, group, value):
+    """A row of lse -infinity adds nothing, whatever its q holds."""
+    b = Batch([(70, 400), (1, 50), (2, 300)], 2, group, D, BF)
+    b.attn(lse=b.lse)
+    b.lse[3] = b.lse[30:36] = b.lse[70] = -math.inf
+    b.lse[71, 1] = -math.inf
+    for window in (0, 64):
+        want = b.weights(torch.zeros(3, 2, b.mb * PAGE, device="cuda"), window=window)
+        assert want[0, :, :300].isfinite().all() and (want[1, :, :50] == 0).all()
+        q = b.q
+        b.q = b.q.clone()
+        b.q[3], b.q[30:36], b.q[70], b.q[71, 1] = value, value, value, value
+        assert torch.equal(b.weights(torch.zeros_like(want), window=window), want)
+        b.q = q
+
+
 # ---- together ----------------------------------------------------------------
 
 @pytest.mark.gpu
