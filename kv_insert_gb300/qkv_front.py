@@ -1036,10 +1036,9 @@ class _NormRotation(torch.autograd.Function):
         if grad.stride(-1) != 1:   # the gradient of a sum, say: one value, expanded
             grad = grad.contiguous()
         eps, layout = ctx.how
-        form = weight is not None and ctx.needs_input_grad[1]
-        dw = torch.empty_like(weight) if form else None
+        dw = torch.empty_like(weight) if weight is not None and ctx.needs_input_grad[1] else False
         dx, dw = norm_rope_backward(grad, x, weight, positions, cos_sin, eps=eps, layout=layout, grad_weight=dw)
-        return dx, dw if form else None, None, None, None, None
+        return dx, dw, None, None, None, None
 
 
 def _norm_rope_with_grad(x, weight, positions, cos_sin, out, eps, layout, stream):
@@ -1119,15 +1118,17 @@ def norm_rope_backward(grad_out, x, weight, positions, cos_sin, eps: float = 1e-
     """The gradients of norm_rope with respect to x and weight, from the gradient
     of its output and its x.  grad_x=grad_out writes it in place; None: a new
     tensor.  grad_weight [head_dim] (fp32 or x's dtype) is written, not added to;
-    None: a new fp32 tensor (no gradient where weight is None).  workspace:
-    uint8, norm_rope_backward_workspace_bytes long; None: made by the call.  A
-    token whose position is no row of cos_sin keeps what grad_x held (zeros in
-    one made by the call) and adds nothing to grad_weight.  Returns
-    (grad_x, grad_weight)."""
+    None: a new fp32 tensor (no gradient where weight is None); False: not formed.
+    workspace, for the weight's gradient: uint8, norm_rope_backward_workspace_bytes
+    long; None: made by the call.  A token whose position is no row of cos_sin
+    keeps what grad_x held (zeros in one made by the call) and adds nothing to
+    grad_weight.  Returns (grad_x, grad_weight or None)."""
     flags = 0
     if grad_x is None:
         grad_x, flags = _new(x.shape, x.dtype, x.device, stream), DTYPE_ZERO_SKIPPED
-    if weight is not None:
+    if grad_weight is False:
+        grad_weight = None
+    elif weight is not None:
         if grad_weight is None:
             grad_weight = _new(weight.shape, torch.float32, x.device, stream)
         if workspace is None and x.is_cuda and x.dim() == 3:

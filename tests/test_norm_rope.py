@@ -531,3 +531,19 @@ def test_gradients_at_the_ends_of_the_range(dev, size, eps, dtype, layout):
         g, gm = turn(grad.double(), cs[pos], layout, -1.0)
         n = x.double() * (x.double().square().mean(-1, keepdim=True) + eps).rsqrt()
         close(dw, (g * n).sum((0, 1)), (gm * n.abs()).sum((0, 1)), FL, 512 * 2.0 ** -24 + 4 * ROUND)
+
+
+@pytest.mark.gpu
+def test_no_weight_gradient(dev, monkeypatch):
+    """grad_weight=False: none is formed (nor by a graph whose weight needs none), and x's gradient is the same."""
+    x, w, pos, cs, grad = inputs(33, 4, 64, 64, BF)
+    dx, dw = qf.norm_rope_backward(grad, x, w, pos, cs)
+    seen, run = [], qf._run
+    monkeypatch.setattr(qf, "_run", lambda name, index, args, stream: (seen.append((name, args)), run(name, index, args, stream)))
+    got, none = qf.norm_rope_backward(grad, x, w, pos, cs, grad_weight=False)
+    assert none is None and torch.equal(got, dx)
+    x.requires_grad_()
+    qf.norm_rope(x, w, pos, cs).backward(grad)
+    assert torch.equal(x.grad, dx)
+    backs = [args for name, args in seen if name == "norm_rope_backward"]
+    assert len(backs) == 2 and all(a[14] == 0 and a[23] == 0 and a[24] == 0 for a in backs)   # dw, workspace, its bytes
