@@ -676,6 +676,15 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _wrote(*tensors) -> None:
+    """Count a change of the caller's tensors that a call writes: a graph of
+    rope or norm_rope that saved one of them must not use what it holds now."""
+    if _Rotation.used:
+        for t in tensors:
+            if t is not None and not t.is_inference():
+                torch.autograd.graph.increment_version(t)
+
+
 _MOST = 1 << 30   # the C ABI's sizes are ints
 
 
@@ -756,8 +765,8 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: str = "n
     elif (not out.is_cuda or out.dtype != torch.float32 or tuple(out.shape) != (rows, rot_dim)
           or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous fp32 CUDA tensor [{rows}, {rot_dim}]")
-    elif _Rotation.used and not out.is_inference():
-        torch.autograd.graph.increment_version(out)   # a graph that rope saved the old table for must not use this one
+    else:
+        _wrote(out)
     if magnitude is None:
         magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "ramp" and factor > 0 else 1.0
     _run("rope_table", out.device.index,
@@ -832,6 +841,8 @@ def _rope(x, positions, cos_sin, out, layout, inverse, stream):
         out, flags = _new(x.shape, x.dtype, x.device, stream), DTYPE_ZERO_SKIPPED
     args = _rope_args(x, positions, cos_sin, out, layout, inverse, flags)
     _run("rope", x.get_device(), args, stream)
+    if not flags:
+        _wrote(out)
     return out
 
 
@@ -905,6 +916,8 @@ def rope_kv_append(q, k, v, positions, slots, cos_sin, kv_cache, q_out=None,
         q_out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED
     args = _append_args(q, k, v, positions, slots, cos_sin, kv_cache, q_out, layout, flags)
     _run("rope_kv_append", k.get_device(), args, stream)
+    if not flags:
+        _wrote(q_out)
     return q_out
 
 
@@ -973,6 +986,8 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens
     args = _prefix_args(q, kv_cache, prefix_pages, prefix_len, block_table, context_lens, workspace, q_len,
                         scale, out, lse, flags)
     _run("prefix_attn", q.get_device(), args, stream)
+    if not flags:
+        _wrote(out)
     return out
 
 
@@ -1068,6 +1083,8 @@ def _norm_rope(x, weight, positions, cos_sin, out, eps, layout, stream):
     if out is None:
         out, flags = _new(x.shape, x.dtype, x.device, stream), DTYPE_ZERO_SKIPPED
     _run("norm_rope", x.get_device(), _norm_args(x, weight, positions, cos_sin, out, eps, layout, flags), stream)
+    if not flags:
+        _wrote(out)
     return out
 
 
@@ -1141,6 +1158,7 @@ def norm_rope_backward(grad_out, x, weight, positions, cos_sin, eps: float = 1e-
             workspace = _new((n,), torch.uint8, x.device, stream)
     args = _norm_back_args(grad_out, x, weight, positions, cos_sin, grad_x, grad_weight, workspace, eps, layout, flags)
     _run("norm_rope_backward", x.get_device(), args, stream)
+    _wrote(None if flags else grad_x, grad_weight)
     return grad_x, grad_weight
 
 
@@ -1177,6 +1195,8 @@ def norm_rope_kv_append(q, k, v, q_weight, k_weight, positions, slots, cos_sin, 
         q_out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED
     args = _norm_append_args(q, k, v, q_weight, k_weight, positions, slots, cos_sin, kv_cache, q_out, eps, layout, flags)
     _run("norm_rope_kv_append", k.get_device(), args, stream)
+    if not flags:
+        _wrote(q_out)
     return q_out
 
 
@@ -1247,6 +1267,8 @@ def chunk_attn(q, kv_cache, starts, block_table, context_lens, workspace, scale=
         out, flags = _new(q.shape, q.dtype, q.device, stream), DTYPE_ZERO_SKIPPED
     args = _chunk_args(q, kv_cache, starts, block_table, context_lens, workspace, scale, out, lse, flags)
     _run("chunk_attn", q.get_device(), args, stream)
+    if not flags:
+        _wrote(out)
     return out
 
 

@@ -547,3 +547,36 @@ def test_no_weight_gradient(dev, monkeypatch):
     assert torch.equal(x.grad, dx)
     backs = [args for name, args in seen if name == "norm_rope_backward"]
     assert len(backs) == 2 and all(a[14] == 0 and a[23] == 0 and a[24] == 0 for a in backs)   # dw, workspace, its bytes
+
+
+@pytest.mark.gpu
+def test_written_tensors_that_a_graph_holds(dev):
+    """A graph saves x and the weight; a call that overwrites them is seen by its backward pass, as torch's own
+    in-place operations are."""
+    def graph():
+        x, w, pos, cs, grad = inputs(6, 4, 64, 64, BF)
+        x.requires_grad_()
+        return qf.norm_rope(x, w, pos, cs), x.detach(), w, pos, cs, grad
+    cache = torch.zeros(4, 4, 16, 128, dtype=BF, device="cuda")
+    slots, starts = torch.arange(6, device="cuda"), torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(qf.chunk_attn_workspace_bytes(6, 1, 4, 4, 64, 1), qf.prefix_attn_workspace_bytes(1, 6, 4, 4, 64, 0, 1)),
+                     dtype=torch.uint8, device="cuda")
+    for write in (lambda x, w, p, c, g: qf.norm_rope(x, w, p, c, out=x),
+                  lambda x, w, p, c, g: qf.rope(x, p, c, out=x),
+                  lambda x, w, p, c, g: qf.norm_rope_backward(g, g.clone(), w, p, c, grad_x=x),
+                  lambda x, w, p, c, g: qf.norm_rope_backward(g, x, w.clone(), p, c, grad_weight=w),
+                  lambda x, w, p, c, g: qf.rope_kv_append(g, g, g, p, slots, c, cache, q_out=x),
+                  lambda x, w, p, c, g: qf.norm_rope_kv_append(g, g, g, w, w, p, slots, c, cache, q_out=x),
+                  lambda x, w, p, c, g: qf.chunk_attn(g, cache, starts, table, starts[1:], ws, out=x),
+                  lambda x, w, p, c, g: qf.prefix_attn(g, cache, None, None, table, starts[1:], ws, q_len=6, out=x)):
+        y, x, w, pos, cs, grad = graph()
+        write(x, w, pos, cs, grad)
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward(grad)
+    y, x, w, pos, cs, grad = graph()   # reading them is no change
+    qf.norm_rope(x, w, pos, cs)
+    y.backward(grad)
+    with torch.inference_mode():
+        z = torch.zeros_like(grad)
+        qf.norm_rope(grad, w, pos, cs, out=z)
