@@ -22,6 +22,7 @@ import struct
 import threading
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _build
 
@@ -685,6 +686,15 @@ def _wrote(*tensors) -> None:
                 torch.autograd.graph.increment_version(t)
 
 
+def _no_tangent(*tensors) -> None:
+    """Refuse forward-mode gradients: the result would come without a tangent."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("no forward-mode gradient is formed: call with the primal "
+                                 "(torch.autograd.forward_ad.unpack_dual)")
+
+
 _MOST = 1 << 30   # the C ABI's sizes are ints
 
 
@@ -834,6 +844,7 @@ def _rope_with_grad(x, positions, cos_sin, out, layout, inverse, stream):
 
 
 def _rope(x, positions, cos_sin, out, layout, inverse, stream):
+    _no_tangent(x, cos_sin)
     if torch.is_grad_enabled() and (x.requires_grad or cos_sin.requires_grad):
         return _rope_with_grad(x, positions, cos_sin, out, layout, inverse, stream)
     flags = 0
@@ -854,7 +865,8 @@ def rope(x, positions, cos_sin, out=None, layout: str = "interleaved", stream=No
     out=x rotates in place.  A token whose position is no row of cos_sin keeps
     what out held, or gets zeros in an out made by the call.  Without out the
     result is part of x's autograd graph; with out, or captured, a call is refused
-    where x requires a gradient (under torch.no_grad() it is not).  Returns out."""
+    where x requires a gradient (under torch.no_grad() it is not).  A tangent of
+    forward mode is refused.  Returns out."""
     return _rope(x, positions, cos_sin, out, layout, 0, stream)
 
 
@@ -1076,6 +1088,7 @@ def _norm_rope_with_grad(x, weight, positions, cos_sin, out, eps, layout, stream
 
 
 def _norm_rope(x, weight, positions, cos_sin, out, eps, layout, stream):
+    _no_tangent(x, weight, cos_sin)
     if torch.is_grad_enabled() and (x.requires_grad or cos_sin.requires_grad
                                     or (weight is not None and weight.requires_grad)):
         return _norm_rope_with_grad(x, weight, positions, cos_sin, out, eps, layout, stream)
@@ -1097,7 +1110,8 @@ def norm_rope(x, weight, positions, cos_sin, out=None, eps: float = 1e-6, layout
     whose position is no row of cos_sin keeps what out held, or gets zeros in an
     out made by the call.  Without out the result is part of the autograd graph
     of x and weight; with out, or captured, a call is refused where one of them
-    requires a gradient (under torch.no_grad() it is not).  Returns out."""
+    requires a gradient (under torch.no_grad() it is not).  A tangent of forward
+    mode is refused.  Returns out."""
     return _norm_rope(x, weight, positions, cos_sin, out, eps, layout, stream)
 
 

@@ -580,3 +580,19 @@ def test_written_tensors_that_a_graph_holds(dev):
     with torch.inference_mode():
         z = torch.zeros_like(grad)
         qf.norm_rope(grad, w, pos, cs, out=z)
+
+
+def test_forward_mode_is_refused():
+    """A tangent would be dropped without a word."""
+    x, pos, cs = torch.zeros(2, 3, 64), torch.zeros(2, dtype=torch.int64), torch.zeros(8, 64)
+    w = torch.ones(64)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(x, torch.ones_like(x))
+        wd = torch.autograd.forward_ad.make_dual(w, torch.ones_like(w))
+        for call in (lambda: qf.norm_rope(dual, w, pos, cs), lambda: qf.norm_rope(x, wd, pos, cs),
+                     lambda: qf.norm_rope(dual, None, pos, cs, out=x), lambda: qf.rope(dual, pos, cs),
+                     lambda: qf.rope_backward(dual, pos, cs)):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+        with pytest.raises(ValueError, match="CUDA"):   # no tangent: the other checks
+            qf.norm_rope(x, w, pos, cs, out=x)
