@@ -882,11 +882,11 @@ __device__ __forceinline__ void ch_plan(const RaggedParams &p, Cost cost, Locate
     const int per = (p.R + kChPlanThreads - 1) / kChPlanThreads, r0 = tid * per, r1 = min(p.R, r0 + per);
     ChRequest q;
     int64_t upto = 0;
-    for (int r = r0; r < r1; ++r) upto += cost(r, true, q);
+    for (int r = r0; r < r1; ++r) upto = ch_add(upto, cost(r, true, q));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+        if (lane >= o) upto = ch_add(upto, y);
     }
     if (lane == 31) warps[warp] = upto;
     __syncthreads();
@@ -895,12 +895,12 @@ __device__ __forceinline__ void ch_plan(const RaggedParams &p, Cost cost, Locate
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += y;
+            if (lane >= o) v = ch_add(v, y);
         }
         warps[lane] = v;
     }
     __syncthreads();
-    if (warp > 0) upto += warps[warp - 1];
+    if (warp > 0) upto = ch_add(upto, warps[warp - 1]);
     before[tid + 1] = upto;
     if (tid == 0) before[0] = 0;
     __syncthreads();

@@ -70,6 +70,14 @@ CH_HD int64_t ch_cost(const ChRequest &q, int group, int b)
            ((int64_t)group * (kChOver + ctx) + (int64_t)kChRows * ((int64_t)b + 1));
 }
 
+// A sum of costs.  A call's own are below 2^57; starts that go up and down, where
+// the same tokens count again and again, stop at 2^61.
+CH_HD int64_t ch_add(int64_t a, int64_t b)
+{
+    const int64_t most = int64_t(1) << 61;
+    return a + b < most ? a + b : most;
+}
+
 // A request's cost for one KV head
 CH_HD int64_t ch_request_cost(const ChRequest &q, int group)
 {

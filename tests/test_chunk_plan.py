@@ -194,3 +194,59 @@ def test_plan_on_the_host(tmp_path):
                     os.path.join(ROOT, "kv_insert_gb300", "csrc"), "-o", str(exe), str(src)], check=True)
     out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=600)
     assert out.returncode == 0 and out.stdout.strip().endswith("ok"), out.stdout + out.stderr
+
+
+OVERLAP = r"""
+#include "chunk_plan.h"
+#include <algorithm>
+#include <cstdio>
+#include <vector>
+using namespace qkvf;
+
+// Starts that go up and down, 0, T, 0, T ...: every other request holds all T tokens, and each of them passes by
+// itself.  Their costs add up past 64 bits; every part still starts at a place within a request.
+static int check(int R, ChRequest q, int nkv, int group)
+{
+    std::vector<int64_t> before(R + 1, 0);
+    for (int r = 0; r < R; ++r)
+        before[r + 1] = ch_add(before[r], r % 2 ? 0 : nkv * ch_request_cost(q, group));
+    const int64_t total = before[R];
+    if (total <= 0 || !std::is_sorted(before.begin(), before.end())) return 1;
+    ChPos last = {0, 0, 0, 0};
+    for (int c = 0; c <= 152; ++c) {
+        const int64_t off = ch_part(total, 152, c);
+        ChPos at = {R, 0, 0, 0};
+        if (off < total) {
+            const int r = (int)(std::upper_bound(before.begin(), before.end(), off) - before.begin()) - 1;
+            if (r < 0 || r >= R || r % 2) return 2;
+            at = ch_locate(q, group, r, off - before[r]);
+            const int steps = ch_steps(ch_keys(q, group, at.b));
+            if (at.g < 0 || at.g >= nkv || at.b < 0 || at.b >= ch_blocks(q.n, group) || at.k < 0 || at.k >= steps) return 3;
+        }
+        if (!ch_reached(at, last)) return 4;
+        last = at;
+    }
+    return 0;
+}
+
+int main()
+{
+    const int far = 1 << 24;
+    const int bad = check(65535, {0, far, far}, 1, 64) + check(65535, {0, far, far}, 64, 1) + check(65535, {0, 1 << 18, far}, 64, 64) +
+                    check(3, {0, far, far}, 1, 64) + check(2, {0, 1, 1}, 1, 1);
+    puts(bad ? "failed" : "ok");
+    return bad;
+}
+"""
+
+
+@pytest.mark.skipif(not shutil.which("g++"), reason="no g++")
+def test_starts_that_overlap(tmp_path):
+    """A sum of costs beyond 64 bits would send a part to a negative place in its table."""
+    src = tmp_path / "overlap.cpp"
+    src.write_text(OVERLAP)
+    exe = tmp_path / "overlap"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I",
+                    os.path.join(ROOT, "kv_insert_gb300", "csrc"), "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=600)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout + out.stderr
