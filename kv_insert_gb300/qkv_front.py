@@ -1333,8 +1333,8 @@ def _evict_args(kv_cache, weights, block_table, context_lens, keep, recent, out_
     if not any(given):
         out_table, out_weights, out_lens = block_table, weights, context_lens
     index, dims = kv_cache.get_device(), kv_cache.shape
-    if kv_cache.dtype not in _HALF_TYPES or kv_cache.dim() != 4 or dims[3] % 2:
-        raise ValueError(f"kv_cache must be {' or '.join(map(str, _HALF_TYPES))} "
+    if index < 0 or kv_cache.dtype not in _HALF_TYPES or kv_cache.dim() != 4 or dims[3] % 2:
+        raise ValueError(f"kv_cache must be a CUDA tensor, {' or '.join(map(str, _HALF_TYPES))} "
                          f"[pages, num_kv_heads, {PAGE_SLOTS}, 2 head_dim]")
     pc, pages, nkv = _cache(kv_cache, dims[3] // 2, kv_cache.dtype, index)
     for name, t in (("block_table", block_table), ("out_table", out_table)):

@@ -249,3 +249,17 @@ def test_reasons(dev):
     with pytest.raises(qf.QkvFrontError, match="keep"):
         qf.kv_evict(c.cache, c.w, c.table, c.context, 0)
     assert qf.kv_evict(c.cache, c.w[:0], c.table[:0], c.context[:0], 40).shape == (0, 2, 40)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_host_tensors_are_refused_before_any_launch(in_place):
+    """All of them on the host: the binding refuses the call itself, on a machine with a GPU too."""
+    cache, w = torch.zeros(4, 1, 16, 128, dtype=BF), torch.zeros(1, 1, 32)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    kept = torch.zeros(1, 1, 8, dtype=torch.int32)
+    other = {} if in_place else {"out_table": table.clone(), "out_weights": w.clone(), "out_lens": lens.clone()}
+    with pytest.raises(ValueError, match="CUDA"):
+        qf._evict_args(cache, w, table, lens, 8, 0, *(other.get(n) for n in ("out_table", "out_weights", "out_lens")), kept)
+    for k in (kept, None):
+        with pytest.raises(ValueError, match="CUDA"):
+            qf.kv_evict(cache, w, table, lens, 8, kept=k, **other)
