@@ -297,6 +297,40 @@ def test_values_that_later_tokens_alone_see(dev, D, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,group", [(64, 8), (128, 4), (128, 1), (64, 64)])
+def test_infinite_keys(dev, D, group):
+    """A column of K is infinite: the rows whose score it makes -infinity leave that key out, those whose score it
+    makes infinite are NaN, and neither reaches a neighbour."""
+    class Without(Batch):
+        def scores(self, r):
+            cache, self.cache = self.cache, self.clean
+            s, es = super().scores(r)
+            self.cache = cache
+            if r == 0:
+                s[..., self.key], es[..., self.key] = -math.inf, 0.0
+            return s, es
+
+    for n, L, key in ((70, 70, 33), (70, 400, 365), (300, 700, 20), (2, 2000, 1500), (1, 5000, 4999)):
+        b = Without([(n, L), (1, 50)], 2, group, D, BF, seed=n)
+        b.q[..., 0] = -b.q[..., 0].abs().clamp_min(0.25)
+        clean = b.attn(lse=b.lse).clone()
+        b.clean, b.key = b.cache.clone(), key
+        b.cache[int(b.table[0, key // PAGE]), :, key % PAGE, 0] = math.inf
+        none = b.attn(lse=b.lse).clone()
+        b.check_attn(none, b.lse)
+        lse = b.lse.clone()
+        up = torch.rand(b.q.shape[:2], device="cuda", generator=torch.Generator(device="cuda").manual_seed(n)) < 0.5
+        up[n:] = False
+        b.q[..., 0] = torch.where(up, -b.q[..., 0], b.q[..., 0])
+        out = b.attn(lse=b.lse)
+        assert torch.equal(out[~up], none[~up]) and torch.equal(b.lse[~up], lse[~up])
+        sees = L - n + torch.arange(n + 1, device="cuda") >= key
+        sees[n:] = False
+        assert out[up & sees[:, None]].isnan().all() and out[up & ~sees[:, None]].isfinite().all()
+        assert torch.equal(out[n:], clean[n:])
+
+
+@pytest.mark.gpu
 def test_rows_of_no_request(dev):
     """Padding requests, rows behind the last and before the first: left alone, or zeros in a new output."""
     b = Batch([(5, 40), (3, 20), (6, 90)], 2, 4, 64, BF, extra=9)

@@ -263,3 +263,55 @@ def test_host_tensors_are_refused_before_any_launch(in_place):
     for k in (kept, None):
         with pytest.raises(ValueError, match="CUDA"):
             qf.kv_evict(cache, w, table, lens, 8, kept=k, **other)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [True, False])
+def test_more_rows_than_a_grid_row(dev, in_place):
+    """33,002 rows (request, KV head): the launches take them in two grid planes, the second partly filled."""
+    R, nkv, D, L, keep = 16501, 2, 8, 11, 5
+    g = torch.Generator(device="cuda").manual_seed(0)
+    pages = torch.randperm(2 * R, generator=g, device="cuda").to(torch.int32)
+    table, other = pages[:R].view(R, 1).contiguous(), pages[R:].view(R, 1).contiguous()
+    cache = torch.randn(2 * R, nkv, PAGE, 2 * D, generator=g, device="cuda").to(BF)
+    old, w = cache.clone(), torch.rand(R, nkv, PAGE, generator=g, device="cuda")
+    old_w, lens = w.clone(), torch.full((R,), L, dtype=torch.int32, device="cuda")
+    kw, out_w, out_lens, to = {}, w, lens, table
+    if not in_place:
+        out_w, out_lens, to = torch.full_like(w, 9.0), torch.zeros_like(lens), other
+        kw = {"out_table": to, "out_weights": out_w, "out_lens": out_lens}
+    kept = qf.kv_evict(cache, w, table, lens, keep, 1, **kw)
+    order = torch.sort(old_w[:, :, :L - 1], dim=-1, descending=True, stable=True).indices[..., :keep - 1]
+    want = torch.cat([order.sort(-1).values, torch.full((R, nkv, 1), L - 1, device="cuda")], -1)
+    assert torch.equal(kept.long(), want) and (out_lens == keep).all()
+    assert torch.equal(out_w[..., :keep], old_w.gather(2, want))
+    end = L if in_place else PAGE
+    assert (out_w[..., keep:end] == 0).all() and (not in_place or torch.equal(w[..., L:], old_w[..., L:]))
+    moved = old[table[:, 0].long()].gather(2, want[..., None].expand(R, nkv, keep, 2 * D))
+    expect = old.clone()
+    expect[to[:, 0].long(), :, :keep] = moved
+    assert torch.equal(cache, expect) and qf.status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [True, False])
+def test_pages_beyond_2_31_elements(dev, in_place):
+    nkv, D, keep = 8, 128, 70
+    count = (1 << 31) // (nkv * PAGE * 2 * D) + 90
+    near = Case([300, 40, 150], nkv, D, BF, keep)
+    cache = torch.zeros(count, nkv, PAGE, 2 * D, dtype=BF, device="cuda")
+    cache[count - len(near.cache):] = near.cache.flip(0)
+    far = Case([300, 40, 150], nkv, D, BF, keep)
+    far.cache, far.table, far.out_table = cache, count - 1 - near.table, count - 1 - near.out_table
+
+    def run(c):
+        kw = {}
+        if not in_place:
+            kw = {"out_table": c.out_table, "out_weights": torch.zeros(3, nkv, c.ob * PAGE, device="cuda"),
+                  "out_lens": torch.zeros(3, dtype=torch.int32, device="cuda")}
+        return qf.kv_evict(c.cache, c.w, c.table, c.context, keep, 9, **kw)
+    near.check(9, in_place)
+    near = Case([300, 40, 150], nkv, D, BF, keep)
+    assert torch.equal(run(near), run(far)) and torch.equal(near.w, far.w) and torch.equal(near.context, far.context)
+    assert torch.equal(cache[count - len(near.cache):].flip(0), near.cache)
+    assert not cache[:count - len(near.cache)].any() and qf.status() == 0
