@@ -34,7 +34,8 @@
 // do not overlap them): three prompts of up to 8192 tokens, 8 x 4 heads of 128,
 // 468 us, 1.2 PFLOP/s.  For single tokens bytes: 64 requests of up to 4096 keys,
 // 103 us, 5.6 TB/s.  A CTA's warps run six programs: their code has to stay in
-// the instruction cache (157 KB of it took twice the time of 55).
+// the instruction cache (157 KB to half, with the producers of K and V split in
+// the same step: 667 to 595 us, 142 to 120).
 
 #include "chunk_plan.h"
 

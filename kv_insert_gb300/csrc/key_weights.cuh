@@ -17,12 +17,14 @@
 // has room for; lse beside them.  Rows of a step that no token of the request
 // has, and rows of lse -infinity, are not counted, whatever they hold.
 //
-// What bounds it: with many rows the exponentials' issue (64 tokens x 4 heads a
-// KV head of 128, 2 requests of up to 32K keys: 37 us, 2.0 T exponentials a second; half
-// of them left out changes nothing, a choice row by row costs 7 us); with single
+// What bounds it: with many rows not the exponentials (29 % of their unit; half of
+// them left out changes nothing) nor any other unit (issue 39 %, products 33 %),
+// but most likely a thread's chain of load from tensor memory, wait and weights,
+// with two computing warps a scheduler (64 tokens x 4 heads a KV head of 128, 2
+// requests of up to 32K keys: 37 us; a choice row by row costs 7 more); with single
 // tokens the 2,500 clocks of instructions that every role spends on a block (16
-// requests of up to 8K keys, 8 x 8 heads of 64: 34 us, 2.4 TB/s of keys, of it 5
-// for the plan).
+// requests of up to 8K keys, 8 x 8 heads of 64: 34 us, 2.4 TB/s of keys).  Plan
+// and merge are 5 and 3 to 4 us of each.
 
 namespace qkvf {
 

@@ -111,8 +111,7 @@ struct NormUnit {
 };
 
 // A chunk's values, and back: two at a time, as are the sums and products on
-// them (the kernels' issue slots, not their bytes, bound them otherwise: the
-// gradients of 8192 x 32 x 128 take 32 instructions a value one by one)
+// them (one by one the gradients of 8192 x 32 x 128 take 54 us instead of 50)
 template <class E, int vec>
 __device__ __forceinline__ void norm_unpack(const RopeChunk<E> &x, float (&v)[vec])
 {
@@ -207,9 +206,10 @@ __device__ __forceinline__ float norm_group_sum(float v, const NormParams &p, in
     return __shfl_sync(0xffffffffu, v, ((threadIdx.x & 31) - sl) & 31);
 }
 
-// One group of lanes takes kHeads neighbouring heads of a token.  Bound by DRAM
-// latency and the loads in flight: two CTAs an SM with four heads a lane keep
-// 64 KB on their way (8192 tokens of 32 heads of 128, 134 MB: 28 us, 4.8 TB/s;
+// One group of lanes takes kHeads neighbouring heads of a token: two CTAs an SM
+// with four heads a lane have 64 KB on their way at first, and nothing while they
+// compute and store (8192 tokens of 32 heads of 128, 134 MB: 28 to 30 us, 4.5 to
+// 4.8 TB/s, with 44 % of the issue slots used; in fp32, 268 MB: 43 us, 6.2 TB/s;
 // three CTAs with two heads a lane 31 us).
 template <class E, int kPairs, int kHeads, int kUnits>
 __global__ void __launch_bounds__(256, 2) norm_vec_kernel(const __grid_constant__ NormParams p)
@@ -392,9 +392,10 @@ __global__ void __launch_bounds__(256) norm_element_kernel(const __grid_constant
 // order and leaves one row of sums, and norm_dw_kernel adds the CTAs' rows in
 // order: a call repeats bitwise.  The next heads' chunks are on their way to
 // shared memory while one is computed (four: 128 KB an SM); two CTAs an SM.
-// Bound by the issue of some 25 instructions a value (unpacking, two sums, the
-// turn, two products of dw): values in pairs of FP32 took 54 us to 50 at 8192
-// tokens of 32 heads of 128 (201 MB, 4.0 TB/s).
+// Bound by neither bytes nor issue (46 % of the slots; 35 % with 25 heads of 80)
+// but by each round's chain: the head, then its angles, then two sums by
+// shuffles.  8192 tokens of 32 heads of 128 (201 MB): 50 us, 4.0 TB/s, and 3 for
+// norm_dw_kernel behind it (5 alone); in fp32 (403 MB) 83 us with it.
 
 constexpr int kNormAhead = 4;
 
