@@ -719,8 +719,11 @@ int64_t norm_back_ctas(int64_t rows, int sms)
 
 // The lanes of a head for its units: a power of two, at most 32, or as many as
 // units where a warp holds more heads so (5 units: six heads instead of four;
-// the sum over a head is one shuffle longer then).  4099 tokens of 25 heads of
-// 80, backward: 21.7 us, with lanes a power of two 24.2.
+// the sum over a head is one shuffle longer then).  That many lanes against a
+// power of two, us in graphs, 16.4 MB of 25 heads, bf16, forward | backward:
+//   3 units (48)  11.0 12.6 | 22.4 22.4      9 (144)  12.6 15.1 | 23.4 27.1
+//   5 (80)        11.1 12.9 | 22.6 25.6     10 (160)  10.9 12.7 | 22.4 25.2
+//   6 (96)        10.8 12.6 | 22.1 23.2
 int norm_lanes(NormParams &prm, int units)
 {
     int lanes = 1;
